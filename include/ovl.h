@@ -479,9 +479,157 @@ ovl_status ovl_check_device(ovl_ctx* ctx, void* stream);
  * faults or hangs; the next forward is normal. */
 ovl_status ovl_debug_inject(ovl_ctx* ctx, uint32_t phase, ovl_status code);
 
+/* ---- 4-bit key/value cache -------------------------------------------------
+ * What a decoder keeps between the projections above: the keys and values of
+ * the tokens seen so far, in the 4-bit blocks the base weights use, in pages
+ * that sequences share.  The source pages stop at the linear layers; every
+ * entry point of this part has no counterpart in them.
+ *
+ * The library keeps no state for a cache.  ovl_kv names caller-owned device
+ * memory (and is itself read during the call only):
+ *   codes     uint8    [n_pages][n_layers][2][n_kv_heads][page_tokens * head_dim / 2]
+ *   scales    binary16 [n_pages][n_layers][2][n_kv_heads][page_tokens][head_dim / 32]
+ *   table     int32    [max_seqs][max_pages]: the page that holds tokens
+ *             page_tokens * i .. of a sequence, -1 beyond its last page
+ *   length    int32    [max_seqs]: tokens of each sequence (0: the row is free)
+ *   refs      int32    [n_pages]: rows that hold the page (0: the page is free)
+ *   workspace          ovl_kv_workspace_bytes bytes, 256-byte aligned, zero-filled
+ *             by the caller before the first call, then left to the library
+ * Index 0 of codes' and scales' third axis holds the keys, 1 the values.  Both
+ * are q4_0 blocks: 32 consecutive channels of a token and head share a scale d,
+ * channel c is worth d * (code - 8).  The order of the 4-bit codes follows the
+ * fragments in which the attention kernels read them:
+ *   keys    a token's row (head_dim / 2 bytes) is [4][head_dim / 32] words of 4
+ *           bytes; word (w, b) holds channels 32 b + 8 w .. + 7, the first in
+ *           the lowest 4 bits;
+ *   values  8 tokens are [8][8 tokens][head_dim / 16 bytes]; unit (g, token)
+ *           holds channels g, g + 8, g + 16, ..., the first in the lowest 4 bits.
+ * head_dim: 64, 128 or 256.  page_tokens: 16, 32, 64, 128 or 256.  codes and
+ * scales 16-byte aligned.  Offsets into the pools are 64-bit.
+ * A page that is not full belongs to one row only; full pages may be shared and
+ * are never written.  ovl_kv_extend, ovl_kv_fork, ovl_kv_compact and
+ * ovl_kv_release keep this, and take the lowest-numbered free pages first, in
+ * the order of their entries, so the same calls give the same tables.
+ *
+ * A batch is n_seqs rows (seqs: device int32, distinct) whose new tokens are
+ * packed one sequence after the other: sequence i owns tokens tok_off[i] ..
+ * tok_off[i+1] - 1 (tok_off: device int32 [n_seqs + 1], tok_off[0] = 0,
+ * non-decreasing), and they are the LAST tokens of the sequence: length already
+ * counts them (ovl_kv_extend).  A step is ovl_kv_extend once, then for each layer
+ * ovl_kv_append and ovl_kv_attention.
+ *
+ * seqs, tables and lengths are read on the device, so nothing here waits for
+ * the host and every call can be captured in a CUDA graph.  What only the
+ * device can see is checked there: a row, page, length or index out of range,
+ * a row listed twice, or too few free pages is latched as a status code that
+ * ovl_kv_check returns and clears; ovl_kv_extend, _fork, _compact and _release
+ * then change nothing, ovl_kv_append writes and ovl_kv_read and
+ * ovl_kv_attention return the rest (zeros for a token that cannot be reached).
+ * Calls on one cache must be stream-ordered: they share its workspace.  They
+ * run on the current device, on `stream`, and allocate nothing.
+ * Errors of every entry point: OVL_E_ARG (null pointer, unknown dtype, layer or
+ * count out of range), OVL_E_SHAPE (dimensions, strides or alignment),
+ * OVL_E_OOM (workspace smaller than ovl_kv_workspace_bytes), OVL_E_CUDA; the
+ * message is ovl_last_error(NULL).  n_seqs = 0 and no tokens are no-ops. */
+typedef struct {
+  void* codes;
+  void* scales;
+  int32_t* table;
+  int32_t* length;
+  int32_t* refs;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t n_pages, page_tokens, n_layers, n_kv_heads, head_dim, max_seqs, max_pages;
+} ovl_kv;
+
+enum { OVL_KV_MAX_BATCH = 1024 };   /* n_seqs and entries of one call */
+
+/* Size of the workspace for kv's dimensions (its pointers are not looked at).
+ * No counterpart in the source pages. */
+ovl_status ovl_kv_workspace_bytes(const ovl_kv* kv, size_t* out);
+
+/* An empty cache: every row free, every page free, workspace zeroed (codes and
+ * scales are left as they are).  No counterpart in the source pages. */
+ovl_status ovl_kv_init(const ovl_kv* kv, void* stream);
+
+/* Room for new tokens: sequence i grows by tok_off[i+1] - tok_off[i] tokens, its
+ * table row gets the pages they need and length counts them.  Latched:
+ * OVL_E_OOM (not enough free pages, or max_pages columns), OVL_E_ARG (row),
+ * OVL_E_DUPLICATE.  No counterpart in the source pages. */
+ovl_status ovl_kv_extend(const ovl_kv* kv, const int32_t* seqs, const int32_t* tok_off, uint32_t n_seqs,
+                         void* stream);
+
+/* Write the keys and values of n_tokens new tokens (= tok_off[n_seqs]) into
+ * layer `layer`.  k, v: device, dtype OVL_F32 or OVL_BF16, [n_tokens][n_kv_heads]
+ * [head_dim] with k_stride and v_stride elements from token to token (heads and
+ * channels contiguous; base and stride multiples of 16 bytes).  Per block of 32
+ * channels d = binary16(min(max|x| / 8, 65504)) and
+ * code = clamp(round_half_away(x / d), -8, 7) + 8, the base weights' q4_0 (code 8
+ * where d = 0); NaN counts as 0, infinities are clipped.  No counterpart in the
+ * source pages. */
+ovl_status ovl_kv_append(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,
+                         uint32_t n_seqs, uint32_t n_tokens, const void* k, const void* v, uint32_t dtype,
+                         uint64_t k_stride, uint64_t v_stride, void* stream);
+
+/* The values that the last tokens of each sequence hold in layer `layer`:
+ * k_out, v_out device float32 [n_tokens][n_kv_heads][head_dim], 16-byte aligned.
+ * No counterpart in the source pages. */
+ovl_status ovl_kv_read(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,
+                       uint32_t n_seqs, uint32_t n_tokens, float* k_out, float* v_out, void* stream);
+
+/* Attention of the batch's new tokens over the cache:
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j
+ * over the tokens j of i's sequence that i sees: j <= p, and, when window > 0,
+ * j > p - window or j < sinks, with p the position of i (its sequence's length
+ * minus the tokens that follow it, minus 1).  window = 0 sees everything up to
+ * p.  A token with nothing to see (a negative position) returns zeros.
+ * q, out: device [n_tokens][n_heads][head_dim] of `dtype` (OVL_F32 or OVL_BF16),
+ * q_stride and out_stride elements from token to token, base and strides
+ * multiples of 16 bytes; out must not overlap q.  n_heads is a multiple of
+ * n_kv_heads; query head h reads kv head h / (n_heads / n_kv_heads).
+ * max_new: an upper bound of the new tokens of any one sequence (the kernel is
+ * chosen by it); more than that is latched as OVL_E_SHAPE, and the tokens
+ * beyond are zeros.  Scores, softmax and sums are 32-bit.  With OVL_F32 every
+ * product is exact to 24 bits; with OVL_BF16 the weights of the values are
+ * rounded to 11 bits, 3 more than the output keeps.  The same inputs give the
+ * same bits.  No counterpart in the source pages. */
+ovl_status ovl_kv_attention(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,
+                            uint32_t n_seqs, uint32_t n_tokens, uint32_t max_new, const void* q, uint32_t dtype,
+                            uint32_t n_heads, uint64_t q_stride, float scale, uint32_t window, uint32_t sinks,
+                            void* out, uint64_t out_stride, void* stream);
+
+/* Entry i makes row dst[i] the first keep[i] tokens of row src[i] (keep NULL:
+ * all of them); what dst[i] held before is released.  Whole pages are shared;
+ * the page that the last token leaves open is copied to a fresh one, every
+ * layer.  dst[i] = src[i] takes a sequence back to keep[i] tokens (drafted
+ * tokens that were not accepted).  A row may be the source of several entries
+ * and the destination of one, and of no other entry's source.  src, dst, keep:
+ * device int32 [n].  Latched: OVL_E_ARG (row, keep[i] > length), OVL_E_DUPLICATE,
+ * OVL_E_OOM.  No counterpart in the source pages. */
+ovl_status ovl_kv_fork(const ovl_kv* kv, const int32_t* src, const int32_t* dst, const int32_t* keep, uint32_t n,
+                       void* stream);
+
+/* Entry i makes row dst[i] the tokens keep[keep_off[i] .. keep_off[i+1] - 1] of
+ * row src[i], in that order, in fresh pages, every layer; what dst[i] held is
+ * released, after the copy where dst[i] = src[i].  keep: device int32 positions
+ * below src[i]'s length, n_keep of them in all; keep_off: device int32 [n + 1],
+ * from 0 to at most n_keep.  Rows as for ovl_kv_fork.  Latched: OVL_E_ARG (row,
+ * position, offsets), OVL_E_DUPLICATE, OVL_E_OOM.  No counterpart in the source pages. */
+ovl_status ovl_kv_compact(const ovl_kv* kv, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                          const int32_t* keep_off, uint32_t n, uint32_t n_keep, void* stream);
+
+/* Rows seqs[0..n) become free and their pages lose a reader each.  Releasing a
+ * free row does nothing.  Latched: OVL_E_ARG, OVL_E_DUPLICATE.  No counterpart
+ * in the source pages. */
+ovl_status ovl_kv_release(const ovl_kv* kv, const int32_t* seqs, uint32_t n, void* stream);
+
+/* Wait for `stream`, then return the first status latched since the last check
+ * and clear it.  No counterpart in the source pages. */
+ovl_status ovl_kv_check(const ovl_kv* kv, void* stream);
+
 /* Message of the last failed call on ctx (static storage owned by ctx; "" after
  * success).  ctx NULL returns the message of the last failed call that has no
- * context on this thread (ovl_create, ovl_manifest_parse).
+ * context on this thread (ovl_create, ovl_manifest_parse, ovl_kv_*).
  * ([MODELD] §"Observability": why an adapter failed to load.) */
 const char* ovl_last_error(ovl_ctx* ctx);
 

@@ -88,6 +88,18 @@ class ovl_manifest(C.Structure):
                 ("n_adapters", C.c_uint32), ("adapters", ovl_manifest_entry * 32)]
 
 
+class ovl_kv(C.Structure):
+    """A 4-bit key/value cache: caller-owned device memory and its dimensions."""
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("table", C.c_void_p), ("length", C.c_void_p),
+                ("refs", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("n_pages", C.c_uint32), ("page_tokens", C.c_uint32), ("n_layers", C.c_uint32),
+                ("n_kv_heads", C.c_uint32), ("head_dim", C.c_uint32), ("max_seqs", C.c_uint32),
+                ("max_pages", C.c_uint32)]
+
+
+OVL_KV_MAX_BATCH = 1024
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libovl.so is not built ({LIB_PATH}); run python quantized_base_lora_gb300/build.py")
@@ -122,6 +134,16 @@ def _load():
         "ovl_stage_activations": ([P, P, SZ, P], I32),
         "ovl_manifest_parse": ([C.c_char_p, SZ, C.POINTER(ovl_manifest)], I32),
         "ovl_activate_manifest": ([P, C.c_char_p, SZ, B32], I32),
+        "ovl_kv_workspace_bytes": ([P, C.POINTER(SZ)], I32),
+        "ovl_kv_init": ([P, P], I32),
+        "ovl_kv_extend": ([P, P, P, U32, P], I32),
+        "ovl_kv_append": ([P, U32, P, P, U32, U32, P, P, U32, U64, U64, P], I32),
+        "ovl_kv_read": ([P, U32, P, P, U32, U32, P, P, P], I32),
+        "ovl_kv_attention": ([P, U32, P, P, U32, U32, U32, P, U32, U32, U64, C.c_float, U32, U32, P, U64, P], I32),
+        "ovl_kv_fork": ([P, P, P, P, U32, P], I32),
+        "ovl_kv_compact": ([P, P, P, P, P, U32, U32, P], I32),
+        "ovl_kv_release": ([P, P, U32, P], I32),
+        "ovl_kv_check": ([P, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -136,7 +158,9 @@ EXPORTED = ("ovl_create", "ovl_destroy", "ovl_load_base", "ovl_stage_adapter", "
             "ovl_segmented_forward", "ovl_base_digest", "ovl_get_state", "ovl_get_entry",
             "ovl_check_device", "ovl_debug_inject", "ovl_last_error", "ovl_sha256",
             "ovl_content_digest", "ovl_version", "ovl_dualpath_forward_noalloc", "ovl_stage_activations",
-            "ovl_manifest_parse", "ovl_activate_manifest")
+            "ovl_manifest_parse", "ovl_activate_manifest", "ovl_kv_workspace_bytes", "ovl_kv_init", "ovl_kv_extend",
+            "ovl_kv_append", "ovl_kv_read", "ovl_kv_attention", "ovl_kv_fork", "ovl_kv_compact", "ovl_kv_release",
+            "ovl_kv_check")
 
 
 class OvlError(RuntimeError):
@@ -355,3 +379,59 @@ def ovl_dualpath_forward_noalloc(qs_ptr: int, d_ptr: int, quant: int, d_out: int
                                             Ap, Bp, _u32s(ranks) if n else None,
                                             (C.c_float * n)(*scales) if n else None, n, C.c_void_p(x_ptr),
                                             int(x_dtype), int(T), C.c_void_p(y_ptr), C.c_void_p(stream))
+
+
+# ---- 4-bit key/value cache (see include/ovl.h).  kv: an ovl_kv, or its address
+# (ctypes.addressof), which saves a conversion a call; the rest device addresses
+# and sizes.
+
+def _kv(kv):
+    return C.byref(kv) if isinstance(kv, ovl_kv) else kv
+
+
+def ovl_kv_workspace_bytes(kv):
+    out = C.c_size_t(0)
+    st = lib.ovl_kv_workspace_bytes(_kv(kv), C.byref(out))
+    return st, int(out.value)
+
+
+def ovl_kv_init(kv, stream: int = 0) -> int:
+    return lib.ovl_kv_init(_kv(kv), stream)
+
+
+def ovl_kv_extend(kv, seqs: int, tok_off: int, n_seqs: int, stream: int = 0) -> int:
+    return lib.ovl_kv_extend(_kv(kv), seqs, tok_off, n_seqs, stream)
+
+
+def ovl_kv_append(kv, layer: int, seqs: int, tok_off: int, n_seqs: int, n_tokens: int, k: int, v: int, dtype: int,
+                  k_stride: int, v_stride: int, stream: int = 0) -> int:
+    return lib.ovl_kv_append(_kv(kv), layer, seqs, tok_off, n_seqs, n_tokens, k, v, dtype, k_stride, v_stride, stream)
+
+
+def ovl_kv_read(kv, layer: int, seqs: int, tok_off: int, n_seqs: int, n_tokens: int, k_out: int, v_out: int,
+                stream: int = 0) -> int:
+    return lib.ovl_kv_read(_kv(kv), layer, seqs, tok_off, n_seqs, n_tokens, k_out, v_out, stream)
+
+
+def ovl_kv_attention(kv, layer: int, seqs: int, tok_off: int, n_seqs: int, n_tokens: int, max_new: int, q: int,
+                     dtype: int, n_heads: int, q_stride: int, scale: float, window: int, sinks: int, out: int,
+                     out_stride: int, stream: int = 0) -> int:
+    return lib.ovl_kv_attention(_kv(kv), layer, seqs, tok_off, n_seqs, n_tokens, max_new, q, dtype, n_heads, q_stride,
+                                scale, window, sinks, out, out_stride, stream)
+
+
+def ovl_kv_fork(kv, src: int, dst: int, keep: int, n: int, stream: int = 0) -> int:
+    """keep: 0 (all tokens) or the address of int32 [n]."""
+    return lib.ovl_kv_fork(_kv(kv), src, dst, keep, n, stream)
+
+
+def ovl_kv_compact(kv, src: int, dst: int, keep: int, keep_off: int, n: int, n_keep: int, stream: int = 0) -> int:
+    return lib.ovl_kv_compact(_kv(kv), src, dst, keep, keep_off, n, n_keep, stream)
+
+
+def ovl_kv_release(kv, seqs: int, n: int, stream: int = 0) -> int:
+    return lib.ovl_kv_release(_kv(kv), seqs, n, stream)
+
+
+def ovl_kv_check(kv, stream: int = 0) -> int:
+    return lib.ovl_kv_check(_kv(kv), stream)

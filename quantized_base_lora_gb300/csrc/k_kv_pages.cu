@@ -1,0 +1,389 @@
+// Pages of the 4-bit cache: growing, forking, compacting and releasing rows.
+//
+// One CTA does the bookkeeping (k_kv_pages): it checks every entry, moves the
+// reader counts, finds the lowest-numbered free pages with a scan over refs and
+// writes the new table rows, or changes nothing and latches a status.  It leaves
+// a list of fresh pages; the copy kernels, launched behind it, fill them.
+//
+// Fresh pages come from what is free before the call, plus what the pure
+// destinations of the same call release.  Pages that an entry releases from its
+// own source row (src = dst) are still read by the copy, so they become free
+// only afterwards.
+#include <type_traits>
+
+#include "kv_internal.h"
+#include "ptx.cuh"
+
+namespace ovl {
+namespace {
+
+constexpr uint32_t kBook = 1024;               // threads of the bookkeeping CTA; entry i belongs to thread i
+static_assert(kBook >= OVL_KV_MAX_BATCH, "one entry per thread");
+constexpr uint32_t kCopy = 256;
+
+struct BookShared {
+  int32_t src[kBook], dst[kBook];
+  int32_t before[kBook];      // pages that the destination held
+  int32_t whole[kBook];       // leading pages that it keeps or shares
+  int32_t length[kBook];      // its new length
+  int32_t limit[kBook];       // compaction: the source's length
+  uint32_t first[kBook + 1];  // prefix sums of the fresh pages
+  uint32_t is_dst[kKvMaxSeqs / 32];
+  uint32_t warp_sum[32];
+  uint32_t found;
+  int32_t error;
+};
+
+// Inclusive scan over the CTA; every thread calls it.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, s);
+    if (lane >= static_cast<uint32_t>(s)) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t w = warp_sum[lane];
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, w, s);
+      if (lane >= static_cast<uint32_t>(s)) w += o;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  return v + (warp ? warp_sum[warp - 1] : 0u);
+}
+
+// The entry that owns position x of a prefix-sum array f[0..n].
+template <class T>
+__device__ __forceinline__ uint32_t owner_of(const T* f, uint32_t n, T x) {
+  uint32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (f[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void add_refs(const KvDev& kv, int32_t page, int32_t by) {
+  if (static_cast<uint32_t>(page) < kv.n_pages) atomicAdd(kv.refs + page, by);
+}
+
+__global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what, const int32_t* __restrict__ src,
+                                                    const int32_t* __restrict__ dst, const int32_t* __restrict__ keep,
+                                                    const int32_t* __restrict__ off, uint32_t n, uint32_t n_keep) {
+  __shared__ BookShared s;
+  const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const bool two = what == KvPages::kFork || what == KvPages::kCompact;
+  const uint32_t page = kv.page, shift = kv.page_shift;
+  for (uint32_t i = t; i < (kv.max_seqs + 31) / 32; i += kBook) s.is_dst[i] = 0;
+  if (t == 0) s.error = 0, s.found = 0;
+  __syncthreads();
+
+  // ---- the entries, checked
+  int32_t from = 0, to = 0;
+  if (t < n) {
+    from = src[t];
+    to = two ? dst[t] : from;
+    if (static_cast<uint32_t>(from) >= kv.max_seqs || static_cast<uint32_t>(to) >= kv.max_seqs) {
+      atomicCAS(&s.error, 0, OVL_E_ARG);
+    } else if (atomicOr(&s.is_dst[to >> 5], 1u << (to & 31)) >> (to & 31) & 1u) {
+      atomicCAS(&s.error, 0, OVL_E_DUPLICATE);
+    }
+  }
+  __syncthreads();
+  uint32_t need = 0;
+  if (t < n && s.error == 0) {
+    if (from != to && (s.is_dst[from >> 5] >> (from & 31) & 1u)) atomicCAS(&s.error, 0, OVL_E_DUPLICATE);
+    const int32_t have = kv.length[from], held = kv.length[to];
+    const int32_t most = static_cast<int32_t>(kv.max_pages << shift);
+    const int32_t* row = kv.table + static_cast<size_t>(from) * kv.max_pages;
+    int64_t len = 0;
+    int32_t whole = 0;
+    if (have < 0 || have > most || held < 0 || held > most) {
+      atomicCAS(&s.error, 0, OVL_E_ARG);
+    } else if (what == KvPages::kExtend) {
+      const int32_t more = off[t + 1] - off[t];
+      len = static_cast<int64_t>(have) + more;
+      if (more < 0) atomicCAS(&s.error, 0, OVL_E_ARG);
+      else if (len > most) atomicCAS(&s.error, 0, OVL_E_OOM);
+      else {
+        whole = (have + page - 1) >> shift;
+        need = static_cast<uint32_t>((len + page - 1) >> shift) - whole;
+      }
+    } else if (what == KvPages::kFork) {
+      len = keep ? keep[t] : have;
+      if (len < 0 || len > have) {
+        atomicCAS(&s.error, 0, OVL_E_ARG);
+      } else {
+        whole = static_cast<int32_t>(len) >> shift;
+        need = (len & (page - 1)) != 0;
+        // taken back inside a page that no one else holds: it stays
+        if (need && from == to) {
+          const int32_t p = row[whole];
+          if (static_cast<uint32_t>(p) < kv.n_pages && __ldcg(kv.refs + p) == 1) need = 0, ++whole;
+        }
+      }
+    } else if (what == KvPages::kCompact) {
+      len = static_cast<int64_t>(off[t + 1]) - off[t];
+      if (len < 0 || off[t] < 0) atomicCAS(&s.error, 0, OVL_E_ARG);
+      else if (len > most) atomicCAS(&s.error, 0, OVL_E_OOM);
+      else need = static_cast<uint32_t>((len + page - 1) >> shift);
+    }
+    s.src[t] = from;
+    s.dst[t] = to;
+    s.before[t] = (held + page - 1) >> shift;
+    s.whole[t] = whole;
+    s.length[t] = static_cast<int32_t>(len);
+    s.limit[t] = have;
+  }
+  if (t == 0 && what == KvPages::kCompact && (off[0] != 0 || off[n] < 0 || static_cast<uint32_t>(off[n]) > n_keep))
+    s.error = OVL_E_ARG;
+  __syncthreads();
+  const bool sound = s.error == 0;
+  __syncthreads();
+  if (what == KvPages::kCompact && sound) {
+    // the entries follow one another from position 0, so owner_of finds each one
+    const int32_t total = off[n];
+    for (int32_t j = static_cast<int32_t>(t); j < total; j += kBook) {
+      const int32_t p = __ldg(keep + j);
+      const uint32_t e = owner_of(off, n, j);
+      if (p < 0 || p >= s.limit[e]) atomicCAS(&s.error, 0, OVL_E_ARG);
+    }
+    __syncthreads();
+  }
+  const uint32_t upto = block_scan(t < n ? need : 0u, s.warp_sum);
+  if (t < n) s.first[t + 1] = upto;
+  if (t == 0) s.first[0] = 0;
+  __syncthreads();
+  if (s.error != 0) {
+    if (t == 0) {
+      kv_latch(kv, s.error);
+      *kv.n_fresh = 0;
+    }
+    return;
+  }
+  const uint32_t total = s.first[n];
+
+  // ---- reader counts before the allocation: what pure destinations held goes,
+  // shared pages gain one.  Signed so that the same loop takes it back.
+  auto count_readers = [&](int32_t sign) {
+    for (uint32_t e = warp; e < n; e += kBook / 32) {
+      if (what == KvPages::kExtend || (two && s.src[e] == s.dst[e])) continue;
+      const int32_t* old = kv.table + static_cast<size_t>(s.dst[e]) * kv.max_pages;
+      for (int32_t c = lane; c < s.before[e]; c += 32) add_refs(kv, old[c], -sign);
+      if (what != KvPages::kFork) continue;
+      const int32_t* row = kv.table + static_cast<size_t>(s.src[e]) * kv.max_pages;
+      for (int32_t c = lane; c < s.whole[e]; c += 32) add_refs(kv, row[c], sign);
+    }
+    __syncthreads();
+  };
+  count_readers(1);
+
+  // ---- the lowest-numbered free pages
+  for (uint32_t base = 0; base < kv.n_pages && s.found < total; base += kBook * 4) {
+    uint32_t free_mask = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t p = base + t * 4 + k;
+      if (p < kv.n_pages && __ldcg(kv.refs + p) == 0) free_mask |= 1u << k;
+    }
+    const uint32_t mine = __popc(free_mask);
+    const uint32_t end = block_scan(mine, s.warp_sum);
+    const uint32_t had = s.found;
+    uint32_t r = had + end - mine;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if ((free_mask >> k & 1u) && r < total) {
+        KvFresh f;
+        f.dst_page = static_cast<int32_t>(base + t * 4 + k);
+        f.entry = static_cast<int32_t>(owner_of(s.first, n, r));
+        f.column = s.whole[f.entry] + static_cast<int32_t>(r - s.first[f.entry]);
+        f.src_page = what == KvPages::kFork
+                         ? kv.table[static_cast<size_t>(s.src[f.entry]) * kv.max_pages + s.whole[f.entry]]
+                         : -1;
+        kv.fresh[r++] = f;
+      }
+    __syncthreads();
+    if (t == kBook - 1) s.found = had + end;
+    __syncthreads();
+  }
+  if (s.found < total) {
+    count_readers(-1);
+    if (t == 0) {
+      kv_latch(kv, OVL_E_OOM);
+      *kv.n_fresh = 0;
+    }
+    return;
+  }
+
+  // ---- rows that are their own source: what they drop, and for the copy of a
+  // compaction where their tokens were
+  for (uint32_t e = warp; e < n; e += kBook / 32) {
+    if (!two || s.src[e] != s.dst[e]) continue;
+    const int32_t* row = kv.table + static_cast<size_t>(s.dst[e]) * kv.max_pages;
+    for (int32_t c = lane; c < s.before[e]; c += 32) {
+      const int32_t p = row[c];
+      if (what == KvPages::kCompact) kv.rows[static_cast<size_t>(e) * kv.max_pages + c] = p;
+      if (c >= s.whole[e]) add_refs(kv, p, -1);
+    }
+  }
+  __syncthreads();
+
+  // ---- the new rows
+  for (uint32_t e = warp; e < n; e += kBook / 32) {
+    const uint32_t fresh = s.first[e + 1] - s.first[e];
+    int32_t* row = kv.table + static_cast<size_t>(s.dst[e]) * kv.max_pages;
+    const int32_t* shared_row = kv.table + static_cast<size_t>(s.src[e]) * kv.max_pages;
+    const int32_t whole = s.whole[e];
+    for (int32_t c = lane; c < static_cast<int32_t>(kv.max_pages); c += 32) {
+      if (c < whole) {
+        if (s.src[e] != s.dst[e]) row[c] = shared_row[c];
+      } else if (c < whole + static_cast<int32_t>(fresh)) {
+        const int32_t p = kv.fresh[s.first[e] + c - whole].dst_page;
+        row[c] = p;
+        kv.refs[p] = 1;
+      } else {
+        row[c] = -1;
+      }
+    }
+    if (lane == 0) kv.length[s.dst[e]] = s.length[e];
+  }
+  if (t == 0) *kv.n_fresh = two ? total : 0;
+}
+
+// Fork: whole pages, every layer.  A page is two contiguous runs.
+__global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
+  griddep_wait();
+  const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
+  const uint64_t nc = units * kv.unit_codes / 16, ns = units * kv.unit_scales / 8;
+  constexpr uint64_t kChunk = kCopy * 4;
+  const uint64_t per = (nc + ns + kChunk - 1) / kChunk;
+  const uint64_t items = per * *kv.n_fresh;
+  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const KvFresh f = kv.fresh[it / per];
+    if (static_cast<uint32_t>(f.src_page) >= kv.n_pages) continue;
+    const uint4* a = reinterpret_cast<const uint4*>(kv.codes) + f.src_page * nc;
+    uint4* b = reinterpret_cast<uint4*>(kv.codes) + f.dst_page * nc;
+    const uint4* as = reinterpret_cast<const uint4*>(kv.scales) + f.src_page * ns;
+    uint4* bs = reinterpret_cast<uint4*>(kv.scales) + f.dst_page * ns;
+    const uint64_t i0 = (it % per) * kChunk + threadIdx.x;
+    uint4 v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint64_t i = i0 + k * kCopy;
+      if (i < nc) v[k] = a[i];
+      else if (i < nc + ns) v[k] = as[i - nc];
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint64_t i = i0 + k * kCopy;
+      if (i < nc) b[i] = v[k];
+      else if (i < nc + ns) bs[i - nc] = v[k];
+    }
+  }
+}
+
+// Compaction: one fresh page, layer and K|V at a time; the tokens' sources are
+// found once and used for every head.
+template <int D>
+__global__ void __launch_bounds__(kCopy) k_kv_gather(const KvDev kv, const int32_t* __restrict__ src,
+                                                     const int32_t* __restrict__ dst,
+                                                     const int32_t* __restrict__ keep,
+                                                     const int32_t* __restrict__ off) {
+  __shared__ int32_t from_page[256], from_slot[256];
+  griddep_wait();
+  const uint64_t items = static_cast<uint64_t>(*kv.n_fresh) * kv.layers * 2;
+  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const uint32_t which = it & 1;
+    const uint32_t layer = (it >> 1) % kv.layers;
+    const KvFresh f = kv.fresh[(it >> 1) / kv.layers];
+    const int32_t s = src[f.entry];
+    const int32_t* row = s == dst[f.entry] ? kv.rows + static_cast<size_t>(f.entry) * kv.max_pages
+                                           : kv.table + static_cast<size_t>(s) * kv.max_pages;
+    const int32_t first = off[f.entry] + f.column * static_cast<int32_t>(kv.page);
+    const uint32_t count = min(static_cast<uint32_t>(off[f.entry + 1] - first), kv.page);
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
+      const int32_t pos = keep[first + i];
+      const int32_t p = row[pos >> kv.page_shift];
+      from_page[i] = static_cast<uint32_t>(p) < kv.n_pages ? p : -1;
+      from_slot[i] = pos & static_cast<int32_t>(kv.page - 1);
+    }
+    __syncthreads();
+    for (uint32_t h = 0; h < kv.heads; ++h) {
+      const uint64_t ud = kv_unit(kv, f.dst_page, layer, which, h);
+      uint8_t* out = kv.codes + ud * kv.unit_codes;
+      if (which == 0) {
+        constexpr uint32_t kRow = D / 32;            // 16-byte pieces of a row
+        for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
+          const uint32_t tok = i / kRow, c = i % kRow;
+          if (from_page[tok] < 0) continue;
+          const uint64_t us = kv_unit(kv, from_page[tok], layer, which, h);
+          const uint8_t* in = kv.codes + us * kv.unit_codes + from_slot[tok] * (D / 2);
+          *reinterpret_cast<uint4*>(out + tok * (D / 2) + c * 16) = *reinterpret_cast<const uint4*>(in + c * 16);
+        }
+      } else {
+        using Unit = typename std::conditional<D == 64, uint32_t,
+                                               typename std::conditional<D == 128, uint2, uint4>::type>::type;
+        for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
+          const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
+          if (tok >= count || from_page[tok] < 0) continue;
+          const uint64_t us = kv_unit(kv, from_page[tok], layer, which, h);
+          const uint32_t slot = from_slot[tok];
+          const uint8_t* in = kv.codes + us * kv.unit_codes + (slot >> 3) * (4 * D) + g * (D / 2) + (slot & 7) * (D / 16);
+          *reinterpret_cast<Unit*>(out + (tok >> 3) * (4 * D) + g * (D / 2) + (tok & 7) * (D / 16)) =
+              *reinterpret_cast<const Unit*>(in);
+        }
+      }
+      using Scales = typename std::conditional<D == 64, uint32_t,
+                                               typename std::conditional<D == 128, uint2, uint4>::type>::type;
+      for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
+        if (from_page[i] < 0) continue;
+        const uint64_t us = kv_unit(kv, from_page[i], layer, which, h);
+        *reinterpret_cast<Scales*>(kv.scales + ud * kv.unit_scales + i * (D / 32)) =
+            *reinterpret_cast<const Scales*>(kv.scales + us * kv.unit_scales + from_slot[i] * (D / 32));
+      }
+    }
+  }
+}
+
+template <class... P, class... A>
+cudaError_t launch_behind(void (*f)(P...), uint32_t grid, uint32_t block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                            const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st) {
+  k_kv_pages<<<1, kBook, 0, st>>>(kv, what, src, dst, keep, off, n, n_keep);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const uint32_t grid = kv_sm_count() * 4;
+  if (what == KvPages::kFork) return launch_behind(k_kv_copy_pages, grid, kCopy, st, kv);
+  if (what == KvPages::kCompact) {
+    switch (kv.dim) {
+      case 64: return launch_behind(k_kv_gather<64>, grid, kCopy, st, kv, src, dst, keep, off);
+      case 128: return launch_behind(k_kv_gather<128>, grid, kCopy, st, kv, src, dst, keep, off);
+      default: return launch_behind(k_kv_gather<256>, grid, kCopy, st, kv, src, dst, keep, off);
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace ovl

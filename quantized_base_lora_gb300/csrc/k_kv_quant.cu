@@ -1,0 +1,173 @@
+// Writing tokens into the 4-bit cache and reading their values back.
+//
+// A block of 32 channels is held as d * (code - 8), d = f16(max|x| / 8).  Eight
+// channels of one token and head (one 32-bit word of codes) belong to one
+// thread, so a block's maximum is a reduction over 4 lanes.  A key word is
+// stored as it is; value words are transposed 8 x 8 (nibbles against lanes) with
+// three exchanges, since a value unit holds every eighth channel.
+// Bound by memory: 2 or 4 bytes read and 0.5625 written per element.
+#include "kv_internal.h"
+#include "ptx.cuh"
+
+namespace ovl {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Lane l of 8 holds nibble g of row l at bits 4 g; afterwards lane g holds row
+// l's nibble at bits 4 l.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x, uint32_t lane) {
+#pragma unroll
+  for (int s = 4; s; s >>= 1) {
+    const uint32_t low = s == 4 ? 0x0000ffffu : s == 2 ? 0x00ff00ffu : 0x0f0f0f0fu;
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, s);
+    x = (lane & s) ? ((x & ~low) | ((y & ~low) >> (4 * s))) : ((x & low) | ((y & low) << (4 * s)));
+  }
+  return x;
+}
+
+// Byte offset of word j (channels 8 j .. for keys; for values, after the
+// transposition, unit j % 8's word j / 8) of a token inside its unit.
+template <int D>
+__device__ __forceinline__ uint32_t word_offset(bool values, uint32_t slot, uint32_t j) {
+  if (!values) return slot * (D / 2) + ((j & 3) * (D / 32) + (j >> 2)) * 4;
+  return (slot >> 3) * (4 * D) + (j & 7) * (D / 2) + (slot & 7) * (D / 16) + (j >> 3) * 4;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, uint64_t at, float (&x)[8]) {
+  if constexpr (BF16) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t layer, const int32_t* seqs,
+                                                        const int32_t* off, uint32_t n, uint32_t n_tokens,
+                                                        const void* k, const void* v, uint64_t ks, uint64_t vs) {
+  constexpr uint32_t kWords = D / 8;
+  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint32_t j = id % kWords;
+  const uint64_t th = id / kWords;
+  const uint32_t head = th % kv.heads;
+  const uint64_t token = th / kv.heads;
+  const bool values = blockIdx.y != 0;
+  const bool live = token < n_tokens;
+  KvPlace at{-1, 0};
+  float x[8] = {};
+  if (live) {
+    at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+    load8<BF16>(values ? v : k, token * (values ? vs : ks) + head * D + j * 8, x);
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (x[i] != x[i]) x[i] = 0.f;
+    m = fmaxf(m, fabsf(x[i]));
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const __half d = __float2half_rn(fminf(m * 0.125f, 65504.f));
+  const float s = __half2float(d);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
+    const float r = fminf(fmaxf(truncf(t + copysignf(0.5f, t)), -8.f), 7.f);
+    w |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * i);
+  }
+  if (values) w = transpose8(w, j & 7);
+  if (at.page < 0) return;
+  const uint64_t u = kv_unit(kv, at.page, layer, values, head);
+  *reinterpret_cast<uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j)) = w;
+  if ((j & 3) == 0) kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)] = d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_kv_read(const KvDev kv, uint32_t layer, const int32_t* seqs,
+                                                      const int32_t* off, uint32_t n, uint32_t n_tokens, float* k,
+                                                      float* v) {
+  constexpr uint32_t kWords = D / 8;
+  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint32_t j = id % kWords;
+  const uint64_t th = id / kWords;
+  const uint32_t head = th % kv.heads;
+  const uint64_t token = th / kv.heads;
+  const bool values = blockIdx.y != 0;
+  const bool live = token < n_tokens;
+  uint32_t w = 0x88888888u;
+  float d = 0.f;
+  if (live) {
+    const KvPlace at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+    if (at.page >= 0) {
+      const uint64_t u = kv_unit(kv, at.page, layer, values, head);
+      w = *reinterpret_cast<const uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j));
+      d = __half2float(kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)]);
+    }
+  }
+  if (values) w = transpose8(w, j & 7);
+  if (!live) return;
+  float4 o[2];
+  float* of = reinterpret_cast<float*>(o);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) of[i] = d * (static_cast<int>((w >> (4 * i)) & 15u) - 8);
+  float4* p = reinterpret_cast<float4*>((values ? v : k) + (token * kv.heads + head) * D + j * 8);
+  p[0] = o[0];
+  p[1] = o[1];
+}
+
+template <int D>
+cudaError_t append_dim(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                       uint32_t n_tokens, const void* k, const void* v, bool bf16, uint64_t ks, uint64_t vs,
+                       cudaStream_t st) {
+  const uint64_t threads = static_cast<uint64_t>(n_tokens) * kv.heads * (D / 8);
+  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<uint32_t>(blocks), 2);
+  if (bf16) k_kv_append<D, true><<<grid, kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs);
+  else k_kv_append<D, false><<<grid, kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t read_dim(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                     uint32_t n_tokens, float* k, float* v, cudaStream_t st) {
+  const uint64_t threads = static_cast<uint64_t>(n_tokens) * kv.heads * (D / 8);
+  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  k_kv_read<D><<<dim3(static_cast<uint32_t>(blocks), 2), kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                             uint32_t n_tokens, const void* k, const void* v, bool bf16, uint64_t ks, uint64_t vs,
+                             cudaStream_t st) {
+  switch (kv.dim) {
+    case 64: return append_dim<64>(kv, layer, seqs, off, n, n_tokens, k, v, bf16, ks, vs, st);
+    case 128: return append_dim<128>(kv, layer, seqs, off, n, n_tokens, k, v, bf16, ks, vs, st);
+    default: return append_dim<256>(kv, layer, seqs, off, n, n_tokens, k, v, bf16, ks, vs, st);
+  }
+}
+
+cudaError_t launch_kv_read(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                           uint32_t n_tokens, float* k, float* v, cudaStream_t st) {
+  switch (kv.dim) {
+    case 64: return read_dim<64>(kv, layer, seqs, off, n, n_tokens, k, v, st);
+    case 128: return read_dim<128>(kv, layer, seqs, off, n, n_tokens, k, v, st);
+    default: return read_dim<256>(kv, layer, seqs, off, n, n_tokens, k, v, st);
+  }
+}
+
+}  // namespace ovl

@@ -1,0 +1,114 @@
+// Shared by the translation units of the 4-bit key/value cache (ovl_kv_*).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ovl.h"
+
+namespace ovl {
+
+constexpr uint32_t kKvMaxSeqs = 65536;       // rows: two bits each in shared memory of the page kernel
+constexpr uint32_t kKvMaxCtas = 640;         // CTAs of an attention launch that may leave partial results
+constexpr uint32_t kKvPartialRows = 16;      // query rows of one partial result
+
+// One fresh page of a fork or compaction: where its bytes come from.
+struct KvFresh {
+  int32_t src_page;   // fork: the page to copy; compaction: unused
+  int32_t dst_page;
+  int32_t entry;
+  int32_t column;
+};
+
+// A cache as the kernels take it: ovl_kv's pointers, the parts of the
+// workspace, and sizes.
+struct KvDev {
+  uint8_t* codes;
+  __half* scales;
+  int32_t* table;
+  int32_t* length;
+  int32_t* refs;
+  uint32_t* status;        // workspace: first latched status code, 0 = none
+  uint32_t* n_fresh;       // workspace: fresh pages of the last fork or compaction
+  uint32_t* joined;        // workspace: arrivals at a split segment, by its first CTA; 0 between calls
+  KvFresh* fresh;          // workspace [n_pages]
+  int32_t* rows;           // workspace [max_seqs][max_pages]: source rows of in-place compactions
+  float* partial;          // workspace: partial attention results
+  uint32_t n_pages, page, page_shift, layers, heads, dim, max_seqs, max_pages;
+  uint32_t unit_codes;     // bytes of one (page, layer, K|V, head): page * dim / 2
+  uint32_t unit_scales;    // binary16 values of the same: page * dim / 32
+};
+
+// Byte offset of the codes (element offset of the scales) of one unit.
+__host__ __device__ __forceinline__ uint64_t kv_unit(const KvDev& kv, uint32_t page, uint32_t layer, uint32_t which,
+                                                     uint32_t head) {
+  return ((static_cast<uint64_t>(page) * kv.layers + layer) * 2 + which) * kv.heads + head;
+}
+
+__device__ __forceinline__ void kv_latch(const KvDev& kv, int32_t code) {
+  atomicCAS(kv.status, 0u, static_cast<uint32_t>(-code));
+}
+
+// The sequence of the batch that owns packed token t: the largest i with
+// off[i] <= t (off[n] > t).
+__device__ __forceinline__ uint32_t kv_owner(const int32_t* off, uint32_t n, int32_t t) {
+  uint32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (__ldg(off + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Where a packed token lives, or page = -1 (the reason is latched).
+struct KvPlace {
+  int32_t page, slot;
+};
+__device__ __forceinline__ KvPlace kv_place(const KvDev& kv, const int32_t* seqs, const int32_t* off, uint32_t n,
+                                            int32_t t) {
+  const uint32_t i = kv_owner(off, n, t);
+  const int32_t s = __ldg(seqs + i), after = __ldg(off + i + 1) - t;
+  if (static_cast<uint32_t>(s) >= kv.max_seqs || after <= 0) {
+    kv_latch(kv, OVL_E_ARG);
+    return {-1, 0};
+  }
+  const int32_t pos = kv.length[s] - after;
+  if (pos < 0 || static_cast<uint32_t>(pos) >= kv.max_pages << kv.page_shift) {
+    kv_latch(kv, OVL_E_SHAPE);
+    return {-1, 0};
+  }
+  const int32_t p = kv.table[static_cast<size_t>(s) * kv.max_pages + (pos >> kv.page_shift)];
+  if (static_cast<uint32_t>(p) >= kv.n_pages) {
+    kv_latch(kv, OVL_E_ARG);
+    return {-1, 0};
+  }
+  return {p, pos & static_cast<int32_t>(kv.page - 1)};
+}
+
+// Query tokens of one attention call.
+struct KvQuery {
+  const int32_t* seqs;
+  const int32_t* off;
+  uint32_t n_seqs, n_tokens, max_new, layer;
+  const void* q;
+  void* out;
+  uint64_t q_stride, out_stride;   // elements
+  uint32_t heads, group;           // query heads; query heads of one kv head
+  float scale;
+  uint32_t window, sinks;
+  bool bf16;
+};
+
+uint32_t kv_sm_count();
+cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                             uint32_t n_tokens, const void* k, const void* v, bool bf16, uint64_t ks, uint64_t vs,
+                             cudaStream_t st);
+cudaError_t launch_kv_read(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                           uint32_t n_tokens, float* k, float* v, cudaStream_t st);
+cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& q, cudaStream_t st);
+enum class KvPages { kExtend, kFork, kCompact, kRelease };
+cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                            const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st);
+
+}  // namespace ovl
