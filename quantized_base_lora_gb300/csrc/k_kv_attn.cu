@@ -1,100 +1,698 @@
-// Attention over the 4-bit cache.
+// Attention over the 4-bit cache for few query rows to a key (decode steps,
+// drafted tokens): the cache is read once and its bytes are the floor.
 //
-// One warp per query token and head walks its sequence's visible tokens with a
-// running maximum and sum; lane c of the warp holds channels c, c + 32, ...
+// Rows.  The query heads that share a kv head, and all new tokens of a sequence,
+// are the rows of one small matrix Q [rows][D]; 8 or 16 rows at a time (one or
+// two column tiles of an MMA) are a group.  A segment is one (sequence, kv head,
+// group); its keys are walked in tiles of 32 tokens.
+//
+// Mathematics.  With code = c + 8 and one scale d for 32 channels,
+//   s_j = sum_b dK_jb (sum_{i in b} c_ji q_i),   o = sum_j p_j dV_jb c_j,
+// so the codes go into the MMA as they are: small integers, exact in bf16 and
+// f16, taken out of a word with one mask (bits 16 + 4 i and 4 i of a word are
+// the two halves of a pair) and an exponent.  A key pair is the bf16 128 + code;
+// the constant 136 sum(q) of a block is the accumulator's start, so keys cost no
+// subtraction.  The scale of a key block multiplies its accumulator (fp32); the
+// scale of a value block multiplies p, once a block.  Nothing is dequantized in
+// memory.  S^T = K Q^T has tokens as rows, so its accumulator has to be
+// transposed to become the second operand of O^T = V^T P: one movmatrix for 8x8.
+//
+// Precision.  bf16 calls: q is exact; p dV is rounded to f16.  The running
+// reference of the softmax is max_j(s_j) + E, 2^E above every value scale of the
+// tile, so p dV <= 1 and keeps 11 bits whatever the scales' size.  f32 calls: q
+// and p dV are split into three bf16 each (24 bits), three MMAs in place of one.
+//
+// Split.  All tiles of the call, segment after segment, are dealt to the CTAs in
+// equal runs, whatever the lengths are (they are known on the device only).  The
+// four warps of a CTA take every fourth tile of its run, each with a running
+// maximum and sum of its own and a private ring of bulk copies, so there is no
+// CTA barrier inside a segment.  A segment that is cut by a run's end is joined
+// by whichever of its CTAs arrives last: partial results go through memory, in
+// the order of the CTAs, so the same call gives the same bits, and no CTA waits.
 #include <math_constants.h>
 
 #include "kv_internal.h"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace ovl {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr uint32_t kWarps = 4;
+constexpr uint32_t kThreads = kWarps * 32;
+constexpr uint32_t kTile = 32;               // tokens
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) k_kv_attend(const KvDev kv, const KvQuery a) {
-  constexpr int NB = D / 32;
-  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t token = id / a.heads;
-  if (token >= a.n_tokens) return;
-  const uint32_t h = id % a.heads, kh = h / a.group;
-  const uint32_t i = kv_owner(a.off, a.n_seqs, static_cast<int32_t>(token));
-  const int32_t s = a.seqs[i], after = a.off[i + 1] - static_cast<int32_t>(token);
-  float q[NB], o[NB] = {};
+template <int D>
+struct Stage {
+  static constexpr uint32_t kCodes = kTile * D / 2;
+  static constexpr uint32_t kScales = kTile * (D / 32) * 2;
+  static constexpr uint32_t kBytes = 2 * (kCodes + kScales);   // keys, values, key scales, value scales
+  static constexpr uint32_t kRing = D == 64 ? 6 : 3;
+  static constexpr uint32_t kWarpBytes = kRing * kBytes;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 16-bit matrix, row i in lanes 4 i .. 4 i + 3: transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// x = hi + rest exactly, hi the bf16 pair of (a, b); a and b become the rest.
+__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
+  const uint32_t r = pack_bf16(a, b);
+  a -= __uint_as_float(r << 16);
+  b -= __uint_as_float(r & 0xffff0000u);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Four pairs of a word's codes, 128 + code in bf16 each (exact), or code - 8.
+template <bool SIGNED>
+__device__ __forceinline__ void pairs_bf16(uint32_t w, uint32_t (&x)[4]) {
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const uint64_t at = token * a.q_stride + h * D + 32 * b + lane;
-    if constexpr (BF16) q[b] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.q)[at]) << 16);
-    else q[b] = static_cast<const float*>(a.q)[at];
+  for (int i = 0; i < 4; ++i) {
+    x[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    if constexpr (SIGNED) x[i] = sub_bf16x2(x[i], 0x43084308u);          // - 136
   }
-  int32_t pos = -1;
-  if (static_cast<uint32_t>(s) >= kv.max_seqs || after <= 0) {
-    if (lane == 0) kv_latch(kv, OVL_E_ARG);
+}
+// Four pairs code - 8 in f16: 1024 + code and 1024 + 16 code come out of a mask.
+__device__ __forceinline__ void pairs_f16(uint32_t w, uint32_t (&x)[4]) {
+  const uint32_t h = w >> 8;
+  x[0] = sub_f16x2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);               // - 1032
+  x[1] = fma_f16x2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+  x[2] = sub_f16x2((h & 0x000f000fu) | 0x64006400u, 0x64086408u);
+  x[3] = fma_f16x2((h & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+}
+
+__device__ __forceinline__ float2 halves(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// N consecutive 32-bit words from shared memory, in loads of up to 16 bytes.
+template <int N>
+__device__ __forceinline__ void lds(const void* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *static_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   } else {
-    pos = kv.length[s] - after;
-    if (pos >= static_cast<int32_t>(kv.max_pages << kv.page_shift) ||
-        static_cast<int32_t>(token) - a.off[i] >= static_cast<int32_t>(a.max_new)) {
-      if (lane == 0) kv_latch(kv, OVL_E_SHAPE);
-      pos = -1;
-    }
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int32_t j = 0; j <= pos; ++j) {
-    if (a.window && j <= pos - static_cast<int32_t>(a.window) && j >= static_cast<int32_t>(a.sinks)) continue;
-    const int32_t p = kv.table[static_cast<size_t>(s) * kv.max_pages + (j >> kv.page_shift)];
-    if (static_cast<uint32_t>(p) >= kv.n_pages) {
-      if (lane == 0) kv_latch(kv, OVL_E_ARG);
-      continue;
-    }
-    const uint32_t slot = j & (kv.page - 1);
-    const uint64_t u = kv_unit(kv, p, a.layer, 0, kh);
-    const uint8_t* kc = kv.codes + u * kv.unit_codes + slot * (D / 2);
-    float x = 0.f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t byte = kc[((lane >> 3) * NB + b) * 4 + ((lane & 7) >> 1)];
-      const int code = (byte >> (4 * (lane & 1))) & 15;
-      x += q[b] * (__half2float(kv.scales[u * kv.unit_scales + slot * NB + b]) * (code - 8));
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-    x *= a.scale;
-    const float mn = fmaxf(m, x), f = expf(m - mn), w = expf(x - mn);
-    l = l * f + w;
-    m = mn;
-    const uint64_t uv = kv_unit(kv, p, a.layer, 1, kh);
-    const uint8_t* vc = kv.codes + uv * kv.unit_codes + (slot >> 3) * (4 * D) + (slot & 7) * (D / 16);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t c = 32 * b + lane;
-      const uint32_t byte = vc[(c & 7) * (D / 2) + (c >> 4)];
-      const int code = (byte >> (4 * ((c >> 3) & 1))) & 15;
-      o[b] = o[b] * f + w * (__half2float(kv.scales[uv * kv.unit_scales + slot * NB + b]) * (code - 8));
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const uint64_t at = token * a.out_stride + h * D + 32 * b + lane;
-    const float r = l > 0.f ? o[b] / l : 0.f;
-    if constexpr (BF16) {
-      uint16_t v;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(v) : "f"(r));
-      static_cast<uint16_t*>(a.out)[at] = v;
-    } else {
-      static_cast<float*>(a.out)[at] = r;
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = static_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
 }
 
+// What the rows of one sequence see, in tiles.
+struct Span {
+  int32_t length;      // 0 if the row cannot be used
+  int32_t first;       // position of its first new token
+  uint32_t tokens;     // new tokens
+  uint32_t lead;       // leading tiles that hold sinks outside the window
+  uint32_t start;      // first tile of the window
+  uint32_t tiles;      // lead + tiles of the window; at least 1, so that every row is written
+};
+
+__device__ __forceinline__ Span span_of(const KvDev& kv, const KvQuery& a, uint32_t i, bool report) {
+  Span s{};
+  const int32_t row = a.seqs[i], o0 = a.off[i], o1 = a.off[i + 1];
+  if (o0 < 0 || o1 < o0 || static_cast<uint32_t>(o1) > a.n_tokens) {
+    if (report) kv_latch(kv, OVL_E_ARG);
+    return s;
+  }
+  s.tokens = o1 - o0;
+  s.tiles = 1;
+  if (static_cast<uint32_t>(row) >= kv.max_seqs) {
+    if (report && s.tokens) kv_latch(kv, OVL_E_ARG);
+    return s;
+  }
+  const int32_t n = kv.length[row];
+  const bool fits = n >= 0 && n <= static_cast<int32_t>(kv.max_pages << kv.page_shift);
+  if (report && (!fits || s.tokens > a.max_new)) kv_latch(kv, OVL_E_SHAPE);
+  if (!fits) return s;
+  s.length = n;
+  s.first = n - static_cast<int32_t>(s.tokens);
+  if (n > 0) {
+    if (a.window) {
+      s.start = static_cast<uint32_t>(max(0, s.first - static_cast<int32_t>(a.window) + 1)) / kTile;
+      s.lead = (a.sinks + kTile - 1) / kTile;
+      if (s.lead >= s.start) s.lead = s.start = 0;
+    }
+    s.tiles = s.lead + (static_cast<uint32_t>(n) + kTile - 1) / kTile - s.start;
+  }
+  return s;
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 2)
+    k_kv_decode(const KvDev kv, const KvQuery a) {
+  using St = Stage<D>;
+  constexpr int NB = D / 32;                  // blocks of 32 channels
+  constexpr int MT = D / 16;                  // row tiles of O^T
+  constexpr int NS = BF16 ? 1 : 3;            // bf16 parts of q and of p dV
+  constexpr uint32_t kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* const ring = smem;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kWarps * St::kWarpBytes);
+  float* const s_m = reinterpret_cast<float*>(full + kWarps * St::kRing);     // [kWarps][kRows]
+  float* const s_l = s_m + kWarps * kRows;
+  uint64_t* const before = reinterpret_cast<uint64_t*>(s_l + kWarps * kRows); // [n_seqs + 1] tiles before a sequence
+  __shared__ uint64_t s_warp[kWarps];
+  __shared__ uint32_t s_last;
+
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t rows_group = a.group;        // query heads of a kv head
+
+  // ---- tiles before every sequence
+  if (lane < St::kRing) mbar_init(full + warp * St::kRing + lane, 1);
+  mbar_fence_init();
+  uint64_t base = 0;
+  for (uint32_t i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
+    const uint32_t i = i0 + tid;
+    uint64_t w = 0;
+    if (i < a.n_seqs) {
+      const Span s = span_of(kv, a, i, blockIdx.x == 0);
+      w = static_cast<uint64_t>(s.tiles) * kv.heads * ((s.tokens * rows_group + kRows - 1) / kRows);
+    }
+    uint64_t inc = w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const uint64_t o = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= static_cast<uint32_t>(k)) inc += o;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    uint64_t add = base;
+    for (uint32_t k = 0; k < kWarps; ++k) {
+      if (k < warp) add += s_warp[k];
+      base += s_warp[k];
+    }
+    if (i < a.n_seqs) before[i] = add + inc - w;
+    __syncthreads();
+  }
+  if (tid == 0) before[a.n_seqs] = base;
+  __syncthreads();
+  const uint64_t total = base;
+  // at least one tile for every warp: shorter runs only add joins
+  const uint64_t chunk = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint64_t>(kWarps));
+  uint64_t at = min(blockIdx.x * chunk, total);
+  const uint64_t end = min(at + chunk, total);
+
+  uint8_t* const my_ring = ring + warp * St::kWarpBytes;
+  uint64_t* const my_full = full + warp * St::kRing;
+  const uint64_t policy = l2_evict_first_policy();
+  uint32_t slot = 0, phase = 0;               // of the ring, across segments
+  const float scale2 = a.scale * kLog2e;
+
+  while (at < end) {
+    // ---- the segment
+    uint32_t lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) >> 1;
+      if (before[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    // sequences without new tokens have no tiles: the last one that starts here owns the tile
+    const uint32_t seq = lo;
+    const Span sp = span_of(kv, a, seq, false);
+    const uint64_t local = at - before[seq];
+    const uint32_t seg = static_cast<uint32_t>(local / sp.tiles), tile0 = static_cast<uint32_t>(local % sp.tiles);
+    const uint32_t tile1 = static_cast<uint32_t>(min(static_cast<uint64_t>(sp.tiles), tile0 + (end - at)));
+    const uint64_t seg_begin = at - tile0, seg_end = seg_begin + sp.tiles;
+    const uint32_t groups = (sp.tokens * rows_group + kRows - 1) / kRows;
+    const uint32_t kh = seg / groups, r0 = (seg % groups) * kRows;
+    const uint32_t n_rows = min(kRows, sp.tokens * rows_group - r0);
+    const int32_t* const pages = kv.table + static_cast<size_t>(sp.length ? a.seqs[seq] : 0) * kv.max_pages;
+    const int32_t token0 = a.off[seq];
+
+    // ---- what this warp's share of the run reads: page numbers 32 tiles ahead
+    const uint32_t n_mine = tile1 > tile0 + warp ? (tile1 - tile0 - warp + kWarps - 1) / kWarps : 0;
+    auto token_of = [&](uint32_t k) {         // first token of this warp's k-th tile
+      const uint32_t x = tile0 + warp + k * kWarps;
+      return (x < sp.lead ? x : x - sp.lead + sp.start) * kTile;
+    };
+    // the page of a tile's first half and, where pages are 16 tokens, of its second
+    auto page_at = [&](uint32_t tok) -> int32_t {
+      if (tok >= static_cast<uint32_t>(sp.length)) return -1;
+      const int32_t p = pages[tok >> kv.page_shift];
+      if (static_cast<uint32_t>(p) < kv.n_pages) return p;
+      kv_latch(kv, OVL_E_ARG);
+      return -1;
+    };
+    auto fetch_pages = [&](uint32_t k0, int32_t& p0, int32_t& p1) {
+      p0 = p1 = -1;
+      if (k0 + lane < n_mine) {
+        const uint32_t tok = token_of(k0 + lane);
+        p0 = page_at(tok);
+        p1 = kv.page == 16 ? page_at(tok + 16) : p0;
+      }
+    };
+    int32_t ids0, ids1;                       // of tiles 32 * (k / 32) + lane
+    fetch_pages(0, ids0, ids1);
+    // The tile's copies into ring slot sl; called by the whole warp.
+    auto issue = [&](uint32_t k, int32_t p0, int32_t p1, uint32_t sl) {
+      if (lane == 0) {
+        uint8_t* const dst = my_ring + sl * St::kBytes;
+        uint64_t* const bar = my_full + sl;
+        const uint32_t in_page = token_of(k) & (kv.page - 1);
+        const uint32_t part = kv.page == 16 ? 2 : 1;
+        const uint32_t codes = St::kCodes / part, scales = St::kScales / part;
+        const uint32_t n = part == 1 ? (p0 >= 0) : (p0 >= 0) + (p1 >= 0);
+        mbar_arrive_expect_tx(bar, n * 2 * (codes + scales));
+        for (uint32_t h = 0; h < part; ++h) {
+          const int32_t p = h ? p1 : p0;
+          if (p < 0) continue;
+          const uint64_t uk = kv_unit(kv, p, a.layer, 0, kh), uv = uk + kv.heads;
+          const uint32_t co = in_page * (D / 2), so = in_page * NB;
+          bulk_g2s(dst + h * codes, kv.codes + uk * kv.unit_codes + co, codes, bar, policy);
+          bulk_g2s(dst + St::kCodes + h * codes, kv.codes + uv * kv.unit_codes + co, codes, bar, policy);
+          bulk_g2s(dst + 2 * St::kCodes + h * scales, kv.scales + uk * kv.unit_scales + so, scales, bar, policy);
+          bulk_g2s(dst + 2 * St::kCodes + St::kScales + h * scales, kv.scales + uv * kv.unit_scales + so, scales, bar,
+                   policy);
+        }
+      }
+    };
+    uint32_t sent = 0, sent_slot = slot;
+#pragma unroll 1
+    for (; sent < min(n_mine, St::kRing); ++sent) {
+      issue(sent, __shfl_sync(0xffffffffu, ids0, sent), __shfl_sync(0xffffffffu, ids1, sent), sent_slot);
+      sent_slot = sent_slot + 1 == St::kRing ? 0 : sent_slot + 1;
+    }
+
+    // ---- the rows: q as the MMA's second operand, and where each column looks
+    uint32_t qf[NT][NS][NB][4];
+    float qc[NT][NB][2];                      // -136 * the block sums of columns 2 t, 2 t + 1
+    int32_t last[NT][2], from[NT][2];         // a column sees tokens <= last and (>= from or < sinks)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t r = nt * 8 + g;
+      const bool on = r < n_rows;
+      const uint32_t row = r0 + (on ? r : 0);
+      const uint64_t qa = static_cast<uint64_t>(token0 + row / rows_group) * a.q_stride +
+                          (kh * rows_group + row % rows_group) * D;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float x[8];
+        if constexpr (BF16) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (on) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qa + 32 * b + 8 * t));
+          qf[nt][0][b][0] = __byte_perm(v.x, v.z, 0x5410);
+          qf[nt][0][b][1] = __byte_perm(v.x, v.z, 0x7632);
+          qf[nt][0][b][2] = __byte_perm(v.y, v.w, 0x5410);
+          qf[nt][0][b][3] = __byte_perm(v.y, v.w, 0x7632);
+          float sum = 0.f;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          qc[nt][b][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t);
+          qc[nt][b][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        } else {
+          float4 u = make_float4(0, 0, 0, 0), v = u;
+          if (on) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qa + 32 * b + 8 * t);
+            u = __ldg(p), v = __ldg(p + 1);
+          }
+          x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) qf[nt][s][b][k] = take_bf16(x[k], x[k + 4]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t c = nt * 8 + 2 * t + e, i = (r0 + c) / rows_group;
+        last[nt][e] = c < n_rows && i < a.max_new && sp.length ? sp.first + static_cast<int32_t>(i) : -1;
+        from[nt][e] = a.window ? last[nt][e] - static_cast<int32_t>(a.window) + 1 : 0;
+      }
+    }
+    // tiles that every row sees whole need no mask
+    const uint32_t i0 = r0 / rows_group, i1 = (r0 + n_rows - 1) / rows_group;
+    const int32_t all_last = i1 < a.max_new ? sp.first + static_cast<int32_t>(i0) : -1;
+    const int32_t all_from = a.window ? sp.first + static_cast<int32_t>(i1) - static_cast<int32_t>(a.window) + 1 : 0;
+    const int32_t sinks = static_cast<int32_t>(a.sinks);
+
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -CUDART_INF_F;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+
+    // ---- the tiles
+    int32_t cur0 = ids0, cur1 = ids1;         // page numbers of the tiles being read
+#pragma unroll 1
+    for (uint32_t k = 0; k < n_mine; ++k) {
+      if (k && (k & 31) == 0) cur0 = ids0, cur1 = ids1;
+      const int32_t p0 = __shfl_sync(0xffffffffu, cur0, k & 31), p1 = __shfl_sync(0xffffffffu, cur1, k & 31);
+      const int32_t tok = static_cast<int32_t>(token_of(k));
+      if (!mbar_wait_bounded(my_full + slot, phase)) {
+        if (lane == 0) kv_latch(kv, OVL_E_DEVICE_TIMEOUT);   // a copy did not land: reported, not waited for again
+      }
+      const uint8_t* const st = my_ring + slot * St::kBytes;
+      const bool masked = tok + static_cast<int32_t>(kTile) - 1 > all_last || p0 < 0 || p1 < 0 ||
+                          !(tok >= all_from || tok + static_cast<int32_t>(kTile) <= sinks);
+
+      // scores: tokens 16 sub + g and + 8 against columns 2 t, 2 t + 1
+      float s[2][NT][4];
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        uint32_t k0[NB], k1[NB], d0[NB / 2], d1[NB / 2];
+        const uint8_t* const kr = st + (16 * sub + g) * (D / 2) + t * (D / 8);
+        lds<NB>(kr, k0);
+        lds<NB>(kr + 8 * (D / 2), k1);
+        const uint8_t* const dr = st + 2 * St::kCodes + (16 * sub + g) * (NB * 2);
+        lds<NB / 2>(dr, d0);
+        lds<NB / 2>(dr + 8 * NB * 2, d1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[sub][nt][0] = s[sub][nt][1] = s[sub][nt][2] = s[sub][nt][3] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t x[4], y[4];
+          pairs_bf16<!BF16>(k0[b], x);
+          pairs_bf16<!BF16>(k1[b], y);
+          const float2 e0 = halves(d0[b / 2]), e1 = halves(d1[b / 2]);
+          const float f0 = b & 1 ? e0.y : e0.x, f1 = b & 1 ? e1.y : e1.x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float c[4];
+            if constexpr (BF16) c[0] = c[2] = qc[nt][b][0], c[1] = c[3] = qc[nt][b][1];
+            else c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+            for (int p = 0; p < NS; ++p) {
+              mma_bf16(c, x[0], y[0], x[1], y[1], qf[nt][p][b][0], qf[nt][p][b][1]);
+              mma_bf16(c, x[2], y[2], x[3], y[3], qf[nt][p][b][2], qf[nt][p][b][3]);
+            }
+            s[sub][nt][0] = fmaf(f0, c[0], s[sub][nt][0]);
+            s[sub][nt][1] = fmaf(f0, c[1], s[sub][nt][1]);
+            s[sub][nt][2] = fmaf(f1, c[2], s[sub][nt][2]);
+            s[sub][nt][3] = fmaf(f1, c[3], s[sub][nt][3]);
+          }
+        }
+      }
+      // the largest value scale of the tile, as the exponent above it (bf16 calls)
+      const uint8_t* const vd = st + 2 * St::kCodes + St::kScales;
+      const uint32_t held0 = p0 < 0 ? 0u : 16u, held1 = p1 < 0 ? 0u : 16u;
+      auto written = [&](uint32_t j) {        // token j of the tile holds data
+        return tok + static_cast<int32_t>(j) < sp.length && (j < 16 ? j < held0 : j - 16 < held1);
+      };
+      float above = 0.f;
+      if constexpr (BF16) {
+        uint32_t v[NB / 2];
+        lds<NB / 2>(vd + lane * NB * 2, v);
+        uint32_t x = v[0];
+#pragma unroll
+        for (int i = 1; i < NB / 2; ++i) x = __vmaxu2(x, v[i]);
+        x = max(x & 0xffffu, x >> 16);
+        if (masked && !written(lane)) x = 0;
+        x = __reduce_max_sync(0xffffffffu, x);
+        above = static_cast<float>(static_cast<int32_t>(x >> 10) - 14);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = s[sub][nt][i] * scale2;
+            if (masked) {
+              const int32_t j = tok + 16 * sub + static_cast<int32_t>(g) + (i & 2 ? 8 : 0);
+              const bool sees = j <= last[nt][i & 1] && (j >= from[nt][i & 1] || j < sinks) &&
+                                (sub ? held1 : held0);
+              if (!sees) v = -CUDART_INF_F;
+            }
+            s[sub][nt][i] = v;
+          }
+      bool grew = false;
+      float ref[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(m[nt][e], x + above);
+          grew |= x > m[nt][e];
+          ref[nt][e] = x;
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = m[nt][e] == -CUDART_INF_F ? 0.f : ex2(m[nt][e] - ref[nt][e]);
+            m[nt][e] = ref[nt][e];
+            l[nt][e] *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[nt][i][e] *= f, o[nt][i][e + 2] *= f;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float r = m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];   // nothing seen yet: every weight is 0
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            s[sub][nt][e] = ex2(s[sub][nt][e] - r);
+            s[sub][nt][e + 2] = ex2(s[sub][nt][e + 2] - r);
+            l[nt][e] += s[sub][nt][e] + s[sub][nt][e + 2];
+          }
+        }
+
+      // values: channels as rows, tokens 2 t, 2 t + 1 and + 8 of a sub-tile as the summed index
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        uint32_t va[NB], vb[NB], d0[NB / 2], d1[NB / 2];     // [token 2t | 2t + 1][NB / 2 words], first and second 8 tokens
+        const uint8_t* const vr = st + St::kCodes + sub * (8 * D) + lane * (D / 8);
+        lds<NB>(vr, va);
+        lds<NB>(vr + 4 * D, vb);
+        const uint8_t* const dr = vd + (16 * sub + g) * (NB * 2);
+        lds<NB / 2>(dr, d0);
+        lds<NB / 2>(dr + 8 * NB * 2, d1);
+        if (masked) {                         // what was never written may hold any bits
+          const bool w0 = written(16 * sub + g), w1 = written(16 * sub + g + 8);
+#pragma unroll
+          for (int i = 0; i < NB / 2; ++i) d0[i] = w0 ? d0[i] : 0u, d1[i] = w1 ? d1[i] : 0u;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float2 e0 = halves(d0[b / 2]), e1 = halves(d1[b / 2]);
+          const float f0 = b & 1 ? e0.y : e0.x, f1 = b & 1 ? e1.y : e1.x;
+          const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
+          const uint32_t wa = __byte_perm(va[b / 2], va[NB / 2 + b / 2], pick);
+          const uint32_t wb = __byte_perm(vb[b / 2], vb[NB / 2 + b / 2], pick);
+          uint32_t x[4], y[4];
+          if constexpr (BF16) pairs_f16(wa, x), pairs_f16(wb, y);
+          else pairs_bf16<true>(wa, x), pairs_bf16<true>(wb, y);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float a0 = s[sub][nt][0] * f0, a1 = s[sub][nt][1] * f0, b0 = s[sub][nt][2] * f1, b1 = s[sub][nt][3] * f1;
+            if constexpr (BF16) {
+              const uint32_t u = transposed(pack_f16(a0, a1)), v = transposed(pack_f16(b0, b1));
+              mma_f16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v);
+              mma_f16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v);
+            } else {
+#pragma unroll
+              for (int p = 0; p < NS; ++p) {
+                const uint32_t u = transposed(take_bf16(a0, a1)), v = transposed(take_bf16(b0, b1));
+                mma_bf16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v);
+                mma_bf16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v);
+              }
+            }
+          }
+        }
+      }
+
+      // this slot is read: refill it
+      __syncwarp();
+      if (sent < n_mine) {
+        if ((sent & 31) == 0) fetch_pages(sent, ids0, ids1);
+        issue(sent, __shfl_sync(0xffffffffu, ids0, sent & 31), __shfl_sync(0xffffffffu, ids1, sent & 31), slot);
+        ++sent;
+      }
+      if (++slot == St::kRing) slot = 0, phase ^= 1;
+    }
+
+    // ---- the warps' results into shared memory (each over its own ring, which is drained)
+    constexpr uint32_t kLd = D + 4;
+    float* const mine = reinterpret_cast<float*>(my_ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nt][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const uint32_t r = nt * 8 + 2 * t + e;
+        if (g == 0) s_m[warp * kRows + r] = m[nt][e], s_l[warp * kRows + r] = x;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          mine[r * kLd + 16 * i + g] = o[nt][i][e];
+          mine[r * kLd + 16 * i + 8 + g] = o[nt][i][e + 2];
+        }
+      }
+    __syncthreads();
+
+    const uint32_t c0 = static_cast<uint32_t>(seg_begin / chunk), c1 = static_cast<uint32_t>((seg_end - 1) / chunk);
+    const bool whole = c0 == c1;
+    constexpr uint32_t kPart = kKvPartialRows * (D + 2);
+    auto part_of = [&](uint32_t c) { return kv.partial + (static_cast<size_t>(c) * 2 + (c == c0)) * kPart; };
+    auto store = [&](uint32_t r, uint32_t c, float4 v) {
+      const uint32_t row = r0 + r;
+      const uint64_t to = static_cast<uint64_t>(token0 + row / rows_group) * a.out_stride +
+                          (kh * rows_group + row % rows_group) * D + c;
+      if constexpr (BF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = v;
+    };
+    for (uint32_t i = tid; i < n_rows * (D / 4); i += kThreads) {
+      const uint32_t r = i / (D / 4), c = i % (D / 4) * 4;
+      float top = s_m[r];
+#pragma unroll
+      for (uint32_t w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w * kRows + r]);
+      float sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float zero = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll
+      for (uint32_t w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w * kRows + r] - zero);
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + w * St::kWarpBytes) +
+                                                          r * kLd + c);
+        sum = fmaf(f, s_l[w * kRows + r], sum);
+        v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);   // nothing seen: zeros
+        store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      } else {
+        float* const p = part_of(blockIdx.x);
+        __stcg(reinterpret_cast<float4*>(p + r * D + c), v);
+        if (c == 0) __stcg(p + kKvPartialRows * D + r, top), __stcg(p + kKvPartialRows * (D + 1) + r, sum);
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t seen = atomicAdd(kv.joined + c0, 1u);
+        s_last = seen == c1 - c0;
+        if (s_last) kv.joined[c0] = 0;        // for the next call
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (uint32_t i = tid; i < n_rows * (D / 4); i += kThreads) {
+          const uint32_t r = i / (D / 4), c = i % (D / 4) * 4;
+          float top = -CUDART_INF_F;
+#pragma unroll 8
+          for (uint32_t k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part_of(k) + kKvPartialRows * D + r));
+          const float zero = top == -CUDART_INF_F ? 0.f : top;
+          float sum = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (uint32_t k = c0; k <= c1; ++k) {
+            const float* const p = part_of(k);
+            const float f = ex2(__ldcg(p + kKvPartialRows * D + r) - zero);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * D + c));
+            sum = fmaf(f, __ldcg(p + kKvPartialRows * (D + 1) + r), sum);
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+          }
+          const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);   // nothing seen: zeros
+          store(r, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        }
+      }
+    }
+    at += tile1 - tile0;
+    // the rings take copies again: order them after the plain accesses above
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+}
+
+template <int D, bool BF16, int NT>
+cudaError_t decode(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
+  using St = Stage<D>;
+  const uint32_t bytes = kWarps * (St::kWarpBytes + 8 * St::kRing + 2 * 4 * 8 * NT) + 8 * (a.n_seqs + 1);
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(k_kv_decode<D, BF16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
+  if (ready != cudaSuccess) return ready;
+  // resident CTAs of an SM: by shared memory (1 KB of it is the system's) and by the launch bound
+  const uint32_t by_smem = 228 * 1024 / (bytes + 1024 + 256), by_regs = D <= 128 && BF16 && NT == 1 ? 4 : 2;
+  const uint32_t per_sm = by_smem < by_regs ? by_smem : by_regs;
+  uint32_t grid = kv_sm_count() * (per_sm ? per_sm : 1);
+  if (grid > kKvMaxCtas) grid = kKvMaxCtas;
+  k_kv_decode<D, BF16, NT><<<grid, kThreads, bytes, st>>>(kv, a);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t attend_dim(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
-  const uint64_t blocks = (static_cast<uint64_t>(a.n_tokens) * a.heads + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  if (a.bf16) k_kv_attend<D, true><<<static_cast<uint32_t>(blocks), kWarps * 32, 0, st>>>(kv, a);
-  else k_kv_attend<D, false><<<static_cast<uint32_t>(blocks), kWarps * 32, 0, st>>>(kv, a);
-  return cudaGetLastError();
+  // 16 rows of 256 channels do not fit the registers
+  if constexpr (D <= 128) {
+    if (static_cast<uint64_t>(a.max_new) * a.group > 8)
+      return a.bf16 ? decode<D, true, 2>(kv, a, st) : decode<D, false, 2>(kv, a, st);
+  }
+  return a.bf16 ? decode<D, true, 1>(kv, a, st) : decode<D, false, 1>(kv, a, st);
 }
 
 }  // namespace
