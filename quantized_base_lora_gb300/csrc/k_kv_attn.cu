@@ -8,19 +8,22 @@
 //
 // Mathematics.  With code = c + 8 and one scale d for 32 channels,
 //   s_j = sum_b dK_jb (sum_{i in b} c_ji q_i),   o = sum_j p_j dV_jb c_j,
-// so the codes go into the MMA as they are: small integers, exact in bf16 and
-// f16, taken out of a word with one mask (bits 16 + 4 i and 4 i of a word are
-// the two halves of a pair) and an exponent.  A key pair is the bf16 128 + code;
-// the constant 136 sum(q) of a block is the accumulator's start, so keys cost no
-// subtraction.  The scale of a key block multiplies its accumulator (fp32); the
-// scale of a value block multiplies p, once a block.  Nothing is dequantized in
-// memory.  S^T = K Q^T has tokens as rows, so its accumulator has to be
-// transposed to become the second operand of O^T = V^T P: one movmatrix for 8x8.
+// so the codes go into the MMA as they are: small integers, exact in f16.  Bits
+// 4 i and 16 + 4 i of a word are the two halves of a pair; one mask with an
+// exponent makes them 1024 + code (even i) or 1024 + 16 code (odd i).  bf16
+// calls leave keys like that: odd channels' q is divided by 16 and the constants'
+// share, a sum of q over the block, is the accumulator's start.  The scale of a
+// key block multiplies its accumulator (fp32); the scale of a value block
+// multiplies p, once a block.  Nothing is dequantized in memory.  S^T = K Q^T has
+// tokens as rows, so its accumulator has to be transposed to become the second
+// operand of O^T = V^T P: one movmatrix for 8x8.
 //
-// Precision.  bf16 calls: q is exact; p dV is rounded to f16.  The running
-// reference of the softmax is max_j(s_j) + E, 2^E above every value scale of the
-// tile, so p dV <= 1 and keeps 11 bits whatever the scales' size.  f32 calls: q
-// and p dV are split into three bf16 each (24 bits), three MMAs in place of one.
+// Precision.  A row of q is scaled by a power of two into f16's range (below
+// 2^10; undone in fp32): exact for bf16 down to 2^-22 of the row's maximum, and as
+// two f16 parts 24 bits of an fp32 q.  The running reference of the softmax is
+// max_j(s_j) + E, E chosen from the tile's largest value scale so that p dV stays
+// below 2^15: bf16 calls round p and p dV to f16 (11 bits each), f32 calls keep
+// p dV as two f16 parts.
 //
 // Split.  All tiles of the call, segment after segment, are dealt to the CTAs in
 // equal runs, whatever the lengths are (they are known on the device only).  The
@@ -58,20 +61,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+               "{%10, %11, %12, %13};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // 8x8 16-bit matrix, row i in lanes 4 i .. 4 i + 3: transposed.
@@ -91,46 +86,53 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// x = hi + rest exactly, hi the bf16 pair of (a, b); a and b become the rest.
-__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
-  const uint32_t r = pack_bf16(a, b);
-  a -= __uint_as_float(r << 16);
-  b -= __uint_as_float(r & 0xffff0000u);
+// (a, b) as f16 pairs, the rounded part first; a and b become the rest.
+__device__ __forceinline__ uint32_t take_f16(float& a, float& b) {
+  const uint32_t r = pack_f16(a, b);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+  a -= f.x;
+  b -= f.y;
   return r;
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-
-// Four pairs of a word's codes, 128 + code in bf16 each (exact), or code - 8.
-template <bool SIGNED>
-__device__ __forceinline__ void pairs_bf16(uint32_t w, uint32_t (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    if constexpr (SIGNED) x[i] = sub_bf16x2(x[i], 0x43084308u);          // - 136
-  }
+// (w & MASK) | magic in one LOP3: only one of the two can be an immediate, so
+// magic is a register that the compiler cannot see through.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return r;
 }
-// Four pairs code - 8 in f16: 1024 + code and 1024 + 16 code come out of a mask.
-__device__ __forceinline__ void pairs_f16(uint32_t w, uint32_t (&x)[4]) {
+
+// The four pairs of a word's codes in f16: 1024 + code, 1024 + 16 code, and both
+// again, or exactly code - 8.  magic: 0x64006400.
+template <bool SIGNED>
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t magic, uint32_t (&x)[4]) {
   const uint32_t h = w >> 8;
-  x[0] = sub_f16x2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);               // - 1032
-  x[1] = fma_f16x2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);  // / 16 - 72
-  x[2] = sub_f16x2((h & 0x000f000fu) | 0x64006400u, 0x64086408u);
-  x[3] = fma_f16x2((h & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);
+  x[0] = mask_or<0x000f000fu>(w, magic);
+  x[1] = mask_or<0x00f000f0u>(w, magic);
+  x[2] = mask_or<0x000f000fu>(h, magic);
+  x[3] = mask_or<0x00f000f0u>(h, magic);
+  if constexpr (SIGNED) {
+    x[0] = sub_f16x2(x[0], 0x64086408u);                  // - 1032
+    x[1] = fma_f16x2(x[1], 0x2c002c00u, 0xd480d480u);     // / 16 - 72
+    x[2] = sub_f16x2(x[2], 0x64086408u);
+    x[3] = fma_f16x2(x[3], 0x2c002c00u, 0xd480d480u);
+  }
 }
 
 __device__ __forceinline__ float2 halves(uint32_t w) {
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   using St = Stage<D>;
   constexpr int NB = D / 32;                  // blocks of 32 channels
   constexpr int MT = D / 16;                  // row tiles of O^T
-  constexpr int NS = BF16 ? 1 : 3;            // bf16 parts of q and of p dV
+  constexpr int NS = BF16 ? 1 : 2;            // f16 parts of q and of p dV
   constexpr uint32_t kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* const ring = smem;
@@ -254,6 +256,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   const uint64_t policy = l2_evict_first_policy();
   uint32_t slot = 0, phase = 0;               // of the ring, across segments
   const float scale2 = a.scale * kLog2e;
+  uint32_t magic;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
   while (at < end) {
     // ---- the segment
@@ -300,28 +304,25 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
     };
     int32_t ids0, ids1;                       // of tiles 32 * (k / 32) + lane
     fetch_pages(0, ids0, ids1);
-    // The tile's copies into ring slot sl; called by the whole warp.
+    // The tile's copies into ring slot sl, called by the whole warp: lanes 0 to 3
+    // take key codes, value codes, key scales and value scales, where pages are 16
+    // tokens for the first half and lanes 4 to 7 for the second.
+    const uint32_t what = lane & 3, part = kv.page == 16 ? 2 : 1;
+    const uint32_t tok_bytes = what < 2 ? D / 2 : NB * 2, copy_bytes = (what < 2 ? St::kCodes : St::kScales) / part;
+    const uint32_t copy_to = (what & 1) * (what < 2 ? St::kCodes : St::kScales) + (what < 2 ? 0 : 2 * St::kCodes) +
+                             (lane >> 2) * copy_bytes;
+    const uint64_t unit_bytes = what < 2 ? kv.unit_codes : 2 * kv.unit_scales;
+    const uint64_t page_bytes = unit_bytes * kv.layers * 2 * kv.heads;
+    const uint8_t* const copy_from = (what < 2 ? kv.codes : reinterpret_cast<const uint8_t*>(kv.scales)) +
+                                     kv_unit(kv, 0, a.layer, what & 1, kh) * unit_bytes;
     auto issue = [&](uint32_t k, int32_t p0, int32_t p1, uint32_t sl) {
-      if (lane == 0) {
-        uint8_t* const dst = my_ring + sl * St::kBytes;
-        uint64_t* const bar = my_full + sl;
-        const uint32_t in_page = token_of(k) & (kv.page - 1);
-        const uint32_t part = kv.page == 16 ? 2 : 1;
-        const uint32_t codes = St::kCodes / part, scales = St::kScales / part;
-        const uint32_t n = part == 1 ? (p0 >= 0) : (p0 >= 0) + (p1 >= 0);
-        mbar_arrive_expect_tx(bar, n * 2 * (codes + scales));
-        for (uint32_t h = 0; h < part; ++h) {
-          const int32_t p = h ? p1 : p0;
-          if (p < 0) continue;
-          const uint64_t uk = kv_unit(kv, p, a.layer, 0, kh), uv = uk + kv.heads;
-          const uint32_t co = in_page * (D / 2), so = in_page * NB;
-          bulk_g2s(dst + h * codes, kv.codes + uk * kv.unit_codes + co, codes, bar, policy);
-          bulk_g2s(dst + St::kCodes + h * codes, kv.codes + uv * kv.unit_codes + co, codes, bar, policy);
-          bulk_g2s(dst + 2 * St::kCodes + h * scales, kv.scales + uk * kv.unit_scales + so, scales, bar, policy);
-          bulk_g2s(dst + 2 * St::kCodes + St::kScales + h * scales, kv.scales + uv * kv.unit_scales + so, scales, bar,
-                   policy);
-        }
-      }
+      const uint32_t in_page = token_of(k) & (kv.page - 1);
+      const int32_t p = lane < 4 ? p0 : p1;
+      const uint32_t n = part == 1 ? 2 * (p0 >= 0) : (p0 >= 0) + (p1 >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(my_full + sl, n * (St::kCodes + St::kScales));
+      if (lane < 4 * part && p >= 0)
+        bulk_g2s(my_ring + sl * St::kBytes + copy_to, copy_from + p * page_bytes + in_page * tok_bytes, copy_bytes,
+                 my_full + sl, policy);
     };
     uint32_t sent = 0, sent_slot = slot;
 #pragma unroll 1
@@ -332,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
     // ---- the rows: q as the MMA's second operand, and where each column looks
     uint32_t qf[NT][NS][NB][4];
-    float qc[NT][NB][2];                      // -136 * the block sums of columns 2 t, 2 t + 1
+    float qc[NT][NB][4];                      // accumulator start of a block, columns 2 t and 2 t + 1
+    float to_log2[NT][2];                     // scale, log2(e) and the row's power of two
     int32_t last[NT][2], from[NT][2];         // a column sees tokens <= last and (>= from or < sinks)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -341,37 +343,62 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       const uint32_t row = r0 + (on ? r : 0);
       const uint64_t qa = static_cast<uint64_t>(token0 + row / rows_group) * a.q_stride +
                           (kh * rows_group + row % rows_group) * D;
+      float x[NB][8], top = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float x[8];
         if constexpr (BF16) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (on) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qa + 32 * b + 8 * t));
-          qf[nt][0][b][0] = __byte_perm(v.x, v.z, 0x5410);
-          qf[nt][0][b][1] = __byte_perm(v.x, v.z, 0x7632);
-          qf[nt][0][b][2] = __byte_perm(v.y, v.w, 0x5410);
-          qf[nt][0][b][3] = __byte_perm(v.y, v.w, 0x7632);
-          float sum = 0.f;
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sum += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          qc[nt][b][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t);
-          qc[nt][b][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+          for (int k = 0; k < 4; ++k)
+            x[b][2 * k] = __uint_as_float(w[k] << 16), x[b][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         } else {
           float4 u = make_float4(0, 0, 0, 0), v = u;
           if (on) {
             const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qa + 32 * b + 8 * t);
             u = __ldg(p), v = __ldg(p + 1);
           }
-          x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+          x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
+          x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
+        }
 #pragma unroll
-          for (int s = 0; s < NS; ++s)
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[b][k]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(9 - ex)
+      const uint32_t ex = min(max(__float_as_uint(top) >> 23, 10u), 254u);
+      const float up = __uint_as_float((263u - ex) << 23), down = __uint_as_float((ex - 9u) << 23);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) qf[nt][s][b][k] = take_bf16(x[k], x[k + 4]);
+      for (int b = 0; b < NB; ++b) {
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float u = x[b][k] * up, v = x[b][k + 4] * up;
+          if constexpr (BF16) {
+            uint32_t h = pack_f16(u, v);
+            const float2 f = halves(h);
+            if (k & 1) odd += f.x + f.y, h = pack_f16(f.x * 0.0625f, f.y * 0.0625f);
+            else even += f.x + f.y;
+            qf[nt][0][b][k] = h;
+          } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) qf[nt][s][b][k] = take_f16(u, v);
+          }
+        }
+        if constexpr (BF16) {
+          float c = -1032.f * even - 72.f * odd;
+          c += __shfl_xor_sync(0xffffffffu, c, 1);
+          c += __shfl_xor_sync(0xffffffffu, c, 2);
+          qc[nt][b][0] = qc[nt][b][2] = __shfl_sync(0xffffffffu, c, 8 * t);
+          qc[nt][b][1] = qc[nt][b][3] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+        } else {
+          qc[nt][b][0] = qc[nt][b][1] = qc[nt][b][2] = qc[nt][b][3] = 0.f;
         }
       }
+      to_log2[nt][0] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t);
+      to_log2[nt][1] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t c = nt * 8 + 2 * t + e, i = (r0 + c) / rows_group;
@@ -424,19 +451,19 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t x[4], y[4];
-          pairs_bf16<!BF16>(k0[b], x);
-          pairs_bf16<!BF16>(k1[b], y);
+          pairs<!BF16>(k0[b], magic, x);
+          pairs<!BF16>(k1[b], magic, y);
           const float2 e0 = halves(d0[b / 2]), e1 = halves(d1[b / 2]);
           const float f0 = b & 1 ? e0.y : e0.x, f1 = b & 1 ? e1.y : e1.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float c[4];
-            if constexpr (BF16) c[0] = c[2] = qc[nt][b][0], c[1] = c[3] = qc[nt][b][1];
-            else c[0] = c[1] = c[2] = c[3] = 0.f;
+            mma_f16(c, x[0], y[0], x[1], y[1], qf[nt][0][b][0], qf[nt][0][b][1], qc[nt][b]);
+            mma_f16(c, x[2], y[2], x[3], y[3], qf[nt][0][b][2], qf[nt][0][b][3], c);
 #pragma unroll
-            for (int p = 0; p < NS; ++p) {
-              mma_bf16(c, x[0], y[0], x[1], y[1], qf[nt][p][b][0], qf[nt][p][b][1]);
-              mma_bf16(c, x[2], y[2], x[3], y[3], qf[nt][p][b][2], qf[nt][p][b][3]);
+            for (int p = 1; p < NS; ++p) {
+              mma_f16(c, x[0], y[0], x[1], y[1], qf[nt][p][b][0], qf[nt][p][b][1], c);
+              mma_f16(c, x[2], y[2], x[3], y[3], qf[nt][p][b][2], qf[nt][p][b][3], c);
             }
             s[sub][nt][0] = fmaf(f0, c[0], s[sub][nt][0]);
             s[sub][nt][1] = fmaf(f0, c[1], s[sub][nt][1]);
@@ -445,39 +472,43 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           }
         }
       }
-      // the largest value scale of the tile, as the exponent above it (bf16 calls)
+      // the largest value scale of the tile, 2^(E - 1) <= it < 2^E, and what that
+      // leaves for p: p dV < 2^15, and where p itself is rounded to f16, p too
       const uint8_t* const vd = st + 2 * St::kCodes + St::kScales;
-      const uint32_t held0 = p0 < 0 ? 0u : 16u, held1 = p1 < 0 ? 0u : 16u;
+      const bool held0 = p0 >= 0, held1 = p1 >= 0;
       auto written = [&](uint32_t j) {        // token j of the tile holds data
-        return tok + static_cast<int32_t>(j) < sp.length && (j < 16 ? j < held0 : j - 16 < held1);
+        return tok + static_cast<int32_t>(j) < sp.length && (j < 16 ? held0 : held1);
       };
-      float above = 0.f;
-      if constexpr (BF16) {
+      uint32_t vmax;
+      {
         uint32_t v[NB / 2];
         lds<NB / 2>(vd + lane * NB * 2, v);
-        uint32_t x = v[0];
+        vmax = v[0];
 #pragma unroll
-        for (int i = 1; i < NB / 2; ++i) x = __vmaxu2(x, v[i]);
-        x = max(x & 0xffffu, x >> 16);
-        if (masked && !written(lane)) x = 0;
-        x = __reduce_max_sync(0xffffffffu, x);
-        above = static_cast<float>(static_cast<int32_t>(x >> 10) - 14);
+        for (int i = 1; i < NB / 2; ++i) vmax = __vmaxu2(vmax, v[i]);
+        vmax = max(vmax & 0xffffu, vmax >> 16);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = s[sub][nt][i] * scale2;
-            if (masked) {
+          for (int i = 0; i < 4; ++i) s[sub][nt][i] *= to_log2[nt][i & 1];
+      if (masked) {
+        if (!written(lane)) vmax = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
               const int32_t j = tok + 16 * sub + static_cast<int32_t>(g) + (i & 2 ? 8 : 0);
-              const bool sees = j <= last[nt][i & 1] && (j >= from[nt][i & 1] || j < sinks) &&
-                                (sub ? held1 : held0);
-              if (!sees) v = -CUDART_INF_F;
+              const bool sees = j <= last[nt][i & 1] && (j >= from[nt][i & 1] || j < sinks) && (sub ? held1 : held0);
+              if (!sees) s[sub][nt][i] = -CUDART_INF_F;
             }
-            s[sub][nt][i] = v;
-          }
+      }
+      const int32_t top_exp = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, vmax) >> 10) - 14;
+      const float above = static_cast<float>((BF16 ? max(top_exp, 0) : top_exp) - 15);
       bool grew = false;
       float ref[NT][2];
 #pragma unroll
@@ -532,29 +563,38 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 #pragma unroll
           for (int i = 0; i < NB / 2; ++i) d0[i] = w0 ? d0[i] : 0u, d1[i] = w1 ? d1[i] : 0u;
         }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float2 e0 = halves(d0[b / 2]), e1 = halves(d1[b / 2]);
-          const float f0 = b & 1 ? e0.y : e0.x, f1 = b & 1 ? e1.y : e1.x;
-          const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
-          const uint32_t wa = __byte_perm(va[b / 2], va[NB / 2 + b / 2], pick);
-          const uint32_t wb = __byte_perm(vb[b / 2], vb[NB / 2 + b / 2], pick);
-          uint32_t x[4], y[4];
-          if constexpr (BF16) pairs_f16(wa, x), pairs_f16(wb, y);
-          else pairs_bf16<true>(wa, x), pairs_bf16<true>(wb, y);
+        uint32_t w0[NT], w1[NT];
+        if constexpr (BF16) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float a0 = s[sub][nt][0] * f0, a1 = s[sub][nt][1] * f0, b0 = s[sub][nt][2] * f1, b1 = s[sub][nt][3] * f1;
+            w0[nt] = pack_f16(s[sub][nt][0], s[sub][nt][1]);
+            w1[nt] = pack_f16(s[sub][nt][2], s[sub][nt][3]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
+          uint32_t x[4], y[4];
+          pairs<true>(__byte_perm(va[b / 2], va[NB / 2 + b / 2], pick), magic, x);
+          pairs<true>(__byte_perm(vb[b / 2], vb[NB / 2 + b / 2], pick), magic, y);
+          const __half2 e0 = *reinterpret_cast<const __half2*>(&d0[b / 2]);
+          const __half2 e1 = *reinterpret_cast<const __half2*>(&d1[b / 2]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
             if constexpr (BF16) {
-              const uint32_t u = transposed(pack_f16(a0, a1)), v = transposed(pack_f16(b0, b1));
-              mma_f16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v);
-              mma_f16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v);
+              const uint32_t u = transposed(mul_f16x2(w0[nt], b & 1 ? __high2half2(e0) : __low2half2(e0)));
+              const uint32_t v = transposed(mul_f16x2(w1[nt], b & 1 ? __high2half2(e1) : __low2half2(e1)));
+              mma_f16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v, o[nt][2 * b]);
+              mma_f16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v, o[nt][2 * b + 1]);
             } else {
+              const float f0 = b & 1 ? __high2float(e0) : __low2float(e0);
+              const float f1 = b & 1 ? __high2float(e1) : __low2float(e1);
+              float a0 = s[sub][nt][0] * f0, a1 = s[sub][nt][1] * f0, b0 = s[sub][nt][2] * f1, b1 = s[sub][nt][3] * f1;
 #pragma unroll
               for (int p = 0; p < NS; ++p) {
-                const uint32_t u = transposed(take_bf16(a0, a1)), v = transposed(take_bf16(b0, b1));
-                mma_bf16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v);
-                mma_bf16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v);
+                const uint32_t u = transposed(take_f16(a0, a1)), v = transposed(take_f16(b0, b1));
+                mma_f16(o[nt][2 * b], x[0], x[1], y[0], y[1], u, v, o[nt][2 * b]);
+                mma_f16(o[nt][2 * b + 1], x[2], x[3], y[2], y[3], u, v, o[nt][2 * b + 1]);
               }
             }
           }
