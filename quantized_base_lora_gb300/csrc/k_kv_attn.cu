@@ -11,32 +11,35 @@
 // so the codes go into the MMA as they are: small integers, exact in f16.  Bits
 // 4 i and 16 + 4 i of a word are the two halves of a pair; one mask with an
 // exponent makes them 1024 + code (even i) or 1024 + 16 code (odd i).  bf16
-// calls leave keys like that: odd channels' q is divided by 16 and the constants'
-// share, a sum of q over the block, is the accumulator's start.  The scale of a
-// key block multiplies its accumulator (fp32); the scale of a value block
+// calls leave keys like that: odd channels' q is divided by 16, and the constants'
+// share sum_b dK_jb Q_b, Q_b a weighted sum of q over the block, is one more MMA
+// (scales against Q, Q in two f16 parts) that the scores start from.  The scale of
+// a key block multiplies its accumulator (fp32); the scale of a value block
 // multiplies p, once a block.  Nothing is dequantized in memory.  S^T = K Q^T has
 // tokens as rows, so its accumulator has to be transposed to become the second
 // operand of O^T = V^T P: one movmatrix for 8x8.
 //
-// Precision.  A row of q is scaled by a power of two into f16's range (below
-// 2^10; undone in fp32): exact for bf16 down to 2^-22 of the row's maximum, and as
-// two f16 parts 24 bits of an fp32 q.  The running reference of the softmax is
+// Precision.  A row of q is scaled by a power of two into f16's range (undone in
+// fp32): exact for bf16 down to 2^-13 of the row's maximum and within 2^-21 of it
+// below, and as two f16 parts 24 bits of an fp32 q.  The running reference of the softmax is
 // max_j(s_j) + E, E chosen from the tile's largest value scale so that p dV stays
-// below 2^15: bf16 calls round p and p dV to f16 (11 bits each), f32 calls keep
+// below 2^15, up to 2^6 of it for a reference that is only moved when it trails by
+// more: bf16 calls round p and p dV to f16 (11 bits each), f32 calls keep
 // p dV as two f16 parts.
 //
 // Split.  All tiles of the call, segment after segment, are dealt to the CTAs in
 // equal runs, whatever the lengths are (they are known on the device only).  The
 // four warps of a CTA take every fourth tile of its run, each with a running
-// maximum and sum of its own and a private ring of bulk copies, so there is no
+// maximum and sum of its own and a private ring of asynchronous copies, so there is no
 // CTA barrier inside a segment.  A segment that is cut by a run's end is joined
 // by whichever of its CTAs arrives last: partial results go through memory, in
 // the order of the CTAs, so the same call gives the same bits, and no CTA waits.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "kv_internal.h"
 #include "ptx.cuh"
-#include "tc.cuh"
 
 namespace ovl {
 namespace {
@@ -45,6 +48,8 @@ constexpr uint32_t kWarps = 4;
 constexpr uint32_t kThreads = kWarps * 32;
 constexpr uint32_t kTile = 32;               // tokens
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLag = 6.f;                  // log2 by which the running reference may trail the maximum
+__device__ constexpr float kZero[4] = {0.f, 0.f, 0.f, 0.f};
 
 template <int D>
 struct Stage {
@@ -135,6 +140,14 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t magic, uint32_t (&x)[
   }
 }
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float2 halves(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
@@ -153,6 +166,17 @@ __device__ __forceinline__ void lds(const void* p, uint32_t (&w)[N]) {
       const uint4 v = static_cast<const uint4*>(p)[i];
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
+  }
+}
+
+// w[i mod N] without indexing registers.
+template <int N>
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[N], uint32_t i) {
+  if constexpr (N == 1) return w[0];
+  if constexpr (N == 2) return i & 1 ? w[1] : w[0];
+  if constexpr (N == 4) {
+    const uint32_t a = i & 1 ? w[1] : w[0], b = i & 1 ? w[3] : w[2];
+    return i & 2 ? b : a;
   }
 }
 
@@ -206,8 +230,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   constexpr uint32_t kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* const ring = smem;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kWarps * St::kWarpBytes);
-  float* const s_m = reinterpret_cast<float*>(full + kWarps * St::kRing);     // [kWarps][kRows]
+  float* const s_m = reinterpret_cast<float*>(smem + kWarps * St::kWarpBytes);   // [kWarps][kRows]
   float* const s_l = s_m + kWarps * kRows;
   uint64_t* const before = reinterpret_cast<uint64_t*>(s_l + kWarps * kRows); // [n_seqs + 1] tiles before a sequence
   __shared__ uint64_t s_warp[kWarps];
@@ -217,8 +240,6 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   const uint32_t rows_group = a.group;        // query heads of a kv head
 
   // ---- tiles before every sequence
-  if (lane < St::kRing) mbar_init(full + warp * St::kRing + lane, 1);
-  mbar_fence_init();
   uint64_t base = 0;
   for (uint32_t i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
     const uint32_t i = i0 + tid;
@@ -252,9 +273,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   const uint64_t end = min(at + chunk, total);
 
   uint8_t* const my_ring = ring + warp * St::kWarpBytes;
-  uint64_t* const my_full = full + warp * St::kRing;
-  const uint64_t policy = l2_evict_first_policy();
-  uint32_t slot = 0, phase = 0;               // of the ring, across segments
+  uint32_t slot = 0;                          // of the ring, across segments
   const float scale2 = a.scale * kLog2e;
   uint32_t magic;
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
@@ -287,11 +306,13 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       return (x < sp.lead ? x : x - sp.lead + sp.start) * kTile;
     };
     // the page of a tile's first half and, where pages are 16 tokens, of its second
+    bool lost = false;                        // a page that is not there: its tokens take no part
     auto page_at = [&](uint32_t tok) -> int32_t {
       if (tok >= static_cast<uint32_t>(sp.length)) return -1;
       const int32_t p = pages[tok >> kv.page_shift];
       if (static_cast<uint32_t>(p) < kv.n_pages) return p;
       kv_latch(kv, OVL_E_ARG);
+      lost = true;
       return -1;
     };
     auto fetch_pages = [&](uint32_t k0, int32_t& p0, int32_t& p1) {
@@ -301,39 +322,80 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         p0 = page_at(tok);
         p1 = kv.page == 16 ? page_at(tok + 16) : p0;
       }
+      lost = __any_sync(0xffffffffu, lost);
     };
     int32_t ids0, ids1;                       // of tiles 32 * (k / 32) + lane
     fetch_pages(0, ids0, ids1);
-    // The tile's copies into ring slot sl, called by the whole warp: lanes 0 to 3
-    // take key codes, value codes, key scales and value scales, where pages are 16
-    // tokens for the first half and lanes 4 to 7 for the second.
-    const uint32_t what = lane & 3, part = kv.page == 16 ? 2 : 1;
-    const uint32_t tok_bytes = what < 2 ? D / 2 : NB * 2, copy_bytes = (what < 2 ? St::kCodes : St::kScales) / part;
-    const uint32_t copy_to = (what & 1) * (what < 2 ? St::kCodes : St::kScales) + (what < 2 ? 0 : 2 * St::kCodes) +
-                             (lane >> 2) * copy_bytes;
-    const uint64_t unit_bytes = what < 2 ? kv.unit_codes : 2 * kv.unit_scales;
-    const uint64_t page_bytes = unit_bytes * kv.layers * 2 * kv.heads;
-    const uint8_t* const copy_from = (what < 2 ? kv.codes : reinterpret_cast<const uint8_t*>(kv.scales)) +
-                                     kv_unit(kv, 0, a.layer, what & 1, kh) * unit_bytes;
+    // A tile's copies, in runs of 512 bytes by the whole warp: key codes, value
+    // codes (16 bytes a lane and run), then both scale arrays together.
+    const uint64_t page_codes = static_cast<uint64_t>(kv.unit_codes) * kv.layers * 2 * kv.heads;
+    const uint64_t page_scales = static_cast<uint64_t>(kv.unit_scales) * 2 * kv.layers * 2 * kv.heads;
+    const uint64_t unit = kv_unit(kv, 0, a.layer, 0, kh);
+    const uint8_t* const k_from = kv.codes + unit * kv.unit_codes + lane * 16;
+    const uint32_t to_values = kv.heads * kv.unit_codes;                     // < 2^32: both below 2^16
+    constexpr uint32_t kScaleLanes = St::kScales / 16 < 16 ? St::kScales / 16 : 16;   // lanes on one array
+    const bool v_lane = lane >= kScaleLanes;
+    const uint8_t* const s_from = reinterpret_cast<const uint8_t*>(kv.scales) +
+                                  (unit + (v_lane ? kv.heads : 0)) * (2 * kv.unit_scales) +
+                                  (lane - (v_lane ? kScaleLanes : 0)) * 16;
+    const uint32_t s_half = (lane - (v_lane ? kScaleLanes : 0)) * 16 >= St::kScales / 2 &&
+                            St::kScales <= 256;                              // this lane's scales are of tokens 16 ..
+    const uint32_t my_ring32 = smem_u32(my_ring) + lane * 16;
+    const uint32_t s_to = 2 * St::kCodes + (v_lane ? St::kScales - kScaleLanes * 16 : 0);
     auto issue = [&](uint32_t k, int32_t p0, int32_t p1, uint32_t sl) {
       const uint32_t in_page = token_of(k) & (kv.page - 1);
-      const int32_t p = lane < 4 ? p0 : p1;
-      const uint32_t n = part == 1 ? 2 * (p0 >= 0) : (p0 >= 0) + (p1 >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(my_full + sl, n * (St::kCodes + St::kScales));
-      if (lane < 4 * part && p >= 0)
-        bulk_g2s(my_ring + sl * St::kBytes + copy_to, copy_from + p * page_bytes + in_page * tok_bytes, copy_bytes,
-                 my_full + sl, policy);
+      const uint32_t dst = my_ring32 + sl * St::kBytes;
+      constexpr uint32_t kRuns = St::kCodes / 512;
+      if (kv.page != 16) {
+        if (p0 >= 0) {
+          const uint8_t* const from = k_from + p0 * page_codes + in_page * (D / 2);
+          const uint8_t* const from_v = from + to_values;
+#pragma unroll
+          for (uint32_t i = 0; i < kRuns; ++i) cp16(dst + i * 512, from + i * 512);
+#pragma unroll
+          for (uint32_t i = 0; i < kRuns; ++i) cp16(dst + St::kCodes + i * 512, from_v + i * 512);
+          const uint8_t* const from_s = s_from + p0 * page_scales + in_page * (NB * 2);
+          if (lane < 2 * kScaleLanes)
+#pragma unroll
+            for (uint32_t i = 0; i < (St::kScales + 255) / 256; ++i) cp16(dst + s_to + i * 256, from_s + i * 256);
+        }
+      } else {
+        // two pages of 16 tokens: the halves of every array have a page each
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+          const int32_t p = h ? p1 : p0;
+          if (p < 0) continue;
+          const uint8_t* const from = k_from + p * page_codes;
+          const uint8_t* const from_v = from + to_values;
+          if (kRuns > 1 || lane < 16)
+#pragma unroll
+            for (uint32_t i = 0; i < (kRuns + 1) / 2; ++i) {
+              cp16(dst + h * (St::kCodes / 2) + i * 512, from + i * 512);
+              cp16(dst + St::kCodes + h * (St::kCodes / 2) + i * 512, from_v + i * 512);
+            }
+          const uint8_t* const from_s = s_from + p * page_scales - (h ? St::kScales / 2 : 0);
+          if (lane < 2 * kScaleLanes) {
+            if constexpr (St::kScales <= 256) {
+              if (s_half == h) cp16(dst + s_to, from_s);
+            } else {
+              cp16(dst + s_to + h * 256, from_s + h * 256);
+            }
+          }
+        }
+      }
     };
     uint32_t sent = 0, sent_slot = slot;
 #pragma unroll 1
-    for (; sent < min(n_mine, St::kRing); ++sent) {
-      issue(sent, __shfl_sync(0xffffffffu, ids0, sent), __shfl_sync(0xffffffffu, ids1, sent), sent_slot);
+    for (; sent < St::kRing; ++sent) {
+      if (sent < n_mine)
+        issue(sent, __shfl_sync(0xffffffffu, ids0, sent), __shfl_sync(0xffffffffu, ids1, sent), sent_slot);
+      cp_async_commit();
       sent_slot = sent_slot + 1 == St::kRing ? 0 : sent_slot + 1;
     }
 
     // ---- the rows: q as the MMA's second operand, and where each column looks
     uint32_t qf[NT][NS][NB][4];
-    float qc[NT][NB][4];                      // accumulator start of a block, columns 2 t and 2 t + 1
+    uint32_t qs[NT][2];                       // bf16 calls: the constants' share, B operand against the key scales
     float to_log2[NT][2];                     // scale, log2(e) and the row's power of two
     int32_t last[NT][2], from[NT][2];         // a column sees tokens <= last and (>= from or < sinks)
 #pragma unroll
@@ -343,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       const uint32_t row = r0 + (on ? r : 0);
       const uint64_t qa = static_cast<uint64_t>(token0 + row / rows_group) * a.q_stride +
                           (kh * rows_group + row % rows_group) * D;
-      float x[NB][8], top = 0.f;
+      float x[NB][8], top = 0.f, sums[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if constexpr (BF16) {
@@ -367,9 +429,11 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(9 - ex)
-      const uint32_t ex = min(max(__float_as_uint(top) >> 23, 10u), 254u);
-      const float up = __uint_as_float((263u - ex) << 23), down = __uint_as_float((ex - 9u) << 23);
+      // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(kUp - ex).  bf16 calls
+      // keep the constants' share inside f16, f32 calls the second part's small end.
+      constexpr uint32_t kUp = BF16 ? 0 : 9;
+      const uint32_t ex = min(max(__float_as_uint(top) >> 23, kUp + 1), 253u);
+      const float up = __uint_as_float((254u + kUp - ex) << 23), down = __uint_as_float((ex - kUp) << 23);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float even = 0.f, odd = 0.f;
@@ -390,11 +454,22 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         if constexpr (BF16) {
           float c = -1032.f * even - 72.f * odd;
           c += __shfl_xor_sync(0xffffffffu, c, 1);
-          c += __shfl_xor_sync(0xffffffffu, c, 2);
-          qc[nt][b][0] = qc[nt][b][2] = __shfl_sync(0xffffffffu, c, 8 * t);
-          qc[nt][b][1] = qc[nt][b][3] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
-        } else {
-          qc[nt][b][0] = qc[nt][b][1] = qc[nt][b][2] = qc[nt][b][3] = 0.f;
+          sums[b] = c + __shfl_xor_sync(0xffffffffu, c, 2);
+        }
+      }
+      qs[nt][0] = qs[nt][1] = 0;
+      if constexpr (BF16) {
+        // summed index 2 i, 2 i + 1: blocks 2 i, 2 i + 1, first all rounded parts, then all rests
+        uint32_t hi[NB / 2], rest[NB / 2];
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+          hi[i] = take_f16(sums[2 * i], sums[2 * i + 1]);
+          rest[i] = pack_f16(sums[2 * i], sums[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+          if (t == i) qs[nt][0] = hi[i];
+          if (NB == 8 ? t == i : t == i + NB / 2) qs[nt][NB == 8] = rest[i];
         }
       }
       to_log2[nt][0] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t);
@@ -426,15 +501,16 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 #pragma unroll 1
     for (uint32_t k = 0; k < n_mine; ++k) {
       if (k && (k & 31) == 0) cur0 = ids0, cur1 = ids1;
-      const int32_t p0 = __shfl_sync(0xffffffffu, cur0, k & 31), p1 = __shfl_sync(0xffffffffu, cur1, k & 31);
       const int32_t tok = static_cast<int32_t>(token_of(k));
-      if (!mbar_wait_bounded(my_full + slot, phase)) {
-        if (lane == 0) kv_latch(kv, OVL_E_DEVICE_TIMEOUT);   // a copy did not land: reported, not waited for again
-      }
+      cp_async_wait<St::kRing - 1>();
+      __syncwarp();
       const uint8_t* const st = my_ring + slot * St::kBytes;
-      const bool masked = tok + static_cast<int32_t>(kTile) - 1 > all_last || p0 < 0 || p1 < 0 ||
+      const bool hidden = tok + static_cast<int32_t>(kTile) - 1 > all_last || lost ||
                           !(tok >= all_from || tok + static_cast<int32_t>(kTile) <= sinks);
 
+      // Two copies of the tile's code: tiles that need no mask take no part of it.
+      auto tile = [&](auto with_mask) {
+      constexpr bool masked = decltype(with_mask)::value;
       // scores: tokens 16 sub + g and + 8 against columns 2 t, 2 t + 1
       float s[2][NT][4];
 #pragma unroll
@@ -447,7 +523,14 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         lds<NB / 2>(dr, d0);
         lds<NB / 2>(dr + 8 * NB * 2, d1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[sub][nt][0] = s[sub][nt][1] = s[sub][nt][2] = s[sub][nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) {
+          s[sub][nt][0] = s[sub][nt][1] = s[sub][nt][2] = s[sub][nt][3] = 0.f;
+          if constexpr (BF16) {
+            // this lane's pair of scales for the sums' index 2 t (and, with 8 blocks, 2 t + 8)
+            const uint32_t u0 = word_of<NB / 2>(d0, t), u1 = word_of<NB / 2>(d1, t);
+            mma_f16(s[sub][nt], u0, u1, NB == 8 ? u0 : 0u, NB == 8 ? u1 : 0u, qs[nt][0], qs[nt][1], kZero);
+          }
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t x[4], y[4];
@@ -458,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float c[4];
-            mma_f16(c, x[0], y[0], x[1], y[1], qf[nt][0][b][0], qf[nt][0][b][1], qc[nt][b]);
+            mma_f16(c, x[0], y[0], x[1], y[1], qf[nt][0][b][0], qf[nt][0][b][1], kZero);
             mma_f16(c, x[2], y[2], x[3], y[3], qf[nt][0][b][2], qf[nt][0][b][3], c);
 #pragma unroll
             for (int p = 1; p < NS; ++p) {
@@ -473,9 +556,14 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         }
       }
       // the largest value scale of the tile, 2^(E - 1) <= it < 2^E, and what that
-      // leaves for p: p dV < 2^15, and where p itself is rounded to f16, p too
+      // leaves for p: p dV < 2^9 (2^15 where the reference trails), and where p itself is
+      // rounded to f16, p too
       const uint8_t* const vd = st + 2 * St::kCodes + St::kScales;
-      const bool held0 = p0 >= 0, held1 = p1 >= 0;
+      bool held0 = true, held1 = true;
+      if constexpr (masked) {
+        held0 = __shfl_sync(0xffffffffu, cur0, k & 31) >= 0;
+        held1 = __shfl_sync(0xffffffffu, cur1, k & 31) >= 0;
+      }
       auto written = [&](uint32_t j) {        // token j of the tile holds data
         return tok + static_cast<int32_t>(j) < sp.length && (j < 16 ? held0 : held1);
       };
@@ -494,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[sub][nt][i] *= to_log2[nt][i & 1];
-      if (masked) {
+      if constexpr (masked) {
         if (!written(lane)) vmax = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -508,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
             }
       }
       const int32_t top_exp = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, vmax) >> 10) - 14;
-      const float above = static_cast<float>((BF16 ? max(top_exp, 0) : top_exp) - 15);
+      const float above = static_cast<float>((BF16 ? max(top_exp, 0) : top_exp) - 9);
       bool grew = false;
       float ref[NT][2];
 #pragma unroll
@@ -520,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
           x = fmaxf(m[nt][e], x + above);
-          grew |= x > m[nt][e];
+          grew |= x > m[nt][e] + kLag;
           ref[nt][e] = x;
         }
       if (__any_sync(0xffffffffu, grew)) {
@@ -558,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         const uint8_t* const dr = vd + (16 * sub + g) * (NB * 2);
         lds<NB / 2>(dr, d0);
         lds<NB / 2>(dr + 8 * NB * 2, d1);
-        if (masked) {                         // what was never written may hold any bits
+        if constexpr (masked) {                         // what was never written may hold any bits
           const bool w0 = written(16 * sub + g), w1 = written(16 * sub + g + 8);
 #pragma unroll
           for (int i = 0; i < NB / 2; ++i) d0[i] = w0 ? d0[i] : 0u, d1[i] = w1 ? d1[i] : 0u;
@@ -601,14 +689,20 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         }
       }
 
+      };
+      if (hidden) tile(std::true_type{});
+      else tile(std::false_type{});
+
       // this slot is read: refill it
       __syncwarp();
       if (sent < n_mine) {
         if ((sent & 31) == 0) fetch_pages(sent, ids0, ids1);
-        issue(sent, __shfl_sync(0xffffffffu, ids0, sent & 31), __shfl_sync(0xffffffffu, ids1, sent & 31), slot);
+        const int32_t p0 = __shfl_sync(0xffffffffu, ids0, sent & 31);
+        issue(sent, p0, kv.page == 16 ? __shfl_sync(0xffffffffu, ids1, sent & 31) : p0, slot);
         ++sent;
       }
-      if (++slot == St::kRing) slot = 0, phase ^= 1;
+      cp_async_commit();
+      if (++slot == St::kRing) slot = 0;
     }
 
     // ---- the warps' results into shared memory (each over its own ring, which is drained)
@@ -703,16 +797,14 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       }
     }
     at += tile1 - tile0;
-    // the rings take copies again: order them after the plain accesses above
-    fence_proxy_async_smem();
-    __syncthreads();
+    __syncthreads();                          // the rings take copies again
   }
 }
 
 template <int D, bool BF16, int NT>
 cudaError_t decode(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   using St = Stage<D>;
-  const uint32_t bytes = kWarps * (St::kWarpBytes + 8 * St::kRing + 2 * 4 * 8 * NT) + 8 * (a.n_seqs + 1);
+  const uint32_t bytes = kWarps * (St::kWarpBytes + 2 * 4 * 8 * NT) + 8 * (a.n_seqs + 1);
   static const cudaError_t ready =
       cudaFuncSetAttribute(k_kv_decode<D, BF16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
   if (ready != cudaSuccess) return ready;
