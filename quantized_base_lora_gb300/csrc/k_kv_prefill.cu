@@ -1,0 +1,591 @@
+// Attention over the 4-bit cache for many query rows to a key (prompts, chunks
+// of prompts): bound by the tensor cores.
+//
+// One CTA takes 256 rows (128 where D = 256) of one sequence and kv head - the
+// query heads that share the kv head are rows too - and walks the visible tokens
+// in tiles of 128 (64).  Both products are tcgen05 MMAs with f16 operands and
+// fp32 accumulators in tensor memory:
+//   S = Q K^T   Q and K in shared memory, S in tensor memory
+//   O += P V    P over S's own columns in tensor memory, V^T in shared memory
+// so the scores never leave the SM.  Roles, each its own warps:
+//   softmax   4 warps for each 128 rows, a thread a row: S -> P, running maximum
+//             and sum in registers; O is rescaled in place, only when a row's
+//             maximum has grown by more than 2^6 since its reference was set
+//   keys, values   4 warps each: 4-bit words from global memory, one mask a pair
+//             of codes, times the block's scale, into the MMA's shared layout;
+//             two buffers each
+//   issue     one warp for each 128 rows.  The two row tiles run against each
+//             other: the MMAs of one overlap the softmax of the other.
+//
+// Layout.  A 32-bit key word is 8 consecutive channels of a token, which is one
+// 16-byte chunk of the f16 operand; its codes come out in the order 0 4 1 5 2 6 3
+// 7, so Q's chunks are stored in that order as well.  A value unit is every eighth
+// channel of a token, so 8 tokens' units give whole 16-byte chunks of V^T (8
+// tokens of a channel) to one thread.  In both, 8 neighbouring lanes write 8 rows'
+// chunks of one column of the 128-byte swizzle: no bank conflicts.
+//
+// Range.  Keys and values of a tile are multiplied by 2^-E, 2^E above the tile's
+// largest scale, before they are rounded to f16 (|x| <= 8); the factor goes back
+// into the scores, and into P for the values.  Rows of q are scaled by a power of
+// two.  So f16's 11 bits hold whatever the size of the data is.
+#include <math_constants.h>
+
+#include "kv_internal.h"
+#include "kv_mma.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace ovl {
+namespace {
+
+constexpr uint32_t kTmemCols = 512;
+
+template <int D>
+struct Shape {
+  static constexpr uint32_t kRowTiles = D == 256 ? 1 : 2;      // of 128 rows
+  static constexpr uint32_t kTokens = D == 256 ? 64 : 128;     // of a tile
+  static constexpr uint32_t kRows = 128 * kRowTiles;
+  static constexpr uint32_t kQ = 128 * D * 2;                  // bytes of one row tile
+  static constexpr uint32_t kBuf = kTokens * D * 2;            // bytes of a K or V buffer
+  static constexpr uint32_t kSmem = kRowTiles * kQ + 4 * kBuf;
+  static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
+  static constexpr uint32_t kWarps = kSoft + 8 + kRowTiles;
+  static constexpr uint32_t kThreads = kWarps * 32;
+  static constexpr uint32_t kOutCol = kRowTiles * kTokens;     // first tensor memory column of O
+  static_assert(kOutCol + kRowTiles * D <= kTmemCols, "S and O fit");
+};
+
+struct Bars {
+  uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+  float k_exp[4], v_exp[4];      // 2^E of the last tiles' scales as E
+  uint32_t taddr;
+};
+
+__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32_async(taddr, r); }
+
+// What one CTA's rows see.
+struct Tiles {
+  uint32_t lead, start, count;
+  __device__ __forceinline__ uint32_t token(uint32_t j, uint32_t size) const {
+    return (j < lead ? j : j - lead + start) * size;
+  }
+};
+
+// The page numbers of a tile's tokens 32 k + lane, -1 beyond the row's length.
+template <int N>
+__device__ __forceinline__ void tile_pages(const KvDev& kv, const int32_t* row, uint32_t length, uint32_t tok,
+                                           uint32_t lane, int32_t (&p)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t t = tok + 32 * k + lane;
+    p[k] = -1;
+    if (t < length) {
+      const int32_t x = __ldg(row + (t >> kv.page_shift));
+      if (static_cast<uint32_t>(x) < kv.n_pages) p[k] = x;
+      else kv_latch(kv, OVL_E_ARG);
+    }
+  }
+}
+
+// E of a tile from every lane's scale words: 2^E above the largest scale.
+template <int N>
+__device__ __forceinline__ int32_t exponent_above(const uint32_t (&w)[N]) {
+  uint32_t x = w[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) x = __vmaxu2(x, w[i]);
+  x = max(x & 0xffffu, x >> 16);
+  return static_cast<int32_t>(__reduce_max_sync(0xffffffffu, x) >> 10) - 14;
+}
+
+// 2^-e in both halves, in two factors, each inside f16's range (|e| <= 17).
+__device__ __forceinline__ uint32_t down_scaled(uint32_t w, int32_t e) {
+  const int32_t h = e / 2;
+  const uint32_t a = static_cast<uint32_t>(15 - h) << 10, b = static_cast<uint32_t>(15 - (e - h)) << 10;
+  const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(a))),
+                            __half2half2(__ushort_as_half(b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDev kv, const KvQuery a) {
+  using Sh = Shape<D>;
+  constexpr uint32_t NB = D / 32, KT = Sh::kTokens, RT = Sh::kRowTiles;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  __shared__ Bars bar;
+  uint8_t* const sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* const sm_q = sm;
+  uint8_t* const sm_k = sm + RT * Sh::kQ;
+  uint8_t* const sm_v = sm_k + 2 * Sh::kBuf;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- this CTA's rows; the ones that see most come first in the grid
+  const uint32_t seq = blockIdx.z, kh = blockIdx.y, row_tile = gridDim.x - 1 - blockIdx.x;
+  const int32_t o0 = a.off[seq], o1 = a.off[seq + 1];
+  if (o0 < 0 || o1 < o0 || static_cast<uint32_t>(o1) > a.n_tokens) return;      // latched by the few-row launch
+  const uint32_t tokens = o1 - o0, group = a.group, r0 = row_tile * Sh::kRows;
+  if (tokens * static_cast<uint64_t>(group) <= a.few) return;                   // served by the few-row launch
+  const uint32_t served = min(tokens, a.max_new);
+  if (row_tile == gridDim.x - 1 && tokens > served) {                           // latched as well: zeros
+    const uint32_t chunks = group * D / 8;
+    for (uint64_t i = tid; i < static_cast<uint64_t>(tokens - served) * chunks; i += Sh::kThreads)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (o0 + served + i / chunks) * a.out_stride +
+                                static_cast<uint64_t>(kh) * group * D + i % chunks * 8) = make_uint4(0, 0, 0, 0);
+  }
+  if (r0 >= served * group) return;
+  const uint32_t n_rows = min(Sh::kRows, served * group - r0);
+  const int32_t seq_row = a.seqs[seq];
+  const bool sound = static_cast<uint32_t>(seq_row) < kv.max_seqs;
+  int32_t length = sound ? kv.length[seq_row] : 0;
+  if (length < 0 || length > static_cast<int32_t>(kv.max_pages << kv.page_shift)) length = 0;
+  const int32_t first = length - static_cast<int32_t>(tokens);                  // position of its first new token
+  const int32_t* const table_row = kv.table + static_cast<size_t>(sound ? seq_row : 0) * kv.max_pages;
+  // the tiles that any of the rows sees
+  const uint32_t i_first = r0 / group, i_last = (r0 + n_rows - 1) / group;
+  Tiles tl{0, 0, 0};
+  const int32_t p_last = length ? first + static_cast<int32_t>(i_last) : -1;
+  if (p_last >= 0) {
+    if (a.window) {
+      tl.start = static_cast<uint32_t>(max(0, first + static_cast<int32_t>(i_first) - static_cast<int32_t>(a.window) + 1)) / KT;
+      tl.lead = (a.sinks + KT - 1) / KT;
+      if (tl.lead >= tl.start) tl.lead = tl.start = 0;
+    }
+    tl.count = tl.lead + static_cast<uint32_t>(p_last) / KT + 1 - tl.start;
+  }
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.taddr)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32) {
+    mbar_init(&bar.q_ready, Sh::kSoft);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], 4);
+      mbar_init(&bar.v_full[i], 4);
+      mbar_init(&bar.k_empty[i], RT);
+      mbar_init(&bar.v_empty[i], RT);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.o_done[i], 1);
+    }
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t taddr = bar.taddr;
+  bool dead = false;                           // a bounded wait ran out: leave
+  auto wait_one = [&](uint64_t* b, uint32_t parity) {
+    if (!mbar_wait_bounded(b, parity)) {
+      dead = true;
+      kv_latch(kv, OVL_E_DEVICE_TIMEOUT);
+    }
+  };
+  auto wait = [&](uint64_t* b, uint32_t parity) {    // a whole warp: all of it leaves together
+    wait_one(b, parity);
+    dead = __any_sync(0xffffffffu, dead);
+  };
+
+  if (warp < Sh::kSoft) {
+    // ================= softmax: one row a thread
+    const uint32_t x = warp >> 2, r = tid & 127;
+    const uint32_t row = r0 + x * 128 + r;
+    const bool on = x * 128 + r < n_rows;
+    const uint32_t i = row / group;
+    const uint64_t q_at = static_cast<uint64_t>(o0 + i) * a.q_stride + (kh * group + row % group) * D;
+    float down = 0.f;
+    {
+      const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (on ? q_at : 0));
+      float top = 0.f;
+      if (on) {
+#pragma unroll 4
+        for (uint32_t c = 0; c < D / 8; ++c) {
+          const uint4 v = __ldg(src + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+        }
+      }
+      // 2^ex <= top < 2^(ex + 1), biased; the row goes to [2^9, 2^10), with scale's sign
+      const uint32_t ex = min(max(__float_as_uint(top) >> 23, 10u), 253u);
+      const float up = copysignf(__uint_as_float((263u - ex) << 23), a.scale);
+      down = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((ex - 9u) << 23);
+      uint8_t* const dst = sm_q + x * Sh::kQ + r * 128;
+#pragma unroll 4
+      for (uint32_t c = 0; c < D / 8; ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on) v = __ldg(src + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          f[2 * k] = __uint_as_float(w[k] << 16) * up, f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * up;
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + ((c & 7) ^ (r & 7)) * 16) =
+            make_uint4(pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_ready);
+    }
+    const int32_t last = on && length ? first + static_cast<int32_t>(i) : -1;
+    const int32_t from = a.window ? last - static_cast<int32_t>(a.window) + 1 : 0;
+    const int32_t sinks = static_cast<int32_t>(a.sinks);
+    // of the rows of this tile: the one that sees least at either end
+    const uint32_t x0 = min(x * 128, n_rows - 1), x1 = min(x * 128 + 127, n_rows - 1);
+    const int32_t all_last = length ? first + static_cast<int32_t>((r0 + x0) / group) : -1;
+    const int32_t all_from =
+        a.window ? first + static_cast<int32_t>((r0 + x1) / group) - static_cast<int32_t>(a.window) + 1 : 0;
+    const uint32_t lanes = (warp & 3) * 32 << 16;
+    const uint32_t s_at = taddr + lanes + x * KT, o_at = taddr + lanes + Sh::kOutCol + x * D;
+    float ref = -CUDART_INF_F, l = 0.f;
+#pragma unroll 1
+    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+      const int32_t tok = static_cast<int32_t>(tl.token(j, KT));
+      const bool hidden = tok + static_cast<int32_t>(KT) - 1 > all_last ||
+                          !(tok >= all_from || tok + static_cast<int32_t>(KT) <= sinks);
+      wait(&bar.v_full[j & 1], (j >> 1) & 1);  // the tile's value exponent
+      wait(&bar.s_full[x], j & 1);
+      tc_fence_after();
+      const float ve = bar.v_exp[j & 3];
+      const float kf = down * exp2f(bar.k_exp[j & 3]);
+      auto sees = [&](uint32_t c) {
+        const int32_t t = tok + static_cast<int32_t>(c);
+        return t <= last && (t >= from || t < sinks);
+      };
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (uint32_t c = 0; c < KT; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(s_at + c, s);
+        if (hidden) {
+#pragma unroll
+          for (uint32_t k = 0; k < 32; ++k)
+            if (!sees(c + k)) s[k] = 0xff800000u;
+        }
+        float t4[4] = {top, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (uint32_t k = 0; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], __uint_as_float(s[k]));
+        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      }
+      // P = 2^(s + ve - ref) <= 2^8, 2^14 where the reference trails
+      const float want = top == -CUDART_INF_F ? -CUDART_INF_F : fmaf(top, kf, ve - 8.f);
+      const bool grew = want > ref + 6.f;
+      if (__any_sync(0xffffffffu, grew)) {
+        const float next = fmaxf(ref, want);
+        const float f = ref == -CUDART_INF_F ? 0.f : ex2(ref - next);
+        ref = next;
+        l *= f;
+        if (j) {
+#pragma unroll 1
+          for (uint32_t c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + c, o);
+#pragma unroll
+            for (uint32_t k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(o_at + c, o);
+          }
+        }
+      }
+      const float add = ref == -CUDART_INF_F ? 0.f : ve - ref;
+      float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (uint32_t c = 0; c < KT; c += 32) {
+        uint32_t s[32], p[16];
+        tmem_ld32(s_at + c, s);
+#pragma unroll
+        for (uint32_t k = 0; k < 32; ++k) {
+          float v = ex2(fmaf(__uint_as_float(s[k]), kf, add));
+          if (hidden && !sees(c + k)) v = 0.f;
+          s[k] = __float_as_uint(v);
+          sum4[k & 3] += v;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 16; ++k) p[k] = pack_f16(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+        tmem_st16_async(s_at + c / 2, p);
+      }
+      l = fmaf((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]), exp2f(-ve), l);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[x]);
+    }
+    if (tl.count) wait(&bar.o_done[x], 0);
+    tc_fence_after();
+    const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+    uint16_t* const to = static_cast<uint16_t*>(a.out) + static_cast<uint64_t>(o0 + i) * a.out_stride +
+                         (kh * group + row % group) * D;
+#pragma unroll 1
+    for (uint32_t c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      if (tl.count && !dead) {
+        tmem_ld32(o_at + c, o);
+      } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 32; ++k) o[k] = 0;
+      }
+      if (on) {
+#pragma unroll
+        for (uint32_t k = 0; k < 32; k += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const float u = l == 0.f ? 0.f : __uint_as_float(o[k + 2 * e]) * inv;
+            const float v = l == 0.f ? 0.f : __uint_as_float(o[k + 2 * e + 1]) * inv;
+            w[e] = pack_bf16(u, v);
+          }
+          *reinterpret_cast<uint4*>(to + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    tc_fence_before();
+  } else if (warp < Sh::kSoft + 4) {
+    // ================= keys
+    constexpr int IT = KT / 32;                // tokens 32 k + 8 * warp + lane % 8, word lane / 8 of each
+    const uint32_t w4 = warp - Sh::kSoft;
+    const uint32_t src_lane = w4 * 8 + (lane & 7), part = lane >> 3;
+    const uint64_t unit = kv_unit(kv, 0, a.layer, 0, kh), page_units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
+    const uint8_t* const codes = kv.codes + unit * kv.unit_codes;
+    const __half* const scales = kv.scales + unit * kv.unit_scales;
+    const uint64_t page_codes = page_units * kv.unit_codes, page_scales = page_units * kv.unit_scales;
+    uint32_t magic;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+    uint32_t words[IT][NB], sc[IT * (NB / 2)];
+    int32_t pages[IT];
+    auto load = [&](uint32_t j) {              // the tile's words and scales, by pages already known
+      const uint32_t tok = tl.token(j, KT);
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const uint32_t t = tok + 32 * k + lane;
+#pragma unroll
+        for (uint32_t i = 0; i < NB / 2; ++i) sc[k * (NB / 2) + i] = 0;
+        if (pages[k] >= 0)
+          ldg<NB / 2>(scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &sc[k * (NB / 2)]);
+        const int32_t p = __shfl_sync(0xffffffffu, pages[k], src_lane);
+        const uint32_t u = tok + 32 * k + src_lane;
+#pragma unroll
+        for (uint32_t i = 0; i < NB; ++i) words[k][i] = 0x88888888u;
+        if (p >= 0) ldg<NB>(codes + p * page_codes + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), words[k]);
+      }
+    };
+    if (tl.count) {
+      tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
+      load(0);
+      if (tl.count > 1) tile_pages<IT>(kv, table_row, length, tl.token(1, KT), lane, pages);
+    }
+#pragma unroll 1
+    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+      const int32_t e = exponent_above(sc);
+      if (j > 1) wait(&bar.k_empty[j & 1], ((j >> 1) - 1) & 1);
+      if (tid == Sh::kSoft * 32) bar.k_exp[j & 3] = static_cast<float>(e);
+      uint8_t* const buf = sm_k + (j & 1) * Sh::kBuf;
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const uint32_t row = 32 * k + src_lane;
+#pragma unroll
+        for (uint32_t b = 0; b < NB; ++b) {
+          const uint32_t d2 = __shfl_sync(0xffffffffu, sc[k * (NB / 2) + b / 2], src_lane);
+          const uint32_t dd = down_scaled(__byte_perm(d2, 0, b & 1 ? 0x3232 : 0x1010), e);
+          uint32_t v[4];
+          pairs<true>(words[k][b], magic, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = mul_f16x2(v[i], dd);
+          const uint32_t c = 4 * b + part;     // chunk of 8 channels
+          *reinterpret_cast<uint4*>(buf + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) ^ (row & 7)) * 16) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.k_full[j & 1]);
+      if (j + 1 < tl.count) {
+        load(j + 1);
+        if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
+      }
+    }
+  } else if (warp < Sh::kSoft + 8) {
+    // ================= values
+    constexpr int IT = KT / 32;
+    constexpr uint32_t WT = D == 64 ? 1 : 2;   // words of a token's unit that this thread takes
+    const uint32_t w4 = warp - Sh::kSoft - 4;
+    const uint32_t half = D == 256 ? w4 >> 1 : 0;                    // D = 256: which half of the unit
+    const uint32_t k_of = D == 256 ? w4 & 1 : w4;                    // its tokens are 32 k_of + 8 (lane / 8) ..
+    const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
+    const uint64_t unit = kv_unit(kv, 0, a.layer, 1, kh), page_units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
+    const uint8_t* const codes = kv.codes + unit * kv.unit_codes;
+    const __half* const scales = kv.scales + unit * kv.unit_scales;
+    const uint64_t page_codes = page_units * kv.unit_codes, page_scales = page_units * kv.unit_scales;
+    uint32_t magic;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+    uint32_t words[8][WT], own[8][WT], sc[IT * (NB / 2)];   // own: the scales of this thread's tokens and blocks
+    int32_t pages[IT];
+    auto load = [&](uint32_t j) {
+      const uint32_t tok = tl.token(j, KT);
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const uint32_t t = tok + 32 * k + lane;
+#pragma unroll
+        for (uint32_t i = 0; i < NB / 2; ++i) sc[k * (NB / 2) + i] = 0;
+        if (pages[k] >= 0)
+          ldg<NB / 2>(scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &sc[k * (NB / 2)]);
+      }
+      int32_t mine = pages[0];
+#pragma unroll
+      for (int k = 1; k < IT; ++k) mine = k_of == static_cast<uint32_t>(k) ? pages[k] : mine;
+      const int32_t p = __shfl_sync(0xffffffffu, mine, lane & 24);
+      const uint32_t slot = (tok + grp * 8) & (kv.page - 1);
+      const uint8_t* const from = codes + (p >= 0 ? p : 0) * page_codes + slot * (D / 2) + g * (D / 2) + half * 8;
+      const __half* const from_s = scales + (p >= 0 ? p : 0) * page_scales + slot * NB + half * 4;
+#pragma unroll
+      for (uint32_t t = 0; t < 8; ++t) {
+#pragma unroll
+        for (uint32_t i = 0; i < WT; ++i) words[t][i] = 0x88888888u, own[t][i] = 0u;
+      }
+      if (p >= 0) {
+        if constexpr (D == 256) {
+#pragma unroll
+          for (uint32_t t = 0; t < 8; ++t) ldg<2>(from + t * 16, words[t]), ldg<2>(from_s + t * NB, own[t]);
+        } else {
+          uint32_t w[8 * WT], s[8 * WT];
+          ldg<8 * WT>(from, w);
+          ldg<8 * WT>(from_s, s);
+#pragma unroll
+          for (uint32_t t = 0; t < 8; ++t)
+#pragma unroll
+            for (uint32_t i = 0; i < WT; ++i) words[t][i] = w[t * WT + i], own[t][i] = s[t * WT + i];
+        }
+        // tokens that were never written may hold any bits
+        const int32_t live = length - static_cast<int32_t>(tok + grp * 8);
+        if (live < 8) {
+#pragma unroll
+          for (int32_t t = 0; t < 8; ++t)
+            if (t >= live)
+#pragma unroll
+              for (uint32_t i = 0; i < WT; ++i) own[t][i] = 0u;
+        }
+      }
+    };
+    if (tl.count) {
+      tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
+      load(0);
+      if (tl.count > 1) tile_pages<IT>(kv, table_row, length, tl.token(1, KT), lane, pages);
+    }
+#pragma unroll 1
+    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+      const int32_t e = exponent_above(sc);
+      if (j > 1) wait(&bar.v_empty[j & 1], ((j >> 1) - 1) & 1);
+      if (tid == (Sh::kSoft + 4) * 32) bar.v_exp[j & 3] = static_cast<float>(e);
+      uint8_t* const buf = sm_v + (j & 1) * Sh::kBuf + (grp >> 3) * (D * 128) + ((grp & 7) ^ g) * 16;
+#pragma unroll
+      for (uint32_t b = 0; b < 2 * WT; ++b) {  // blocks of 32 channels: 4 of this thread's channels each
+        const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
+        uint32_t v[4][4];                      // [channel][token pair]
+#pragma unroll
+        for (uint32_t t = 0; t < 4; ++t) {
+          uint32_t x[4];
+          pairs<true>(__byte_perm(words[2 * t][b / 2], words[2 * t + 1][b / 2], pick), magic, x);
+          const uint32_t d = down_scaled(__byte_perm(own[2 * t][b / 2], own[2 * t + 1][b / 2], pick), e);
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) v[i][t] = mul_f16x2(x[i], d);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t c = half * 128 + 32 * b + 8 * i + g;
+          *reinterpret_cast<uint4*>(buf + c * 128) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.v_full[j & 1]);
+      if (j + 1 < tl.count) {
+        load(j + 1);
+        if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
+      }
+    }
+  } else if (lane == 0) {
+    // ================= issue: one thread for each row tile
+    const uint32_t x = warp - Sh::kSoft - 8;
+    constexpr uint32_t kF32 = 1u << 4;         // accumulators; both operands f16
+    constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((128u >> 4) << 24);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(sm_q + x * Sh::kQ));
+    const uint64_t k_desc = sdesc_sw128(smem_u32(sm_k)), v_desc = sdesc_sw128(smem_u32(sm_v));
+    const uint32_t s_at = taddr + x * KT, o_at = taddr + Sh::kOutCol + x * D;
+    if (tl.count) wait_one(&bar.q_ready, 0);
+#pragma unroll 1
+    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+      const uint32_t parity = (j >> 1) & 1, b = j & 1;
+      wait_one(&bar.k_full[b], parity);
+      if (dead) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t k = 0; k < D / 16; ++k)    // 64 channels a region of 128-byte rows
+        umma_f16(s_at, q_desc + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                 k_desc + b * (Sh::kBuf / 16) + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), kQK, k != 0);
+      umma_commit(&bar.k_empty[b]);
+      umma_commit(&bar.s_full[x]);
+      wait_one(&bar.v_full[b], parity);
+      wait_one(&bar.p_full[x], j & 1);
+      if (dead) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t k = 0; k < KT / 16; ++k)   // 64 tokens a region
+        umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
+                    (j | k) != 0);
+      umma_commit(&bar.v_empty[b]);
+    }
+    // nothing of this CTA may still run when its tensor memory goes
+    if (tl.count) {
+      umma_commit(&bar.o_done[x]);
+      wait_one(&bar.o_done[x], 0);
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+
+template <int D>
+cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
+  using Sh = Shape<D>;
+  constexpr uint32_t bytes = Sh::kSmem + 1024;
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(k_kv_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (ready != cudaSuccess) return ready;
+  const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + Sh::kRows - 1) / Sh::kRows;
+  if (tiles > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  k_kv_prefill<D><<<dim3(static_cast<uint32_t>(tiles), kv.heads, a.n_seqs), Sh::kThreads, bytes, st>>>(kv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
+  switch (kv.dim) {
+    case 64: return prefill<64>(kv, a, st);
+    case 128: return prefill<128>(kv, a, st);
+    default: return prefill<256>(kv, a, st);
+  }
+}
+
+}  // namespace ovl

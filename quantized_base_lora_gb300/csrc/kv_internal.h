@@ -98,6 +98,7 @@ struct KvQuery {
   float scale;
   uint32_t window, sinks;
   bool bf16;
+  uint32_t few;                    // rows of a sequence up to which the few-row kernel serves it
 };
 
 uint32_t kv_sm_count();
@@ -107,6 +108,7 @@ cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seq
 cudaError_t launch_kv_read(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                            uint32_t n_tokens, float* k, float* v, cudaStream_t st);
 cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& q, cudaStream_t st);
+cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& q, cudaStream_t st);
 enum class KvPages { kExtend, kFork, kCompact, kRelease };
 cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, const int32_t* dst, const int32_t* keep,
                             const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st);
