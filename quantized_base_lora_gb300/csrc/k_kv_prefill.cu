@@ -11,10 +11,10 @@
 //   softmax   4 warps for each 128 rows, a thread a row: S -> P, running maximum
 //             and sum in registers; O is rescaled in place, only when a row's
 //             maximum has grown by more than 2^6 since its reference was set
-//   keys, values   4 warps each: 4-bit words from global memory, one mask a pair
-//             of codes, times the block's scale, into the MMA's shared layout;
-//             two buffers each
-//   issue     one warp for each 128 rows.  The two row tiles run against each
+//   cache     4 warps, keys and values in turn: 4-bit words from global memory, one
+//             mask a pair of codes, times the block's scale, into the MMA's shared
+//             layout; two buffers each; the next words are in flight meanwhile
+//   issue     one thread for each 128 rows.  The two row tiles run against each
 //             other: the MMAs of one overlap the softmax of the other.
 //
 // Layout.  A 32-bit key word is 8 consecutive channels of a token, which is one
@@ -29,6 +29,8 @@
 // into the scores, and into P for the values.  Rows of q are scaled by a power of
 // two.  So f16's 11 bits hold whatever the size of the data is.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "kv_mma.cuh"
@@ -49,7 +51,7 @@ struct Shape {
   static constexpr uint32_t kBuf = kTokens * D * 2;            // bytes of a K or V buffer
   static constexpr uint32_t kSmem = kRowTiles * kQ + 4 * kBuf;
   static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
-  static constexpr uint32_t kWarps = kSoft + 8 + kRowTiles;
+  static constexpr uint32_t kWarps = kSoft + 8;                // softmax, 4 cache, 4 issue (1 or 2 of them busy)
   static constexpr uint32_t kThreads = kWarps * 32;
   static constexpr uint32_t kOutCol = kRowTiles * kTokens;     // first tensor memory column of O
   static_assert(kOutCol + kRowTiles * D <= kTmemCols, "S and O fit");
@@ -77,7 +79,58 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32_async(taddr, r); }
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Loads in flight have landed: the registers may be used from here on.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void landed(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
+// The lowest n bits, n clamped to 0..32.
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
 
 // What one CTA's rows see.
 struct Tiles {
@@ -111,15 +164,6 @@ __device__ __forceinline__ int32_t exponent_above(const uint32_t (&w)[N]) {
   for (int i = 1; i < N; ++i) x = __vmaxu2(x, w[i]);
   x = max(x & 0xffffu, x >> 16);
   return static_cast<int32_t>(__reduce_max_sync(0xffffffffu, x) >> 10) - 14;
-}
-
-// 2^-e in both halves, in two factors, each inside f16's range (|e| <= 17).
-__device__ __forceinline__ uint32_t down_scaled(uint32_t w, int32_t e) {
-  const int32_t h = e / 2;
-  const uint32_t a = static_cast<uint32_t>(15 - h) << 10, b = static_cast<uint32_t>(15 - (e - h)) << 10;
-  const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(a))),
-                            __half2half2(__ushort_as_half(b)));
-  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 template <int D>
@@ -205,6 +249,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
 
   if (warp < Sh::kSoft) {
     // ================= softmax: one row a thread
+    if constexpr (RT == 2) more_registers<168>();
     const uint32_t x = warp >> 2, r = tid & 127;
     const uint32_t row = r0 + x * 128 + r;
     const bool on = x * 128 + r < n_rows;
@@ -266,62 +311,78 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       tc_fence_after();
       const float ve = bar.v_exp[j & 3];
       const float kf = down * exp2f(bar.k_exp[j & 3]);
-      auto sees = [&](uint32_t c) {
-        const int32_t t = tok + static_cast<int32_t>(c);
-        return t <= last && (t >= from || t < sinks);
-      };
-      float top = -CUDART_INF_F;
+      // Two copies of the code: most tiles are seen whole.
+      auto tile = [&](auto with_mask) {
+        constexpr bool masked = decltype(with_mask)::value;
+        uint32_t seen[KT / 32];
+        if constexpr (masked) {
 #pragma unroll
-      for (uint32_t c = 0; c < KT; c += 32) {
-        uint32_t s[32];
-        tmem_ld32(s_at + c, s);
-        if (hidden) {
-#pragma unroll
-          for (uint32_t k = 0; k < 32; ++k)
-            if (!sees(c + k)) s[k] = 0xff800000u;
-        }
-        float t4[4] = {top, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-        for (uint32_t k = 0; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], __uint_as_float(s[k]));
-        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      }
-      // P = 2^(s + ve - ref) <= 2^8, 2^14 where the reference trails
-      const float want = top == -CUDART_INF_F ? -CUDART_INF_F : fmaf(top, kf, ve - 8.f);
-      const bool grew = want > ref + 6.f;
-      if (__any_sync(0xffffffffu, grew)) {
-        const float next = fmaxf(ref, want);
-        const float f = ref == -CUDART_INF_F ? 0.f : ex2(ref - next);
-        ref = next;
-        l *= f;
-        if (j) {
-#pragma unroll 1
-          for (uint32_t c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_at + c, o);
-#pragma unroll
-            for (uint32_t k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(o_at + c, o);
+          for (uint32_t c = 0; c < KT; c += 32) {
+            const int32_t t = tok + static_cast<int32_t>(c);
+            seen[c / 32] = low_bits(last + 1 - t) & (~low_bits(from - t) | low_bits(sinks - t));
           }
         }
-      }
-      const float add = ref == -CUDART_INF_F ? 0.f : ve - ref;
-      float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t s[KT];
 #pragma unroll
-      for (uint32_t c = 0; c < KT; c += 32) {
-        uint32_t s[32], p[16];
-        tmem_ld32(s_at + c, s);
+        for (uint32_t c = 0; c < KT; c += 32) tmem_ld32_async(s_at + c, s + c);
+        tmem_wait_ld();
+        float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (uint32_t k = 0; k < 32; ++k) {
-          float v = ex2(fmaf(__uint_as_float(s[k]), kf, add));
-          if (hidden && !sees(c + k)) v = 0.f;
-          s[k] = __float_as_uint(v);
-          sum4[k & 3] += v;
+        for (uint32_t c = 0; c < KT; c += 32) {
+          landed(s + c);
+#pragma unroll
+          for (uint32_t k = c; k < c + 32; ++k) {
+            if constexpr (masked) s[k] = seen[c / 32] & (1u << (k - c)) ? s[k] : 0xff800000u;
+            t4[k & 3] = fmaxf(t4[k & 3], __uint_as_float(s[k]));
+          }
         }
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        // P = 2^(s + ve - ref) <= 2^8, 2^14 where the reference trails
+        const float want = top == -CUDART_INF_F ? -CUDART_INF_F : fmaf(top, kf, ve - 8.f);
+        const bool grew = want > ref + 6.f;
+        if (__any_sync(0xffffffffu, grew)) {
+          const float next = fmaxf(ref, want);
+          const float f = ref == -CUDART_INF_F ? 0.f : ex2(ref - next);
+          ref = next;
+          l *= f;
+          if (j) {
+#pragma unroll 1
+            for (uint32_t c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c, o);
 #pragma unroll
-        for (uint32_t k = 0; k < 16; ++k) p[k] = pack_f16(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-        tmem_st16_async(s_at + c / 2, p);
-      }
-      l = fmaf((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]), exp2f(-ve), l);
+              for (uint32_t k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32_async(o_at + c, o);
+            }
+          }
+        }
+        const float add = ref == -CUDART_INF_F ? 0.f : ve - ref;
+        const uint64_t kf2 = pair(__float_as_uint(kf), __float_as_uint(kf));
+        const uint64_t add_2 = pair(__float_as_uint(add), __float_as_uint(add));
+        uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < KT; c += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (uint32_t k = 0; k < 32; k += 2) {
+            const float2 e = both(fma2(pair(s[c + k], s[c + k + 1]), kf2, add_2));
+            float u = ex2(e.x), v = ex2(e.y);
+            if constexpr (masked) {            // -inf times a scale of 0 is no number
+              u = seen[c / 32] & (1u << k) ? u : 0.f;
+              v = seen[c / 32] & (2u << k) ? v : 0.f;
+            }
+            const uint64_t w = pair(__float_as_uint(u), __float_as_uint(v));
+            if (k & 2) sum1 = add2(sum1, w);
+            else sum0 = add2(sum0, w);
+            p[k / 2] = pack_f16(u, v);
+          }
+          tmem_st16_async(s_at + c / 2, p);
+        }
+        const float2 total = both(add2(sum0, sum1));
+        l = fmaf(total.x + total.y, exp2f(-ve), l);
+      };
+      if (hidden) tile(std::true_type{});
+      else tile(std::false_type{});
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -357,111 +418,64 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
     }
     tc_fence_before();
   } else if (warp < Sh::kSoft + 4) {
-    // ================= keys
-    constexpr int IT = KT / 32;                // tokens 32 k + 8 * warp + lane % 8, word lane / 8 of each
+    // ================= cache
+    if constexpr (RT == 2) more_registers<136>();
+    constexpr int IT = KT / 32;
+    constexpr uint32_t NW = NB / 2;            // scale words of a token
+    constexpr uint32_t WT = D == 64 ? 1 : 2;   // words of a token's value unit that a thread takes
     const uint32_t w4 = warp - Sh::kSoft;
-    const uint32_t src_lane = w4 * 8 + (lane & 7), part = lane >> 3;
+    // keys: tokens 32 k + 8 w4 + lane % 8, words lane / 8 of every block
+    const uint32_t k_lane = w4 * 8 + (lane & 7), part = lane >> 3;
+    // values: the 8 tokens from 32 k_of + 8 (lane / 8), unit g; D = 256: half of it
+    const uint32_t half = D == 256 ? w4 >> 1 : 0, k_of = D == 256 ? w4 & 1 : w4;
+    const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
     const uint64_t unit = kv_unit(kv, 0, a.layer, 0, kh), page_units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
-    const uint8_t* const codes = kv.codes + unit * kv.unit_codes;
-    const __half* const scales = kv.scales + unit * kv.unit_scales;
     const uint64_t page_codes = page_units * kv.unit_codes, page_scales = page_units * kv.unit_scales;
+    const uint8_t* const k_codes = kv.codes + unit * kv.unit_codes + part * (D / 8);
+    const __half* const k_scales = kv.scales + unit * kv.unit_scales;
+    const uint8_t* const v_codes = kv.codes + (unit + kv.heads) * kv.unit_codes + g * (D / 2) + half * 8;
+    const __half* const v_scales = kv.scales + (unit + kv.heads) * kv.unit_scales;
     uint32_t magic;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    uint32_t words[IT][NB], sc[IT * (NB / 2)];
-    int32_t pages[IT];
-    auto load = [&](uint32_t j) {              // the tile's words and scales, by pages already known
-      const uint32_t tok = tl.token(j, KT);
+    uint32_t kw[IT][NB], ks[IT * NW];          // keys: words; scales of tokens 32 k + lane
+    uint32_t vw[8][WT], vo[8][WT], vs[IT * NW];   // values: words; scales of this thread's; of tokens 32 k + lane
+    int32_t pages[IT];                         // of tokens 32 k + lane of the next tile to load
+    auto load_keys = [&](uint32_t tok) {
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
-        const uint32_t t = tok + 32 * k + lane;
+        const uint32_t t = tok + 32 * k + lane, u = tok + 32 * k + k_lane;
 #pragma unroll
-        for (uint32_t i = 0; i < NB / 2; ++i) sc[k * (NB / 2) + i] = 0;
-        if (pages[k] >= 0)
-          ldg<NB / 2>(scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &sc[k * (NB / 2)]);
-        const int32_t p = __shfl_sync(0xffffffffu, pages[k], src_lane);
-        const uint32_t u = tok + 32 * k + src_lane;
+        for (uint32_t i = 0; i < NW; ++i) ks[k * NW + i] = 0;
+        if (pages[k] >= 0) ldg<NW>(k_scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &ks[k * NW]);
+        const int32_t p = __shfl_sync(0xffffffffu, pages[k], k_lane);
 #pragma unroll
-        for (uint32_t i = 0; i < NB; ++i) words[k][i] = 0x88888888u;
-        if (p >= 0) ldg<NB>(codes + p * page_codes + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), words[k]);
+        for (uint32_t i = 0; i < NB; ++i) kw[k][i] = 0x88888888u;
+        if (p >= 0) ldg<NB>(k_codes + p * page_codes + (u & (kv.page - 1)) * (D / 2), kw[k]);
       }
     };
-    if (tl.count) {
-      tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
-      load(0);
-      if (tl.count > 1) tile_pages<IT>(kv, table_row, length, tl.token(1, KT), lane, pages);
-    }
-#pragma unroll 1
-    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-      const int32_t e = exponent_above(sc);
-      if (j > 1) wait(&bar.k_empty[j & 1], ((j >> 1) - 1) & 1);
-      if (tid == Sh::kSoft * 32) bar.k_exp[j & 3] = static_cast<float>(e);
-      uint8_t* const buf = sm_k + (j & 1) * Sh::kBuf;
-#pragma unroll
-      for (int k = 0; k < IT; ++k) {
-        const uint32_t row = 32 * k + src_lane;
-#pragma unroll
-        for (uint32_t b = 0; b < NB; ++b) {
-          const uint32_t d2 = __shfl_sync(0xffffffffu, sc[k * (NB / 2) + b / 2], src_lane);
-          const uint32_t dd = down_scaled(__byte_perm(d2, 0, b & 1 ? 0x3232 : 0x1010), e);
-          uint32_t v[4];
-          pairs<true>(words[k][b], magic, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = mul_f16x2(v[i], dd);
-          const uint32_t c = 4 * b + part;     // chunk of 8 channels
-          *reinterpret_cast<uint4*>(buf + (c >> 3) * (KT * 128) + row * 128 + ((c & 7) ^ (row & 7)) * 16) =
-              make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.k_full[j & 1]);
-      if (j + 1 < tl.count) {
-        load(j + 1);
-        if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
-      }
-    }
-  } else if (warp < Sh::kSoft + 8) {
-    // ================= values
-    constexpr int IT = KT / 32;
-    constexpr uint32_t WT = D == 64 ? 1 : 2;   // words of a token's unit that this thread takes
-    const uint32_t w4 = warp - Sh::kSoft - 4;
-    const uint32_t half = D == 256 ? w4 >> 1 : 0;                    // D = 256: which half of the unit
-    const uint32_t k_of = D == 256 ? w4 & 1 : w4;                    // its tokens are 32 k_of + 8 (lane / 8) ..
-    const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
-    const uint64_t unit = kv_unit(kv, 0, a.layer, 1, kh), page_units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
-    const uint8_t* const codes = kv.codes + unit * kv.unit_codes;
-    const __half* const scales = kv.scales + unit * kv.unit_scales;
-    const uint64_t page_codes = page_units * kv.unit_codes, page_scales = page_units * kv.unit_scales;
-    uint32_t magic;
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    uint32_t words[8][WT], own[8][WT], sc[IT * (NB / 2)];   // own: the scales of this thread's tokens and blocks
-    int32_t pages[IT];
-    auto load = [&](uint32_t j) {
-      const uint32_t tok = tl.token(j, KT);
+    auto load_values = [&](uint32_t tok) {
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
         const uint32_t t = tok + 32 * k + lane;
 #pragma unroll
-        for (uint32_t i = 0; i < NB / 2; ++i) sc[k * (NB / 2) + i] = 0;
-        if (pages[k] >= 0)
-          ldg<NB / 2>(scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &sc[k * (NB / 2)]);
+        for (uint32_t i = 0; i < NW; ++i) vs[k * NW + i] = 0;
+        if (pages[k] >= 0) ldg<NW>(v_scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &vs[k * NW]);
       }
       int32_t mine = pages[0];
 #pragma unroll
       for (int k = 1; k < IT; ++k) mine = k_of == static_cast<uint32_t>(k) ? pages[k] : mine;
       const int32_t p = __shfl_sync(0xffffffffu, mine, lane & 24);
       const uint32_t slot = (tok + grp * 8) & (kv.page - 1);
-      const uint8_t* const from = codes + (p >= 0 ? p : 0) * page_codes + slot * (D / 2) + g * (D / 2) + half * 8;
-      const __half* const from_s = scales + (p >= 0 ? p : 0) * page_scales + slot * NB + half * 4;
 #pragma unroll
-      for (uint32_t t = 0; t < 8; ++t) {
+      for (uint32_t t = 0; t < 8; ++t)
 #pragma unroll
-        for (uint32_t i = 0; i < WT; ++i) words[t][i] = 0x88888888u, own[t][i] = 0u;
-      }
+        for (uint32_t i = 0; i < WT; ++i) vw[t][i] = 0x88888888u, vo[t][i] = 0u;
       if (p >= 0) {
+        const uint8_t* const from = v_codes + p * page_codes + slot * (D / 2);
+        const __half* const from_s = v_scales + p * page_scales + slot * NB + half * 4;
         if constexpr (D == 256) {
 #pragma unroll
-          for (uint32_t t = 0; t < 8; ++t) ldg<2>(from + t * 16, words[t]), ldg<2>(from_s + t * NB, own[t]);
+          for (uint32_t t = 0; t < 8; ++t) ldg<2>(from + t * 16, vw[t]), ldg<2>(from_s + t * NB, vo[t]);
         } else {
           uint32_t w[8 * WT], s[8 * WT];
           ldg<8 * WT>(from, w);
@@ -469,59 +483,91 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
 #pragma unroll
           for (uint32_t t = 0; t < 8; ++t)
 #pragma unroll
-            for (uint32_t i = 0; i < WT; ++i) words[t][i] = w[t * WT + i], own[t][i] = s[t * WT + i];
-        }
-        // tokens that were never written may hold any bits
-        const int32_t live = length - static_cast<int32_t>(tok + grp * 8);
-        if (live < 8) {
-#pragma unroll
-          for (int32_t t = 0; t < 8; ++t)
-            if (t >= live)
-#pragma unroll
-              for (uint32_t i = 0; i < WT; ++i) own[t][i] = 0u;
+            for (uint32_t i = 0; i < WT; ++i) vw[t][i] = w[t * WT + i], vo[t][i] = s[t * WT + i];
         }
       }
     };
+    // 2^-e as f16, |e| <= 16: exact, at the far end as a subnormal
+    auto down_by = [](int32_t e) { return __half2half2(__float2half_rn(__int_as_float((127 - e) << 23))); };
     if (tl.count) {
       tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
-      load(0);
-      if (tl.count > 1) tile_pages<IT>(kv, table_row, length, tl.token(1, KT), lane, pages);
+      load_keys(tl.token(0, KT));
     }
 #pragma unroll 1
     for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-      const int32_t e = exponent_above(sc);
-      if (j > 1) wait(&bar.v_empty[j & 1], ((j >> 1) - 1) & 1);
-      if (tid == (Sh::kSoft + 4) * 32) bar.v_exp[j & 3] = static_cast<float>(e);
-      uint8_t* const buf = sm_v + (j & 1) * Sh::kBuf + (grp >> 3) * (D * 128) + ((grp & 7) ^ g) * 16;
+      const uint32_t tok = tl.token(j, KT), b = j & 1;
+      load_values(tok);
+      if (j + 1 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 1, KT), lane, pages);
+      {
+        const int32_t e = exponent_above(ks);
+        const __half2 down = down_by(e);
 #pragma unroll
-      for (uint32_t b = 0; b < 2 * WT; ++b) {  // blocks of 32 channels: 4 of this thread's channels each
-        const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
-        uint32_t v[4][4];                      // [channel][token pair]
+        for (uint32_t i = 0; i < IT * NW; ++i) ks[i] = mul_f16x2(ks[i], down);
+        if (j > 1) wait(&bar.k_empty[b], ((j >> 1) - 1) & 1);
+        if (tid == Sh::kSoft * 32) bar.k_exp[j & 3] = static_cast<float>(e);
+        uint8_t* const buf = sm_k + b * Sh::kBuf + k_lane * 128;
 #pragma unroll
-        for (uint32_t t = 0; t < 4; ++t) {
-          uint32_t x[4];
-          pairs<true>(__byte_perm(words[2 * t][b / 2], words[2 * t + 1][b / 2], pick), magic, x);
-          const uint32_t d = down_scaled(__byte_perm(own[2 * t][b / 2], own[2 * t + 1][b / 2], pick), e);
+        for (int k = 0; k < IT; ++k) {
+          uint32_t d[NW];
 #pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) v[i][t] = mul_f16x2(x[i], d);
+          for (uint32_t i = 0; i < NW; ++i) d[i] = __shfl_sync(0xffffffffu, ks[k * NW + i], k_lane);
+#pragma unroll
+          for (uint32_t i = 0; i < NB; ++i) {
+            const __half2 d2 = *reinterpret_cast<const __half2*>(&d[i / 2]);
+            const __half2 dd = i & 1 ? __high2half2(d2) : __low2half2(d2);
+            uint32_t v[4];
+            pairs<true>(kw[k][i], magic, v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = mul_f16x2(v[x], dd);
+            const uint32_t c = 4 * i + part;   // chunk of 8 channels
+            *reinterpret_cast<uint4*>(buf + (i >> 1) * (KT * 128) + 32 * k * 128 + ((c & 7) ^ (lane & 7)) * 16) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t c = half * 128 + 32 * b + 8 * i + g;
-          *reinterpret_cast<uint4*>(buf + c * 128) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.k_full[b]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.v_full[j & 1]);
-      if (j + 1 < tl.count) {
-        load(j + 1);
-        if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
+      if (j + 1 < tl.count) load_keys(tl.token(j + 1, KT));
+      {
+        const int32_t e = exponent_above(vs);
+        const __half2 down = down_by(e);
+        // tokens that were never written may hold any bits
+        const int32_t live = length - static_cast<int32_t>(tok + grp * 8);
+#pragma unroll
+        for (int32_t t = 0; t < 8; ++t)
+#pragma unroll
+          for (uint32_t i = 0; i < WT; ++i) vo[t][i] = t < live ? mul_f16x2(vo[t][i], down) : 0u;
+        if (j > 1) wait(&bar.v_empty[b], ((j >> 1) - 1) & 1);
+        if (tid == Sh::kSoft * 32) bar.v_exp[j & 3] = static_cast<float>(e);
+        uint8_t* const buf =
+            sm_v + b * Sh::kBuf + (grp >> 3) * (D * 128) + (half * 128 + g) * 128 + ((grp & 7) ^ g) * 16;
+#pragma unroll
+        for (uint32_t i = 0; i < 2 * WT; ++i) {   // blocks of 32 channels: 4 of this thread's channels each
+          const uint32_t pick = i & 1 ? 0x7632u : 0x5410u;
+          uint32_t v[4][4];                    // [channel][token pair]
+#pragma unroll
+          for (uint32_t t = 0; t < 4; ++t) {
+            uint32_t x[4];
+            pairs<true>(__byte_perm(vw[2 * t][i / 2], vw[2 * t + 1][i / 2], pick), magic, x);
+            const uint32_t d = __byte_perm(vo[2 * t][i / 2], vo[2 * t + 1][i / 2], pick);
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) v[c][t] = mul_f16x2(x[c], d);
+          }
+#pragma unroll
+          for (uint32_t c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(buf + (32 * i + 8 * c) * 128) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_full[b]);
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ================= issue: one thread for each row tile
-    const uint32_t x = warp - Sh::kSoft - 8;
+    if constexpr (RT == 2) fewer_registers<40>();
+    if (lane == 0 && warp - Sh::kSoft - 4 < RT) {
+    const uint32_t x = warp - Sh::kSoft - 4;
     constexpr uint32_t kF32 = 1u << 4;         // accumulators; both operands f16
     constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((128u >> 4) << 24);
@@ -557,6 +603,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       wait_one(&bar.o_done[x], 0);
     }
     tc_fence_before();
+    }
   }
   __syncwarp();
   __syncthreads();
