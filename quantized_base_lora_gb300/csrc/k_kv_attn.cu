@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t rows_group = a.group;        // query heads of a kv head
 
+  griddep_launch_dependents();
+  griddep_wait();
   // ---- tiles before every sequence
   uint64_t base = 0;
   for (uint32_t i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
@@ -727,8 +729,7 @@ cudaError_t decode(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   const uint32_t per_sm = by_smem < by_regs ? by_smem : by_regs;
   uint32_t grid = kv_sm_count() * (per_sm ? per_sm : 1);
   if (grid > kKvMaxCtas) grid = kKvMaxCtas;
-  k_kv_decode<D, BF16, NT><<<grid, kThreads, bytes, st>>>(kv, a);
-  return cudaGetLastError();
+  return launch_chained(k_kv_decode<D, BF16, NT>, dim3(grid), kThreads, bytes, st, kv, a);
 }
 
 template <int D>

@@ -28,6 +28,7 @@ struct BookShared {
   int32_t length[kBook];      // its new length
   int32_t limit[kBook];       // compaction: the source's length
   uint32_t first[kBook + 1];  // prefix sums of the fresh pages
+  int32_t off[kBook + 1];     // compaction: keep_off
   uint32_t is_dst[kKvMaxSeqs / 32];
   uint32_t warp_sum[32];
   uint32_t found;
@@ -81,12 +82,16 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const bool two = what == KvPages::kFork || what == KvPages::kCompact;
   const uint32_t page = kv.page, shift = kv.page_shift;
+  griddep_launch_dependents();
   for (uint32_t i = t; i < (kv.max_seqs + 31) / 32; i += kBook) s.is_dst[i] = 0;
+  griddep_wait();
   if (t == 0) s.error = 0, s.found = 0;
   __syncthreads();
 
   // ---- the entries, checked
   int32_t from = 0, to = 0;
+  if (what == KvPages::kCompact)
+    for (uint32_t i = t; i <= n; i += kBook) s.off[i] = off[i];
   if (t < n) {
     from = src[t];
     to = two ? dst[t] : from;
@@ -149,11 +154,12 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
   __syncthreads();
   if (what == KvPages::kCompact && sound) {
     // the entries follow one another from position 0, so owner_of finds each one
-    const int32_t total = off[n];
+    const int32_t total = s.off[n];
+#pragma unroll 4
     for (int32_t j = static_cast<int32_t>(t); j < total; j += kBook) {
       const int32_t p = __ldg(keep + j);
-      const uint32_t e = owner_of(off, n, j);
-      if (p < 0 || p >= s.limit[e]) atomicCAS(&s.error, 0, OVL_E_ARG);
+      const uint32_t e = owner_of(s.off, n, j);
+      if (p < 0 || p >= s.limit[e]) s.error = OVL_E_ARG;
     }
     __syncthreads();
   }
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
 
 // Fork: whole pages, every layer.  A page is two contiguous runs.
 __global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
+  griddep_launch_dependents();
   griddep_wait();
   const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
   const uint64_t nc = units * kv.unit_codes / 16, ns = units * kv.unit_scales / 8;
@@ -289,16 +296,37 @@ __global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
   }
 }
 
+// Runs f(src, dst) for every head of a page with kHeads loads in flight: heads
+// are a constant distance apart on both sides.
+template <class T>
+__device__ __forceinline__ void copy_heads(uint8_t* pool, uint64_t from, uint64_t to, uint32_t heads, uint32_t step) {
+  constexpr uint32_t kHeads = 4;
+  for (uint32_t h = 0; h < heads; h += kHeads) {
+    T v[kHeads];
+#pragma unroll
+    for (uint32_t k = 0; k < kHeads; ++k)
+      if (h + k < heads) v[k] = *reinterpret_cast<const T*>(pool + from + static_cast<uint64_t>(h + k) * step);
+#pragma unroll
+    for (uint32_t k = 0; k < kHeads; ++k)
+      if (h + k < heads) *reinterpret_cast<T*>(pool + to + static_cast<uint64_t>(h + k) * step) = v[k];
+  }
+}
+
 // Compaction: one fresh page, layer and K|V at a time; the tokens' sources are
-// found once and used for every head.
+// found once and used for every head.  Bound by memory; a value unit is 4 to 16
+// bytes, so scattered tokens read whole sectors of values for a part of them.
 template <int D>
-__global__ void __launch_bounds__(kCopy) k_kv_gather(const KvDev kv, const int32_t* __restrict__ src,
+__global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* __restrict__ src,
                                                      const int32_t* __restrict__ dst,
                                                      const int32_t* __restrict__ keep,
                                                      const int32_t* __restrict__ off) {
-  __shared__ int32_t from_page[256], from_slot[256];
+  constexpr uint32_t kNone = 0xffffffffu;
+  __shared__ uint64_t from_codes[256], from_scales[256];   // of head 0; kNone in the upper half: no source
+  griddep_launch_dependents();
   griddep_wait();
   const uint64_t items = static_cast<uint64_t>(*kv.n_fresh) * kv.layers * 2;
+  const uint32_t code_step = kv.unit_codes, scale_step = kv.unit_scales * 2;
+  uint8_t* const scales = reinterpret_cast<uint8_t*>(kv.scales);
   for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const uint32_t which = it & 1;
     const uint32_t layer = (it >> 1) % kv.layers;
@@ -312,75 +340,52 @@ __global__ void __launch_bounds__(kCopy) k_kv_gather(const KvDev kv, const int32
     for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
       const int32_t pos = keep[first + i];
       const int32_t p = row[pos >> kv.page_shift];
-      from_page[i] = static_cast<uint32_t>(p) < kv.n_pages ? p : -1;
-      from_slot[i] = pos & static_cast<int32_t>(kv.page - 1);
+      const uint32_t slot = pos & (kv.page - 1);
+      const uint64_t unit = kv_unit(kv, p, layer, which, 0);
+      const bool there = static_cast<uint32_t>(p) < kv.n_pages;
+      from_codes[i] = there ? unit * code_step + (which ? (slot >> 3) * (4 * D) + (slot & 7) * (D / 16) : slot * (D / 2))
+                            : static_cast<uint64_t>(kNone) << 32;
+      from_scales[i] = unit * scale_step + slot * (D / 16);
     }
     __syncthreads();
-    for (uint32_t h = 0; h < kv.heads; ++h) {
-      const uint64_t ud = kv_unit(kv, f.dst_page, layer, which, h);
-      uint8_t* out = kv.codes + ud * kv.unit_codes;
-      if (which == 0) {
-        constexpr uint32_t kRow = D / 32;            // 16-byte pieces of a row
-        for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
-          const uint32_t tok = i / kRow, c = i % kRow;
-          if (from_page[tok] < 0) continue;
-          const uint64_t us = kv_unit(kv, from_page[tok], layer, which, h);
-          const uint8_t* in = kv.codes + us * kv.unit_codes + from_slot[tok] * (D / 2);
-          *reinterpret_cast<uint4*>(out + tok * (D / 2) + c * 16) = *reinterpret_cast<const uint4*>(in + c * 16);
-        }
-      } else {
-        using Unit = typename std::conditional<D == 64, uint32_t,
-                                               typename std::conditional<D == 128, uint2, uint4>::type>::type;
-        for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
-          const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
-          if (tok >= count || from_page[tok] < 0) continue;
-          const uint64_t us = kv_unit(kv, from_page[tok], layer, which, h);
-          const uint32_t slot = from_slot[tok];
-          const uint8_t* in = kv.codes + us * kv.unit_codes + (slot >> 3) * (4 * D) + g * (D / 2) + (slot & 7) * (D / 16);
-          *reinterpret_cast<Unit*>(out + (tok >> 3) * (4 * D) + g * (D / 2) + (tok & 7) * (D / 16)) =
-              *reinterpret_cast<const Unit*>(in);
-        }
+    const uint64_t unit = kv_unit(kv, f.dst_page, layer, which, 0);
+    using Small = typename std::conditional<D == 64, uint32_t, typename std::conditional<D == 128, uint2, uint4>::type>::type;
+    if (which == 0) {
+      constexpr uint32_t kRow = D / 32;              // 16-byte pieces of a row
+      for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
+        const uint64_t from = from_codes[i / kRow];
+        if (from >> 32 == kNone) continue;
+        copy_heads<uint4>(kv.codes, from + i % kRow * 16, unit * code_step + i * 16, kv.heads, code_step);
       }
-      using Scales = typename std::conditional<D == 64, uint32_t,
-                                               typename std::conditional<D == 128, uint2, uint4>::type>::type;
-      for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
-        if (from_page[i] < 0) continue;
-        const uint64_t us = kv_unit(kv, from_page[i], layer, which, h);
-        *reinterpret_cast<Scales*>(kv.scales + ud * kv.unit_scales + i * (D / 32)) =
-            *reinterpret_cast<const Scales*>(kv.scales + us * kv.unit_scales + from_slot[i] * (D / 32));
+    } else {
+      for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
+        const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
+        if (tok >= count) continue;
+        const uint64_t from = from_codes[tok];
+        if (from >> 32 == kNone) continue;
+        copy_heads<Small>(kv.codes, from + g * (D / 2), unit * code_step + i * (D / 16), kv.heads, code_step);
       }
     }
+    for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
+      if (from_codes[i] >> 32 == kNone) continue;
+      copy_heads<Small>(scales, from_scales[i], unit * scale_step + i * (D / 16), kv.heads, scale_step);
+    }
   }
-}
-
-template <class... P, class... A>
-cudaError_t launch_behind(void (*f)(P...), uint32_t grid, uint32_t block, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, args...);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, const int32_t* dst, const int32_t* keep,
                             const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st) {
-  k_kv_pages<<<1, kBook, 0, st>>>(kv, what, src, dst, keep, off, n, n_keep);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_chained(k_kv_pages, dim3(1), kBook, 0, st, kv, what, src, dst, keep, off, n, n_keep);
   if (e != cudaSuccess) return e;
   const uint32_t grid = kv_sm_count() * 4;
-  if (what == KvPages::kFork) return launch_behind(k_kv_copy_pages, grid, kCopy, st, kv);
+  if (what == KvPages::kFork) return launch_chained(k_kv_copy_pages, dim3(grid), kCopy, 0, st, kv);
   if (what == KvPages::kCompact) {
     switch (kv.dim) {
-      case 64: return launch_behind(k_kv_gather<64>, grid, kCopy, st, kv, src, dst, keep, off);
-      case 128: return launch_behind(k_kv_gather<128>, grid, kCopy, st, kv, src, dst, keep, off);
-      default: return launch_behind(k_kv_gather<256>, grid, kCopy, st, kv, src, dst, keep, off);
+      case 64: return launch_chained(k_kv_gather<64>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
+      case 128: return launch_chained(k_kv_gather<128>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
+      default: return launch_chained(k_kv_gather<256>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
     }
   }
   return cudaSuccess;

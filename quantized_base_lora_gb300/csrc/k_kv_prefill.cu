@@ -178,14 +178,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   uint8_t* const sm_v = sm_k + 2 * Sh::kBuf;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  griddep_launch_dependents();
+  griddep_wait();
   // ---- this CTA's rows; the ones that see most come first in the grid
-  const uint32_t seq = blockIdx.z, kh = blockIdx.y, row_tile = gridDim.x - 1 - blockIdx.x;
+  const uint32_t seq = blockIdx.y, kh = blockIdx.x, row_tile = gridDim.z - 1 - blockIdx.z;
   const int32_t o0 = a.off[seq], o1 = a.off[seq + 1];
   if (o0 < 0 || o1 < o0 || static_cast<uint32_t>(o1) > a.n_tokens) return;      // latched by the few-row launch
   const uint32_t tokens = o1 - o0, group = a.group, r0 = row_tile * Sh::kRows;
   if (tokens * static_cast<uint64_t>(group) <= a.few) return;                   // served by the few-row launch
   const uint32_t served = min(tokens, a.max_new);
-  if (row_tile == gridDim.x - 1 && tokens > served) {                           // latched as well: zeros
+  if (row_tile == gridDim.z - 1 && tokens > served) {                           // latched as well: zeros
     const uint32_t chunks = group * D / 8;
     for (uint64_t i = tid; i < static_cast<uint64_t>(tokens - served) * chunks; i += Sh::kThreads)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (o0 + served + i / chunks) * a.out_stride +
@@ -620,9 +622,9 @@ cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
       cudaFuncSetAttribute(k_kv_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (ready != cudaSuccess) return ready;
   const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + Sh::kRows - 1) / Sh::kRows;
-  if (tiles > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  k_kv_prefill<D><<<dim3(static_cast<uint32_t>(tiles), kv.heads, a.n_seqs), Sh::kThreads, bytes, st>>>(kv, a);
-  return cudaGetLastError();
+  if (tiles > 65535u) return cudaErrorInvalidConfiguration;
+  return launch_chained(k_kv_prefill<D>, dim3(kv.heads, a.n_seqs, static_cast<uint32_t>(tiles)), Sh::kThreads, bytes, st,
+                        kv, a);
 }
 
 }  // namespace

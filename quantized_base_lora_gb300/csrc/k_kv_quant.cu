@@ -51,102 +51,157 @@ __device__ __forceinline__ void load8(const void* base, uint64_t at, float (&x)[
   }
 }
 
-template <int D, bool BF16>
+// Heads of one thread: the token's place is found once for them and their loads
+// are in flight together.  A call with few tokens has them one by one, so that
+// its latency is that of one.
+constexpr uint32_t kHeadsMany = 4;
+
+template <int D, bool BF16, uint32_t HT>
 __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t layer, const int32_t* seqs,
                                                         const int32_t* off, uint32_t n, uint32_t n_tokens,
                                                         const void* k, const void* v, uint64_t ks, uint64_t vs) {
+  griddep_launch_dependents();
+  griddep_wait();
   constexpr uint32_t kWords = D / 8;
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t j = id % kWords;
+  const uint32_t j = id % kWords, parts = (kv.heads + HT - 1) / HT;
   const uint64_t th = id / kWords;
-  const uint32_t head = th % kv.heads;
-  const uint64_t token = th / kv.heads;
+  const uint32_t h0 = th % parts * HT;
+  const uint64_t token = th / parts;
   const bool values = blockIdx.y != 0;
   const bool live = token < n_tokens;
+  float x[HT][8];
+#pragma unroll
+  for (uint32_t h = 0; h < HT; ++h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[h][i] = 0.f;
+    if (live && h0 + h < kv.heads) load8<BF16>(values ? v : k, token * (values ? vs : ks) + (h0 + h) * D + j * 8, x[h]);
+  }
   KvPlace at{-1, 0};
-  float x[8] = {};
-  if (live) {
-    at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
-    load8<BF16>(values ? v : k, token * (values ? vs : ks) + head * D + j * 8, x);
-  }
-  float m = 0.f;
+  if (live) at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (x[i] != x[i]) x[i] = 0.f;
-    m = fmaxf(m, fabsf(x[i]));
-  }
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const __half d = __float2half_rn(fminf(m * 0.125f, 65504.f));
-  const float s = __half2float(d);
-  uint32_t w = 0;
+  for (uint32_t h = 0; h < HT; ++h) {
+    float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
-    const float r = fminf(fmaxf(truncf(t + copysignf(0.5f, t)), -8.f), 7.f);
-    w |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      if (x[h][i] != x[h][i]) x[h][i] = 0.f;
+      m = fmaxf(m, fabsf(x[h][i]));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const __half d = __float2half_rn(fminf(m * 0.125f, 65504.f));
+    const float s = __half2float(d);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = s > 0.f ? __fdiv_rn(x[h][i], s) : 0.f;
+      const float r = fminf(fmaxf(truncf(t + copysignf(0.5f, t)), -8.f), 7.f);
+      w |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * i);
+    }
+    if (values) w = transpose8(w, j & 7);
+    if (at.page < 0 || h0 + h >= kv.heads) continue;
+    const uint64_t u = kv_unit(kv, at.page, layer, values, h0 + h);
+    *reinterpret_cast<uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j)) = w;
+    if ((j & 3) == 0) kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)] = d;
   }
-  if (values) w = transpose8(w, j & 7);
-  if (at.page < 0) return;
-  const uint64_t u = kv_unit(kv, at.page, layer, values, head);
-  *reinterpret_cast<uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j)) = w;
-  if ((j & 3) == 0) kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)] = d;
 }
 
-template <int D>
+template <int D, uint32_t HT>
 __global__ void __launch_bounds__(kThreads) k_kv_read(const KvDev kv, uint32_t layer, const int32_t* seqs,
                                                       const int32_t* off, uint32_t n, uint32_t n_tokens, float* k,
                                                       float* v) {
+  griddep_launch_dependents();
+  griddep_wait();
   constexpr uint32_t kWords = D / 8;
   const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t j = id % kWords;
+  const uint32_t j = id % kWords, parts = (kv.heads + HT - 1) / HT;
   const uint64_t th = id / kWords;
-  const uint32_t head = th % kv.heads;
-  const uint64_t token = th / kv.heads;
+  const uint32_t h0 = th % parts * HT;
+  const uint64_t token = th / parts;
   const bool values = blockIdx.y != 0;
   const bool live = token < n_tokens;
-  uint32_t w = 0x88888888u;
-  float d = 0.f;
-  if (live) {
-    const KvPlace at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
-    if (at.page >= 0) {
-      const uint64_t u = kv_unit(kv, at.page, layer, values, head);
-      w = *reinterpret_cast<const uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j));
-      d = __half2float(kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)]);
+  uint32_t w[HT];
+  float d[HT];
+  KvPlace at{-1, 0};
+  if (live) at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+#pragma unroll
+  for (uint32_t h = 0; h < HT; ++h) {
+    w[h] = 0x88888888u;
+    d[h] = 0.f;
+    if (at.page >= 0 && h0 + h < kv.heads) {
+      const uint64_t u = kv_unit(kv, at.page, layer, values, h0 + h);
+      w[h] = *reinterpret_cast<const uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j));
+      d[h] = __half2float(kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)]);
     }
   }
-  if (values) w = transpose8(w, j & 7);
-  if (!live) return;
-  float4 o[2];
-  float* of = reinterpret_cast<float*>(o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) of[i] = d * (static_cast<int>((w >> (4 * i)) & 15u) - 8);
-  float4* p = reinterpret_cast<float4*>((values ? v : k) + (token * kv.heads + head) * D + j * 8);
-  p[0] = o[0];
-  p[1] = o[1];
+  for (uint32_t h = 0; h < HT; ++h) {
+    if (values) w[h] = transpose8(w[h], j & 7);
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = d[h] * (static_cast<int>((w[h] >> (4 * i)) & 15u) - 8);
+    // a pair of lanes swaps halves, so that each store is 32 whole bytes of the pair
+    const bool odd = j & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float give = odd ? o[i] : o[i + 4];
+      const float take = __shfl_xor_sync(0xffffffffu, give, 1);
+      if (odd) o[i] = take;
+      else o[i + 4] = take;
+    }
+    if (!live || h0 + h >= kv.heads) continue;
+    float* const p = (values ? v : k) + (token * kv.heads + h0 + h) * D + (j & ~1u) * 8 + (odd ? 4 : 0);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
+    __stcs(reinterpret_cast<float4*>(p + 8), make_float4(o[4], o[5], o[6], o[7]));
+  }
+}
+
+// Blocks of a launch, 0 where there are too many.
+template <int D, uint32_t HT>
+uint32_t blocks_for(const KvDev& kv, uint32_t n_tokens) {
+  const uint64_t threads = static_cast<uint64_t>(n_tokens) * ((kv.heads + HT - 1) / HT) * (D / 8);
+  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
+  return blocks <= 0x7fffffffu ? static_cast<uint32_t>(blocks) : 0u;
+}
+// Whether one head a thread leaves SMs idle or barely fills them.
+template <int D>
+bool few_tokens(const KvDev& kv, uint32_t n_tokens) {
+  return blocks_for<D, 1>(kv, n_tokens) <= 4 * kv_sm_count();
+}
+
+template <int D, bool BF16, uint32_t HT>
+cudaError_t append_heads(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                         uint32_t n_tokens, const void* k, const void* v, uint64_t ks, uint64_t vs, cudaStream_t st) {
+  const uint32_t blocks = blocks_for<D, HT>(kv, n_tokens);
+  if (!blocks) return cudaErrorInvalidConfiguration;
+  return launch_chained(k_kv_append<D, BF16, HT>, dim3(blocks, 2), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k,
+                        v, ks, vs);
 }
 
 template <int D>
 cudaError_t append_dim(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                        uint32_t n_tokens, const void* k, const void* v, bool bf16, uint64_t ks, uint64_t vs,
                        cudaStream_t st) {
-  const uint64_t threads = static_cast<uint64_t>(n_tokens) * kv.heads * (D / 8);
-  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  const dim3 grid(static_cast<uint32_t>(blocks), 2);
-  if (bf16) k_kv_append<D, true><<<grid, kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs);
-  else k_kv_append<D, false><<<grid, kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs);
-  return cudaGetLastError();
+  if (few_tokens<D>(kv, n_tokens))
+    return bf16 ? append_heads<D, true, 1>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs, st)
+                : append_heads<D, false, 1>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs, st);
+  return bf16 ? append_heads<D, true, kHeadsMany>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs, st)
+              : append_heads<D, false, kHeadsMany>(kv, layer, seqs, off, n, n_tokens, k, v, ks, vs, st);
+}
+
+template <int D, uint32_t HT>
+cudaError_t read_heads(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
+                       uint32_t n_tokens, float* k, float* v, cudaStream_t st) {
+  const uint32_t blocks = blocks_for<D, HT>(kv, n_tokens);
+  if (!blocks) return cudaErrorInvalidConfiguration;
+  return launch_chained(k_kv_read<D, HT>, dim3(blocks, 2), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k, v);
 }
 
 template <int D>
 cudaError_t read_dim(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                      uint32_t n_tokens, float* k, float* v, cudaStream_t st) {
-  const uint64_t threads = static_cast<uint64_t>(n_tokens) * kv.heads * (D / 8);
-  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  k_kv_read<D><<<dim3(static_cast<uint32_t>(blocks), 2), kThreads, 0, st>>>(kv, layer, seqs, off, n, n_tokens, k, v);
-  return cudaGetLastError();
+  return few_tokens<D>(kv, n_tokens) ? read_heads<D, 1>(kv, layer, seqs, off, n, n_tokens, k, v, st)
+                                     : read_heads<D, kHeadsMany>(kv, layer, seqs, off, n, n_tokens, k, v, st);
 }
 
 }  // namespace

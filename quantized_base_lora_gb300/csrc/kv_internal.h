@@ -102,6 +102,26 @@ struct KvQuery {
 };
 
 uint32_t kv_sm_count();
+
+// Launches f in the stream's programmatic chain: its CTAs may be scheduled while
+// the kernel before it still runs, so f calls griddep_wait() before it reads or
+// writes anything, and griddep_launch_dependents() as early as that is sound for
+// the next one (at once: every kernel here waits first).
+template <class... P, class... A>
+cudaError_t launch_chained(void (*f)(P...), dim3 grid, uint32_t block, uint32_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
 cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                              uint32_t n_tokens, const void* k, const void* v, bool bf16, uint64_t ks, uint64_t vs,
                              cudaStream_t st);

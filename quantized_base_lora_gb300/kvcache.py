@@ -24,6 +24,14 @@ from . import (OVL_BF16, OVL_F32, OVL_OK, OvlError, lib, ovl_kv, ovl_kv_workspac
 _DTYPE = {torch.float32: OVL_F32, torch.bfloat16: OVL_BF16}
 
 
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle without a Stream object around it (2 us a call less), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 class KvCache:
     """codes uint8 [pages][layers][2][kv heads][page tokens * D / 2], scales float16 [pages][layers][2][kv heads]
     [page tokens][D / 32], table int32 [rows][columns], length int32 [rows], refs int32 [pages]: contiguous, on one
@@ -46,6 +54,7 @@ class KvCache:
                 raise ValueError(f"{name} must be a contiguous {dt} tensor on the cache's CUDA device")
         self.codes, self.scales, self.table, self.length, self.refs = codes, scales, table, length, refs
         self.device, self.n_kv_heads, self.head_dim, self.page_tokens = codes.device, heads, dim, page
+        self._index, self._scale = codes.get_device(), 1.0 / math.sqrt(dim)
         self.kv = ovl_kv(codes.data_ptr(), scales.data_ptr(), table.data_ptr(), length.data_ptr(), refs.data_ptr(),
                          None, 0, pages, page, layers, heads, dim, table.shape[0], table.shape[1])
         st, nbytes = ovl_kv_workspace_bytes(self.kv)
@@ -76,52 +85,61 @@ class KvCache:
             raise OvlError(st, ovl_last_error(None))
 
     def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _raw_stream(self._index)
 
-    def _ints(self, name: str, t: torch.Tensor, n: int | None = None) -> int:
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
-            raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
-        if n is not None and t.shape[0] != n:
-            raise ValueError(f"{name} has {t.shape[0]} entries, {n} are wanted")
+    # The checks below run at every call, for every tensor: they read each property once.
+
+    def _ints(self, name: str, t: torch.Tensor, n: int) -> int:
+        """Address of an int32 vector of n entries."""
+        if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on the cache's device, not "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
-    def _tokens(self, name: str, t: torch.Tensor, heads: int | None = None) -> int:
-        """Address of packed tokens [tokens][heads][head_dim]; their stride is t.stride(0)."""
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
+    def _tokens(self, name: str, t: torch.Tensor, heads: int | None = None):
+        """(address, tokens, heads, dtype code, stride) of packed tokens [tokens][heads][head_dim]."""
+        if t.dim() != 3:
+            raise ValueError(f"{name} {tuple(t.shape)} is not [tokens][heads][{self.head_dim}]")
+        n, h, d = t.shape
+        step, by_head, by_channel = t.stride()
+        code = _DTYPE.get(t.dtype)
+        if d != self.head_dim or (heads is not None and h != heads):
             raise ValueError(f"{name} {tuple(t.shape)} is not [tokens][{heads or 'heads'}][{self.head_dim}]")
-        if t.dtype not in _DTYPE or t.device != self.device:
+        if code is None or t.get_device() != self._index:
             raise ValueError(f"{name} must be float32 or bfloat16 on the cache's device")
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != self.head_dim):
+        if by_channel != 1 or (h > 1 and by_head != d):
             raise ValueError(f"the heads and channels of {name} must be contiguous")
-        return t.data_ptr()
-
-    def _stride(self, t: torch.Tensor) -> int:
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        return t.data_ptr(), n, h, code, (step if n > 1 else h * d)
 
     def extend(self, seqs: torch.Tensor, tok_off: torch.Tensor):
         """Pages for tok_off[i+1] - tok_off[i] more tokens of row seqs[i]; length counts them."""
         n = seqs.shape[0]
-        self._check(lib.ovl_kv_extend(self._at, self._ints("seqs", seqs), self._ints("tok_off", tok_off, n + 1), n,
-                                      self._stream()))
+        self._check(lib.ovl_kv_extend(self._at, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                                      _raw_stream(self._index)))
 
     def append(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
         """Write the last tokens of the rows: k, v [tokens][kv heads][head_dim] float32 or bfloat16."""
         n = seqs.shape[0]
-        kp, vp = self._tokens("k", k, self.n_kv_heads), self._tokens("v", v, self.n_kv_heads)
-        if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        kp, tokens, _, code, ks = self._tokens("k", k, self.n_kv_heads)
+        vp, v_tokens, _, v_code, vs = self._tokens("v", v, self.n_kv_heads)
+        if code != v_code or tokens != v_tokens:
             raise ValueError("k and v must have one type and length")
-        self._check(lib.ovl_kv_append(self._at, layer, self._ints("seqs", seqs), self._ints("tok_off", tok_off, n + 1),
-                                      n, k.shape[0], kp, vp, _DTYPE[k.dtype], self._stride(k), self._stride(v),
-                                      self._stream()))
+        st = lib.ovl_kv_append(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                               tokens, kp, vp, code, ks, vs, _raw_stream(self._index))
+        if st:
+            self._check(st)
 
     def read(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, n_tokens: int):
         """The values of the rows' last tokens: float32 (k, v), each [n_tokens][kv heads][head_dim]."""
         n = seqs.shape[0]
         out = torch.empty((2, n_tokens, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
-        k, v = out[0], out[1]
-        self._check(lib.ovl_kv_read(self._at, layer, self._ints("seqs", seqs), self._ints("tok_off", tok_off, n + 1),
-                                    n, n_tokens, k.data_ptr(), v.data_ptr(), self._stream()))
-        return k, v
+        at = out.data_ptr()
+        st = lib.ovl_kv_read(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                             n_tokens, at, at + 4 * n_tokens * self.n_kv_heads * self.head_dim,
+                             _raw_stream(self._index))
+        if st:
+            self._check(st)
+        return out.unbind(0)
 
     def attention(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, q: torch.Tensor, max_new: int,
                   scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -129,35 +147,40 @@ class KvCache:
         """Attention of the rows' last tokens over the cache: q [tokens][heads][head_dim] -> the same shape and type.
         max_new: upper bound of the new tokens of one row; scale: 1 / sqrt(head_dim) unless given."""
         n = seqs.shape[0]
-        qp = self._tokens("q", q)
+        qp, tokens, heads, code, qs = self._tokens("q", q)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        elif out.dtype != q.dtype or out.shape != q.shape:
-            raise ValueError("out must have q's shape and type")
-        if scale is None:
-            scale = 1.0 / math.sqrt(self.head_dim)
-        self._check(lib.ovl_kv_attention(self._at, layer, self._ints("seqs", seqs),
-                                         self._ints("tok_off", tok_off, n + 1), n, q.shape[0], max_new, qp,
-                                         _DTYPE[q.dtype], q.shape[1], self._stride(q), scale, window, sinks,
-                                         self._tokens("out", out), self._stride(out), self._stream()))
+            out = torch.empty((tokens, heads, self.head_dim), dtype=q.dtype, device=self.device)
+            op, os_ = out.data_ptr(), heads * self.head_dim
+        else:
+            op, o_tokens, o_heads, o_code, os_ = self._tokens("out", out)
+            if (o_tokens, o_heads, o_code) != (tokens, heads, code):
+                raise ValueError("out must have q's shape and type")
+        st = lib.ovl_kv_attention(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1),
+                                  n, tokens, max_new, qp, code, heads, qs, self._scale if scale is None else scale,
+                                  window, sinks, op, os_, _raw_stream(self._index))
+        if st:
+            self._check(st)
         return out
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor | None = None):
         """Row dst[i] becomes the first keep[i] tokens of row src[i] (all without keep), sharing whole pages."""
         n = src.shape[0]
-        self._check(lib.ovl_kv_fork(self._at, self._ints("src", src), self._ints("dst", dst, n),
-                                    None if keep is None else self._ints("keep", keep, n), n, self._stream()))
+        self._check(lib.ovl_kv_fork(self._at, self._ints("src", src, n), self._ints("dst", dst, n),
+                                    None if keep is None else self._ints("keep", keep, n), n,
+                                    _raw_stream(self._index)))
 
     def compact(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor, keep_off: torch.Tensor):
         """Row dst[i] becomes tokens keep[keep_off[i] .. keep_off[i+1] - 1] of row src[i], in fresh pages."""
         n = src.shape[0]
-        self._check(lib.ovl_kv_compact(self._at, self._ints("src", src), self._ints("dst", dst, n),
-                                       self._ints("keep", keep), self._ints("keep_off", keep_off, n + 1), n,
-                                       keep.shape[0], self._stream()))
+        m = keep.shape[0]
+        self._check(lib.ovl_kv_compact(self._at, self._ints("src", src, n), self._ints("dst", dst, n),
+                                       self._ints("keep", keep, m), self._ints("keep_off", keep_off, n + 1), n, m,
+                                       _raw_stream(self._index)))
 
     def release(self, seqs: torch.Tensor):
         """The rows become free."""
-        self._check(lib.ovl_kv_release(self._at, self._ints("seqs", seqs), seqs.shape[0], self._stream()))
+        n = seqs.shape[0]
+        self._check(lib.ovl_kv_release(self._at, self._ints("seqs", seqs, n), n, _raw_stream(self._index)))
 
     def check(self):
         """Wait for the current stream; raise what a call latched on the device since the last check."""
