@@ -9,6 +9,7 @@
 // destinations of the same call release.  Pages that an entry releases from its
 // own source row (src = dst) are still read by the copy, so they become free
 // only afterwards.
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -263,41 +264,37 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
   if (t == 0) *kv.n_fresh = two ? total : 0;
 }
 
-// Fork: whole pages, every layer.  A page is two contiguous runs.
+// Fork: whole pages, every layer.  A page is two contiguous runs; row blockIdx.y
+// of the grid copies fresh page blockIdx.y (a fork has at most one an entry).
 __global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
   griddep_launch_dependents();
   griddep_wait();
+  if (blockIdx.y >= *kv.n_fresh) return;
+  const KvFresh f = kv.fresh[blockIdx.y];
+  if (static_cast<uint32_t>(f.src_page) >= kv.n_pages) return;
   const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
   const uint64_t nc = units * kv.unit_codes / 16, ns = units * kv.unit_scales / 8;
-  constexpr uint64_t kChunk = kCopy * 4;
-  const uint64_t per = (nc + ns + kChunk - 1) / kChunk;
-  const uint64_t items = per * *kv.n_fresh;
-  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const KvFresh f = kv.fresh[it / per];
-    if (static_cast<uint32_t>(f.src_page) >= kv.n_pages) continue;
-    const uint4* a = reinterpret_cast<const uint4*>(kv.codes) + f.src_page * nc;
-    uint4* b = reinterpret_cast<uint4*>(kv.codes) + f.dst_page * nc;
-    const uint4* as = reinterpret_cast<const uint4*>(kv.scales) + f.src_page * ns;
-    uint4* bs = reinterpret_cast<uint4*>(kv.scales) + f.dst_page * ns;
-    const uint64_t i0 = (it % per) * kChunk + threadIdx.x;
-    uint4 v[4];
+  constexpr uint32_t kEach = 8;
+  constexpr uint64_t kChunk = kCopy * kEach;
+  auto run = [&](uint4* pool, uint64_t n) {
+    const uint4* const a = pool + f.src_page * n;
+    uint4* const b = pool + f.dst_page * n;
+    for (uint64_t i0 = blockIdx.x * kChunk + threadIdx.x; i0 < n; i0 += gridDim.x * kChunk) {
+      uint4 v[kEach];
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint64_t i = i0 + k * kCopy;
-      if (i < nc) v[k] = a[i];
-      else if (i < nc + ns) v[k] = as[i - nc];
-    }
+      for (uint32_t k = 0; k < kEach; ++k)
+        if (i0 + k * kCopy < n) v[k] = __ldcs(a + i0 + k * kCopy);
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint64_t i = i0 + k * kCopy;
-      if (i < nc) b[i] = v[k];
-      else if (i < nc + ns) bs[i - nc] = v[k];
+      for (uint32_t k = 0; k < kEach; ++k)
+        if (i0 + k * kCopy < n) b[i0 + k * kCopy] = v[k];
     }
-  }
+  };
+  run(reinterpret_cast<uint4*>(kv.codes), nc);
+  run(reinterpret_cast<uint4*>(kv.scales), ns);
 }
 
-// Runs f(src, dst) for every head of a page with kHeads loads in flight: heads
-// are a constant distance apart on both sides.
+// One T of every head of a page, kHeads loads in flight: heads are a constant
+// distance apart on both sides.
 template <class T>
 __device__ __forceinline__ void copy_heads(uint8_t* pool, uint64_t from, uint64_t to, uint32_t heads, uint32_t step) {
   constexpr uint32_t kHeads = 4;
@@ -312,25 +309,23 @@ __device__ __forceinline__ void copy_heads(uint8_t* pool, uint64_t from, uint64_
   }
 }
 
-// Compaction: one fresh page, layer and K|V at a time; the tokens' sources are
-// found once and used for every head.  Bound by memory; a value unit is 4 to 16
-// bytes, so scattered tokens read whole sectors of values for a part of them.
+// Compaction: fresh page after fresh page, blockIdx.y's share of the layers of
+// each; the tokens' sources are found once and used for all its layers and heads.
+// Bound by memory; a value unit is 4 to 16 bytes, so scattered tokens read whole
+// sectors of values for a part of them.
 template <int D>
 __global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* __restrict__ src,
                                                      const int32_t* __restrict__ dst,
                                                      const int32_t* __restrict__ keep,
-                                                     const int32_t* __restrict__ off) {
-  constexpr uint32_t kNone = 0xffffffffu;
-  __shared__ uint64_t from_codes[256], from_scales[256];   // of head 0; kNone in the upper half: no source
+                                                     const int32_t* __restrict__ off, uint32_t layers_each) {
+  __shared__ int32_t from_page[256], from_slot[256];
   griddep_launch_dependents();
   griddep_wait();
-  const uint64_t items = static_cast<uint64_t>(*kv.n_fresh) * kv.layers * 2;
-  const uint32_t code_step = kv.unit_codes, scale_step = kv.unit_scales * 2;
+  const uint32_t fresh = *kv.n_fresh, code_step = kv.unit_codes, scale_step = kv.unit_scales * 2;
+  const uint32_t layer0 = blockIdx.y * layers_each, layer1 = min(kv.layers, layer0 + layers_each);
   uint8_t* const scales = reinterpret_cast<uint8_t*>(kv.scales);
-  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const uint32_t which = it & 1;
-    const uint32_t layer = (it >> 1) % kv.layers;
-    const KvFresh f = kv.fresh[(it >> 1) / kv.layers];
+  for (uint32_t r = blockIdx.x; r < fresh; r += gridDim.x) {
+    const KvFresh f = kv.fresh[r];
     const int32_t s = src[f.entry];
     const int32_t* row = s == dst[f.entry] ? kv.rows + static_cast<size_t>(f.entry) * kv.max_pages
                                            : kv.table + static_cast<size_t>(s) * kv.max_pages;
@@ -340,35 +335,38 @@ __global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const in
     for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
       const int32_t pos = keep[first + i];
       const int32_t p = row[pos >> kv.page_shift];
-      const uint32_t slot = pos & (kv.page - 1);
-      const uint64_t unit = kv_unit(kv, p, layer, which, 0);
-      const bool there = static_cast<uint32_t>(p) < kv.n_pages;
-      from_codes[i] = there ? unit * code_step + (which ? (slot >> 3) * (4 * D) + (slot & 7) * (D / 16) : slot * (D / 2))
-                            : static_cast<uint64_t>(kNone) << 32;
-      from_scales[i] = unit * scale_step + slot * (D / 16);
+      from_page[i] = static_cast<uint32_t>(p) < kv.n_pages ? p : -1;
+      from_slot[i] = pos & static_cast<int32_t>(kv.page - 1);
     }
     __syncthreads();
-    const uint64_t unit = kv_unit(kv, f.dst_page, layer, which, 0);
     using Small = typename std::conditional<D == 64, uint32_t, typename std::conditional<D == 128, uint2, uint4>::type>::type;
-    if (which == 0) {
-      constexpr uint32_t kRow = D / 32;              // 16-byte pieces of a row
+    for (uint32_t layer = layer0; layer < layer1; ++layer) {
+      const uint64_t to = kv_unit(kv, f.dst_page, layer, 0, 0);
+      // keys: 16-byte pieces of rows
+      constexpr uint32_t kRow = D / 32;
       for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
-        const uint64_t from = from_codes[i / kRow];
-        if (from >> 32 == kNone) continue;
-        copy_heads<uint4>(kv.codes, from + i % kRow * 16, unit * code_step + i * 16, kv.heads, code_step);
+        const int32_t p = from_page[i / kRow];
+        if (p < 0) continue;
+        copy_heads<uint4>(kv.codes, kv_unit(kv, p, layer, 0, 0) * code_step + from_slot[i / kRow] * (D / 2) + i % kRow * 16,
+                          to * code_step + i * 16, kv.heads, code_step);
       }
-    } else {
+      // values: units, in the order in which they are stored
       for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
         const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
-        if (tok >= count) continue;
-        const uint64_t from = from_codes[tok];
-        if (from >> 32 == kNone) continue;
-        copy_heads<Small>(kv.codes, from + g * (D / 2), unit * code_step + i * (D / 16), kv.heads, code_step);
+        if (tok >= count || from_page[tok] < 0) continue;
+        const uint32_t slot = from_slot[tok];
+        copy_heads<Small>(kv.codes,
+                          kv_unit(kv, from_page[tok], layer, 1, 0) * code_step + (slot >> 3) * (4 * D) + (slot & 7) * (D / 16) +
+                              g * (D / 2),
+                          (to + kv.heads) * code_step + i * (D / 16), kv.heads, code_step);
       }
-    }
-    for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
-      if (from_codes[i] >> 32 == kNone) continue;
-      copy_heads<Small>(scales, from_scales[i], unit * scale_step + i * (D / 16), kv.heads, scale_step);
+      // scales of both
+      for (uint32_t i = threadIdx.x; i < 2 * count; i += kCopy) {
+        const uint32_t which = i >= count, tok = which ? i - count : i;
+        if (from_page[tok] < 0) continue;
+        copy_heads<Small>(scales, kv_unit(kv, from_page[tok], layer, which, 0) * scale_step + from_slot[tok] * (D / 16),
+                          (to + which * kv.heads) * scale_step + tok * (D / 16), kv.heads, scale_step);
+      }
     }
   }
 }
@@ -379,13 +377,23 @@ cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, c
                             const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st) {
   const cudaError_t e = launch_chained(k_kv_pages, dim3(1), kBook, 0, st, kv, what, src, dst, keep, off, n, n_keep);
   if (e != cudaSuccess) return e;
-  const uint32_t grid = kv_sm_count() * 4;
-  if (what == KvPages::kFork) return launch_chained(k_kv_copy_pages, dim3(grid), kCopy, 0, st, kv);
+  const uint32_t full = kv_sm_count() * 4;           // CTAs resident at a time
+  if (what == KvPages::kFork) {
+    const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
+    const uint64_t per_page = (units * kv.unit_codes / 16 + kCopy * 8 - 1) / (kCopy * 8);
+    const uint32_t x = static_cast<uint32_t>(std::min<uint64_t>(per_page, (full + n - 1) / n));
+    return launch_chained(k_kv_copy_pages, dim3(x, n), kCopy, 0, st, kv);
+  }
   if (what == KvPages::kCompact) {
+    // at most this many fresh pages; as many layers to a CTA as leave two runs of CTAs
+    const uint64_t pages = n_keep / kv.page + n;
+    const uint32_t each = static_cast<uint32_t>(
+        std::min<uint64_t>(kv.layers, std::max<uint64_t>(1, pages * kv.layers / (2 * full))));
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(pages, 2 * full)), (kv.layers + each - 1) / each);
     switch (kv.dim) {
-      case 64: return launch_chained(k_kv_gather<64>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
-      case 128: return launch_chained(k_kv_gather<128>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
-      default: return launch_chained(k_kv_gather<256>, dim3(grid), kCopy, 0, st, kv, src, dst, keep, off);
+      case 64: return launch_chained(k_kv_gather<64>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
+      case 128: return launch_chained(k_kv_gather<128>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
+      default: return launch_chained(k_kv_gather<256>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
     }
   }
   return cudaSuccess;

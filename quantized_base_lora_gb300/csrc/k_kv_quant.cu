@@ -51,6 +51,19 @@ __device__ __forceinline__ void load8(const void* base, uint64_t at, float (&x)[
   }
 }
 
+// clamp(round_half_away(x / s), -8, 7) + 8, with inv the reciprocal of s rounded
+// to nearest (0 where s is 0).  x inv is corrected by one residual step, which
+// gives the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990; s
+// has 11 significant bits, so the method's one exception does not occur).  A
+// block costs one reciprocal instead of 32 divisions.
+__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
+  x = x == x ? fminf(fmaxf(x, -3.4e38f), 3.4e38f) : 0.f;         // infinities are clipped
+  const float q = x * inv;
+  float t = fmaf(fmaf(-q, s, x), inv, q);
+  t = fminf(fmaxf(t, -8.f), 7.f);
+  return static_cast<uint32_t>(__float2int_rz(t + copysignf(0.5f, t)) + 8);
+}
+
 // Heads of one thread: the token's place is found once for them and their loads
 // are in flight together.  A call with few tokens has them one by one, so that
 // its latency is that of one.
@@ -83,21 +96,14 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t
   for (uint32_t h = 0; h < HT; ++h) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (x[h][i] != x[h][i]) x[h][i] = 0.f;
-      m = fmaxf(m, fabsf(x[h][i]));
-    }
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[h][i]));   // a NaN is no maximum
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const __half d = __float2half_rn(fminf(m * 0.125f, 65504.f));
-    const float s = __half2float(d);
+    const float s = __half2float(d), inv = s > 0.f ? __frcp_rn(s) : 0.f;
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = s > 0.f ? __fdiv_rn(x[h][i], s) : 0.f;
-      const float r = fminf(fmaxf(truncf(t + copysignf(0.5f, t)), -8.f), 7.f);
-      w |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i) w |= code_of(x[h][i], s, inv) << (4 * i);
     if (values) w = transpose8(w, j & 7);
     if (at.page < 0 || h0 + h >= kv.heads) continue;
     const uint64_t u = kv_unit(kv, at.page, layer, values, h0 + h);
@@ -139,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvDev kv, uint32_t l
     if (values) w[h] = transpose8(w[h], j & 7);
     float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = d[h] * (static_cast<int>((w[h] >> (4 * i)) & 15u) - 8);
+    for (int i = 0; i < 8; ++i)                // 2^23 + code, exactly
+      o[i] = d[h] * (__uint_as_float(((w[h] >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f);
     // a pair of lanes swaps halves, so that each store is 32 whole bytes of the pair
     const bool odd = j & 1;
 #pragma unroll

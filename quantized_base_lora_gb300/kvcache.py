@@ -132,14 +132,13 @@ class KvCache:
     def read(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, n_tokens: int):
         """The values of the rows' last tokens: float32 (k, v), each [n_tokens][kv heads][head_dim]."""
         n = seqs.shape[0]
-        out = torch.empty((2, n_tokens, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
-        at = out.data_ptr()
+        k = torch.empty((n_tokens, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
+        v = torch.empty_like(k)
         st = lib.ovl_kv_read(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
-                             n_tokens, at, at + 4 * n_tokens * self.n_kv_heads * self.head_dim,
-                             _raw_stream(self._index))
+                             n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
         if st:
             self._check(st)
-        return out.unbind(0)
+        return k, v
 
     def attention(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, q: torch.Tensor, max_new: int,
                   scale: float | None = None, window: int = 0, sinks: int = 0,
