@@ -155,12 +155,19 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
   __syncthreads();
   if (what == KvPages::kCompact && sound) {
     // the entries follow one another from position 0, so owner_of finds each one
-    const int32_t total = s.off[n];
-#pragma unroll 4
-    for (int32_t j = static_cast<int32_t>(t); j < total; j += kBook) {
-      const int32_t p = __ldg(keep + j);
-      const uint32_t e = owner_of(s.off, n, j);
-      if (p < 0 || p >= s.limit[e]) s.error = OVL_E_ARG;
+    const int64_t total = s.off[n];
+    uint32_t e = 0;                            // the entry of position j: only ever grows
+    for (int64_t j0 = t; j0 < total; j0 += 8 * kBook) {
+      int32_t p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = j0 + i * kBook < total ? __ldg(keep + j0 + i * kBook) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t j = j0 + i * kBook;
+        if (j >= total) break;
+        while (s.off[e + 1] <= j) ++e;
+        if (p[i] < 0 || p[i] >= s.limit[e]) s.error = OVL_E_ARG;
+      }
     }
     __syncthreads();
   }
@@ -207,13 +214,17 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k)
       if ((free_mask >> k & 1u) && r < total) {
-        KvFresh f;
+        KvFresh f{};
         f.dst_page = static_cast<int32_t>(base + t * 4 + k);
-        f.entry = static_cast<int32_t>(owner_of(s.first, n, r));
-        f.column = s.whole[f.entry] + static_cast<int32_t>(r - s.first[f.entry]);
-        f.src_page = what == KvPages::kFork
-                         ? kv.table[static_cast<size_t>(s.src[f.entry]) * kv.max_pages + s.whole[f.entry]]
-                         : -1;
+        const uint32_t e = owner_of(s.first, n, r);
+        f.row = kv.table + static_cast<size_t>(s.src[e]) * kv.max_pages;
+        if (what == KvPages::kFork) f.src_page = f.row[s.whole[e]];
+        if (what == KvPages::kCompact) {
+          if (s.src[e] == s.dst[e]) f.row = kv.rows + static_cast<size_t>(e) * kv.max_pages;
+          const int32_t at = static_cast<int32_t>((r - s.first[e]) << shift);
+          f.first = s.off[e] + at;
+          f.count = min(s.length[e] - at, static_cast<int32_t>(page));
+        }
         kv.fresh[r++] = f;
       }
     __syncthreads();
@@ -269,17 +280,18 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
 __global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
   griddep_launch_dependents();
   griddep_wait();
-  if (blockIdx.y >= *kv.n_fresh) return;
-  const KvFresh f = kv.fresh[blockIdx.y];
-  if (static_cast<uint32_t>(f.src_page) >= kv.n_pages) return;
+  if (blockIdx.y >= kv.n_pages) return;
+  const uint32_t fresh = *kv.n_fresh;
+  const KvFresh f = kv.fresh[blockIdx.y];            // read beside the count, not after it
+  if (blockIdx.y >= fresh || static_cast<uint32_t>(f.src_page) >= kv.n_pages) return;
   const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
   const uint64_t nc = units * kv.unit_codes / 16, ns = units * kv.unit_scales / 8;
   constexpr uint32_t kEach = 8;
   constexpr uint64_t kChunk = kCopy * kEach;
-  auto run = [&](uint4* pool, uint64_t n) {
+  auto run = [&](uint4* pool, uint64_t n, uint32_t part, uint32_t parts) {
     const uint4* const a = pool + f.src_page * n;
     uint4* const b = pool + f.dst_page * n;
-    for (uint64_t i0 = blockIdx.x * kChunk + threadIdx.x; i0 < n; i0 += gridDim.x * kChunk) {
+    for (uint64_t i0 = part * kChunk + threadIdx.x; i0 < n; i0 += parts * kChunk) {
       uint4 v[kEach];
 #pragma unroll
       for (uint32_t k = 0; k < kEach; ++k)
@@ -289,8 +301,10 @@ __global__ void __launch_bounds__(kCopy) k_kv_copy_pages(const KvDev kv) {
         if (i0 + k * kCopy < n) b[i0 + k * kCopy] = v[k];
     }
   };
-  run(reinterpret_cast<uint4*>(kv.codes), nc);
-  run(reinterpret_cast<uint4*>(kv.scales), ns);
+  // the scales, an eighth of the codes, are the last ninth of the CTAs'
+  const uint32_t last = (gridDim.x + 8) / 9, most = gridDim.x - last;
+  if (blockIdx.x < most) run(reinterpret_cast<uint4*>(kv.codes), nc, blockIdx.x, most);
+  else run(reinterpret_cast<uint4*>(kv.scales), ns, blockIdx.x - most, last);
 }
 
 // One T of every head of a page, kHeads loads in flight: heads are a constant
@@ -310,63 +324,56 @@ __device__ __forceinline__ void copy_heads(uint8_t* pool, uint64_t from, uint64_
 }
 
 // Compaction: fresh page after fresh page, blockIdx.y's share of the layers of
-// each; the tokens' sources are found once and used for all its layers and heads.
+// each, keys or values by blockIdx.z; the tokens' sources are found once and used
+// for all its layers and heads.
 // Bound by memory; a value unit is 4 to 16 bytes, so scattered tokens read whole
 // sectors of values for a part of them.
 template <int D>
-__global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* __restrict__ src,
-                                                     const int32_t* __restrict__ dst,
-                                                     const int32_t* __restrict__ keep,
-                                                     const int32_t* __restrict__ off, uint32_t layers_each) {
+__global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* __restrict__ keep,
+                                                        uint32_t layers_each) {
   __shared__ int32_t from_page[256], from_slot[256];
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t fresh = *kv.n_fresh, code_step = kv.unit_codes, scale_step = kv.unit_scales * 2;
-  const uint32_t layer0 = blockIdx.y * layers_each, layer1 = min(kv.layers, layer0 + layers_each);
+  const uint32_t which = blockIdx.z, layer0 = blockIdx.y * layers_each, layer1 = min(kv.layers, layer0 + layers_each);
   uint8_t* const scales = reinterpret_cast<uint8_t*>(kv.scales);
   for (uint32_t r = blockIdx.x; r < fresh; r += gridDim.x) {
     const KvFresh f = kv.fresh[r];
-    const int32_t s = src[f.entry];
-    const int32_t* row = s == dst[f.entry] ? kv.rows + static_cast<size_t>(f.entry) * kv.max_pages
-                                           : kv.table + static_cast<size_t>(s) * kv.max_pages;
-    const int32_t first = off[f.entry] + f.column * static_cast<int32_t>(kv.page);
-    const uint32_t count = min(static_cast<uint32_t>(off[f.entry + 1] - first), kv.page);
+    const uint32_t count = f.count;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < count; i += kCopy) {
-      const int32_t pos = keep[first + i];
-      const int32_t p = row[pos >> kv.page_shift];
+      const int32_t pos = keep[f.first + i];
+      const int32_t p = f.row[pos >> kv.page_shift];
       from_page[i] = static_cast<uint32_t>(p) < kv.n_pages ? p : -1;
       from_slot[i] = pos & static_cast<int32_t>(kv.page - 1);
     }
     __syncthreads();
     using Small = typename std::conditional<D == 64, uint32_t, typename std::conditional<D == 128, uint2, uint4>::type>::type;
     for (uint32_t layer = layer0; layer < layer1; ++layer) {
-      const uint64_t to = kv_unit(kv, f.dst_page, layer, 0, 0);
-      // keys: 16-byte pieces of rows
-      constexpr uint32_t kRow = D / 32;
-      for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
-        const int32_t p = from_page[i / kRow];
-        if (p < 0) continue;
-        copy_heads<uint4>(kv.codes, kv_unit(kv, p, layer, 0, 0) * code_step + from_slot[i / kRow] * (D / 2) + i % kRow * 16,
-                          to * code_step + i * 16, kv.heads, code_step);
+      const uint64_t to = kv_unit(kv, f.dst_page, layer, which, 0);
+      if (which == 0) {                              // 16-byte pieces of rows
+        constexpr uint32_t kRow = D / 32;
+        for (uint32_t i = threadIdx.x; i < count * kRow; i += kCopy) {
+          const int32_t p = from_page[i / kRow];
+          if (p < 0) continue;
+          copy_heads<uint4>(kv.codes, kv_unit(kv, p, layer, 0, 0) * code_step + from_slot[i / kRow] * (D / 2) + i % kRow * 16,
+                            to * code_step + i * 16, kv.heads, code_step);
+        }
+      } else {                                       // units, in the order in which they are stored
+        for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
+          const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
+          if (tok >= count || from_page[tok] < 0) continue;
+          const uint32_t slot = from_slot[tok];
+          copy_heads<Small>(kv.codes,
+                            kv_unit(kv, from_page[tok], layer, 1, 0) * code_step + (slot >> 3) * (4 * D) +
+                                (slot & 7) * (D / 16) + g * (D / 2),
+                            to * code_step + i * (D / 16), kv.heads, code_step);
+        }
       }
-      // values: units, in the order in which they are stored
-      for (uint32_t i = threadIdx.x; i < ((count + 7) & ~7u) * 8; i += kCopy) {
-        const uint32_t tok = (i >> 6) * 8 + (i & 7), g = (i >> 3) & 7;
-        if (tok >= count || from_page[tok] < 0) continue;
-        const uint32_t slot = from_slot[tok];
-        copy_heads<Small>(kv.codes,
-                          kv_unit(kv, from_page[tok], layer, 1, 0) * code_step + (slot >> 3) * (4 * D) + (slot & 7) * (D / 16) +
-                              g * (D / 2),
-                          (to + kv.heads) * code_step + i * (D / 16), kv.heads, code_step);
-      }
-      // scales of both
-      for (uint32_t i = threadIdx.x; i < 2 * count; i += kCopy) {
-        const uint32_t which = i >= count, tok = which ? i - count : i;
-        if (from_page[tok] < 0) continue;
-        copy_heads<Small>(scales, kv_unit(kv, from_page[tok], layer, which, 0) * scale_step + from_slot[tok] * (D / 16),
-                          (to + which * kv.heads) * scale_step + tok * (D / 16), kv.heads, scale_step);
-      }
+      for (uint32_t i = threadIdx.x; i < count; i += kCopy)
+        if (from_page[i] >= 0)
+          copy_heads<Small>(scales, kv_unit(kv, from_page[i], layer, which, 0) * scale_step + from_slot[i] * (D / 16),
+                            to * scale_step + i * (D / 16), kv.heads, scale_step);
     }
   }
 }
@@ -381,19 +388,20 @@ cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, c
   if (what == KvPages::kFork) {
     const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
     const uint64_t per_page = (units * kv.unit_codes / 16 + kCopy * 8 - 1) / (kCopy * 8);
-    const uint32_t x = static_cast<uint32_t>(std::min<uint64_t>(per_page, (full + n - 1) / n));
+    const uint32_t x = static_cast<uint32_t>(
+        std::max<uint64_t>(2, std::min<uint64_t>(per_page + (per_page + 7) / 8, (full + n - 1) / n)));
     return launch_chained(k_kv_copy_pages, dim3(x, n), kCopy, 0, st, kv);
   }
   if (what == KvPages::kCompact) {
-    // at most this many fresh pages; as many layers to a CTA as leave two runs of CTAs
+    // at most this many fresh pages; as many layers to a CTA as leave eight rounds of CTAs
     const uint64_t pages = n_keep / kv.page + n;
     const uint32_t each = static_cast<uint32_t>(
-        std::min<uint64_t>(kv.layers, std::max<uint64_t>(1, pages * kv.layers / (2 * full))));
-    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(pages, 2 * full)), (kv.layers + each - 1) / each);
+        std::min<uint64_t>(kv.layers, std::max<uint64_t>(1, pages * kv.layers * 2 / (8 * full))));
+    const dim3 grid(static_cast<uint32_t>(std::min<uint64_t>(pages, 2 * full)), (kv.layers + each - 1) / each, 2);
     switch (kv.dim) {
-      case 64: return launch_chained(k_kv_gather<64>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
-      case 128: return launch_chained(k_kv_gather<128>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
-      default: return launch_chained(k_kv_gather<256>, grid, kCopy, 0, st, kv, src, dst, keep, off, each);
+      case 64: return launch_chained(k_kv_gather<64>, grid, kCopy, 0, st, kv, keep, each);
+      case 128: return launch_chained(k_kv_gather<128>, grid, kCopy, 0, st, kv, keep, each);
+      default: return launch_chained(k_kv_gather<256>, grid, kCopy, 0, st, kv, keep, each);
     }
   }
   return cudaSuccess;

@@ -51,22 +51,31 @@ __device__ __forceinline__ void load8(const void* base, uint64_t at, float (&x)[
   }
 }
 
-// clamp(round_half_away(x / s), -8, 7) + 8, with inv the reciprocal of s rounded
-// to nearest (0 where s is 0).  x inv is corrected by one residual step, which
-// gives the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990; s
-// has 11 significant bits, so the method's one exception does not occur).  A
-// block costs one reciprocal instead of 32 divisions.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
-  x = x == x ? fminf(fmaxf(x, -3.4e38f), 3.4e38f) : 0.f;         // infinities are clipped
-  const float q = x * inv;
-  float t = fmaf(fmaf(-q, s, x), inv, q);
-  t = fminf(fmaxf(t, -8.f), 7.f);
-  return static_cast<uint32_t>(__float2int_rz(t + copysignf(0.5f, t)) + 8);
+// The codes of 8 channels, each clamp(round_half_away(x / s), -8, 7) + 8, from
+// the lowest 4 bits on.  inv: the reciprocal of s rounded to nearest, 0 where s is
+// 0.  x inv is corrected by one residual step, which gives the correctly rounded
+// quotient (Markstein, IBM J. Res. Dev. 34, 1990; s has 11 significant bits, so
+// the method's one exception does not occur): a block costs one reciprocal
+// instead of 32 divisions.
+template <bool TAME>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float inv) {
+  uint32_t w = 0x88888888u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = x[i] * inv;
+    float t = fminf(fmaf(fmaf(-q, s, x[i]), inv, q), 7.f);
+    if constexpr (!TAME) t = fmaxf(t, -8.f);       // a tame block's |t| is below 8.01
+    w += static_cast<uint32_t>(__float2int_rz(t + copysignf(0.5f, t))) << (4 * i);
+  }
+  return w;
 }
 
 // Heads of one thread: the token's place is found once for them and their loads
 // are in flight together.  A call with few tokens has them one by one, so that
-// its latency is that of one.
+// its latency is that of one.  Bound by memory (reads 2 or 4, writes 0.5625 bytes
+// a channel) with the arithmetic close behind: most blocks are tame - finite and
+// neither so small nor so large that d is subnormal or saturated - and need no
+// care for single channels.
 constexpr uint32_t kHeadsMany = 4;
 
 template <int D, bool BF16, uint32_t HT>
@@ -76,11 +85,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t
   griddep_launch_dependents();
   griddep_wait();
   constexpr uint32_t kWords = D / 8;
-  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t j = id % kWords, parts = (kv.heads + HT - 1) / HT;
-  const uint64_t th = id / kWords;
-  const uint32_t h0 = th % parts * HT;
-  const uint64_t token = th / parts;
+  const uint32_t j = threadIdx.x % kWords, h0 = blockIdx.z * HT;
+  const uint64_t token = static_cast<uint64_t>(blockIdx.x) * (kThreads / kWords) + threadIdx.x / kWords;
   const bool values = blockIdx.y != 0;
   const bool live = token < n_tokens;
   float x[HT][8];
@@ -92,23 +98,34 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t
   }
   KvPlace at{-1, 0};
   if (live) at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+  const uint64_t u0 = kv_unit(kv, at.page < 0 ? 0 : at.page, layer, values, h0);
+  uint8_t* const codes = kv.codes + u0 * kv.unit_codes + word_offset<D>(values, at.slot, j);
+  __half* const scales = kv.scales + u0 * kv.unit_scales + at.slot * (D / 32) + (j >> 2);
 #pragma unroll
   for (uint32_t h = 0; h < HT; ++h) {
-    float m = 0.f;
+    float m = 0.f, odd = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[h][i]));   // a NaN is no maximum
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[h][i])), odd = fmaf(x[h][i], 0.f, odd);   // odd: NaN or 0
+    const bool tame = odd == 0.f && (m == 0.f || (m >= 0x1p-10f && m <= 8.f * 65504.f));
+    if (!__all_sync(0xffffffffu, tame)) {
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[h][i] = x[h][i] == x[h][i] ? fminf(fmaxf(x[h][i], -8.f * 65504.f), 8.f * 65504.f) : 0.f;
+        m = fmaxf(m, fabsf(x[h][i]));
+      }
+    }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const __half d = __float2half_rn(fminf(m * 0.125f, 65504.f));
+    const __half d = __float2half_rn(m * 0.125f);
     const float s = __half2float(d), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= code_of(x[h][i], s, inv) << (4 * i);
+    uint32_t w;
+    if (__all_sync(0xffffffffu, tame)) w = codes_of<true>(x[h], s, inv);
+    else w = codes_of<false>(x[h], s, inv);
     if (values) w = transpose8(w, j & 7);
     if (at.page < 0 || h0 + h >= kv.heads) continue;
-    const uint64_t u = kv_unit(kv, at.page, layer, values, h0 + h);
-    *reinterpret_cast<uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j)) = w;
-    if ((j & 3) == 0) kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)] = d;
+    *reinterpret_cast<uint32_t*>(codes + static_cast<uint64_t>(h) * kv.unit_codes) = w;
+    if ((j & 3) == 0) scales[static_cast<uint64_t>(h) * kv.unit_scales] = d;
   }
 }
 
@@ -119,69 +136,64 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvDev kv, uint32_t l
   griddep_launch_dependents();
   griddep_wait();
   constexpr uint32_t kWords = D / 8;
-  const uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t j = id % kWords, parts = (kv.heads + HT - 1) / HT;
-  const uint64_t th = id / kWords;
-  const uint32_t h0 = th % parts * HT;
-  const uint64_t token = th / parts;
+  const uint32_t j = threadIdx.x % kWords, h0 = blockIdx.z * HT;
+  const uint64_t token = static_cast<uint64_t>(blockIdx.x) * (kThreads / kWords) + threadIdx.x / kWords;
   const bool values = blockIdx.y != 0;
   const bool live = token < n_tokens;
   uint32_t w[HT];
   float d[HT];
   KvPlace at{-1, 0};
   if (live) at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+  const uint64_t u0 = kv_unit(kv, at.page < 0 ? 0 : at.page, layer, values, h0);
+  const uint8_t* const codes = kv.codes + u0 * kv.unit_codes + word_offset<D>(values, at.slot, j);
+  const __half* const scales = kv.scales + u0 * kv.unit_scales + at.slot * (D / 32) + (j >> 2);
 #pragma unroll
   for (uint32_t h = 0; h < HT; ++h) {
     w[h] = 0x88888888u;
     d[h] = 0.f;
     if (at.page >= 0 && h0 + h < kv.heads) {
-      const uint64_t u = kv_unit(kv, at.page, layer, values, h0 + h);
-      w[h] = *reinterpret_cast<const uint32_t*>(kv.codes + u * kv.unit_codes + word_offset<D>(values, at.slot, j));
-      d[h] = __half2float(kv.scales[u * kv.unit_scales + at.slot * (D / 32) + (j >> 2)]);
+      w[h] = *reinterpret_cast<const uint32_t*>(codes + static_cast<uint64_t>(h) * kv.unit_codes);
+      d[h] = __half2float(scales[static_cast<uint64_t>(h) * kv.unit_scales]);
     }
   }
+  // A pair of lanes has 16 channels; each store of the pair is 32 bytes of them, so
+  // a lane takes half of its own word's channels and half of its neighbour's.
+  const bool odd = j & 1;
+  float* const out = (values ? v : k) + (token * kv.heads + h0) * D + (j & ~1u) * 8 + (odd ? 4 : 0);
 #pragma unroll
   for (uint32_t h = 0; h < HT; ++h) {
     if (values) w[h] = transpose8(w[h], j & 7);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w[h], 1);
+    const uint32_t lo = (odd ? other : w[h]) >> (odd ? 16 : 0), hi = (odd ? w[h] : other) >> (odd ? 16 : 0);
     float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)                // 2^23 + code, exactly
-      o[i] = d[h] * (__uint_as_float(((w[h] >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f);
-    // a pair of lanes swaps halves, so that each store is 32 whole bytes of the pair
-    const bool odd = j & 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float give = odd ? o[i] : o[i + 4];
-      const float take = __shfl_xor_sync(0xffffffffu, give, 1);
-      if (odd) o[i] = take;
-      else o[i + 4] = take;
+    for (int i = 0; i < 4; ++i) {              // 2^23 + code, exactly
+      o[i] = d[h] * (__uint_as_float(((lo >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f);
+      o[i + 4] = d[h] * (__uint_as_float(((hi >> (4 * i)) & 15u) | 0x4b000000u) - 8388616.f);
     }
     if (!live || h0 + h >= kv.heads) continue;
-    float* const p = (values ? v : k) + (token * kv.heads + h0 + h) * D + (j & ~1u) * 8 + (odd ? 4 : 0);
-    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
-    __stcs(reinterpret_cast<float4*>(p + 8), make_float4(o[4], o[5], o[6], o[7]));
+    __stcs(reinterpret_cast<float4*>(out + h * D), make_float4(o[0], o[1], o[2], o[3]));
+    __stcs(reinterpret_cast<float4*>(out + h * D + 8), make_float4(o[4], o[5], o[6], o[7]));
   }
 }
 
-// Blocks of a launch, 0 where there are too many.
+// The launch's grid: tokens, K | V, heads in groups of HT.
 template <int D, uint32_t HT>
-uint32_t blocks_for(const KvDev& kv, uint32_t n_tokens) {
-  const uint64_t threads = static_cast<uint64_t>(n_tokens) * ((kv.heads + HT - 1) / HT) * (D / 8);
-  const uint64_t blocks = (threads + kThreads - 1) / kThreads;
-  return blocks <= 0x7fffffffu ? static_cast<uint32_t>(blocks) : 0u;
+dim3 grid_for(const KvDev& kv, uint32_t n_tokens) {
+  constexpr uint32_t kTokens = kThreads / (D / 8);
+  return dim3((n_tokens + kTokens - 1) / kTokens, 2, (kv.heads + HT - 1) / HT);
 }
 // Whether one head a thread leaves SMs idle or barely fills them.
 template <int D>
 bool few_tokens(const KvDev& kv, uint32_t n_tokens) {
-  return blocks_for<D, 1>(kv, n_tokens) <= 4 * kv_sm_count();
+  const dim3 g = grid_for<D, 1>(kv, n_tokens);
+  return static_cast<uint64_t>(g.x) * g.z <= 4 * kv_sm_count();
 }
 
 template <int D, bool BF16, uint32_t HT>
 cudaError_t append_heads(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                          uint32_t n_tokens, const void* k, const void* v, uint64_t ks, uint64_t vs, cudaStream_t st) {
-  const uint32_t blocks = blocks_for<D, HT>(kv, n_tokens);
-  if (!blocks) return cudaErrorInvalidConfiguration;
-  return launch_chained(k_kv_append<D, BF16, HT>, dim3(blocks, 2), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k,
+  return launch_chained(k_kv_append<D, BF16, HT>, grid_for<D, HT>(kv, n_tokens), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k,
                         v, ks, vs);
 }
 
@@ -199,9 +211,7 @@ cudaError_t append_dim(const KvDev& kv, uint32_t layer, const int32_t* seqs, con
 template <int D, uint32_t HT>
 cudaError_t read_heads(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                        uint32_t n_tokens, float* k, float* v, cudaStream_t st) {
-  const uint32_t blocks = blocks_for<D, HT>(kv, n_tokens);
-  if (!blocks) return cudaErrorInvalidConfiguration;
-  return launch_chained(k_kv_read<D, HT>, dim3(blocks, 2), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k, v);
+  return launch_chained(k_kv_read<D, HT>, grid_for<D, HT>(kv, n_tokens), kThreads, 0, st, kv, layer, seqs, off, n, n_tokens, k, v);
 }
 
 template <int D>

@@ -14,10 +14,10 @@ constexpr uint32_t kKvPartialRows = 16;      // query rows of one partial result
 
 // One fresh page of a fork or compaction: where its bytes come from.
 struct KvFresh {
-  int32_t src_page;   // fork: the page to copy; compaction: unused
+  const int32_t* row;   // compaction: the source's row
+  int32_t src_page;     // fork: the page to copy
   int32_t dst_page;
-  int32_t entry;
-  int32_t column;
+  int32_t first, count; // compaction: the page's tokens in the list of positions
 };
 
 // A cache as the kernels take it: ovl_kv's pointers, the parts of the
