@@ -504,8 +504,8 @@ ovl_status ovl_debug_inject(ovl_ctx* ctx, uint32_t phase, ovl_status code);
  *           the lowest 4 bits;
  *   values  8 tokens are [8][8 tokens][head_dim / 16 bytes]; unit (g, token)
  *           holds channels g, g + 8, g + 16, ..., the first in the lowest 4 bits.
- * head_dim: 64, 128 or 256.  page_tokens: 16, 32, 64, 128 or 256.  codes and
- * scales 16-byte aligned.  Offsets into the pools are 64-bit.
+ * head_dim: 64, 128 or 256.  page_tokens: 16, 32, 64, 128 or 256.  A page's
+ * codes, all layers, are below 2^31 bytes.  codes and scales 16-byte aligned.  Offsets into the pools are 64-bit.
  * A page that is not full belongs to one row only; full pages may be shared and
  * are never written.  ovl_kv_extend, ovl_kv_fork, ovl_kv_compact and
  * ovl_kv_release keep this, and take the lowest-numbered free pages first, in

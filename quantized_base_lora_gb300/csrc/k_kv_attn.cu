@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
   const uint64_t end = min(at + chunk, total);
 
   uint8_t* const my_ring = ring + warp * St::kWarpBytes;
-  uint32_t slot = 0;                          // of the ring, across segments
-  const float scale2 = a.scale * kLog2e;
+  uint32_t slot = 0;                          // of the ring, in bytes, across segments
+  const float scale2 = fabsf(a.scale) * kLog2e;   // the sign goes into q
   uint32_t magic;
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
@@ -215,12 +215,10 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
     const int32_t* const pages = kv.table + static_cast<size_t>(sp.length ? a.seqs[seq] : 0) * kv.max_pages;
     const int32_t token0 = a.off[seq];
 
-    // ---- what this warp's share of the run reads: page numbers 32 tiles ahead
-    const uint32_t n_mine = tile1 > tile0 + warp ? (tile1 - tile0 - warp + kWarps - 1) / kWarps : 0;
-    auto token_of = [&](uint32_t k) {         // first token of this warp's k-th tile
-      const uint32_t x = tile0 + warp + k * kWarps;
-      return (x < sp.lead ? x : x - sp.lead + sp.start) * kTile;
-    };
+    // ---- what this warp's share of the run reads: tiles x0, x0 + 4, ..; page numbers
+    // 32 of them ahead
+    const uint32_t x0 = tile0 + warp, skip = sp.start - sp.lead;
+    auto token_of = [&](uint32_t x) { return (x < sp.lead ? x : x + skip) * kTile; };
     // the page of a tile's first half and, where pages are 16 tokens, of its second
     bool lost = false;                        // a page that is not there: its tokens take no part
     auto page_at = [&](uint32_t tok) -> int32_t {
@@ -231,24 +229,25 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       lost = true;
       return -1;
     };
-    auto fetch_pages = [&](uint32_t k0, int32_t& p0, int32_t& p1) {
-      p0 = p1 = -1;
-      if (k0 + lane < n_mine) {
-        const uint32_t tok = token_of(k0 + lane);
-        p0 = page_at(tok);
-        p1 = kv.page == 16 ? page_at(tok + 16) : p0;
+    int32_t ids0, ids1;                       // of the next 32 tiles, one a lane
+    auto fetch_pages = [&](uint32_t x) {
+      x += lane * kWarps;
+      ids0 = ids1 = -1;
+      if (x < tile1) {
+        const uint32_t tok = token_of(x);
+        ids0 = page_at(tok);
+        ids1 = kv.page == 16 ? page_at(tok + 16) : ids0;
       }
       lost = __any_sync(0xffffffffu, lost);
     };
-    int32_t ids0, ids1;                       // of tiles 32 * (k / 32) + lane
-    fetch_pages(0, ids0, ids1);
+    fetch_pages(x0);
     // A tile's copies, in runs of 512 bytes by the whole warp: key codes, value
     // codes (16 bytes a lane and run), then both scale arrays together.
-    const uint64_t page_codes = static_cast<uint64_t>(kv.unit_codes) * kv.layers * 2 * kv.heads;
-    const uint64_t page_scales = static_cast<uint64_t>(kv.unit_scales) * 2 * kv.layers * 2 * kv.heads;
+    const uint32_t page_codes = kv.unit_codes * kv.layers * 2 * kv.heads;    // a page is below 2^31 bytes
+    const uint32_t page_scales = page_codes / 8;
     const uint64_t unit = kv_unit(kv, 0, a.layer, 0, kh);
     const uint8_t* const k_from = kv.codes + unit * kv.unit_codes + lane * 16;
-    const uint32_t to_values = kv.heads * kv.unit_codes;                     // < 2^32: both below 2^16
+    const uint32_t to_values = kv.heads * kv.unit_codes;
     constexpr uint32_t kScaleLanes = St::kScales / 16 < 16 ? St::kScales / 16 : 16;   // lanes on one array
     const bool v_lane = lane >= kScaleLanes;
     const uint8_t* const s_from = reinterpret_cast<const uint8_t*>(kv.scales) +
@@ -258,30 +257,31 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
                             St::kScales <= 256;                              // this lane's scales are of tokens 16 ..
     const uint32_t my_ring32 = smem_u32(my_ring) + lane * 16;
     const uint32_t s_to = 2 * St::kCodes + (v_lane ? St::kScales - kScaleLanes * 16 : 0);
-    auto issue = [&](uint32_t k, int32_t p0, int32_t p1, uint32_t sl) {
-      const uint32_t in_page = token_of(k) & (kv.page - 1);
-      const uint32_t dst = my_ring32 + sl * St::kBytes;
+    auto issue = [&](uint32_t x, uint32_t lane_of, uint32_t dst) {
+      const int32_t p0 = __shfl_sync(0xffffffffu, ids0, lane_of);
       constexpr uint32_t kRuns = St::kCodes / 512;
       if (kv.page != 16) {
         if (p0 >= 0) {
-          const uint8_t* const from = k_from + p0 * page_codes + in_page * (D / 2);
+          const uint32_t in_page = token_of(x) & (kv.page - 1);
+          const uint8_t* const from = k_from + wide(p0, page_codes) + in_page * (D / 2);
           const uint8_t* const from_v = from + to_values;
 #pragma unroll
           for (uint32_t i = 0; i < kRuns; ++i) cp16(dst + i * 512, from + i * 512);
 #pragma unroll
           for (uint32_t i = 0; i < kRuns; ++i) cp16(dst + St::kCodes + i * 512, from_v + i * 512);
-          const uint8_t* const from_s = s_from + p0 * page_scales + in_page * (NB * 2);
+          const uint8_t* const from_s = s_from + wide(p0, page_scales) + in_page * (NB * 2);
           if (lane < 2 * kScaleLanes)
 #pragma unroll
             for (uint32_t i = 0; i < (St::kScales + 255) / 256; ++i) cp16(dst + s_to + i * 256, from_s + i * 256);
         }
       } else {
         // two pages of 16 tokens: the halves of every array have a page each
+        const int32_t p1 = __shfl_sync(0xffffffffu, ids1, lane_of);
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
           const int32_t p = h ? p1 : p0;
           if (p < 0) continue;
-          const uint8_t* const from = k_from + p * page_codes;
+          const uint8_t* const from = k_from + wide(p, page_codes);
           const uint8_t* const from_v = from + to_values;
           if (kRuns > 1 || lane < 16)
 #pragma unroll
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
               cp16(dst + h * (St::kCodes / 2) + i * 512, from + i * 512);
               cp16(dst + St::kCodes + h * (St::kCodes / 2) + i * 512, from_v + i * 512);
             }
-          const uint8_t* const from_s = s_from + p * page_scales - (h ? St::kScales / 2 : 0);
+          const uint8_t* const from_s = s_from + wide(p, page_scales) - (h ? St::kScales / 2 : 0);
           if (lane < 2 * kScaleLanes) {
             if constexpr (St::kScales <= 256) {
               if (s_half == h) cp16(dst + s_to, from_s);
@@ -300,20 +300,21 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         }
       }
     };
-    uint32_t sent = 0, sent_slot = slot;
+    uint32_t ahead = x0, ahead_of = 0;        // the next tile to request, and its number
+    {
+      uint32_t at_slot = slot;
 #pragma unroll 1
-    for (; sent < St::kRing; ++sent) {
-      if (sent < n_mine)
-        issue(sent, __shfl_sync(0xffffffffu, ids0, sent), __shfl_sync(0xffffffffu, ids1, sent), sent_slot);
-      cp_async_commit();
-      sent_slot = sent_slot + 1 == St::kRing ? 0 : sent_slot + 1;
+      for (; ahead_of < St::kRing; ++ahead_of, ahead += kWarps) {
+        if (ahead < tile1) issue(ahead, ahead_of, my_ring32 + at_slot);
+        cp_async_commit();
+        at_slot = at_slot + St::kBytes == St::kWarpBytes ? 0 : at_slot + St::kBytes;
+      }
     }
 
     // ---- the rows: q as the MMA's second operand, and where each column looks
     uint32_t qf[NT][NS][NB][4];
     uint32_t qs[NT][2];                       // bf16 calls: the constants' share, B operand against the key scales
     float to_log2[NT][2];                     // scale, log2(e) and the row's power of two
-    int32_t last[NT][2], from[NT][2];         // a column sees tokens <= last and (>= from or < sinks)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint32_t r = nt * 8 + g;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       // keep the constants' share inside f16, f32 calls the second part's small end.
       constexpr uint32_t kUp = BF16 ? 0 : 9;
       const uint32_t ex = min(max(__float_as_uint(top) >> 23, kUp + 1), 253u);
-      const float up = __uint_as_float((254u + kUp - ex) << 23), down = __uint_as_float((ex - kUp) << 23);
+      const float up = copysignf(__uint_as_float((254u + kUp - ex) << 23), a.scale), down = __uint_as_float((ex - kUp) << 23);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float even = 0.f, odd = 0.f;
@@ -390,12 +391,6 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       }
       to_log2[nt][0] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t);
       to_log2[nt][1] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t c = nt * 8 + 2 * t + e, i = (r0 + c) / rows_group;
-        last[nt][e] = c < n_rows && i < a.max_new && sp.length ? sp.first + static_cast<int32_t>(i) : -1;
-        from[nt][e] = a.window ? last[nt][e] - static_cast<int32_t>(a.window) + 1 : 0;
-      }
     }
     // tiles that every row sees whole need no mask
     const uint32_t i0 = r0 / rows_group, i1 = (r0 + n_rows - 1) / rows_group;
@@ -413,16 +408,14 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
     }
 
     // ---- the tiles
-    int32_t cur0 = ids0, cur1 = ids1;         // page numbers of the tiles being read
 #pragma unroll 1
-    for (uint32_t k = 0; k < n_mine; ++k) {
-      if (k && (k & 31) == 0) cur0 = ids0, cur1 = ids1;
-      const int32_t tok = static_cast<int32_t>(token_of(k));
+    for (uint32_t x = x0; x < tile1; x += kWarps) {
+      const int32_t tok = static_cast<int32_t>(token_of(x));
       cp_async_wait<St::kRing - 1>();
       __syncwarp();
-      const uint8_t* const st = my_ring + slot * St::kBytes;
-      const bool hidden = tok + static_cast<int32_t>(kTile) - 1 > all_last || lost ||
-                          !(tok >= all_from || tok + static_cast<int32_t>(kTile) <= sinks);
+      const uint8_t* const st = my_ring + slot;
+      const bool hidden = tok > all_last - static_cast<int32_t>(kTile - 1) || lost ||
+                          (tok < all_from && tok > sinks - static_cast<int32_t>(kTile));
 
       // Two copies of the tile's code: tiles that need no mask take no part of it.
       auto tile = [&](auto with_mask) {
@@ -475,10 +468,13 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       // leaves for p: p dV < 2^9 (2^15 where the reference trails), and where p itself is
       // rounded to f16, p too
       const uint8_t* const vd = st + 2 * St::kCodes + St::kScales;
-      bool held0 = true, held1 = true;
-      if constexpr (masked) {
-        held0 = __shfl_sync(0xffffffffu, cur0, k & 31) >= 0;
-        held1 = __shfl_sync(0xffffffffu, cur1, k & 31) >= 0;
+      bool held0 = true, held1 = true;        // the tile's halves have a page
+      if (masked && lost) {
+        auto there = [&](uint32_t t0) {
+          return t0 < static_cast<uint32_t>(sp.length) &&
+                 static_cast<uint32_t>(pages[t0 >> kv.page_shift]) < kv.n_pages;
+        };
+        held0 = there(tok), held1 = there(tok + 16);
       }
       auto written = [&](uint32_t j) {        // token j of the tile holds data
         return tok + static_cast<int32_t>(j) < sp.length && (j < 16 ? held0 : held1);
@@ -492,24 +488,27 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         for (int i = 1; i < NB / 2; ++i) vmax = __vmaxu2(vmax, v[i]);
         vmax = max(vmax & 0xffffu, vmax >> 16);
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[sub][nt][i] *= to_log2[nt][i & 1];
+      uint32_t seen = 0;                      // a bit for each of this lane's scores
       if constexpr (masked) {
         if (!written(lane)) vmax = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int sub = 0; sub < 2; ++sub)
+          for (int e = 0; e < 2; ++e) {
+            // the column's row sees tokens <= last and (>= from or < sinks)
+            const uint32_t c = nt * 8 + 2 * t + e, i = (r0 + c) / rows_group;
+            const int32_t last = c < n_rows && i < a.max_new && sp.length ? sp.first + static_cast<int32_t>(i) : -1;
+            const int32_t from = a.window ? last - static_cast<int32_t>(a.window) + 1 : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int32_t j = tok + 16 * sub + static_cast<int32_t>(g) + (i & 2 ? 8 : 0);
-              const bool sees = j <= last[nt][i & 1] && (j >= from[nt][i & 1] || j < sinks) && (sub ? held1 : held0);
-              if (!sees) s[sub][nt][i] = -CUDART_INF_F;
-            }
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int32_t j = tok + 16 * sub + 8 * h + static_cast<int32_t>(g);
+                const bool sees = j <= last && (j >= from || j < sinks) && (sub ? held1 : held0);
+                if (sees) seen |= 1u << (nt * 8 + sub * 4 + e + 2 * h);
+                else s[sub][nt][e + 2 * h] = -CUDART_INF_F;
+              }
+          }
       }
       const int32_t top_exp = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, vmax) >> 10) - 14;
       const float above = static_cast<float>((BF16 ? max(top_exp, 0) : top_exp) - 9);
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(m[nt][e], x + above);
+          x = fmaxf(m[nt][e], fmaf(x, to_log2[nt][e], above));
           grew |= x > m[nt][e] + kLag;
           ref[nt][e] = x;
         }
@@ -543,11 +542,15 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float r = m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];   // nothing seen yet: every weight is 0
+          const float r = masked && m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];   // nothing seen yet: every weight is 0
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub) {
-            s[sub][nt][e] = ex2(s[sub][nt][e] - r);
-            s[sub][nt][e + 2] = ex2(s[sub][nt][e + 2] - r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& w = s[sub][nt][e + 2 * h];
+              w = ex2(fmaf(w, to_log2[nt][e], -r));
+              if (masked && !(seen >> (nt * 8 + sub * 4 + e + 2 * h) & 1u)) w = 0.f;   // -inf times a scale of 0
+            }
             l[nt][e] += s[sub][nt][e] + s[sub][nt][e + 2];
           }
         }
@@ -611,14 +614,14 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
       // this slot is read: refill it
       __syncwarp();
-      if (sent < n_mine) {
-        if ((sent & 31) == 0) fetch_pages(sent, ids0, ids1);
-        const int32_t p0 = __shfl_sync(0xffffffffu, ids0, sent & 31);
-        issue(sent, p0, kv.page == 16 ? __shfl_sync(0xffffffffu, ids1, sent & 31) : p0, slot);
-        ++sent;
+      if (ahead < tile1) {
+        if ((ahead_of & 31) == 0) fetch_pages(ahead);
+        issue(ahead, ahead_of & 31, my_ring32 + slot);
+        ++ahead_of;
+        ahead += kWarps;
       }
       cp_async_commit();
-      if (++slot == St::kRing) slot = 0;
+      slot = slot + St::kBytes == St::kWarpBytes ? 0 : slot + St::kBytes;
     }
 
     // ---- the warps' results into shared memory (each over its own ring, which is drained)

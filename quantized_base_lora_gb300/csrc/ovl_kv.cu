@@ -53,6 +53,8 @@ ovl_status check_dims(const ovl_kv* kv) {
   if (!kv->n_pages || kv->n_pages > 0x7fffffffu / 16 || !kv->n_layers || kv->n_layers > 65535 || !kv->n_kv_heads ||
       kv->n_kv_heads > 65535)
     return fail(OVL_E_SHAPE, "n_pages, n_layers or n_kv_heads out of range");
+  if (static_cast<uint64_t>(kv->n_layers) * kv->n_kv_heads * p * d >= (1ull << 31))
+    return fail(OVL_E_SHAPE, "the codes of a page, all layers, must be below 2^31 bytes");
   if (!kv->max_seqs || kv->max_seqs > kKvMaxSeqs) return fail(OVL_E_SHAPE, "max_seqs must be 1..65536");
   if (!kv->max_pages || static_cast<uint64_t>(kv->max_pages) * p > 0x3fffffffu)
     return fail(OVL_E_SHAPE, "max_pages * page_tokens must be 1..2^30 - 1");
