@@ -684,16 +684,16 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       }
     }
     if (!whole) {
-      __threadfence();
+      // The barrier orders the CTA's stores before its one arrival, which releases
+      // them; the last arrival acquires all.
       __syncthreads();
       if (tid == 0) {
-        const uint32_t seen = atomicAdd(kv.joined + c0, 1u);
-        s_last = seen == c1 - c0;
+        const uint32_t arrived = arrive_acq_rel(kv.joined + c0);
+        s_last = arrived == c1 - c0;
         if (s_last) kv.joined[c0] = 0;        // for the next call
       }
       __syncthreads();
       if (s_last) {
-        __threadfence();
         for (uint32_t i = tid; i < n_rows * (D / 4); i += kThreads) {
           const uint32_t r = i / (D / 4), c = i % (D / 4) * 4;
           float top = -CUDART_INF_F;

@@ -88,6 +88,13 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t magic, uint32_t (&x)[
   }
 }
 
+// Adds 1, returns what was there; releases and acquires at the GPU's scope.
+__device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t* p) {
+  uint32_t v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // a * b in 64 bits, one instruction.
 __device__ __forceinline__ uint64_t wide(uint32_t a, uint32_t b) {
   uint64_t r;
