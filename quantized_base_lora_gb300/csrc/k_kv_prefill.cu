@@ -99,6 +99,17 @@ __device__ __forceinline__ void landed(uint32_t* r) {
                    "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -238,15 +249,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   tc_fence_after();
   const uint32_t taddr = bar.taddr;
   bool dead = false;                           // a bounded wait ran out: leave
-  auto wait_one = [&](uint64_t* b, uint32_t parity) {
-    if (!mbar_wait_bounded(b, parity)) {
-      dead = true;
-      kv_latch(kv, OVL_E_DEVICE_TIMEOUT);
-    }
-  };
   auto wait = [&](uint64_t* b, uint32_t parity) {    // a whole warp: all of it leaves together
-    wait_one(b, parity);
-    dead = __any_sync(0xffffffffu, dead);
+    const bool landed = mbar_wait_spin(b, parity);
+    if (!__all_sync(0xffffffffu, landed)) {
+      dead = true;
+      if (lane == 0) kv_latch(kv, OVL_E_DEVICE_TIMEOUT);
+    }
   };
 
   if (warp < Sh::kSoft) {
@@ -568,43 +576,52 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   } else {
     // ================= issue: one thread for each row tile
     if constexpr (RT == 2) fewer_registers<40>();
-    if (lane == 0 && warp - Sh::kSoft - 4 < RT) {
-    const uint32_t x = warp - Sh::kSoft - 4;
-    constexpr uint32_t kF32 = 1u << 4;         // accumulators; both operands f16
-    constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((128u >> 4) << 24);
-    const uint64_t q_desc = sdesc_sw128(smem_u32(sm_q + x * Sh::kQ));
-    const uint64_t k_desc = sdesc_sw128(smem_u32(sm_k)), v_desc = sdesc_sw128(smem_u32(sm_v));
-    const uint32_t s_at = taddr + x * KT, o_at = taddr + Sh::kOutCol + x * D;
-    if (tl.count) wait_one(&bar.q_ready, 0);
+    // The whole warp walks the loop and one elected thread issues: descriptors stay in
+    // uniform registers, which the MMA instruction takes its operands from.
+    const uint32_t x = __shfl_sync(0xffffffffu, warp, 0) - Sh::kSoft - 4;
+    if (x < RT) {
+      constexpr uint32_t kF32 = 1u << 4;       // accumulators; both operands f16
+      constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((128u >> 4) << 24);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sm_q) + x * Sh::kQ);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sm_k)), v_desc = sdesc_sw128(smem_u32(sm_v));
+      const uint32_t s_at = taddr + x * KT, o_at = taddr + Sh::kOutCol + x * D;
+      if (tl.count) wait(&bar.q_ready, 0);
 #pragma unroll 1
-    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-      const uint32_t parity = (j >> 1) & 1, b = j & 1;
-      wait_one(&bar.k_full[b], parity);
-      if (dead) break;
-      tc_fence_after();
+      for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+        const uint32_t parity = (j >> 1) & 1, b = j & 1;
+        wait(&bar.k_full[b], parity);
+        if (dead) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-      for (uint32_t k = 0; k < D / 16; ++k)    // 64 channels a region of 128-byte rows
-        umma_f16(s_at, q_desc + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
-                 k_desc + b * (Sh::kBuf / 16) + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), kQK, k != 0);
-      umma_commit(&bar.k_empty[b]);
-      umma_commit(&bar.s_full[x]);
-      wait_one(&bar.v_full[b], parity);
-      wait_one(&bar.p_full[x], j & 1);
-      if (dead) break;
-      tc_fence_after();
+          for (uint32_t k = 0; k < D / 16; ++k)   // 64 channels a region of 128-byte rows
+            umma_f16(s_at, q_desc + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                     k_desc + b * (Sh::kBuf / 16) + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), kQK, k != 0);
+          umma_commit(&bar.s_full[x]);
+          umma_commit(&bar.k_empty[b]);
+        }
+        __syncwarp();
+        wait(&bar.v_full[b], parity);
+        wait(&bar.p_full[x], j & 1);
+        if (dead) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-      for (uint32_t k = 0; k < KT / 16; ++k)   // 64 tokens a region
-        umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
-                    (j | k) != 0);
-      umma_commit(&bar.v_empty[b]);
-    }
-    // nothing of this CTA may still run when its tensor memory goes
-    if (tl.count) {
-      umma_commit(&bar.o_done[x]);
-      wait_one(&bar.o_done[x], 0);
-    }
-    tc_fence_before();
+          for (uint32_t k = 0; k < KT / 16; ++k)  // 64 tokens a region
+            umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
+                        (j | k) != 0);
+          umma_commit(&bar.v_empty[b]);
+        }
+        __syncwarp();
+      }
+      // nothing of this CTA may still run when its tensor memory goes
+      if (tl.count) {
+        if (elect_one()) umma_commit(&bar.o_done[x]);
+        __syncwarp();
+        wait(&bar.o_done[x], 0);
+      }
+      tc_fence_before();
     }
   }
   __syncwarp();
