@@ -8,14 +8,15 @@
 //   S = Q K^T   Q and K in shared memory, S in tensor memory
 //   O += P V    P over S's own columns in tensor memory, V^T in shared memory
 // so the scores never leave the SM.  Roles, each its own warps:
-//   softmax   4 warps for each 128 rows, a thread a row: S -> P, running maximum
-//             and sum in registers; O is rescaled in place, only when a row's
-//             maximum has grown by more than 2^6 since its reference was set
-//   cache     4 warps, keys and values in turn: 4-bit words from global memory, one
-//             mask a pair of codes, times the block's scale, into the MMA's shared
-//             layout; two buffers each; the next words are in flight meanwhile
-//   issue     one thread for each 128 rows.  The two row tiles run against each
-//             other: the MMAs of one overlap the softmax of the other.
+//   softmax   4 warps for each 128 rows, a thread a row: S -> P in registers, running
+//             maximum and sum; O is rescaled in place, only when a row's maximum
+//             has grown by more than 2^6 since its reference was set
+//   keys, values   4 warps each: 4-bit words from global memory, one mask a pair
+//             of codes, times the block's scale, into the MMA's shared layout;
+//             two buffers each; the next words are in flight meanwhile
+//   issue     one warp for each 128 rows.  The two row tiles run against each
+//             other: the MMAs of one overlap the softmax of the other; and P goes
+//             over in two halves, so that O's MMAs start with the first.
 //
 // Layout.  A 32-bit key word is 8 consecutive channels of a token, which is one
 // 16-byte chunk of the f16 operand; its codes come out in the order 0 4 1 5 2 6 3
@@ -51,14 +52,14 @@ struct Shape {
   static constexpr uint32_t kBuf = kTokens * D * 2;            // bytes of a K or V buffer
   static constexpr uint32_t kSmem = kRowTiles * kQ + 4 * kBuf;
   static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
-  static constexpr uint32_t kWarps = kSoft + 8;                // softmax, 4 cache, 4 issue (1 or 2 of them busy)
+  static constexpr uint32_t kWarps = kSoft + 12;               // softmax, 4 keys, 4 values, 4 issue (1 or 2 of them busy)
   static constexpr uint32_t kThreads = kWarps * 32;
-  static constexpr uint32_t kOutCol = kRowTiles * kTokens;     // first tensor memory column of O
+  static constexpr uint32_t kOutCol = kRowTiles * kTokens;     // first tensor memory column of O, behind S
   static_assert(kOutCol + kRowTiles * D <= kTmemCols, "S and O fit");
 };
 
 struct Bars {
-  uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2];   // p_full: [row tile][half of the tile's tokens]
   float k_exp[4], v_exp[4];      // 2^E of the last tiles' scales as E
   uint32_t taddr;
 };
@@ -88,6 +89,15 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 // Loads in flight have landed: the registers may be used from here on.
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -151,7 +161,8 @@ struct Tiles {
   }
 };
 
-// The page numbers of a tile's tokens 32 k + lane, -1 beyond the row's length.
+// What the table says of a tile's tokens 32 k + lane, -1 beyond the row's length;
+// judged when it is used, a tile later, so that nothing waits for it here.
 template <int N>
 __device__ __forceinline__ void tile_pages(const KvDev& kv, const int32_t* row, uint32_t length, uint32_t tok,
                                            uint32_t lane, int32_t (&p)[N]) {
@@ -159,11 +170,7 @@ __device__ __forceinline__ void tile_pages(const KvDev& kv, const int32_t* row, 
   for (int k = 0; k < N; ++k) {
     const uint32_t t = tok + 32 * k + lane;
     p[k] = -1;
-    if (t < length) {
-      const int32_t x = __ldg(row + (t >> kv.page_shift));
-      if (static_cast<uint32_t>(x) < kv.n_pages) p[k] = x;
-      else kv_latch(kv, OVL_E_ARG);
-    }
+    if (t < length) p[k] = __ldg(row + (t >> kv.page_shift));
   }
 }
 
@@ -239,7 +246,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       mbar_init(&bar.k_empty[i], RT);
       mbar_init(&bar.v_empty[i], RT);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.p_full[i][0], 4);
+      mbar_init(&bar.p_full[i][1], 4);
       mbar_init(&bar.o_done[i], 1);
     }
     mbar_fence_init();
@@ -248,9 +256,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   __syncthreads();
   tc_fence_after();
   const uint32_t taddr = bar.taddr;
-  bool dead = false;                           // a bounded wait ran out: leave
-  auto wait = [&](uint64_t* b, uint32_t parity) {    // a whole warp: all of it leaves together
-    const bool landed = mbar_wait_spin(b, parity);
+  bool dead = false;                           // a bounded wait ran out
+  // A whole warp waits.  After one wait has run out its others return at once: every
+  // role walks its loop to the end, so no barrier between warps is left half full.
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (dead) return;
+    const bool landed = warp >= Sh::kSoft + 8 ? mbar_wait_spin(b, parity) : mbar_wait_bounded(b, parity);
     if (!__all_sync(0xffffffffu, landed)) {
       dead = true;
       if (lane == 0) kv_latch(kv, OVL_E_DEVICE_TIMEOUT);
@@ -259,18 +270,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
 
   if (warp < Sh::kSoft) {
     // ================= softmax: one row a thread
-    if constexpr (RT == 2) more_registers<168>();
+    if constexpr (RT == 2) more_registers<160>();
     const uint32_t x = warp >> 2, r = tid & 127;
     const uint32_t row = r0 + x * 128 + r;
     const bool on = x * 128 + r < n_rows;
     const uint32_t i = row / group;
-    const uint64_t q_at = static_cast<uint64_t>(o0 + i) * a.q_stride + (kh * group + row % group) * D;
     float down = 0.f;
     {
+      const uint64_t q_at = static_cast<uint64_t>(o0 + i) * a.q_stride + (kh * group + row % group) * D;
       const uint4* const src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (on ? q_at : 0));
       float top = 0.f;
       if (on) {
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t c = 0; c < D / 8; ++c) {
           const uint4 v = __ldg(src + c);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -284,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       const float up = copysignf(__uint_as_float((263u - ex) << 23), a.scale);
       down = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((ex - 9u) << 23);
       uint8_t* const dst = sm_q + x * Sh::kQ + r * 128;
-#pragma unroll 4
+#pragma unroll 8
       for (uint32_t c = 0; c < D / 8; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (on) v = __ldg(src + c);
@@ -312,10 +323,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
     const uint32_t s_at = taddr + lanes + x * KT, o_at = taddr + lanes + Sh::kOutCol + x * D;
     float ref = -CUDART_INF_F, l = 0.f;
 #pragma unroll 1
-    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+    for (uint32_t j = 0; j < tl.count; ++j) {
       const int32_t tok = static_cast<int32_t>(tl.token(j, KT));
-      const bool hidden = tok + static_cast<int32_t>(KT) - 1 > all_last ||
-                          !(tok >= all_from || tok + static_cast<int32_t>(KT) <= sinks);
+      const bool hidden = tok > all_last - static_cast<int32_t>(KT - 1) ||
+                          (tok < all_from && tok > sinks - static_cast<int32_t>(KT));
       wait(&bar.v_full[j & 1], (j >> 1) & 1);  // the tile's value exponent
       wait(&bar.s_full[x], j & 1);
       tc_fence_after();
@@ -355,14 +366,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
           const float f = ref == -CUDART_INF_F ? 0.f : ex2(ref - next);
           ref = next;
           l *= f;
-          if (j) {
+          if (j) {                             // S of this tile was issued behind O of the last
 #pragma unroll 1
-            for (uint32_t c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + c, o);
+            for (uint32_t c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
 #pragma unroll
-              for (uint32_t k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32_async(o_at + c, o);
+              for (uint32_t k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16_async(o_at + c, o);
             }
           }
         }
@@ -387,6 +398,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
             p[k / 2] = pack_f16(u, v);
           }
           tmem_st16_async(s_at + c / 2, p);
+          if (c + 32 == KT / 2) {              // the first half may go ahead
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[x][0]);
+          }
         }
         const float2 total = both(add2(sum0, sum1));
         l = fmaf(total.x + total.y, exp2f(-ve), l);
@@ -396,7 +413,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[x]);
+      if (lane == 0) mbar_arrive(&bar.p_full[x][1]);
     }
     if (tl.count) wait(&bar.o_done[x], 0);
     tc_fence_after();
@@ -427,100 +444,84 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       }
     }
     tc_fence_before();
-  } else if (warp < Sh::kSoft + 4) {
-    // ================= cache
-    if constexpr (RT == 2) more_registers<136>();
+  } else if (warp < Sh::kSoft + 8) {
+    if constexpr (RT == 2) fewer_registers<64>();
     constexpr int IT = KT / 32;
     constexpr uint32_t NW = NB / 2;            // scale words of a token
-    constexpr uint32_t WT = D == 64 ? 1 : 2;   // words of a token's value unit that a thread takes
-    const uint32_t w4 = warp - Sh::kSoft;
-    // keys: tokens 32 k + 8 w4 + lane % 8, words lane / 8 of every block
-    const uint32_t k_lane = w4 * 8 + (lane & 7), part = lane >> 3;
-    // values: the 8 tokens from 32 k_of + 8 (lane / 8), unit g; D = 256: half of it
-    const uint32_t half = D == 256 ? w4 >> 1 : 0, k_of = D == 256 ? w4 & 1 : w4;
-    const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
-    const uint64_t unit = kv_unit(kv, 0, a.layer, 0, kh), page_units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
-    const uint64_t page_codes = page_units * kv.unit_codes, page_scales = page_units * kv.unit_scales;
-    const uint8_t* const k_codes = kv.codes + unit * kv.unit_codes + part * (D / 8);
-    const __half* const k_scales = kv.scales + unit * kv.unit_scales;
-    const uint8_t* const v_codes = kv.codes + (unit + kv.heads) * kv.unit_codes + g * (D / 2) + half * 8;
-    const __half* const v_scales = kv.scales + (unit + kv.heads) * kv.unit_scales;
+    const uint32_t w4 = warp & 3;
+    const bool values = warp >= Sh::kSoft + 4;
+    const uint64_t unit = kv_unit(kv, 0, a.layer, values, kh);
+    const uint32_t page_codes = kv.unit_codes * kv.layers * 2 * kv.heads, page_scales = page_codes / 16;
+    const uint8_t* const codes = kv.codes + unit * kv.unit_codes;
+    const __half* const scales = kv.scales + unit * kv.unit_scales;
     uint32_t magic;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    uint32_t kw[IT][NB], ks[IT * NW];          // keys: words; scales of tokens 32 k + lane
-    uint32_t vw[8][WT], vo[8][WT], vs[IT * NW];   // values: words; scales of this thread's; of tokens 32 k + lane
+    // 2^-e as f16, |e| <= 16: exact, at the far end as a subnormal
+    auto down_by = [](int32_t e) { return __half2half2(__float2half_rn(__int_as_float((127 - e) << 23))); };
     int32_t pages[IT];                         // of tokens 32 k + lane of the next tile to load
-    auto load_keys = [&](uint32_t tok) {
-#pragma unroll
-      for (int k = 0; k < IT; ++k) {
-        const uint32_t t = tok + 32 * k + lane, u = tok + 32 * k + k_lane;
-#pragma unroll
-        for (uint32_t i = 0; i < NW; ++i) ks[k * NW + i] = 0;
-        if (pages[k] >= 0) ldg<NW>(k_scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &ks[k * NW]);
-        const int32_t p = __shfl_sync(0xffffffffu, pages[k], k_lane);
-#pragma unroll
-        for (uint32_t i = 0; i < NB; ++i) kw[k][i] = 0x88888888u;
-        if (p >= 0) ldg<NB>(k_codes + p * page_codes + (u & (kv.page - 1)) * (D / 2), kw[k]);
-      }
-    };
-    auto load_values = [&](uint32_t tok) {
+    uint32_t sc[IT * NW];                      // scales of tokens 32 k + lane; 0 for tokens never written
+    auto load_scales = [&](uint32_t tok) {
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
         const uint32_t t = tok + 32 * k + lane;
-#pragma unroll
-        for (uint32_t i = 0; i < NW; ++i) vs[k * NW + i] = 0;
-        if (pages[k] >= 0) ldg<NW>(v_scales + pages[k] * page_scales + (t & (kv.page - 1)) * NB, &vs[k * NW]);
-      }
-      int32_t mine = pages[0];
-#pragma unroll
-      for (int k = 1; k < IT; ++k) mine = k_of == static_cast<uint32_t>(k) ? pages[k] : mine;
-      const int32_t p = __shfl_sync(0xffffffffu, mine, lane & 24);
-      const uint32_t slot = (tok + grp * 8) & (kv.page - 1);
-#pragma unroll
-      for (uint32_t t = 0; t < 8; ++t)
-#pragma unroll
-        for (uint32_t i = 0; i < WT; ++i) vw[t][i] = 0x88888888u, vo[t][i] = 0u;
-      if (p >= 0) {
-        const uint8_t* const from = v_codes + p * page_codes + slot * (D / 2);
-        const __half* const from_s = v_scales + p * page_scales + slot * NB + half * 4;
-        if constexpr (D == 256) {
-#pragma unroll
-          for (uint32_t t = 0; t < 8; ++t) ldg<2>(from + t * 16, vw[t]), ldg<2>(from_s + t * NB, vo[t]);
-        } else {
-          uint32_t w[8 * WT], s[8 * WT];
-          ldg<8 * WT>(from, w);
-          ldg<8 * WT>(from_s, s);
-#pragma unroll
-          for (uint32_t t = 0; t < 8; ++t)
-#pragma unroll
-            for (uint32_t i = 0; i < WT; ++i) vw[t][i] = w[t * WT + i], vo[t][i] = s[t * WT + i];
+        if (static_cast<uint32_t>(pages[k]) >= kv.n_pages) {
+          if (t < static_cast<uint32_t>(length)) kv_latch(kv, OVL_E_ARG);
+          pages[k] = -1;
         }
+#pragma unroll
+        for (uint32_t i = 0; i < NW; ++i) sc[k * NW + i] = 0;
+        if (pages[k] >= 0) ldg<NW>(scales + wide(pages[k], page_scales) + (t & (kv.page - 1)) * NB, &sc[k * NW]);
       }
     };
-    // 2^-e as f16, |e| <= 16: exact, at the far end as a subnormal
-    auto down_by = [](int32_t e) { return __half2half2(__float2half_rn(__int_as_float((127 - e) << 23))); };
-    if (tl.count) {
-      tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
-      load_keys(tl.token(0, KT));
-    }
-#pragma unroll 1
-    for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-      const uint32_t tok = tl.token(j, KT), b = j & 1;
-      load_values(tok);
-      if (j + 1 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 1, KT), lane, pages);
-      {
-        const int32_t e = exponent_above(ks);
-        const __half2 down = down_by(e);
+    // The exponent above the tile's scales, which are multiplied by 2^-it.
+    auto settle = [&] {
+      const int32_t e = exponent_above(sc);
+      const __half2 down = down_by(e);
 #pragma unroll
-        for (uint32_t i = 0; i < IT * NW; ++i) ks[i] = mul_f16x2(ks[i], down);
+      for (uint32_t i = 0; i < IT * NW; ++i) sc[i] = mul_f16x2(sc[i], down);
+      return e;
+    };
+    // Words are requested behind the conversion of the ones before, page numbers a tile
+    // earlier.
+    auto first = [&](auto load) {
+      if (tl.count) {
+        tile_pages<IT>(kv, table_row, length, tl.token(0, KT), lane, pages);
+        load(tl.token(0, KT));
+      }
+      if (tl.count > 1) tile_pages<IT>(kv, table_row, length, tl.token(1, KT), lane, pages);
+    };
+    auto next = [&](uint32_t j, auto load) {
+      if (j + 1 < tl.count) load(tl.token(j + 1, KT));
+      if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
+    };
+    if (!values) {
+      // ================= keys: tokens 32 k + 8 w4 + lane % 8, words lane / 8 of every block
+      const uint32_t from = w4 * 8 + (lane & 7), part = lane >> 3;
+      uint32_t kw[IT][NB];
+      auto load = [&](uint32_t tok) {
+        load_scales(tok);
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+          const uint32_t u = tok + 32 * k + from;
+          const int32_t p = __shfl_sync(0xffffffffu, pages[k], from);
+#pragma unroll
+          for (uint32_t i = 0; i < NB; ++i) kw[k][i] = 0x88888888u;
+          if (p >= 0) ldg<NB>(codes + wide(p, page_codes) + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), kw[k]);
+        }
+      };
+      first(load);
+#pragma unroll 1
+      for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+        const uint32_t b = j & 1;
+        const int32_t e = settle();
         if (j > 1) wait(&bar.k_empty[b], ((j >> 1) - 1) & 1);
-        if (tid == Sh::kSoft * 32) bar.k_exp[j & 3] = static_cast<float>(e);
-        uint8_t* const buf = sm_k + b * Sh::kBuf + k_lane * 128;
+        if (w4 == 0 && lane == 0) bar.k_exp[j & 3] = static_cast<float>(e);
+        uint8_t* const buf = sm_k + b * Sh::kBuf + from * 128;
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
           uint32_t d[NW];
 #pragma unroll
-          for (uint32_t i = 0; i < NW; ++i) d[i] = __shfl_sync(0xffffffffu, ks[k * NW + i], k_lane);
+          for (uint32_t i = 0; i < NW; ++i) d[i] = __shfl_sync(0xffffffffu, sc[k * NW + i], from);
 #pragma unroll
           for (uint32_t i = 0; i < NB; ++i) {
             const __half2 d2 = *reinterpret_cast<const __half2*>(&d[i / 2]);
@@ -534,51 +535,95 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
                 make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
+        next(j, load);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.k_full[b]);
       }
-      if (j + 1 < tl.count) load_keys(tl.token(j + 1, KT));
-      {
-        const int32_t e = exponent_above(vs);
-        const __half2 down = down_by(e);
-        // tokens that were never written may hold any bits
-        const int32_t live = length - static_cast<int32_t>(tok + grp * 8);
+    } else {
+      // ================= values: the 8 tokens from 32 k_of + 8 (lane / 8), unit lane % 8
+      // (D = 256: half of it)
+      constexpr uint32_t WT = D == 64 ? 1 : 2; // words of a token's unit that a thread takes
+      const uint32_t half = D == 256 ? w4 >> 1 : 0, k_of = D == 256 ? w4 & 1 : w4;
+      const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
+      uint32_t vw[8][WT];
+      auto load = [&](uint32_t tok) {
+        load_scales(tok);
+        int32_t mine = pages[0];
 #pragma unroll
-        for (int32_t t = 0; t < 8; ++t)
+        for (int k = 1; k < IT; ++k) mine = k_of == static_cast<uint32_t>(k) ? pages[k] : mine;
+        const int32_t p = __shfl_sync(0xffffffffu, mine, lane & 24);
 #pragma unroll
-          for (uint32_t i = 0; i < WT; ++i) vo[t][i] = t < live ? mul_f16x2(vo[t][i], down) : 0u;
+        for (uint32_t t = 0; t < 8; ++t)
+#pragma unroll
+          for (uint32_t i = 0; i < WT; ++i) vw[t][i] = 0x88888888u;
+        if (p >= 0) {
+          const uint8_t* const at = codes + wide(p, page_codes) + ((tok + grp * 8) & (kv.page - 1)) * (D / 2) + g * (D / 2) +
+                                    half * 8;
+          if constexpr (D == 256) {
+#pragma unroll
+            for (uint32_t t = 0; t < 8; ++t) ldg<2>(at + t * 16, vw[t]);
+          } else {
+            uint32_t w[8 * WT];
+            ldg<8 * WT>(at, w);
+#pragma unroll
+            for (uint32_t t = 0; t < 8; ++t)
+#pragma unroll
+              for (uint32_t i = 0; i < WT; ++i) vw[t][i] = w[t * WT + i];
+          }
+        }
+      };
+      first(load);
+#pragma unroll 1
+      for (uint32_t j = 0; j < tl.count && !dead; ++j) {
+        const uint32_t b = j & 1;
+        const int32_t e = settle();
+        uint32_t own[WT];                      // lane l: the scales of token 32 k_of + l, this thread's blocks
+#pragma unroll
+        for (uint32_t i = 0; i < WT; ++i) {
+          own[i] = sc[half * (NW / 2) + i];
+#pragma unroll
+          for (int k = 1; k < IT; ++k) own[i] = k_of == static_cast<uint32_t>(k) ? sc[k * NW + half * (NW / 2) + i] : own[i];
+        }
         if (j > 1) wait(&bar.v_empty[b], ((j >> 1) - 1) & 1);
-        if (tid == Sh::kSoft * 32) bar.v_exp[j & 3] = static_cast<float>(e);
+        if (w4 == 0 && lane == 0) bar.v_exp[j & 3] = static_cast<float>(e);
         uint8_t* const buf =
             sm_v + b * Sh::kBuf + (grp >> 3) * (D * 128) + (half * 128 + g) * 128 + ((grp & 7) ^ g) * 16;
 #pragma unroll
-        for (uint32_t i = 0; i < 2 * WT; ++i) {   // blocks of 32 channels: 4 of this thread's channels each
-          const uint32_t pick = i & 1 ? 0x7632u : 0x5410u;
-          uint32_t v[4][4];                    // [channel][token pair]
+        for (uint32_t w = 0; w < WT; ++w) {
+          uint32_t d[8];
 #pragma unroll
-          for (uint32_t t = 0; t < 4; ++t) {
-            uint32_t x[4];
-            pairs<true>(__byte_perm(vw[2 * t][i / 2], vw[2 * t + 1][i / 2], pick), magic, x);
-            const uint32_t d = __byte_perm(vo[2 * t][i / 2], vo[2 * t + 1][i / 2], pick);
+          for (uint32_t t = 0; t < 8; ++t) d[t] = __shfl_sync(0xffffffffu, own[w], (lane & 24) + t);
 #pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) v[c][t] = mul_f16x2(x[c], d);
+          for (uint32_t h = 0; h < 2; ++h) {   // a block of 32 channels: 4 of this thread's each
+            const uint32_t pick = h ? 0x7632u : 0x5410u;
+            uint32_t v[4][4];                  // [channel][token pair]
+#pragma unroll
+            for (uint32_t t = 0; t < 4; ++t) {
+              uint32_t x[4];
+              pairs<true>(__byte_perm(vw[2 * t][w], vw[2 * t + 1][w], pick), magic, x);
+              const uint32_t dd = __byte_perm(d[2 * t], d[2 * t + 1], pick);
+#pragma unroll
+              for (uint32_t c = 0; c < 4; ++c) v[c][t] = mul_f16x2(x[c], dd);
+            }
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(buf + (64 * w + 32 * h + 8 * c) * 128) =
+                  make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
           }
-#pragma unroll
-          for (uint32_t c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(buf + (32 * i + 8 * c) * 128) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
         }
+        next(j, load);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.v_full[b]);
       }
     }
   } else {
-    // ================= issue: one thread for each row tile
-    if constexpr (RT == 2) fewer_registers<40>();
+    // ================= issue: one warp for each row tile
+    if constexpr (RT == 2) fewer_registers<32>();
     // The whole warp walks the loop and one elected thread issues: descriptors stay in
     // uniform registers, which the MMA instruction takes its operands from.
-    const uint32_t x = __shfl_sync(0xffffffffu, warp, 0) - Sh::kSoft - 4;
+    const uint32_t x = __shfl_sync(0xffffffffu, warp, 0) - Sh::kSoft - 8;
     if (x < RT) {
       constexpr uint32_t kF32 = 1u << 4;       // accumulators; both operands f16
       constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
@@ -603,17 +648,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
         }
         __syncwarp();
         wait(&bar.v_full[b], parity);
-        wait(&bar.p_full[x], j & 1);
-        if (dead) break;
-        tc_fence_after();
-        if (elect_one()) {
 #pragma unroll
-          for (uint32_t k = 0; k < KT / 16; ++k)  // 64 tokens a region
-            umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
-                        (j | k) != 0);
-          umma_commit(&bar.v_empty[b]);
+        for (uint32_t h = 0; h < 2; ++h) {
+          wait(&bar.p_full[x][h], j & 1);
+          if (dead) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)   // 64 tokens a region
+              umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
+                          (j | k) != 0);
+            if (h) umma_commit(&bar.v_empty[b]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       // nothing of this CTA may still run when its tensor memory goes
       if (tl.count) {
