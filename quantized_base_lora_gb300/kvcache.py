@@ -148,7 +148,7 @@ class KvCache:
         n = seqs.shape[0]
         qp, tokens, heads, code, qs = self._tokens("q", q)
         if out is None:
-            out = torch.empty((tokens, heads, self.head_dim), dtype=q.dtype, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
             op, os_ = out.data_ptr(), heads * self.head_dim
         else:
             op, o_tokens, o_heads, o_code, os_ = self._tokens("out", out)

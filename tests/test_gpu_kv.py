@@ -207,6 +207,25 @@ def test_long_context_split_over_many_blocks():
         np.testing.assert_array_equal(first, again)              # the same inputs, the same bits
 
 
+@pytest.mark.parametrize("dim,page,kv,group,new,window,sinks", [
+    (128, 64, 1, 4, 300, 0, 0),        # 1200 rows: five tiles of rows, twelve tiles of tokens
+    (128, 16, 2, 3, 97, 0, 0),
+    (64, 32, 1, 8, 200, 300, 5),
+    (256, 128, 1, 1, 260, 0, 0),
+    (256, 16, 1, 2, 150, 200, 40),
+    (128, 64, 1, 2, 130, 600, 300)])
+def test_chunks_over_a_long_context(dim, page, kv, group, new, window, sinks):
+    rng = np.random.default_rng(new)
+    lengths = [1500, new, 700]
+    c = make(n_pages=250, page=page, kv=kv, dim=dim, rows=3, cols=1500 // page + 1)
+    held = fill(c, [2, 0, 1], lengths, rng, bf16=True)
+    first = attend_and_compare(c, held, [2, 0, 1], [new, new, 3], kv * group, np.random.default_rng(1), True, window,
+                               sinks)          # 3 new tokens in the same call: served beside the others
+    again = attend_and_compare(c, held, [2, 0, 1], [new, new, 3], kv * group, np.random.default_rng(1), True, window,
+                               sinks)
+    np.testing.assert_array_equal(first, again)
+
+
 @pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
 def test_many_sequences_of_every_length(bf16):
     rng = np.random.default_rng(11)
@@ -556,3 +575,15 @@ def test_refusals_of_the_torch_side():
         KvCache(c.codes, c.scales[:, :, :1], c.table, c.length, c.refs)
     with pytest.raises(ValueError):
         KvCache(c.codes, c.scales, c.table.long(), c.length, c.refs)
+
+
+def test_the_example_runs(capsys):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_block.py")
+    spec = importlib.util.spec_from_file_location("decode_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.main()
+    said = capsys.readouterr().out
+    assert "lengths: [307, 36, 305, 0]" in said and "after the release: 0" in said and "finite: True" in said
