@@ -524,7 +524,8 @@ ovl_status ovl_debug_inject(ovl_ctx* ctx, uint32_t phase, ovl_status code);
  * a row listed twice, or too few free pages is latched as a status code that
  * ovl_kv_check returns and clears; ovl_kv_extend, _fork, _compact and _release
  * then change nothing, ovl_kv_append writes and ovl_kv_read and
- * ovl_kv_attention return the rest (zeros for a token that cannot be reached).
+ * ovl_kv_attention return the rest (zeros for a token that cannot be reached;
+ * where a page of the context is missing, outputs that need it mean nothing).
  * Calls on one cache must be stream-ordered: they share its workspace.  They
  * run on the current device, on `stream`, and allocate nothing.
  * Errors of every entry point: OVL_E_ARG (null pointer, unknown dtype, layer or

@@ -34,8 +34,22 @@
 // CTA barrier inside a segment.  A segment that is cut by a run's end is joined
 // by whichever of its CTAs arrives last: partial results go through memory, in
 // the order of the CTAs, so the same call gives the same bits, and no CTA waits.
+//
+// Measured (GB300, 8 kv heads of 128, 32 query heads, bf16): 16 sequences of
+// 60001 to 131072 tokens, 291 us = 5.7 TB/s, 0.85 of the measured copy rate; 32
+// sequences of 500 to 8000 tokens, 33 us (0.38: starting, joining and the first
+// loads are two thirds of it); 64 sequences, window 2048 and 4 sinks, 45 us
+// (0.48).  The copies alone take 241 us of the first, the arithmetic alone
+// about 280: a tile of 32 tokens is some 620 instructions of a warp, 128 of them
+// the masks that take the codes apart, at 0.6 to 0.7 of the issue slots with
+// four warps a scheduler (128 registers).  What brought it there, in order, on
+// that case: 489 us with keys in bf16 and two instructions a mask; 356 with f16
+// codes and one; 314 with asynchronous copies by the whole warp in place of bulk
+// copies by four lanes (whose operands went through uniform registers one lane
+// after the other) and a reference that trails; 291 with a shorter loop.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -748,11 +762,23 @@ cudaError_t attend_dim(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& call, cudaStream_t st) {
-  // Rows (new tokens x query heads of a kv head) up to which a sequence is served
-  // here; above it k_kv_prefill takes it, where the scores' precision allows.
-  constexpr uint32_t kFew = 32;
+  // Which kernel.  Measured (bf16, contexts of 1024 to 16384 tokens, 1 to 64 sequences of
+  // 3 to 192 new tokens, head_dim 64, 128 and 256): this one takes a constant time for a
+  // group of rows and token tile, k_kv_prefill one for a CTA's token tile, whether its
+  // rows are full or not; they break even at 4 groups an SM for each round of the
+  // other's CTAs (all lengths alike, 16 sequences over 4096 tokens, 8 x 4 heads of 128:
+  // 12 new tokens 76 here and 82 us there, 24 new tokens 125 and 85; one sequence over
+  // 16384, 192 new tokens: 232 and 294).  Where the other is used, sequences of up to
+  // kFew rows (new tokens x query heads of a kv head) stay here.  f32 calls need the
+  // exact products of this one.
+  constexpr uint32_t kFew = 48;
   KvQuery a = call;
-  const bool many = a.bf16 && static_cast<uint64_t>(a.max_new) * a.group > kFew;
+  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, small = kv.dim == 256 ? 8 : 16, sms = kv_sm_count();
+  const uint64_t groups = kv.heads * ((rows + small - 1) / small);
+  const uint64_t large = kv.dim == 256 ? 128 : 256, served = std::min<uint64_t>(a.n_seqs, rows / (kFew + 1));
+  const uint64_t ctas = kv.heads * std::max((rows + large - 1) / large, served);
+  const bool many = a.bf16 && static_cast<uint64_t>(a.max_new) * a.group > kFew &&
+                    groups > 4 * sms * ((ctas + sms - 1) / sms);
   a.few = many ? kFew : 0xffffffffu;
   cudaError_t e;
   switch (kv.dim) {

@@ -9,6 +9,12 @@
 // destinations of the same call release.  Pages that an entry releases from its
 // own source row (src = dst) are still read by the copy, so they become free
 // only afterwards.
+//
+// Measured: the bookkeeping 7 us for one entry, 9 for 24, 14 for 16 entries with
+// 17000 positions to check (cold; a chain of six dependent loads and a dozen
+// barriers).  Copying 24 pages of 2.36 MB 16 us, 7 TB/s of reads and writes;
+// compacting 16 rows of 8 layers by half 70 us, 4.5 TB/s (5.6 with the sectors of
+// values that are read for a part of them).
 #include <algorithm>
 #include <type_traits>
 

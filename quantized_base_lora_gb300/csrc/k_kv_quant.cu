@@ -75,7 +75,11 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float
 // its latency is that of one.  Bound by memory (reads 2 or 4, writes 0.5625 bytes
 // a channel) with the arithmetic close behind: most blocks are tame - finite and
 // neither so small nor so large that d is subnormal or saturated - and need no
-// care for single channels.
+// care for single channels.  Measured: 26600 tokens of 8 heads of 128 in fp32 (218
+// MB in, 31 MB out), 58 us; reading their values back (218 MB out), 43 us.  Both
+// together 162 us with one head a thread and a division a channel, 115 with four
+// heads and one reciprocal a block, 101 without the care.  8 tokens: 5 us each, of
+// which the launch and six dependent loads are all.
 constexpr uint32_t kHeadsMany = 4;
 
 template <int D, bool BF16, uint32_t HT>

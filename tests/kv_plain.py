@@ -48,25 +48,25 @@ def unpack(unit, page, D, which):
 
 def attention(q, k, v, positions, scale, window=0, sinks=0):
     """q [T][H][D], k and v [n][Hkv][D] (64-bit values), positions [T] -> (out [T][H][D], bound of its error per
-    unit of relative error of the scores, largest |v| that a row can weigh)."""
+    unit of relative error of the scores, largest |v| that the rows can weigh)."""
     T, H, D = q.shape
     n, hk = k.shape[0], k.shape[1]
     out, spread, top = np.zeros((T, H, D)), np.zeros((T, H, 1)), np.zeros((T, H, D))
-    j = np.arange(n)
-    for t in range(T):
-        p = positions[t]
-        seen = j <= p
-        if window:
-            seen &= (j > p - window) | (j < sinks)
-        if not seen.any():
-            continue
-        for h in range(H):
-            kk, vv = k[seen, h * hk // H], v[seen, h * hk // H]
-            s = kk @ q[t, h] * scale
-            e = np.exp(s - s.max())
-            out[t, h] = (e / e.sum()) @ vv
-            spread[t, h] = (np.abs(kk) @ np.abs(q[t, h])).max() * abs(scale)
-            top[t, h] = np.abs(vv).max(0)
+    j, p = np.arange(n), np.asarray(positions)[:, None]
+    seen = j <= p
+    if window:
+        seen &= (j > p - window) | (j < sinks)
+    some = seen.any(1)
+    if not some.any():
+        return out, spread, top
+    seen = seen[some]
+    for h in range(H):
+        kk, vv = k[:, h * hk // H], v[:, h * hk // H]
+        s = np.where(seen, q[some, h] @ kk.T * scale, -np.inf)
+        e = np.exp(s - s.max(1, keepdims=True))
+        out[some, h] = (e / e.sum(1, keepdims=True)) @ vv
+        spread[some, h, 0] = (np.where(seen, np.abs(q[some, h]) @ np.abs(kk).T, 0)).max(1) * abs(scale)
+        top[some, h] = np.abs(vv[seen.any(0)]).max(0)
     return out, spread, top
 
 

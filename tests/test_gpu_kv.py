@@ -170,31 +170,33 @@ def test_window_and_sinks(window, sinks, new, bf16):
     attend_and_compare(c, held, [1, 0, 3], [new] * 3, 8, rng, bf16, window, sinks)
 
 
-@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("new", [1, 60])
 @pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
 def test_sharp_and_flat_scores(new, bf16):
     """Scores that single one token out, scores that are all equal, and a negative scale."""
     rng = np.random.default_rng(new)
-    c = make(n_pages=60, page=32, kv=1, dim=128, rows=2, cols=16)
+    kv = 48 if new > 1 else 1                                    # wide enough for the kernel for many rows
+    c = make(n_pages=60, page=32, kv=kv, dim=128, rows=2, cols=16)
     held = fill(c, [0], [300], rng, bf16=bf16)
     for scale, spike in ((3.0, 4.0), (0.0, 1.0), (-0.2, 1.0)):
-        attend_and_compare(c, held, [0], [new], 4, rng, bf16, scale=scale, spike=spike)
+        attend_and_compare(c, held, [0], [new], 4 * kv, rng, bf16, scale=scale, spike=spike)
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 60])
 @pytest.mark.parametrize("size", [1e-6, 3e4])
 def test_values_and_keys_of_any_size(new, size):
     """Scales at both ends of binary16: tiny and large keys and values, one token far above the others."""
     rng = np.random.default_rng(3)
-    c = make(n_pages=20, page=32, kv=1, dim=128, rows=2, cols=16)
+    kv = 48 if new > 1 else 1                                    # wide enough for the kernel for many rows
+    c = make(n_pages=20, page=32, kv=kv, dim=128, rows=2, cols=16)
     s, off, n = dev([0]), dev([0, 200]), 200
     c.extend(s, off)
-    k, v = (draw(rng, (n, 1, 128), True).float() * size for _ in range(2))
+    k, v = (draw(rng, (n, kv, 128), True).float() * size for _ in range(2))
     v[100] *= 3
     k, v = k.bfloat16(), v.bfloat16()
     c.append(0, s, off, k, v)
     held = {0: tuple(K.values_of(*K.quantize(x.float().cpu().numpy())) for x in (k, v))}
-    attend_and_compare(c, held, [0], [new], 4, rng, True, scale=0.1 / size)
+    attend_and_compare(c, held, [0], [new], 4 * kv, rng, True, scale=0.1 / size)
 
 
 def test_long_context_split_over_many_blocks():
@@ -207,13 +209,38 @@ def test_long_context_split_over_many_blocks():
         np.testing.assert_array_equal(first, again)              # the same inputs, the same bits
 
 
+# Enough rows in all (new tokens x query heads / 16 x kv heads above four an SM) that bf16 calls go to the
+# kernel for many rows.
+WIDE = [
+    # dim, page, kv, group, lengths, new
+    (128, 64, 48, 2, [250, 97, 60], [50, 50, 33]),
+    (64, 16, 40, 3, [300, 64, 33], [64, 64, 33]),
+    (256, 32, 40, 1, [140, 129], [129, 70]),
+    (128, 128, 64, 1, [600, 1, 40], [200, 1, 0]),                # and sequences of one token and of none
+    (128, 16, 40, 7, [90, 45], [37, 45]),
+    (64, 256, 48, 8, [513], [31]),
+    (256, 16, 48, 2, [300, 20], [131, 3]),
+]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: f"d{s[0]}p{s[1]}h{s[2]}x{s[3]}n{max(s[5])}")
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 1), (16, 70), (1000, 4), (1, 0)])
+def test_many_rows(shape, window, sinks):
+    dim, page, kv, group, lengths, new = shape
+    rng = np.random.default_rng(sum(lengths) + window)
+    c = make(n_pages=70, page=page, kv=kv, dim=dim, rows=5, cols=-(-max(lengths) // page) + 1)
+    rows = [4, 0, 2][:len(lengths)]
+    held = fill(c, rows, lengths, rng, bf16=True)
+    attend_and_compare(c, held, rows, new, kv * group, rng, True, window, sinks)
+
+
 @pytest.mark.parametrize("dim,page,kv,group,new,window,sinks", [
-    (128, 64, 1, 4, 300, 0, 0),        # 1200 rows: five tiles of rows, twelve tiles of tokens
-    (128, 16, 2, 3, 97, 0, 0),
-    (64, 32, 1, 8, 200, 300, 5),
-    (256, 128, 1, 1, 260, 0, 0),
-    (256, 16, 1, 2, 150, 200, 40),
-    (128, 64, 1, 2, 130, 600, 300)])
+    (128, 64, 16, 4, 300, 0, 0),       # 1200 rows: five tiles of rows, twelve tiles of tokens
+    (128, 16, 32, 3, 97, 0, 0),
+    (64, 32, 8, 8, 200, 300, 5),
+    (256, 128, 20, 1, 260, 0, 0),
+    (256, 16, 20, 2, 150, 200, 40),
+    (128, 64, 24, 2, 230, 600, 300)])
 def test_chunks_over_a_long_context(dim, page, kv, group, new, window, sinks):
     rng = np.random.default_rng(new)
     lengths = [1500, new, 700]
@@ -238,20 +265,21 @@ def test_many_sequences_of_every_length(bf16):
 
 
 @pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
-@pytest.mark.parametrize("new", [1, 24])
-def test_tokens_with_nothing_to_see_are_zero(bf16, new):
+@pytest.mark.parametrize("new,kv", [(1, 1), (24, 1), (30, 64)])   # the last: the kernel for many rows
+def test_tokens_with_nothing_to_see_are_zero(bf16, new, kv):
     """More new tokens than the row has: positions below zero see nothing."""
     rng = np.random.default_rng(2)
-    c = make(page=16, kv=1, dim=128)
-    held = fill(c, [0, 1], [5, 30], rng, bf16=bf16)
+    c = make(page=16, kv=kv, dim=128)
+    first = 5 if kv == 1 else 25
+    held = fill(c, [0, 1], [first, 30], rng, bf16=bf16)
     extra = 3
-    off = offsets([5 + extra, new, 1])
-    x = draw(rng, (int(off[-1]), 4, 128), bf16)
+    off = offsets([first + extra, new, 1])
+    x = draw(rng, (int(off[-1]), 4 * kv, 128), bf16)
     out = torch.full_like(x, float("nan"))
-    c.attention(0, dev([0, 1, 2]), dev(off), x, max(8, new), out=out)      # row 2 is free: its token sees nothing
+    c.attention(0, dev([0, 1, 2]), dev(off), x, max(first + extra, new), out=out)   # row 2 is free: its token sees nothing
     got = out.double().cpu().numpy()
     assert (got[:extra] == 0).all() and (got[-1] == 0).all()
-    for row, a, b in ((0, extra, 8), (1, 8, 8 + new)):
+    for row, a, b in ((0, extra, off[1]), (1, off[1], off[2])):
         k, v = held[row]
         w, spread, top = K.attention(x[a:b].double().cpu().numpy(), k, v, np.arange(k.shape[0] - (b - a), k.shape[0]),
                                      128 ** -0.5)
@@ -261,25 +289,25 @@ def test_tokens_with_nothing_to_see_are_zero(bf16, new):
 
 def test_strided_queries_outputs_and_another_stream():
     rng = np.random.default_rng(4)
-    c = make(page=32, layers=2, kv=2, dim=64)
-    held = fill(c, [3, 1], [50, 33], rng, layer=1)
+    c = make(page=32, layers=2, kv=40, dim=64)
+    held = fill(c, [3, 1], [50, 33], rng, layer=1, bf16=True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        for new in ([1, 1], [20, 9]):
+        for new, bf16 in (([1, 1], False), ([20, 9], False), ([50, 33], True)):   # the last: many rows
             off = offsets(new)
-            wide = draw(rng, (int(off[-1]), 12, 64))
-            x, out = wide[:, 4:8], torch.full((int(off[-1]), 7, 64), 7.0, device="cuda")
-            c.attention(1, dev([3, 1]), dev(off), x, max(new), out=out[:, 2:6])
+            wide = draw(rng, (int(off[-1]), 168, 64), bf16)
+            x, out = wide[:, 4:164], torch.full((int(off[-1]), 163, 64), 7.0, device="cuda", dtype=wide.dtype)
+            c.attention(1, dev([3, 1]), dev(off), x, max(new), out=out[:, 2:162])
             c.check()
-            o = out.cpu().numpy()
-            assert (o[:, :2] == 7).all() and (o[:, 6:] == 7).all()
+            o = out.double().cpu().numpy()
+            assert (o[:, :2] == 7).all() and (o[:, 162:] == 7).all()
             for i, row in enumerate([3, 1]):
                 k, v = held[row]
                 n = k.shape[0]
                 w, spread, top = K.attention(x[off[i]:off[i + 1]].double().cpu().numpy(), k, v,
                                              np.arange(n - new[i], n), 0.125)
-                assert (np.abs(o[off[i]:off[i + 1], 2:6] - w) <= K.allowed(w, spread, top, False)).all()
+                assert (np.abs(o[off[i]:off[i + 1], 2:162] - w) <= K.allowed(w, spread, top, bf16)).all()
 
 
 def test_pages_beyond_4_gib():
@@ -290,8 +318,8 @@ def test_pages_beyond_4_gib():
     c.refs[:2190] = 1
     held = fill(c, [0], [150], rng, layer=31, bf16=True)
     assert int(c.table[0, 0]) == 2190
-    for new in (1, 64):
-        attend_and_compare(c, held, [0], [new], 32, rng, True, layer=31)
+    attend_and_compare(c, held, [0], [1], 32, rng, True, layer=31)
+    attend_and_compare(c, held, [0], [150], 72, rng, True, layer=31)      # 1350 rows: the kernel for many
     c.fork(dev([0]), dev([1]))
     c.compact(dev([0]), dev([2]), dev(np.arange(0, 150, 3)), dev([0, 50]))
     c.check()
@@ -497,6 +525,23 @@ def test_tokens_out_of_reach_are_latched_and_the_rest_is_served():
     assert (got[0] == 0).all() and (got[1] != 0).any()
     with pytest.raises(q.OvlError):
         c.check()
+    wide = make(n_pages=20, page=16, kv=64, dim=64, rows=4, cols=3)
+    held = fill(wide, [0], [40], rng, bf16=True)
+    x2 = draw(rng, (60, 256, 64), True)
+    got = wide.attention(0, dev([0, -1]), dev([0, 40, 60]), x2, 30)        # one row too long for max_new, one unknown
+    with pytest.raises(q.OvlError):
+        wide.check()
+    k2, v2 = held[0]
+    w, spread, top = K.attention(x2[:30].double().cpu().numpy(), k2, v2, np.arange(30), 0.125)
+    assert (np.abs(got[:30].double().cpu().numpy() - w) <= K.allowed(w, spread, top, True)).all()
+    assert (got[30:] == 0).all()
+    wide.table[0, 1] = -7                                        # a page that is not there: rows that do not need it
+    got = wide.attention(0, dev([0]), dev([0, 40]), x2[:40], 40).double().cpu().numpy()
+    with pytest.raises(q.OvlError):
+        wide.check()
+    assert np.isfinite(got).all()
+    w, spread, top = K.attention(x2[:16].double().cpu().numpy(), k2, v2, np.arange(16), 0.125)
+    assert (np.abs(got[:16] - w) <= K.allowed(w, spread, top, True)).all()
     c.length[1] = 40                                             # a row that counts tokens but has no pages
     got = c.attention(0, dev([1]), dev([0, 1]), x[:1], 1)
     with pytest.raises(q.OvlError):
