@@ -56,15 +56,19 @@ namespace ovl {
 namespace {
 
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kPairRows = 256;          // a sequence's rows above which CTAs work in pairs
 
-template <int D>
+// PAIR: CTAs that work on one MMA.
+template <int D, int PAIR>
 struct Shape {
-  static constexpr uint32_t kRowTiles = D == 256 ? 1 : 2;      // of 128 rows
+  static_assert(PAIR == 1 || D == 128, "pairs take 128 channels");
+  static constexpr uint32_t kRowTiles = D == 256 ? 1 : 2;      // of 128 rows a CTA
   static constexpr uint32_t kTokens = D == 256 ? 64 : 128;     // of a tile
-  static constexpr uint32_t kRows = 128 * kRowTiles;
+  static constexpr uint32_t kRows = 128 * kRowTiles;           // of a CTA
   static constexpr uint32_t kQ = 128 * D * 2;                  // bytes of one row tile
-  static constexpr uint32_t kBuf = kTokens * D * 2;            // bytes of a K or V buffer
-  static constexpr uint32_t kSmem = kRowTiles * kQ + 4 * kBuf;
+  static constexpr uint32_t kBuf = kTokens * D * 2 / PAIR;     // bytes of a CTA's share of a K or V tile
+  static constexpr uint32_t kBufs = 2 * PAIR;
+  static constexpr uint32_t kSmem = kRowTiles * kQ + 2 * kBufs * kBuf;
   static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
   static constexpr uint32_t kWarps = kSoft + 12;               // softmax, 4 keys, 4 values, 4 issue (1 or 2 of them busy)
   static constexpr uint32_t kThreads = kWarps * 32;
@@ -73,27 +77,80 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2];   // p_full: [row tile][half of the tile's tokens]
-  float k_exp[4], v_exp[4];      // 2^E of the last tiles' scales as E
+  // waited for by the issuing warps (of a pair: the first CTA's, for both)
+  uint64_t q_ready, k_full[4], v_full[4], p_full[2][2];        // p_full: [row tile][half of the tile's tokens]
+  uint64_t k_empty[4], v_empty[4], s_full[2], o_done[2];       // arrived at by the MMAs, in each CTA
+  uint64_t e_ready[4];                                         // the tile's v_exp is written
+  float k_exp[8], v_exp[8];      // 2^E of the last tiles' scales as E
   uint32_t taddr;
 };
 
+template <int PAIR>
 __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
+template <int PAIR>
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
+// One arrival on `bar` (in both CTAs of a pair) when the MMAs so far are done.
+template <int PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+template <int PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t* where) {
+  if constexpr (PAIR == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t taddr) {
+  if constexpr (PAIR == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -198,35 +255,39 @@ __device__ __forceinline__ int32_t exponent_above(const uint32_t (&w)[N]) {
   return static_cast<int32_t>(__reduce_max_sync(0xffffffffu, x) >> 10) - 14;
 }
 
-template <int D>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDev kv, const KvQuery a) {
-  using Sh = Shape<D>;
-  constexpr uint32_t NB = D / 32, KT = Sh::kTokens, RT = Sh::kRowTiles;
+template <int D, int PAIR>
+__global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(const KvDev kv, const KvQuery a) {
+  using Sh = Shape<D, PAIR>;
+  constexpr uint32_t NB = D / 32, KT = Sh::kTokens, RT = Sh::kRowTiles, NBUF = Sh::kBufs;
   extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ Bars bar;
   uint8_t* const sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint8_t* const sm_q = sm;
   uint8_t* const sm_k = sm + RT * Sh::kQ;
-  uint8_t* const sm_v = sm_k + 2 * Sh::kBuf;
+  uint8_t* const sm_v = sm_k + NBUF * Sh::kBuf;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   griddep_launch_dependents();
   griddep_wait();
   // ---- this CTA's rows; the ones that see most come first in the grid
-  const uint32_t seq = blockIdx.y, kh = blockIdx.x, row_tile = gridDim.z - 1 - blockIdx.z;
+  const uint32_t rank = PAIR == 2 ? cluster_ctarank() : 0u;
+  const uint32_t seq = blockIdx.y, kh = blockIdx.x / PAIR, row_tile = gridDim.z - 1 - blockIdx.z;
   const int32_t o0 = a.off[seq], o1 = a.off[seq + 1];
   if (o0 < 0 || o1 < o0 || static_cast<uint32_t>(o1) > a.n_tokens) return;      // latched by the few-row launch
-  const uint32_t tokens = o1 - o0, group = a.group, r0 = row_tile * Sh::kRows;
+  const uint32_t tokens = o1 - o0, group = a.group, pair0 = row_tile * (PAIR * Sh::kRows);
   if (tokens * static_cast<uint64_t>(group) <= a.few) return;                   // served by the few-row launch
   const uint32_t served = min(tokens, a.max_new);
-  if (row_tile == gridDim.z - 1 && tokens > served) {                           // latched as well: zeros
+  if (row_tile == gridDim.z - 1 && rank == 0 && tokens > served) {                           // latched as well: zeros
     const uint32_t chunks = group * D / 8;
     for (uint64_t i = tid; i < static_cast<uint64_t>(tokens - served) * chunks; i += Sh::kThreads)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (o0 + served + i / chunks) * a.out_stride +
                                 static_cast<uint64_t>(kh) * group * D + i % chunks * 8) = make_uint4(0, 0, 0, 0);
   }
-  if (r0 >= served * group) return;
-  const uint32_t n_rows = min(Sh::kRows, served * group - r0);
+  if (pair0 >= served * group) return;
+  const uint32_t pair_rows = min(PAIR * Sh::kRows, served * group - pair0);
+  // of them this CTA's: the second of a pair may have none and then only shares the work
+  const uint32_t r0 = pair0 + rank * Sh::kRows;
+  const uint32_t n_rows = pair_rows > rank * Sh::kRows ? min(Sh::kRows, pair_rows - rank * Sh::kRows) : 0u;
   const int32_t seq_row = a.seqs[seq];
   const bool sound = static_cast<uint32_t>(seq_row) < kv.max_seqs;
   int32_t length = sound ? kv.length[seq_row] : 0;
@@ -234,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   const int32_t first = length - static_cast<int32_t>(tokens);                  // position of its first new token
   const int32_t* const table_row = kv.table + static_cast<size_t>(sound ? seq_row : 0) * kv.max_pages;
   // the tiles that any of the rows sees
-  const uint32_t i_first = r0 / group, i_last = (r0 + n_rows - 1) / group;
+  const uint32_t i_first = pair0 / group, i_last = (pair0 + pair_rows - 1) / group;
   Tiles tl{0, 0, 0};
   const int32_t p_last = length ? first + static_cast<int32_t>(i_last) : -1;
   if (p_last >= 0) {
@@ -246,28 +307,28 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
     tl.count = tl.lead + static_cast<uint32_t>(p_last) / KT + 1 - tl.start;
   }
 
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.taddr)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc<PAIR>(&bar.taddr);
   if (tid == 32) {
-    mbar_init(&bar.q_ready, Sh::kSoft);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], 4);
-      mbar_init(&bar.v_full[i], 4);
+    mbar_init(&bar.q_ready, PAIR * Sh::kSoft);
+    for (uint32_t i = 0; i < NBUF; ++i) {
+      mbar_init(&bar.k_full[i], PAIR * 4);
+      mbar_init(&bar.v_full[i], PAIR * 4);
       mbar_init(&bar.k_empty[i], RT);
       mbar_init(&bar.v_empty[i], RT);
+      mbar_init(&bar.e_ready[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i][0], 4);
-      mbar_init(&bar.p_full[i][1], 4);
+      mbar_init(&bar.p_full[i][0], PAIR * 4);
+      mbar_init(&bar.p_full[i][1], PAIR * 4);
       mbar_init(&bar.o_done[i], 1);
     }
     mbar_fence_init();
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (PAIR == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t taddr = bar.taddr;
   bool dead = false;                           // a bounded wait ran out
@@ -275,11 +336,26 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
   // role walks its loop to the end, so no barrier between warps is left half full.
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (dead) return;
-    const bool landed = warp >= Sh::kSoft + 8 ? mbar_wait_spin(b, parity) : mbar_wait_bounded(b, parity);
+    const bool landed = warp < Sh::kSoft + 8 ? mbar_wait_bounded(b, parity)
+                        : PAIR == 2          ? mbar_wait_cluster(b, parity)
+                                             : mbar_wait_spin(b, parity);
     if (!__all_sync(0xffffffffu, landed)) {
       dead = true;
       if (lane == 0) kv_latch(kv, OVL_E_DEVICE_TIMEOUT);
     }
+  };
+
+  // One arrival at the issuing CTA's barrier, releasing what was written to shared memory.
+  auto arrive = [&](uint64_t* b) {
+    if constexpr (PAIR == 2) mbar_arrive_remote(cluster_map(b, 0));
+    else mbar_arrive(b);
+  };
+  // The same for P: tensor memory is ordered by its own fence, and a release over the
+  // cluster would wait a thousand clocks for memory that no one asks for.
+  auto arrive_p = [&](uint64_t* b) {
+    if constexpr (PAIR == 2)
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(b, 0)) : "memory");
+    else mbar_arrive(b);
   };
 
   if (warp < Sh::kSoft) {
@@ -323,14 +399,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_ready);
+      if (lane == 0) arrive(&bar.q_ready);
     }
     const int32_t last = on && length ? first + static_cast<int32_t>(i) : -1;
     const int32_t from = a.window ? last - static_cast<int32_t>(a.window) + 1 : 0;
     const int32_t sinks = static_cast<int32_t>(a.sinks);
     // of the rows of this tile: the one that sees least at either end
-    const uint32_t x0 = min(x * 128, n_rows - 1), x1 = min(x * 128 + 127, n_rows - 1);
-    const int32_t all_last = length ? first + static_cast<int32_t>((r0 + x0) / group) : -1;
+    const bool any = x * 128 < n_rows;
+    const uint32_t x0 = x * 128, x1 = any ? min(x * 128 + 127, n_rows - 1) : x0;
+    const int32_t all_last = length && any ? first + static_cast<int32_t>((r0 + x0) / group) : -1;
     const int32_t all_from =
         a.window ? first + static_cast<int32_t>((r0 + x1) / group) - static_cast<int32_t>(a.window) + 1 : 0;
     const uint32_t lanes = (warp & 3) * 32 << 16;
@@ -341,11 +418,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       const int32_t tok = static_cast<int32_t>(tl.token(j, KT));
       const bool hidden = tok > all_last - static_cast<int32_t>(KT - 1) ||
                           (tok < all_from && tok > sinks - static_cast<int32_t>(KT));
-      wait(&bar.v_full[j & 1], (j >> 1) & 1);  // the tile's value exponent
+      wait(&bar.e_ready[j % NBUF], (j / NBUF) & 1);
       wait(&bar.s_full[x], j & 1);
       tc_fence_after();
-      const float ve = bar.v_exp[j & 3];
-      const float kf = down * exp2f(bar.k_exp[j & 3]);
+      const float ve = bar.v_exp[j & 7];
+      const float kf = down * exp2f(bar.k_exp[j & 7]);
       // Two copies of the code: most tiles are seen whole.
       auto tile = [&](auto with_mask) {
         constexpr bool masked = decltype(with_mask)::value;
@@ -416,7 +493,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full[x][0]);
+            if (lane == 0) arrive_p(&bar.p_full[x][0]);
           }
         }
         const float2 total = both(add2(sum0, sum1));
@@ -427,7 +504,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[x][1]);
+      if (lane == 0) arrive_p(&bar.p_full[x][1]);
     }
     if (tl.count) wait(&bar.o_done[x], 0);
     tc_fence_after();
@@ -509,15 +586,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       if (j + 2 < tl.count) tile_pages<IT>(kv, table_row, length, tl.token(j + 2, KT), lane, pages);
     };
     if (!values) {
-      // ================= keys: tokens 32 k + 8 w4 + lane % 8, words lane / 8 of every block
+      // ================= keys: tokens 32 k + 8 w4 + lane % 8, words lane / 8 of every block;
+      // of a pair each CTA converts half of the tokens
+      constexpr int KI = IT / PAIR;
       const uint32_t from = w4 * 8 + (lane & 7), part = lane >> 3;
-      uint32_t kw[IT][NB];
+      uint32_t kw[KI][NB];
       auto load = [&](uint32_t tok) {
         load_scales(tok);
 #pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const uint32_t u = tok + 32 * k + from;
-          const int32_t p = __shfl_sync(0xffffffffu, pages[k], from);
+        for (int k = 0; k < KI; ++k) {
+          const uint32_t u = tok + 32 * (rank * KI + k) + from;
+          const int32_t p = __shfl_sync(0xffffffffu, PAIR == 2 && rank ? pages[(PAIR - 1) * KI + k] : pages[k], from);
 #pragma unroll
           for (uint32_t i = 0; i < NB; ++i) kw[k][i] = 0x88888888u;
           if (p >= 0) ldg<NB>(codes + wide(p, page_codes) + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), kw[k]);
@@ -526,16 +605,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       first(load);
 #pragma unroll 1
       for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-        const uint32_t b = j & 1;
+        const uint32_t b = j % NBUF;
         const int32_t e = settle();
-        if (j > 1) wait(&bar.k_empty[b], ((j >> 1) - 1) & 1);
-        if (w4 == 0 && lane == 0) bar.k_exp[j & 3] = static_cast<float>(e);
+        if (j >= NBUF) wait(&bar.k_empty[b], (j / NBUF - 1) & 1);
+        if (w4 == 0 && lane == 0) bar.k_exp[j & 7] = static_cast<float>(e);
         uint8_t* const buf = sm_k + b * Sh::kBuf + from * 128;
 #pragma unroll
-        for (int k = 0; k < IT; ++k) {
+        for (int k = 0; k < KI; ++k) {
           uint32_t d[NW];
 #pragma unroll
-          for (uint32_t i = 0; i < NW; ++i) d[i] = __shfl_sync(0xffffffffu, sc[k * NW + i], from);
+          for (uint32_t i = 0; i < NW; ++i)
+            d[i] = __shfl_sync(0xffffffffu, PAIR == 2 && rank ? sc[((PAIR - 1) * KI + k) * NW + i] : sc[k * NW + i], from);
 #pragma unroll
           for (uint32_t i = 0; i < NB; ++i) {
             const __half2 d2 = *reinterpret_cast<const __half2*>(&d[i / 2]);
@@ -545,20 +625,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[x] = mul_f16x2(v[x], dd);
             const uint32_t c = 4 * i + part;   // chunk of 8 channels
-            *reinterpret_cast<uint4*>(buf + (i >> 1) * (KT * 128) + 32 * k * 128 + ((c & 7) ^ (lane & 7)) * 16) =
+            *reinterpret_cast<uint4*>(buf + (i >> 1) * (KT / PAIR * 128) + 32 * k * 128 + ((c & 7) ^ (lane & 7)) * 16) =
                 make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
         next(j, load);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[b]);
+        if (lane == 0) arrive(&bar.k_full[b]);
       }
     } else {
       // ================= values: the 8 tokens from 32 k_of + 8 (lane / 8), unit lane % 8
-      // (D = 256: half of it)
-      constexpr uint32_t WT = D == 64 ? 1 : 2; // words of a token's unit that a thread takes
-      const uint32_t half = D == 256 ? w4 >> 1 : 0, k_of = D == 256 ? w4 & 1 : w4;
+      // (D = 256: half of it; of a pair each CTA converts half of the channels)
+      constexpr bool kSplit = D == 256 || PAIR == 2;
+      constexpr uint32_t WT = D == 64 || PAIR == 2 ? 1 : 2;   // words of a token's unit that a thread takes
+      const uint32_t half = PAIR == 2 ? rank : D == 256 ? w4 >> 1 : 0, k_of = D == 256 ? w4 & 1 : w4;
       const uint32_t g = lane & 7, grp = k_of * 4 + (lane >> 3);
       uint32_t vw[8][WT];
       auto load = [&](uint32_t tok) {
@@ -573,10 +654,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
           for (uint32_t i = 0; i < WT; ++i) vw[t][i] = 0x88888888u;
         if (p >= 0) {
           const uint8_t* const at = codes + wide(p, page_codes) + ((tok + grp * 8) & (kv.page - 1)) * (D / 2) + g * (D / 2) +
-                                    half * 8;
-          if constexpr (D == 256) {
+                                    half * (4 * WT);
+          if constexpr (kSplit) {
 #pragma unroll
-            for (uint32_t t = 0; t < 8; ++t) ldg<2>(at + t * 16, vw[t]);
+            for (uint32_t t = 0; t < 8; ++t) ldg<WT>(at + t * (D / 16), vw[t]);
           } else {
             uint32_t w[8 * WT];
             ldg<8 * WT>(at, w);
@@ -590,19 +671,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
       first(load);
 #pragma unroll 1
       for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-        const uint32_t b = j & 1;
+        const uint32_t b = j % NBUF;
         const int32_t e = settle();
         uint32_t own[WT];                      // lane l: the scales of token 32 k_of + l, this thread's blocks
 #pragma unroll
         for (uint32_t i = 0; i < WT; ++i) {
-          own[i] = sc[half * (NW / 2) + i];
+          auto mine = [&](uint32_t k) { return kSplit && half ? sc[k * NW + NW / 2 + i] : sc[k * NW + i]; };
+          own[i] = mine(0);
 #pragma unroll
-          for (int k = 1; k < IT; ++k) own[i] = k_of == static_cast<uint32_t>(k) ? sc[k * NW + half * (NW / 2) + i] : own[i];
+          for (int k = 1; k < IT; ++k) own[i] = k_of == static_cast<uint32_t>(k) ? mine(k) : own[i];
         }
-        if (j > 1) wait(&bar.v_empty[b], ((j >> 1) - 1) & 1);
-        if (w4 == 0 && lane == 0) bar.v_exp[j & 3] = static_cast<float>(e);
-        uint8_t* const buf =
-            sm_v + b * Sh::kBuf + (grp >> 3) * (D * 128) + (half * 128 + g) * 128 + ((grp & 7) ^ g) * 16;
+        if (j >= NBUF) wait(&bar.v_empty[b], (j / NBUF - 1) & 1);
+        if (w4 == 0 && lane == 0) {
+          bar.v_exp[j & 7] = static_cast<float>(e);
+          mbar_arrive(&bar.e_ready[b]);
+        }
+        uint8_t* const buf = sm_v + b * Sh::kBuf + (grp >> 3) * (D / PAIR * 128) + ((PAIR == 1 ? half * 128 : 0) + g) * 128 +
+                             ((grp & 7) ^ g) * 16;
 #pragma unroll
         for (uint32_t w = 0; w < WT; ++w) {
           uint32_t d[8];
@@ -629,7 +714,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
         next(j, load);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[b]);
+        if (lane == 0) arrive(&bar.v_full[b]);
       }
     }
   } else {
@@ -638,27 +723,27 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
     // The whole warp walks the loop and one elected thread issues: descriptors stay in
     // uniform registers, which the MMA instruction takes its operands from.
     const uint32_t x = __shfl_sync(0xffffffffu, warp, 0) - Sh::kSoft - 8;
-    if (x < RT) {
+    if (x < RT && rank == 0) {
       constexpr uint32_t kF32 = 1u << 4;       // accumulators; both operands f16
-      constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((128u >> 4) << 24);
-      constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t kQK = kF32 | ((KT >> 3) << 17) | ((PAIR * 128u >> 4) << 24);
+      constexpr uint32_t kPV = kF32 | ((D >> 3) << 17) | ((PAIR * 128u >> 4) << 24);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sm_q) + x * Sh::kQ);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sm_k)), v_desc = sdesc_sw128(smem_u32(sm_v));
       const uint32_t s_at = taddr + x * KT, o_at = taddr + Sh::kOutCol + x * D;
       if (tl.count) wait(&bar.q_ready, 0);
 #pragma unroll 1
       for (uint32_t j = 0; j < tl.count && !dead; ++j) {
-        const uint32_t parity = (j >> 1) & 1, b = j & 1;
+        const uint32_t parity = (j / NBUF) & 1, b = j % NBUF;
         wait(&bar.k_full[b], parity);
         if (dead) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (uint32_t k = 0; k < D / 16; ++k)   // 64 channels a region of 128-byte rows
-            umma_f16(s_at, q_desc + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
-                     k_desc + b * (Sh::kBuf / 16) + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), kQK, k != 0);
-          umma_commit(&bar.s_full[x]);
-          umma_commit(&bar.k_empty[b]);
+            umma_f16<PAIR>(s_at, q_desc + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                           k_desc + b * (Sh::kBuf / 16) + (k >> 2) * (KT / PAIR * 128 / 16) + 2 * (k & 3), kQK, k != 0);
+          commit<PAIR>(&bar.s_full[x]);
+          commit<PAIR>(&bar.k_empty[b]);
         }
         __syncwarp();
         wait(&bar.v_full[b], parity);
@@ -670,16 +755,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
           if (elect_one()) {
 #pragma unroll
             for (uint32_t k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)   // 64 tokens a region
-              umma_f16_ts(o_at, s_at + 8 * k, v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), kPV,
-                          (j | k) != 0);
-            if (h) umma_commit(&bar.v_empty[b]);
+              umma_f16_ts<PAIR>(o_at, s_at + 8 * k,
+                                v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D / PAIR * 128 / 16) + 2 * (k & 3), kPV,
+                                (j | k) != 0);
+            if (h) commit<PAIR>(&bar.v_empty[b]);
           }
           __syncwarp();
         }
       }
       // nothing of this CTA may still run when its tensor memory goes
       if (tl.count) {
-        if (elect_one()) umma_commit(&bar.o_done[x]);
+        if (elect_one()) commit<PAIR>(&bar.o_done[x]);
         __syncwarp();
         wait(&bar.o_done[x], 0);
       }
@@ -687,32 +773,33 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv_prefill(const KvDe
     }
   }
   __syncwarp();
-  __syncthreads();
+  // of a pair, neither leaves while the other's MMAs or arrivals may still reach it
+  if constexpr (PAIR == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+  if (warp == 0) tmem_free<PAIR>(taddr);
 }
 
-template <int D>
+template <int D, int PAIR>
 cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
-  using Sh = Shape<D>;
-  constexpr uint32_t bytes = Sh::kSmem + 1024;
+  using Sh = Shape<D, PAIR>;
+  constexpr uint32_t bytes = Sh::kSmem + 1024, rows = PAIR * Sh::kRows;
   static const cudaError_t ready =
-      cudaFuncSetAttribute(k_kv_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      cudaFuncSetAttribute(k_kv_prefill<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (ready != cudaSuccess) return ready;
-  const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + Sh::kRows - 1) / Sh::kRows;
+  const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + rows - 1) / rows;
   if (tiles > 65535u) return cudaErrorInvalidConfiguration;
-  return launch_chained(k_kv_prefill<D>, dim3(kv.heads, a.n_seqs, static_cast<uint32_t>(tiles)), Sh::kThreads, bytes, st,
-                        kv, a);
+  return launch_clustered(k_kv_prefill<D, PAIR>, dim3(PAIR * kv.heads, a.n_seqs, static_cast<uint32_t>(tiles)),
+                          Sh::kThreads, bytes, st, PAIR, kv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   switch (kv.dim) {
-    case 64: return prefill<64>(kv, a, st);
-    case 128: return prefill<128>(kv, a, st);
-    default: return prefill<256>(kv, a, st);
+    case 64: return prefill<64, 1>(kv, a, st);
+    case 128: return static_cast<uint64_t>(a.max_new) * a.group > kPairRows ? prefill<128, 2>(kv, a, st) : prefill<128, 1>(kv, a, st);
+    default: return prefill<256, 1>(kv, a, st);
   }
 }
 

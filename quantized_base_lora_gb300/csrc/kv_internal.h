@@ -107,19 +107,28 @@ uint32_t kv_sm_count();
 // the kernel before it still runs, so f calls griddep_wait() before it reads or
 // writes anything, and griddep_launch_dependents() as early as that is sound for
 // the next one (at once: every kernel here waits first).
+// `cluster`: CTAs of a cluster, along x.
 template <class... P, class... A>
-cudaError_t launch_chained(void (*f)(P...), dim3 grid, uint32_t block, uint32_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_clustered(void (*f)(P...), dim3 grid, uint32_t block, uint32_t smem, cudaStream_t st, uint32_t cluster,
+                             A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, f, args...);
+}
+template <class... P, class... A>
+cudaError_t launch_chained(void (*f)(P...), dim3 grid, uint32_t block, uint32_t smem, cudaStream_t st, A... args) {
+  return launch_clustered(f, grid, block, smem, st, 1, args...);
 }
 
 cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
