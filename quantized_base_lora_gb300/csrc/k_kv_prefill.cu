@@ -72,6 +72,9 @@ struct Shape {
   static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
   static constexpr uint32_t kWarps = kSoft + 12;               // softmax, 4 keys, 4 values, 4 issue (1 or 2 of them busy)
   static constexpr uint32_t kThreads = kWarps * 32;
+  // Registers a thread, of the launch's 96: 2 x softmax + 2 x conversion + issue = 5 x 96.
+  // A pair's CTA converts half a tile and keeps less in hand for it.
+  static constexpr int kSoftRegs = PAIR == 2 ? 168 : 160, kCacheRegs = PAIR == 2 ? 56 : 64, kIssueRegs = 32;
   static constexpr uint32_t kOutCol = kRowTiles * kTokens;     // first tensor memory column of O, behind S
   static_assert(kOutCol + kRowTiles * D <= kTmemCols, "S and O fit");
 };
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
 
   if (warp < Sh::kSoft) {
     // ================= softmax: one row a thread
-    if constexpr (RT == 2) more_registers<160>();
+    if constexpr (RT == 2) more_registers<Sh::kSoftRegs>();
     const uint32_t x = warp >> 2, r = tid & 127;
     const uint32_t row = r0 + x * 128 + r;
     const bool on = x * 128 + r < n_rows;
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
     }
     tc_fence_before();
   } else if (warp < Sh::kSoft + 8) {
-    if constexpr (RT == 2) fewer_registers<64>();
+    if constexpr (RT == 2) fewer_registers<Sh::kCacheRegs>();
     constexpr int IT = KT / 32;
     constexpr uint32_t NW = NB / 2;            // scale words of a token
     const uint32_t w4 = warp & 3;
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
     }
   } else {
     // ================= issue: one warp for each row tile
-    if constexpr (RT == 2) fewer_registers<32>();
+    if constexpr (RT == 2) fewer_registers<Sh::kIssueRegs>();
     // The whole warp walks the loop and one elected thread issues: descriptors stay in
     // uniform registers, which the MMA instruction takes its operands from.
     const uint32_t x = __shfl_sync(0xffffffffu, warp, 0) - Sh::kSoft - 8;
