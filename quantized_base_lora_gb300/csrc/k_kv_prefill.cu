@@ -7,16 +7,20 @@
 // fp32 accumulators in tensor memory:
 //   S = Q K^T   Q and K in shared memory, S in tensor memory
 //   O += P V    P over S's own columns in tensor memory, V^T in shared memory
-// so the scores never leave the SM.  Roles, each its own warps:
+// so the scores never leave the SM.  Most sequences of more than 256 rows of 128
+// channels (in_pairs) are taken by pairs of CTAs, clusters of two: each has its own
+// 256 rows, converts half of a tile - half of the tokens for K, half of the
+// channels for V - and every MMA runs over both CTAs' rows with the two halves as
+// its second operand, issued by the first.  Roles, each its own warps:
 //   softmax   4 warps for each 128 rows, a thread a row: S -> P in registers, running
 //             maximum and sum; O is rescaled in place, only when a row's maximum
 //             has grown by more than 2^6 since its reference was set
 //   keys, values   4 warps each: 4-bit words from global memory, one mask a pair
 //             of codes, times the block's scale, into the MMA's shared layout;
-//             two buffers each; the next words are in flight meanwhile
+//             two (four) buffers each; the next words are in flight meanwhile
 //   issue     one warp for each 128 rows.  The two row tiles run against each
 //             other: the MMAs of one overlap the softmax of the other; and P goes
-//             over in two halves, so that O's MMAs start with the first.
+//             over in parts, so that O's MMAs start with the first.
 //
 // Layout.  A 32-bit key word is 8 consecutive channels of a token, which is one
 // 16-byte chunk of the f16 operand; its codes come out in the order 0 4 1 5 2 6 3
@@ -31,20 +35,27 @@
 // two.  So f16's 11 bits hold whatever the size of the data is.
 //
 // Measured (GB300, 8 kv heads of 128, 32 query heads): 2 x 2048 new tokens over
-// 6000 to 8192, 452 us = 864 TFLOP/s, 0.45 of the measured bf16 burst rate; 4
-// chunks of up to 777 tokens, 3 kv heads of 64, window 1024, 62 us.  Bound by
-// shared memory and the softmax warps together: a tile's operand reads (192 KB),
-// the converted keys' and values' stores (64 KB) take the 128 bytes a clock for as
-// long as the MMAs run, and the stores then wait (a key warp spends 2200 of 5000
-// clocks a tile behind them); a softmax warp is busy for 3400.  With the softmax
-// left out 352 us, without the conversions 393, without both 277.
-// On the way there: one warp role for keys and values 492; MMAs issued by one
-// lane of a diverged warp (operands moved to uniform registers for each) 507; the
-// scores read twice from tensor memory, in chunks, 643; masks tested one by one
-// 1123.  Not adopted: two threads a row (584), scores in two buffers of 64 tokens
-// so that they run ahead of the softmax (498: N = 64 MMAs read Q twice as often).
+// 6000 to 8192, 405 us = 963 TFLOP/s, 0.50 of the measured bf16 burst rate (452 us
+// without pairs); 4 chunks of up to 777 tokens, 3 kv heads of 64, window 1024, 62 us
+// (267 CTAs of 4 to 11 tiles on 152 SMs: two rounds, each with its prologue).
+// Bound by the chain from scores to P and back: of 4800 clocks a tile (timed inside,
+// which adds some) a softmax warp is busy for 3300 - scores from tensor memory 250,
+// their maximum 310, exponentials and packing 2050 for 128 columns a thread - and
+// waits 1500 for the next scores; the key warps wait 800 for a free buffer, so it is
+// not the conversion, which without pairs it is as well (1300 of 5500 clocks behind
+// shared memory, where a tile's operand reads, 192 KB, meet the stores of 64).
+// With the softmax left out 352, without the conversions 393, without both 277 (all
+// three without pairs).
+// On the way there: pairs whose P was released over the cluster 547, whose softmax
+// had fewer registers 437, P in two parts 410; one warp role for keys and values
+// 492; MMAs issued by one lane of a diverged warp (operands moved to uniform
+// registers for each) 507; the scores read twice from tensor memory, in chunks,
+// 643; masks tested one by one 1123.  Not adopted: two threads a row (584), scores
+// in two buffers of 64 tokens so that they run ahead of the softmax (498: N = 64 MMAs
+// read Q twice as often), in pairs one role for keys and values (591).
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -56,8 +67,6 @@ namespace ovl {
 namespace {
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kPairRows = 256;          // a sequence's rows above which CTAs work in pairs
-
 // PAIR: CTAs that work on one MMA.
 template <int D, int PAIR>
 struct Shape {
@@ -69,6 +78,8 @@ struct Shape {
   static constexpr uint32_t kBuf = kTokens * D * 2 / PAIR;     // bytes of a CTA's share of a K or V tile
   static constexpr uint32_t kBufs = 2 * PAIR;
   static constexpr uint32_t kSmem = kRowTiles * kQ + 2 * kBufs * kBuf;
+  static constexpr uint32_t kParts = 2 * PAIR;                 // in which P goes over; measured 4 : 2 parts, pairs 403 : 410 us,
+                                                               // single CTAs (4 x 777 rows of 64) 66 : 62
   static constexpr uint32_t kSoft = 4 * kRowTiles;             // warps
   static constexpr uint32_t kWarps = kSoft + 12;               // softmax, 4 keys, 4 values, 4 issue (1 or 2 of them busy)
   static constexpr uint32_t kThreads = kWarps * 32;
@@ -81,7 +92,7 @@ struct Shape {
 
 struct Bars {
   // waited for by the issuing warps (of a pair: the first CTA's, for both)
-  uint64_t q_ready, k_full[4], v_full[4], p_full[2][2];        // p_full: [row tile][half of the tile's tokens]
+  uint64_t q_ready, k_full[4], v_full[4], p_full[2][4];        // p_full: [row tile][part of the tile's tokens]
   uint64_t k_empty[4], v_empty[4], s_full[2], o_done[2];       // arrived at by the MMAs, in each CTA
   uint64_t e_ready[4];                                         // the tile's v_exp is written
   float k_exp[8], v_exp[8];      // 2^E of the last tiles' scales as E
@@ -322,8 +333,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i][0], PAIR * 4);
-      mbar_init(&bar.p_full[i][1], PAIR * 4);
+      for (uint32_t k = 0; k < Sh::kParts; ++k) mbar_init(&bar.p_full[i][k], PAIR * 4);
       mbar_init(&bar.o_done[i], 1);
     }
     mbar_fence_init();
@@ -407,12 +417,12 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
     const int32_t last = on && length ? first + static_cast<int32_t>(i) : -1;
     const int32_t from = a.window ? last - static_cast<int32_t>(a.window) + 1 : 0;
     const int32_t sinks = static_cast<int32_t>(a.sinks);
-    // of the rows of this tile: the one that sees least at either end
-    const bool any = x * 128 < n_rows;
-    const uint32_t x0 = x * 128, x1 = any ? min(x * 128 + 127, n_rows - 1) : x0;
-    const int32_t all_last = length && any ? first + static_cast<int32_t>((r0 + x0) / group) : -1;
+    // Of the rows of this tile: the ones that see least at either end.  A tile without rows
+    // goes by the sequence's last one (by the masks, seeing nothing, it took 145 us beside 98).
+    const uint32_t y0 = min(r0 + x * 128, pair0 + pair_rows - 1), y1 = min(r0 + x * 128 + 127, pair0 + pair_rows - 1);
+    const int32_t all_last = length ? first + static_cast<int32_t>(y0 / group) : -1;
     const int32_t all_from =
-        a.window ? first + static_cast<int32_t>((r0 + x1) / group) - static_cast<int32_t>(a.window) + 1 : 0;
+        a.window ? first + static_cast<int32_t>(y1 / group) - static_cast<int32_t>(a.window) + 1 : 0;
     const uint32_t lanes = (warp & 3) * 32 << 16;
     const uint32_t s_at = taddr + lanes + x * KT, o_at = taddr + lanes + Sh::kOutCol + x * D;
     float ref = -CUDART_INF_F, l = 0.f;
@@ -492,11 +502,12 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
             p[k / 2] = pack_f16(u, v);
           }
           tmem_st16_async(s_at + c / 2, p);
-          if (c + 32 == KT / 2) {              // the first half may go ahead
+          constexpr uint32_t kPart = KT / Sh::kParts;
+          if ((c + 32) % kPart == 0 && c + 32 < KT) {   // a part may go ahead
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_p(&bar.p_full[x][0]);
+            if (lane == 0) arrive_p(&bar.p_full[x][c / kPart]);
           }
         }
         const float2 total = both(add2(sum0, sum1));
@@ -507,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_p(&bar.p_full[x][1]);
+      if (lane == 0) arrive_p(&bar.p_full[x][Sh::kParts - 1]);
     }
     if (tl.count) wait(&bar.o_done[x], 0);
     tc_fence_after();
@@ -751,17 +762,17 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
         __syncwarp();
         wait(&bar.v_full[b], parity);
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
+        for (uint32_t h = 0; h < Sh::kParts; ++h) {
           wait(&bar.p_full[x][h], j & 1);
           if (dead) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (uint32_t k = h * (KT / 32); k < (h + 1) * (KT / 32); ++k)   // 64 tokens a region
+            for (uint32_t k = h * (KT / 16 / Sh::kParts); k < (h + 1) * (KT / 16 / Sh::kParts); ++k)   // 64 tokens a region
               umma_f16_ts<PAIR>(o_at, s_at + 8 * k,
                                 v_desc + b * (Sh::kBuf / 16) + (k >> 2) * (D / PAIR * 128 / 16) + 2 * (k & 3), kPV,
                                 (j | k) != 0);
-            if (h) commit<PAIR>(&bar.v_empty[b]);
+            if (h == Sh::kParts - 1) commit<PAIR>(&bar.v_empty[b]);
           }
           __syncwarp();
         }
@@ -796,12 +807,30 @@ cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
                           Sh::kThreads, bytes, st, PAIR, kv, a);
 }
 
+// Whether pairs serve a call's sequences of 128 channels.  Per token tile a pair's CTA
+// takes 97 us / 47 where a single one takes 110 (8 x 4 heads over 6000 tokens), but a
+// sequence whose rows end in the pair's first 256 leaves the second CTA without any.
+// So pairs serve as long as they need no more rounds of CTAs on the SMs; measured pairs :
+// single, 8 x 4 heads, sequences alike within a factor of two: 2 of 2048 rows over
+// 6000 tokens 109 : 119 us, 8 of up to 260 108 : 121, 8 of up to 768 210 : 232; but with
+// a round more, 32 of up to 260 over 1024 114 : 83, 32 of up to 768 207 : 159.  Over few
+// tokens, which the host does not know, a pair's start shows: 8 of 512 rows over 512 29 : 26.
+bool in_pairs(const KvDev& kv, const KvQuery& a) {
+  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, most = static_cast<uint64_t>(a.max_new) * a.group;
+  if (most <= 256) return false;
+  // as many sequences alike as the rows make; short ones beside long ones do not count
+  const uint64_t seqs = std::max<uint64_t>(1, std::min<uint64_t>(a.n_seqs, 2 * rows / most));
+  const uint64_t each = std::min(most, (rows + seqs - 1) / seqs), sms = kv_sm_count();
+  auto rounds = [&](uint64_t ctas) { return (ctas * seqs * kv.heads + sms - 1) / sms; };
+  return rounds((each + 511) / 512 * 2) <= rounds((each + 255) / 256);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   switch (kv.dim) {
     case 64: return prefill<64, 1>(kv, a, st);
-    case 128: return static_cast<uint64_t>(a.max_new) * a.group > kPairRows ? prefill<128, 2>(kv, a, st) : prefill<128, 1>(kv, a, st);
+    case 128: return in_pairs(kv, a) ? prefill<128, 2>(kv, a, st) : prefill<128, 1>(kv, a, st);
     default: return prefill<256, 1>(kv, a, st);
   }
 }

@@ -253,6 +253,18 @@ def test_chunks_over_a_long_context(dim, page, kv, group, new, window, sinks):
     np.testing.assert_array_equal(first, again)
 
 
+# Sequences that end anywhere in the tiles of rows of their CTAs: so many rows that pairs of CTAs take them, and
+# the longest just above one CTA's rows, where single CTAs do.
+@pytest.mark.parametrize("new", [[130, 65, 100, 70], [65, 33, 33, 40]], ids=["pairs", "single"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_ragged_row_tiles(new, window, sinks):
+    rng = np.random.default_rng(sum(new) + window)
+    c = make(n_pages=40, page=64, kv=24, dim=128, rows=4, cols=7)
+    lengths = [390, 65, 257, 128]
+    held = fill(c, [2, 0, 3, 1], lengths, rng, bf16=True)
+    attend_and_compare(c, held, [2, 0, 3, 1], new, 96, rng, True, window, sinks)
+
+
 @pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
 def test_many_sequences_of_every_length(bf16):
     rng = np.random.default_rng(11)
