@@ -770,8 +770,8 @@ cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& call, cudaStream
   // group of rows and token tile, k_kv_prefill one for a CTA's token tile, whether its
   // rows are full or not; they break even at 4 groups an SM for each round of the
   // other's CTAs (all lengths alike, 16 sequences over 4096 tokens, 8 x 4 heads of 128:
-  // 12 new tokens 76 here and 82 us there, 24 new tokens 125 and 85; one sequence over
-  // 16384, 192 new tokens: 232 and 294).  Where the other is used, sequences of up to
+  // 12 new tokens 74 here and 82 us there, 24 new tokens 124 and 85; one sequence over
+  // 16384, 192 new tokens: 230 and 262).  Where the other is used, sequences of up to
   // kFew rows (new tokens x query heads of a kv head) stay here.  f32 calls need the
   // exact products of this one.
   constexpr uint32_t kFew = 48;
