@@ -521,7 +521,8 @@ ovl_status ovl_debug_inject(ovl_ctx* ctx, uint32_t phase, ovl_status code);
  * seqs, tables and lengths are read on the device, so nothing here waits for
  * the host and every call can be captured in a CUDA graph.  What only the
  * device can see is checked there: a row, page, length or index out of range,
- * a row listed twice, or too few free pages is latched as a status code that
+ * a row listed twice, a token that tok_off gives to no sequence, or too few free
+ * pages is latched as a status code that
  * ovl_kv_check returns and clears; ovl_kv_extend, _fork, _compact and _release
  * then change nothing, ovl_kv_append writes and ovl_kv_read and
  * ovl_kv_attention return the rest (zeros for a token that cannot be reached;

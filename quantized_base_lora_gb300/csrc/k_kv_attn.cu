@@ -106,6 +106,36 @@ __device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[N], uint32_t i) 
   }
 }
 
+// Whether sequence i's part of tok_off names tokens of the call.
+__device__ __forceinline__ bool owns(const KvQuery& a, uint32_t i) {
+  const int32_t o0 = a.off[i], o1 = a.off[i + 1];
+  return o0 >= 0 && o1 >= o0 && static_cast<uint32_t>(o1) <= a.n_tokens;
+}
+
+// Zeros for the tokens that no sequence owns (a call padded beyond tok_off's last
+// entry, or a tok_off that does not ascend from 0), a token a warp; latched.
+__device__ __forceinline__ void zero_strays(const KvDev& kv, const KvQuery& a, uint32_t head_bytes) {
+  const uint32_t lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (blockIdx.x == 0 && threadIdx.x == 0) kv_latch(kv, OVL_E_ARG);
+  const uint32_t words = head_bytes / 16 * a.heads;
+  const uint64_t stride = a.out_stride * (a.bf16 ? 2 : 4);
+#pragma unroll 1
+  for (uint64_t t = blockIdx.x * warps + (threadIdx.x >> 5); t < a.n_tokens; t += static_cast<uint64_t>(gridDim.x) * warps) {
+    bool owned = false;
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < a.n_seqs && !owned; i0 += 32) {
+      const uint32_t i = i0 + lane;
+      const bool mine = i < a.n_seqs && owns(a, i) && static_cast<uint64_t>(a.off[i]) <= t &&
+                        t < static_cast<uint64_t>(a.off[i + 1]);
+      owned = __any_sync(0xffffffffu, mine);
+    }
+    if (owned) continue;
+    uint4* const to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + t * stride);
+#pragma unroll 1
+    for (uint32_t w = lane; w < words; w += 32) to[w] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // What the rows of one sequence see, in tiles.
 struct Span {
   int32_t length;      // 0 if the row cannot be used
@@ -119,7 +149,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const KvDev& kv, const KvQuery& a, uint32_t i, bool report) {
   Span s{};
   const int32_t row = a.seqs[i], o0 = a.off[i], o1 = a.off[i + 1];
-  if (o0 < 0 || o1 < o0 || static_cast<uint32_t>(o1) > a.n_tokens) {
+  if (!owns(a, i)) {
     if (report) kv_latch(kv, OVL_E_ARG);
     return s;
   }
@@ -172,12 +202,16 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
   griddep_launch_dependents();
   griddep_wait();
-  // ---- tiles before every sequence
+  // ---- tiles before every sequence, and whether tok_off gives every token to one
   uint64_t base = 0;
+  bool strays = false;
   for (uint32_t i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
     const uint32_t i = i0 + tid;
     uint64_t w = 0;
+    bool gap = false;
     if (i < a.n_seqs) {
+      gap = !owns(a, i) || (i == 0 && a.off[0] != 0) ||
+            (i + 1 == a.n_seqs && static_cast<uint32_t>(a.off[a.n_seqs]) != a.n_tokens);
       const Span s = span_of(kv, a, i, blockIdx.x == 0);
       w = static_cast<uint64_t>(s.tiles) * kv.heads * ((s.tokens * rows_group + kRows - 1) / kRows);
     }
@@ -195,8 +229,9 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       base += s_warp[k];
     }
     if (i < a.n_seqs) before[i] = add + inc - w;
-    __syncthreads();
+    strays |= __syncthreads_or(gap) != 0;
   }
+  if (strays) zero_strays(kv, a, D * (BF16 ? 2 : 4));
   if (tid == 0) before[a.n_seqs] = base;
   __syncthreads();
   const uint64_t total = base;

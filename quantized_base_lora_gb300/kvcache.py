@@ -134,6 +134,8 @@ class KvCache:
         n = seqs.shape[0]
         k = torch.empty((n_tokens, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
         v = torch.empty_like(k)
+        if n == 0:                                   # no sequence, so no call: tokens that no one owns are zeros
+            return k.zero_(), v.zero_()
         st = lib.ovl_kv_read(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
                              n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
         if st:
@@ -154,6 +156,8 @@ class KvCache:
             op, o_tokens, o_heads, o_code, os_ = self._tokens("out", out)
             if (o_tokens, o_heads, o_code) != (tokens, heads, code):
                 raise ValueError("out must have q's shape and type")
+        if n == 0:
+            return out.zero_()
         st = lib.ovl_kv_attention(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1),
                                   n, tokens, max_new, qp, code, heads, qs, self._scale if scale is None else scale,
                                   window, sinks, op, os_, _raw_stream(self._index))
