@@ -9,19 +9,24 @@
 // Mathematics.  With code = c + 8 and one scale d for 32 channels,
 //   s_j = sum_b dK_jb (sum_{i in b} c_ji q_i),   o = sum_j p_j dV_jb c_j,
 // so the codes go into the MMA as they are: small integers, exact in f16.  Bits
-// 4 i and 16 + 4 i of a word are the two halves of a pair; one mask with an
-// exponent makes them 1024 + code (even i) or 1024 + 16 code (odd i).  bf16
-// calls leave keys like that: odd channels' q is divided by 16, and the constants'
-// share sum_b dK_jb Q_b, Q_b a weighted sum of q over the block, is one more MMA
-// (scales against Q, Q in two f16 parts) that the scores start from.  The scale of
-// a key block multiplies its accumulator (fp32); the scale of a value block
-// multiplies p, once a block.  Nothing is dequantized in memory.  S^T = K Q^T has
-// tokens as rows, so its accumulator has to be transposed to become the second
-// operand of O^T = V^T P: one movmatrix for 8x8.
+// 4 i and 16 + 4 i of a word are the two halves of a pair.  For keys in bf16 calls
+// a mask alone makes operands of them: the bits of a subnormal, code 2^-24 (even
+// i) or 16 code 2^-24 (odd i).  Odd channels' q is divided by 16, and the share of
+// the 8 in every code, sum_b dK_jb Q_b with Q_b = -8 sum_i q_i over the block, is
+// one more MMA (scales against Q, Q in two f16 parts) that the scores start from:
+// of the size of the rest, so nothing of the 32-bit sums is lost to it (as
+// 1024 + code, from which 1032 sum_i q_i has to be taken, scores were off by 100
+// times as much).  Elsewhere the same mask with an exponent gives 1024 + code and
+// 1024 + 16 code, and one instruction a pair makes code - 8 of it, exactly.  The
+// scale of a key block multiplies its accumulator (fp32); the scale of a value
+// block multiplies p, once a block.  Nothing is dequantized in memory.
+// S^T = K Q^T has tokens as rows, so its accumulator has to be transposed to
+// become the second operand of O^T = V^T P: one movmatrix for 8x8.
 //
 // Precision.  A row of q is scaled by a power of two into f16's range (undone in
-// fp32): exact for bf16 down to 2^-13 of the row's maximum and within 2^-21 of it
-// below, and as two f16 parts 24 bits of an fp32 q.  The running reference of the softmax is
+// fp32): exact for bf16 down to 2^-28 of the row's maximum (2^-24 in odd channels),
+// and within 2^-23 of each element of an fp32 q as two f16 parts (2^-34 of the
+// row's maximum where that is more).  The running reference of the softmax is
 // max_j(s_j) + E, E chosen from the tile's largest value scale so that p dV stays
 // below 2^15, up to 2^6 of it for a reference that is only moved when it trails by
 // more: bf16 calls round p and p dV to f16 (11 bits each), f32 calls keep
@@ -242,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
   uint8_t* const my_ring = ring + warp * St::kWarpBytes;
   uint32_t slot = 0;                          // of the ring, in bytes, across segments
-  const float scale2 = fabsf(a.scale) * kLog2e;   // the sign goes into q
+  // the sign goes into q; the key codes of bf16 calls stand for 2^-24 of themselves
+  const float scale2 = fabsf(a.scale) * kLog2e * (BF16 ? 0x1p24f : 1.f);
   uint32_t magic;
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
     // ---- the rows: q as the MMA's second operand, and where each column looks
     uint32_t qf[NT][NS][NB][4];
-    uint32_t qs[NT][2];                       // bf16 calls: the constants' share, B operand against the key scales
+    uint32_t qs[NT][2];                       // bf16 calls: the share of the codes' 8, B operand against the key scales
     float to_log2[NT][2];                     // scale, log2(e) and the row's power of two
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -398,9 +404,9 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(kUp - ex).  bf16 calls
-      // keep the constants' share inside f16, f32 calls the second part's small end.
-      constexpr uint32_t kUp = BF16 ? 0 : 9;
+      // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(kUp - ex): as far up
+      // as f16 goes for a bf16 number, and for two parts so that both keep their small end.
+      constexpr uint32_t kUp = BF16 ? 15 : 9;
       const uint32_t ex = min(max(__float_as_uint(top) >> 23, kUp + 1), 253u);
       const float up = copysignf(__uint_as_float((254u + kUp - ex) << 23), a.scale), down = __uint_as_float((ex - kUp) << 23);
 #pragma unroll
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           }
         }
         if constexpr (BF16) {
-          float c = -1032.f * even - 72.f * odd;
+          float c = -0x1p-21f * (even + odd);       // -8 2^-24; below 1, since q is below 2^16
           c += __shfl_xor_sync(0xffffffffu, c, 1);
           sums[b] = c + __shfl_xor_sync(0xffffffffu, c, 2);
         }
@@ -441,8 +447,9 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           if (NB == 8 ? t == i : t == i + NB / 2) qs[nt][NB == 8] = rest[i];
         }
       }
-      to_log2[nt][0] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t);
-      to_log2[nt][1] = scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      // finite, so that a score of 0 stays one: above 2^128 only one token counts anyway
+      to_log2[nt][0] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t), 0x1.fffffep127f);
+      to_log2[nt][1] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4), 0x1.fffffep127f);
     }
     // tiles that every row sees whole need no mask
     const uint32_t i0 = r0 / rows_group, i1 = (r0 + n_rows - 1) / rows_group;
@@ -495,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t x[4], y[4];
-          pairs<!BF16>(k0[b], magic, x);
-          pairs<!BF16>(k1[b], magic, y);
+          if constexpr (BF16) masked_pairs(k0[b], x), masked_pairs(k1[b], y);
+          else signed_pairs(k0[b], magic, x), signed_pairs(k1[b], magic, y);
           const float2 e0 = halves(d0[b / 2]), e1 = halves(d1[b / 2]);
           const float f0 = b & 1 ? e0.y : e0.x, f1 = b & 1 ? e1.y : e1.x;
 #pragma unroll
@@ -634,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         for (int b = 0; b < NB; ++b) {
           const uint32_t pick = b & 1 ? 0x7632u : 0x5410u;
           uint32_t x[4], y[4];
-          pairs<true>(__byte_perm(va[b / 2], va[NB / 2 + b / 2], pick), magic, x);
-          pairs<true>(__byte_perm(vb[b / 2], vb[NB / 2 + b / 2], pick), magic, y);
+          signed_pairs(__byte_perm(va[b / 2], va[NB / 2 + b / 2], pick), magic, x);
+          signed_pairs(__byte_perm(vb[b / 2], vb[NB / 2 + b / 2], pick), magic, y);
           const __half2 e0 = *reinterpret_cast<const __half2*>(&d0[b / 2]);
           const __half2 e1 = *reinterpret_cast<const __half2*>(&d1[b / 2]);
 #pragma unroll

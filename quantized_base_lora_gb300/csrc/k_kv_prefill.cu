@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
             const __half2 d2 = *reinterpret_cast<const __half2*>(&d[i / 2]);
             const __half2 dd = i & 1 ? __high2half2(d2) : __low2half2(d2);
             uint32_t v[4];
-            pairs<true>(kw[k][i], magic, v);
+            signed_pairs(kw[k][i], magic, v);
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[x] = mul_f16x2(v[x], dd);
             const uint32_t c = 4 * i + part;   // chunk of 8 channels
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
 #pragma unroll
             for (uint32_t t = 0; t < 4; ++t) {
               uint32_t x[4];
-              pairs<true>(__byte_perm(vw[2 * t][w], vw[2 * t + 1][w], pick), magic, x);
+              signed_pairs(__byte_perm(vw[2 * t][w], vw[2 * t + 1][w], pick), magic, x);
               const uint32_t dd = __byte_perm(d[2 * t], d[2 * t + 1], pick);
 #pragma unroll
               for (uint32_t c = 0; c < 4; ++c) v[c][t] = mul_f16x2(x[c], dd);

@@ -71,21 +71,22 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t magic) {
   return r;
 }
 
-// The four pairs of a word's codes in f16: 1024 + code, 1024 + 16 code, and both
-// again, or exactly code - 8.  magic: 0x64006400.
-template <bool SIGNED>
-__device__ __forceinline__ void pairs(uint32_t w, uint32_t magic, uint32_t (&x)[4]) {
+// The four pairs of a word's codes in f16.  As they lie, the bits of subnormals:
+// code 2^-24 in pairs 0 and 2, 16 code 2^-24 in pairs 1 and 3.
+__device__ __forceinline__ void masked_pairs(uint32_t w, uint32_t (&x)[4]) {
   const uint32_t h = w >> 8;
-  x[0] = mask_or<0x000f000fu>(w, magic);
-  x[1] = mask_or<0x00f000f0u>(w, magic);
-  x[2] = mask_or<0x000f000fu>(h, magic);
-  x[3] = mask_or<0x00f000f0u>(h, magic);
-  if constexpr (SIGNED) {
-    x[0] = sub_f16x2(x[0], 0x64086408u);                  // - 1032
-    x[1] = fma_f16x2(x[1], 0x2c002c00u, 0xd480d480u);     // / 16 - 72
-    x[2] = sub_f16x2(x[2], 0x64086408u);
-    x[3] = fma_f16x2(x[3], 0x2c002c00u, 0xd480d480u);
-  }
+  x[0] = w & 0x000f000fu;
+  x[1] = w & 0x00f000f0u;
+  x[2] = h & 0x000f000fu;
+  x[3] = h & 0x00f000f0u;
+}
+// Exactly code - 8, from 1024 + code and 1024 + 16 code.  magic: 0x64006400.
+__device__ __forceinline__ void signed_pairs(uint32_t w, uint32_t magic, uint32_t (&x)[4]) {
+  const uint32_t h = w >> 8;
+  x[0] = sub_f16x2(mask_or<0x000f000fu>(w, magic), 0x64086408u);                // - 1032
+  x[1] = fma_f16x2(mask_or<0x00f000f0u>(w, magic), 0x2c002c00u, 0xd480d480u);   // / 16 - 72
+  x[2] = sub_f16x2(mask_or<0x000f000fu>(h, magic), 0x64086408u);
+  x[3] = fma_f16x2(mask_or<0x00f000f0u>(h, magic), 0x2c002c00u, 0xd480d480u);
 }
 
 // Adds 1, returns what was there; releases and acquires at the GPU's scope.

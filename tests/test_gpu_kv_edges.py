@@ -58,3 +58,47 @@ def test_a_call_without_sequences_returns_zeros():
               *c.read(0, none, off, 3)):
         assert (t == 0).all()
     c.check()
+
+
+# ---------------------------------------------------------------- precision of bf16 calls
+
+@pytest.mark.parametrize("dim,most", [(64, 1), (128, 1), (256, 1), (64, 9), (128, 9)])   # 9: two tiles of rows
+def test_scores_of_bf16_calls_are_32_bit(dim, most):
+    """Queries of one sign and two keys whose scores, in the thousands, all but agree: what the scores lose is what the
+    outputs show.  A score is summed in 32 bits, three roundings a block of partial sums that are at most
+    C = scale sum d code |q|, each within 2^-23 and most of them of a part of C: 2^-22 C in the mean square is more
+    than that.  Two tokens of weight near 1/2 and values near +-1: half of the difference of their two errors.  The
+    weights are rounded to 11 bits twice, the output to 8."""
+    rng = np.random.default_rng(dim + most)
+    n, kv, blocks = 64, 8, dim // 32
+    qs = torch.from_numpy((8 * 2 ** (-6 * rng.random((n, kv, dim)))).astype(np.float32)).bfloat16()
+    x = qs.double().numpy()
+    a = rng.integers(4, 7, (n, kv, dim))
+    a[..., ::32] = 8                                                 # the block's largest: d = 1 / 8
+    b = a.copy()
+    for i in range(n):
+        for h in range(kv):
+            u, w = rng.permutation(blocks)[:2]                       # two blocks; of 31 x 31 pairs the closest queries
+            cu, cw = np.arange(32 * u + 1, 32 * u + 32), np.arange(32 * w + 1, 32 * w + 32)
+            far = np.abs(x[i, h, cu][:, None] - x[i, h, cw][None])
+            at = np.where(far > 0, far, 9).argmin()
+            b[i, h, cu[at // 31]] -= 1
+            b[i, h, cw[at % 31]] += 1
+    k = torch.from_numpy(np.stack([a, b], 1).reshape(2 * n, kv, dim).astype(np.float32) / 8).cuda()
+    v = torch.ones((2 * n, kv, dim), device="cuda")
+    v[1::2] = -1
+    c = make(n_pages=n, page=16, kv=kv, dim=dim, rows=n, cols=1)
+    rows, off = dev(range(n)), dev(np.arange(n + 1) * 2)
+    c.extend(rows, off)
+    c.append(0, rows, off, k, v)
+    scale = 4096 / dim
+    got = c.attention(0, rows, dev(range(n + 1)), qs.cuda(), most, scale=scale).double().cpu().numpy()
+    c.check()
+    want, size = np.empty_like(got), 0.0
+    kk, vv = (K.values_of(*K.quantize(t.cpu().numpy())).reshape(n, 2, kv, dim) for t in (k, v))
+    for i in range(n):
+        out, spread, _ = K.attention(x[i:i + 1], kk[i], vv[i], [1], scale)
+        want[i], size = out[0], max(size, float((spread * (8 + 7) / 7).max()))        # code <= (8 + 7) / 7 |code - 8| here
+    assert size > 8000 and np.abs(want).mean() < 0.25
+    rms = np.sqrt(((got - want) ** 2).mean())
+    assert rms <= 2 ** -22 * size * 2 ** 0.5 / 2 + 2 ** -11 + 2 ** -9 * np.sqrt((want ** 2).mean()), (rms, size)
