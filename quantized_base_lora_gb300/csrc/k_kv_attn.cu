@@ -111,9 +111,8 @@ __device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[N], uint32_t i) 
   }
 }
 
-// Whether sequence i's part of tok_off names tokens of the call.
-__device__ __forceinline__ bool owns(const KvQuery& a, uint32_t i) {
-  const int32_t o0 = a.off[i], o1 = a.off[i + 1];
+// Whether a sequence's part of tok_off names tokens of the call.
+__device__ __forceinline__ bool owns(const KvQuery& a, int32_t o0, int32_t o1) {
   return o0 >= 0 && o1 >= o0 && static_cast<uint32_t>(o1) <= a.n_tokens;
 }
 
@@ -130,8 +129,11 @@ __device__ __forceinline__ void zero_strays(const KvDev& kv, const KvQuery& a, u
 #pragma unroll 1
     for (uint32_t i0 = 0; i0 < a.n_seqs && !owned; i0 += 32) {
       const uint32_t i = i0 + lane;
-      const bool mine = i < a.n_seqs && owns(a, i) && static_cast<uint64_t>(a.off[i]) <= t &&
-                        t < static_cast<uint64_t>(a.off[i + 1]);
+      bool mine = false;
+      if (i < a.n_seqs) {
+        const int32_t o0 = a.off[i], o1 = a.off[i + 1];
+        mine = owns(a, o0, o1) && static_cast<uint64_t>(o0) <= t && t < static_cast<uint64_t>(o1);
+      }
       owned = __any_sync(0xffffffffu, mine);
     }
     if (owned) continue;
@@ -149,12 +151,14 @@ struct Span {
   uint32_t lead;       // leading tiles that hold sinks outside the window
   uint32_t start;      // first tile of the window
   uint32_t tiles;      // lead + tiles of the window; at least 1, so that every row is written
+  bool gap;            // tok_off leaves out tokens here, as far as this sequence shows
 };
 
 __device__ __forceinline__ Span span_of(const KvDev& kv, const KvQuery& a, uint32_t i, bool report) {
   Span s{};
   const int32_t row = a.seqs[i], o0 = a.off[i], o1 = a.off[i + 1];
-  if (!owns(a, i)) {
+  s.gap = !owns(a, o0, o1) || (i == 0 && o0 != 0) || (i + 1 == a.n_seqs && static_cast<uint32_t>(o1) != a.n_tokens);
+  if (!owns(a, o0, o1)) {
     if (report) kv_latch(kv, OVL_E_ARG);
     return s;
   }
@@ -215,9 +219,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
     uint64_t w = 0;
     bool gap = false;
     if (i < a.n_seqs) {
-      gap = !owns(a, i) || (i == 0 && a.off[0] != 0) ||
-            (i + 1 == a.n_seqs && static_cast<uint32_t>(a.off[a.n_seqs]) != a.n_tokens);
       const Span s = span_of(kv, a, i, blockIdx.x == 0);
+      gap = s.gap;
       w = static_cast<uint64_t>(s.tiles) * kv.heads * ((s.tokens * rows_group + kRows - 1) / kRows);
     }
     uint64_t inc = w;
