@@ -29,8 +29,9 @@
 // row's maximum where that is more).  The running reference of the softmax is
 // max_j(s_j) + E, E chosen from the tile's largest value scale so that p dV stays
 // below 2^15, up to 2^6 of it for a reference that is only moved when it trails by
-// more: bf16 calls round p and p dV to f16 (11 bits each), f32 calls keep
-// p dV as two f16 parts.
+// more: bf16 calls round p and p dV to f16 (11 bits each, with 2^E moved from dV to
+// p where it is not near 1), f32 calls keep p dV as two f16 parts.  A block whose
+// scale is below 2^-14 of its tile's largest meets f16's end earlier.
 //
 // Split.  All tiles of the call, segment after segment, are dealt to the CTAs in
 // equal runs, whatever the lengths are (they are known on the device only).  The
@@ -41,7 +42,7 @@
 // the order of the CTAs, so the same call gives the same bits, and no CTA waits.
 //
 // Measured (GB300, 8 kv heads of 128, 32 query heads, bf16): 16 sequences of
-// 60001 to 131072 tokens, 289 us = 5.7 TB/s, 0.86 of the measured copy rate; 32
+// 60001 to 131072 tokens, 292 us = 5.7 TB/s, 0.85 of the measured copy rate; 32
 // sequences of 500 to 8000 tokens, 32 us (0.39: starting, joining and the first
 // loads are two thirds of it); 64 sequences, window 2048 and 4 sinks, 43 us
 // (0.50).  The copies alone take 241 us of the first, the arithmetic alone
@@ -72,6 +73,7 @@ constexpr uint32_t kThreads = kWarps * 32;
 constexpr uint32_t kTile = 32;               // tokens
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 6.f;                  // log2 by which the running reference may trail the maximum
+constexpr int32_t kNear = 6;                 // |log2| of a tile's value scales up to which p and p dV fit f16 as they are
 __device__ constexpr float kZero[4] = {0.f, 0.f, 0.f, 0.f};
 
 template <int D>
@@ -99,6 +101,9 @@ __device__ __forceinline__ void lds(const void* p, uint32_t (&w)[N]) {
     }
   }
 }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int32_t e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // w[i mod N] without indexing registers.
 template <int N>
@@ -480,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       const bool hidden = tok > all_last - static_cast<int32_t>(kTile - 1) || lost ||
                           (tok < all_from && tok > sinks - static_cast<int32_t>(kTile));
 
-      // Two copies of the tile's code: tiles that need no mask take no part of it.
+      // Two copies of the tile's code: tiles that need no mask take no part of it.  Without
+      // the mask it returns false, having changed nothing, if the tile's scales are far from 1.
       auto tile = [&](auto with_mask) {
       constexpr bool masked = decltype(with_mask)::value;
       // scores: tokens 16 sub + g and + 8 against columns 2 t, 2 t + 1
@@ -574,7 +580,13 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           }
       }
       const int32_t top_exp = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, vmax) >> 10) - 14;
-      const float above = static_cast<float>((BF16 ? max(top_exp, 0) : top_exp) - 9);
+      // bf16 calls: with |E| <= kNear p and p dV both have f16's room (11 bits down to 2^-17 of
+      // the largest weight); further off, p is multiplied and dV divided by 2^E, in the
+      // masked copy.  The other finds out where the reference has to move, which an infinite
+      // `above` makes it do (16 sequences of up to 131072 tokens: 288.6 us without the case,
+      // 291.9 like this, 297.2 with the factors in both copies).
+      const bool far = BF16 && (top_exp > kNear || top_exp < -kNear), shift = masked && far;
+      const float above = !masked && far ? CUDART_INF_F : static_cast<float>((BF16 && !far ? max(top_exp, 0) : top_exp) - 9);
       bool grew = false;
       float ref[NT][2];
 #pragma unroll
@@ -590,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           ref[nt][e] = x;
         }
       if (__any_sync(0xffffffffu, grew)) {
+        if (!masked && far) return false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -605,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float r = masked && m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];   // nothing seen yet: every weight is 0
+          float r = masked && m[nt][e] == -CUDART_INF_F ? 0.f : m[nt][e];   // nothing seen yet: every weight is 0
+          if (shift) r -= static_cast<float>(top_exp);
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub) {
 #pragma unroll
@@ -614,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
               w = ex2(fmaf(w, to_log2[nt][e], -r));
               if (masked && !(seen >> (nt * 8 + sub * 4 + e + 2 * h) & 1u)) w = 0.f;   // -inf times a scale of 0
             }
-            l[nt][e] += s[sub][nt][e] + s[sub][nt][e + 2];
+            l[nt][e] = fmaf(s[sub][nt][e] + s[sub][nt][e + 2], shift ? pow2(-top_exp) : 1.f, l[nt][e]);
           }
         }
 
@@ -635,6 +649,11 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         }
         uint32_t w0[NT], w1[NT];
         if constexpr (BF16) {
+          if (shift) {
+            const __half2 f = __float2half2_rn(pow2(-top_exp));
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) d0[i] = mul_f16x2(d0[i], f), d1[i] = mul_f16x2(d1[i], f);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             w0[nt] = pack_f16(s[sub][nt][0], s[sub][nt][1]);
@@ -671,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
         }
       }
 
+      return true;
       };
-      if (hidden) tile(std::true_type{});
-      else tile(std::false_type{});
+      if (hidden || !tile(std::false_type{})) tile(std::true_type{});
 
       // this slot is read: refill it
       __syncwarp();

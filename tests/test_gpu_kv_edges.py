@@ -102,3 +102,31 @@ def test_scores_of_bf16_calls_are_32_bit(dim, most):
     assert size > 8000 and np.abs(want).mean() < 0.25
     rms = np.sqrt(((got - want) ** 2).mean())
     assert rms <= 2 ** -22 * size * 2 ** 0.5 / 2 + 2 ** -11 + 2 ** -9 * np.sqrt((want ** 2).mean()), (rms, size)
+
+
+@pytest.mark.parametrize("size", [1e-6, 1.0, 2e5])
+@pytest.mark.parametrize("dim,most", [(64, 1), (128, 1), (256, 1), (64, 9), (128, 9)])
+def test_a_tail_of_small_weights_at_any_size_of_values(dim, most, size):
+    """Every 64th token far above the others, which hold 2 % of the weight together and all of the value but in channel
+    0: whatever the values' size is, the weights of the others may not fall out of f16.  Scores are good to 2^-18 of
+    sum |q k| (32-bit sums), weights rounded to 11 bits twice, the output to 8."""
+    rng = np.random.default_rng(dim + most)
+    n, kv = 6000, 32
+    c = make(n_pages=n // 64 + 1, page=64, kv=kv, dim=dim, rows=1, cols=n // 64 + 1, garbage=False)
+    k = torch.zeros((n, kv, dim), device="cuda")
+    k[17::64, :, 0] = -8.0                                           # held exactly: code 0, d = 1
+    v = draw(rng, (n, kv, dim)).abs().clamp(0.5, 2.0) * (size / 2)
+    v[17::64] = 0
+    v[17::64, :, 0] = -size
+    rows, off = dev([0]), dev([0, n])
+    c.extend(rows, off)
+    c.append(0, rows, off, k, v)
+    x = torch.zeros((1, kv, dim), device="cuda", dtype=torch.bfloat16)
+    x[:, :, 0] = -1.5
+    scale = 11.5 * np.log(2) / 12                                    # the others 2^-11.5 of such a token's weight
+    got = c.attention(0, rows, dev([0, 1]), x, most, scale=scale).double().cpu().numpy()
+    c.check()
+    kk, vv = (K.values_of(*K.quantize(t.cpu().numpy())) for t in (k, v))
+    w, spread, top = K.attention(x.double().cpu().numpy(), kk, vv, [n - 1], scale)
+    assert (np.abs(got - w) <= (2 ** -17 * spread + 2 ** -10) * top + 2 ** -8 * np.abs(w)).all(), \
+        float(np.abs(got - w).max() / size)
