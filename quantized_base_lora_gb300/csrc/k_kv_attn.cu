@@ -807,13 +807,13 @@ template <int D, bool BF16, int NT>
 cudaError_t decode(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   using St = Stage<D>;
   const uint32_t bytes = kWarps * (St::kWarpBytes + 2 * 4 * 8 * NT) + 8 * (a.n_seqs + 1);
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(k_kv_decode<D, BF16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 512);
-  if (ready != cudaSuccess) return ready;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_decode<D, BF16, NT>), 227 * 1024 - 512, &ready);
+  if (e != cudaSuccess) return e;
   // resident CTAs of an SM: by shared memory (1 KB of it is the system's) and by the launch bound
   const uint32_t by_smem = 228 * 1024 / (bytes + 1024 + 256), by_regs = D <= 128 && BF16 && NT == 1 ? 4 : 2;
   const uint32_t per_sm = by_smem < by_regs ? by_smem : by_regs;
-  uint32_t grid = kv_sm_count() * (per_sm ? per_sm : 1);
+  uint32_t grid = sm_count() * (per_sm ? per_sm : 1);
   if (grid > kKvMaxCtas) grid = kKvMaxCtas;
   return launch_chained(k_kv_decode<D, BF16, NT>, dim3(grid), kThreads, bytes, st, kv, a);
 }
@@ -842,7 +842,7 @@ cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& call, cudaStream
   // exact products of this one.
   constexpr uint32_t kFew = 48;
   KvQuery a = call;
-  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, small = kv.dim == 256 ? 8 : 16, sms = kv_sm_count();
+  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, small = kv.dim == 256 ? 8 : 16, sms = sm_count();
   const uint64_t groups = kv.heads * ((rows + small - 1) / small);
   const uint64_t large = kv.dim == 256 ? 128 : 256, served = std::min<uint64_t>(a.n_seqs, rows / (kFew + 1));
   const uint64_t ctas = kv.heads * std::max((rows + large - 1) / large, served);

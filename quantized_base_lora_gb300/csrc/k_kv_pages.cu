@@ -390,7 +390,7 @@ cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, c
                             const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st) {
   const cudaError_t e = launch_chained(k_kv_pages, dim3(1), kBook, 0, st, kv, what, src, dst, keep, off, n, n_keep);
   if (e != cudaSuccess) return e;
-  const uint32_t full = kv_sm_count() * 4;           // CTAs resident at a time
+  const uint32_t full = sm_count() * 4;           // CTAs resident at a time
   if (what == KvPages::kFork) {
     const uint64_t units = static_cast<uint64_t>(kv.layers) * 2 * kv.heads;
     const uint64_t per_page = (units * kv.unit_codes / 16 + kCopy * 8 - 1) / (kCopy * 8);

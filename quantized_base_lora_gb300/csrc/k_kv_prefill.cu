@@ -798,9 +798,9 @@ template <int D, int PAIR>
 cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   using Sh = Shape<D, PAIR>;
   constexpr uint32_t bytes = Sh::kSmem + 1024, rows = PAIR * Sh::kRows;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(k_kv_prefill<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (ready != cudaSuccess) return ready;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_prefill<D, PAIR>), bytes, &ready);
+  if (e != cudaSuccess) return e;
   const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + rows - 1) / rows;
   if (tiles > 65535u) return cudaErrorInvalidConfiguration;
   return launch_clustered(k_kv_prefill<D, PAIR>, dim3(PAIR * kv.heads, a.n_seqs, static_cast<uint32_t>(tiles)),
@@ -820,7 +820,7 @@ bool in_pairs(const KvDev& kv, const KvQuery& a) {
   if (most <= 256) return false;
   // as many sequences alike as the rows make; short ones beside long ones do not count
   const uint64_t seqs = std::max<uint64_t>(1, std::min<uint64_t>(a.n_seqs, 2 * rows / most));
-  const uint64_t each = std::min(most, (rows + seqs - 1) / seqs), sms = kv_sm_count();
+  const uint64_t each = std::min(most, (rows + seqs - 1) / seqs), sms = sm_count();
   auto rounds = [&](uint64_t ctas) { return (ctas * seqs * kv.heads + sms - 1) / sms; };
   return rounds((each + 511) / 512 * 2) <= rounds((each + 255) / 256);
 }

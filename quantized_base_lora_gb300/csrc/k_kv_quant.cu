@@ -193,7 +193,7 @@ dim3 grid_for(const KvDev& kv, uint32_t n_tokens) {
 template <int D>
 bool few_tokens(const KvDev& kv, uint32_t n_tokens) {
   const dim3 g = grid_for<D, 1>(kv, n_tokens);
-  return static_cast<uint64_t>(g.x) * g.z <= 4 * kv_sm_count();
+  return static_cast<uint64_t>(g.x) * g.z <= 4 * sm_count();
 }
 
 template <int D, bool BF16, uint32_t HT>

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ovl.h"
 
 namespace ovl {
@@ -101,7 +103,20 @@ struct KvQuery {
   uint32_t few;                    // rows of a sequence up to which the few-row kernel serves it
 };
 
-uint32_t kv_sm_count();
+uint32_t sm_count();             // of the current device (k_fused_gemm.cu)
+
+// Lets f use `bytes` of dynamic shared memory on the current device.  The attribute is
+// a device's own: `done` has a bit for each device that has it.
+inline cudaError_t allow_smem(const void* f, uint32_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t set = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (set == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return set;
+}
 
 // Launches f in the stream's programmatic chain: its CTAs may be scheduled while
 // the kernel before it still runs, so f calls griddep_wait() before it reads or

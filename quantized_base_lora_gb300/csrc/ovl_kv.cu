@@ -9,19 +9,6 @@
 
 namespace ovl {
 
-uint32_t kv_sm_count() {
-  static const uint32_t n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return 1u;
-    }
-    return v > 0 ? static_cast<uint32_t>(v) : 1u;
-  }();
-  return n;
-}
-
 namespace {
 
 ovl_status fail(ovl_status st, const char* msg) {

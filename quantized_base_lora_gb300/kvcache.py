@@ -10,8 +10,9 @@ device memory and streams only; all computation is libovl's.
         cache.append(layer, seqs, off, k, v)       # k, v [tokens][kv heads][head_dim]
         o = cache.attention(layer, seqs, off, q, max_new)
 
-Calls go to the current stream of the cache's device; calls on one cache must
-be ordered by streams or events, since they share its workspace."""
+Calls go to the current stream of the cache's device, whichever device is current;
+calls on one cache must be ordered by streams or events, since they share its
+workspace."""
 from __future__ import annotations
 
 import ctypes
@@ -30,6 +31,7 @@ def _stream_of(index: int) -> int:
 
 # The current stream's handle without a Stream object around it (2 us a call less), where torch offers it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class KvCache:
@@ -75,8 +77,7 @@ class KvCache:
         self = cls(codes, scales, torch.empty((max_seqs, max_pages), dtype=torch.int32, device=dev),
                    torch.empty(max_seqs, dtype=torch.int32, device=dev),
                    torch.empty(n_pages, dtype=torch.int32, device=dev))
-        with torch.cuda.device(dev):
-            self._check(lib.ovl_kv_init(self._at, self._stream()))
+        self._call(lib.ovl_kv_init)
         return self
 
     @staticmethod
@@ -84,8 +85,15 @@ class KvCache:
         if st != OVL_OK:
             raise OvlError(st, ovl_last_error(None))
 
-    def _stream(self) -> int:
-        return _raw_stream(self._index)
+    def _call(self, fn, *args):
+        """fn(the cache, *args, stream) on the cache's device (the library launches on the current one)."""
+        if _current_device() == self._index:
+            st = fn(self._at, *args, _raw_stream(self._index))
+        else:
+            with torch.cuda.device(self._index):
+                st = fn(self._at, *args, _raw_stream(self._index))
+        if st:
+            self._check(st)
 
     # The checks below run at every call, for every tensor: they read each property once.
 
@@ -114,8 +122,7 @@ class KvCache:
     def extend(self, seqs: torch.Tensor, tok_off: torch.Tensor):
         """Pages for tok_off[i+1] - tok_off[i] more tokens of row seqs[i]; length counts them."""
         n = seqs.shape[0]
-        self._check(lib.ovl_kv_extend(self._at, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
-                                      _raw_stream(self._index)))
+        self._call(lib.ovl_kv_extend, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n)
 
     def append(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
         """Write the last tokens of the rows: k, v [tokens][kv heads][head_dim] float32 or bfloat16."""
@@ -124,10 +131,8 @@ class KvCache:
         vp, v_tokens, _, v_code, vs = self._tokens("v", v, self.n_kv_heads)
         if code != v_code or tokens != v_tokens:
             raise ValueError("k and v must have one type and length")
-        st = lib.ovl_kv_append(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
-                               tokens, kp, vp, code, ks, vs, _raw_stream(self._index))
-        if st:
-            self._check(st)
+        self._call(lib.ovl_kv_append, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                   tokens, kp, vp, code, ks, vs)
 
     def read(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, n_tokens: int):
         """The values of the rows' last tokens: float32 (k, v), each [n_tokens][kv heads][head_dim]."""
@@ -136,10 +141,8 @@ class KvCache:
         v = torch.empty_like(k)
         if n == 0:                                   # no sequence, so no call: tokens that no one owns are zeros
             return k.zero_(), v.zero_()
-        st = lib.ovl_kv_read(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
-                             n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
-        if st:
-            self._check(st)
+        self._call(lib.ovl_kv_read, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                   n_tokens, k.data_ptr(), v.data_ptr())
         return k, v
 
     def attention(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, q: torch.Tensor, max_new: int,
@@ -158,33 +161,28 @@ class KvCache:
                 raise ValueError("out must have q's shape and type")
         if n == 0:
             return out.zero_()
-        st = lib.ovl_kv_attention(self._at, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1),
-                                  n, tokens, max_new, qp, code, heads, qs, self._scale if scale is None else scale,
-                                  window, sinks, op, os_, _raw_stream(self._index))
-        if st:
-            self._check(st)
+        self._call(lib.ovl_kv_attention, layer, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n,
+                   tokens, max_new, qp, code, heads, qs, self._scale if scale is None else scale, window, sinks, op, os_)
         return out
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor | None = None):
         """Row dst[i] becomes the first keep[i] tokens of row src[i] (all without keep), sharing whole pages."""
         n = src.shape[0]
-        self._check(lib.ovl_kv_fork(self._at, self._ints("src", src, n), self._ints("dst", dst, n),
-                                    None if keep is None else self._ints("keep", keep, n), n,
-                                    _raw_stream(self._index)))
+        self._call(lib.ovl_kv_fork, self._ints("src", src, n), self._ints("dst", dst, n),
+                   None if keep is None else self._ints("keep", keep, n), n)
 
     def compact(self, src: torch.Tensor, dst: torch.Tensor, keep: torch.Tensor, keep_off: torch.Tensor):
         """Row dst[i] becomes tokens keep[keep_off[i] .. keep_off[i+1] - 1] of row src[i], in fresh pages."""
         n = src.shape[0]
         m = keep.shape[0]
-        self._check(lib.ovl_kv_compact(self._at, self._ints("src", src, n), self._ints("dst", dst, n),
-                                       self._ints("keep", keep, m), self._ints("keep_off", keep_off, n + 1), n, m,
-                                       _raw_stream(self._index)))
+        self._call(lib.ovl_kv_compact, self._ints("src", src, n), self._ints("dst", dst, n), self._ints("keep", keep, m),
+                   self._ints("keep_off", keep_off, n + 1), n, m)
 
     def release(self, seqs: torch.Tensor):
         """The rows become free."""
         n = seqs.shape[0]
-        self._check(lib.ovl_kv_release(self._at, self._ints("seqs", seqs, n), n, _raw_stream(self._index)))
+        self._call(lib.ovl_kv_release, self._ints("seqs", seqs, n), n)
 
     def check(self):
         """Wait for the current stream; raise what a call latched on the device since the last check."""
-        self._check(lib.ovl_kv_check(self._at, self._stream()))
+        self._call(lib.ovl_kv_check)

@@ -1,0 +1,95 @@
+"""The torch side of the 4-bit cache without a device: what reaches the library, and on which device."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Library:
+    """Stands in for the library: records each call with the device that is current."""
+
+    def __init__(self, where):
+        self.where, self.calls = where, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, self.where["device"], args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def stand_in(monkeypatch):
+    """A cache of CPU tensors (their device's index is -1) while device 0 is current, and the library's stand-in."""
+    pytest.importorskip("quantized_base_lora_gb300")
+    from quantized_base_lora_gb300 import kvcache, ovl_kv
+    where = {"device": 0}
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, where["device"] = where["device"], self.index
+
+        def __exit__(self, *_):
+            where["device"] = self.before
+
+    lib = Library(where)
+    monkeypatch.setattr(kvcache, "lib", lib)
+    monkeypatch.setattr(kvcache, "_raw_stream", lambda index: 7000 + index)
+    monkeypatch.setattr(kvcache, "_current_device", lambda: where["device"], raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: where["device"])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    c = object.__new__(kvcache.KvCache)
+    c.kv = ovl_kv()
+    c._at, c._index, c._scale = ctypes.addressof(c.kv), -1, 0.125
+    c.device, c.n_kv_heads, c.head_dim, c.page_tokens = torch.device("cpu"), 2, 64, 16
+    return c, lib, where
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def every_call(c):
+    one, off, x = ints(0), ints(0, 1), torch.zeros((1, 2, 64))
+    c.extend(one, off)
+    c.append(0, one, off, x, x)
+    c.read(0, one, off, 1)
+    c.attention(0, one, off, x, 1)
+    c.attention(0, one, off, x, 1, out=torch.zeros((1, 2, 64)))
+    c.fork(one, ints(1))
+    c.fork(one, ints(1), ints(1))
+    c.compact(one, ints(1), ints(0), off)
+    c.release(one)
+    c.check()
+
+
+def test_every_call_runs_on_the_caches_device(stand_in):
+    c, lib, where = stand_in
+    every_call(c)
+    assert [n for n, _, _ in lib.calls] == ["ovl_kv_" + n for n in (
+        "extend", "append", "read", "attention", "attention", "fork", "fork", "compact", "release", "check")]
+    for name, device, args in lib.calls:
+        assert device == -1, name                        # the cache's device was current
+        assert args[0] == c._at and args[-1] == 6999     # and the stream is that device's
+    assert where["device"] == 0                          # the caller's device is current again
+
+
+def test_a_cache_on_the_current_device_changes_no_device(stand_in, monkeypatch):
+    c, lib, where = stand_in
+    where["device"] = -1
+    monkeypatch.setattr(torch.cuda, "device", None)
+    every_call(c)
+    assert all(device == -1 for _, device, _ in lib.calls) and len(lib.calls) == 10
+
+
+def test_the_device_is_restored_when_a_call_is_refused(stand_in):
+    c, lib, where = stand_in
+    from quantized_base_lora_gb300 import OvlError
+    lib.ovl_kv_release = lambda *a: -1
+    with pytest.raises(OvlError):
+        c.release(ints(0))
+    assert where["device"] == 0
