@@ -629,6 +629,13 @@ ovl_status ovl_kv_release(const ovl_kv* kv, const int32_t* seqs, uint32_t n, voi
  * and clear it.  No counterpart in the source pages. */
 ovl_status ovl_kv_check(const ovl_kv* kv, void* stream);
 
+/* Testing aid: which kernels ovl_kv_attention would launch for a call of these
+ * sizes on a device of n_sms SMs (no device is looked at).  *route: 0 the one for
+ * few rows alone; 1 the one for many rows beside it; 2 that one in pairs of CTAs.
+ * No counterpart in the source pages. */
+ovl_status ovl_debug_kv_route(const ovl_kv* kv, uint32_t n_seqs, uint32_t n_tokens, uint32_t max_new, uint32_t dtype,
+                              uint32_t n_heads, uint32_t n_sms, uint32_t* route);
+
 /* Message of the last failed call on ctx (static storage owned by ctx; "" after
  * success).  ctx NULL returns the message of the last failed call that has no
  * context on this thread (ovl_create, ovl_manifest_parse, ovl_kv_*).

@@ -144,6 +144,7 @@ def _load():
         "ovl_kv_compact": ([P, P, P, P, P, U32, U32, P], I32),
         "ovl_kv_release": ([P, P, U32, P], I32),
         "ovl_kv_check": ([P, P], I32),
+        "ovl_debug_kv_route": ([P, U32, U32, U32, U32, U32, U32, C.POINTER(U32)], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -160,7 +161,7 @@ EXPORTED = ("ovl_create", "ovl_destroy", "ovl_load_base", "ovl_stage_adapter", "
             "ovl_content_digest", "ovl_version", "ovl_dualpath_forward_noalloc", "ovl_stage_activations",
             "ovl_manifest_parse", "ovl_activate_manifest", "ovl_kv_workspace_bytes", "ovl_kv_init", "ovl_kv_extend",
             "ovl_kv_append", "ovl_kv_read", "ovl_kv_attention", "ovl_kv_fork", "ovl_kv_compact", "ovl_kv_release",
-            "ovl_kv_check")
+            "ovl_kv_check", "ovl_debug_kv_route")
 
 
 class OvlError(RuntimeError):
@@ -435,3 +436,9 @@ def ovl_kv_release(kv, seqs: int, n: int, stream: int = 0) -> int:
 
 def ovl_kv_check(kv, stream: int = 0) -> int:
     return lib.ovl_kv_check(_kv(kv), stream)
+
+
+def ovl_debug_kv_route(kv, n_seqs: int, n_tokens: int, max_new: int, dtype: int, n_heads: int, n_sms: int):
+    out = C.c_uint32(0)
+    st = lib.ovl_debug_kv_route(_kv(kv), n_seqs, n_tokens, max_new, dtype, n_heads, n_sms, C.byref(out))
+    return st, int(out.value)

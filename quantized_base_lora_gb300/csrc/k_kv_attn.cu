@@ -830,32 +830,39 @@ cudaError_t attend_dim(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& call, cudaStream_t st) {
+// Rows (new tokens x query heads of a kv head) of a sequence up to which this kernel
+// serves it where the other is used.
+constexpr uint32_t kFew = 48;
+
+KvRoute kv_route(const KvDev& kv, const KvQuery& a, uint32_t sms) {
   // Which kernel.  Measured (bf16, contexts of 1024 to 16384 tokens, 1 to 64 sequences of
   // 3 to 192 new tokens, head_dim 64, 128 and 256): this one takes a constant time for a
   // group of rows and token tile, k_kv_prefill one for a CTA's token tile, whether its
   // rows are full or not; they break even at 4 groups an SM for each round of the
   // other's CTAs (all lengths alike, 16 sequences over 4096 tokens, 8 x 4 heads of 128:
   // 12 new tokens 74 here and 82 us there, 24 new tokens 124 and 85; one sequence over
-  // 16384, 192 new tokens: 230 and 262).  Where the other is used, sequences of up to
-  // kFew rows (new tokens x query heads of a kv head) stay here.  f32 calls need the
-  // exact products of this one.
-  constexpr uint32_t kFew = 48;
-  KvQuery a = call;
-  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, small = kv.dim == 256 ? 8 : 16, sms = sm_count();
-  const uint64_t groups = kv.heads * ((rows + small - 1) / small);
+  // 16384, 192 new tokens: 230 and 262).  f32 calls need the exact products of this one,
+  // and so do sequences of more row tiles than the other's grid has.
+  const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, most = static_cast<uint64_t>(a.max_new) * a.group;
+  const uint64_t groups = kv.heads * ((rows + (kv.dim == 256 ? 8 : 16) - 1) / (kv.dim == 256 ? 8 : 16));
   const uint64_t large = kv.dim == 256 ? 128 : 256, served = std::min<uint64_t>(a.n_seqs, rows / (kFew + 1));
   const uint64_t ctas = kv.heads * std::max((rows + large - 1) / large, served);
-  const bool many = a.bf16 && static_cast<uint64_t>(a.max_new) * a.group > kFew &&
-                    groups > 4 * sms * ((ctas + sms - 1) / sms);
-  a.few = many ? kFew : 0xffffffffu;
+  if (!a.bf16 || most <= kFew || (most + large - 1) / large > 65535 || groups <= 4 * sms * ((ctas + sms - 1) / sms))
+    return KvRoute::kFewRows;
+  return kv.dim == 128 && kv_in_pairs(kv, a, sms) ? KvRoute::kPairs : KvRoute::kSingle;
+}
+
+cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& call, cudaStream_t st) {
+  KvQuery a = call;
+  const KvRoute route = kv_route(kv, a, sm_count());
+  a.few = route == KvRoute::kFewRows ? 0xffffffffu : kFew;
   cudaError_t e;
   switch (kv.dim) {
     case 64: e = attend_dim<64>(kv, a, st); break;
     case 128: e = attend_dim<128>(kv, a, st); break;
     default: e = attend_dim<256>(kv, a, st); break;
   }
-  return e == cudaSuccess && many ? launch_kv_prefill(kv, a, st) : e;
+  return e == cudaSuccess && route != KvRoute::kFewRows ? launch_kv_prefill(kv, a, route, st) : e;
 }
 
 }  // namespace ovl

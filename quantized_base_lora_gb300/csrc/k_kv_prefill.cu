@@ -8,7 +8,7 @@
 //   S = Q K^T   Q and K in shared memory, S in tensor memory
 //   O += P V    P over S's own columns in tensor memory, V^T in shared memory
 // so the scores never leave the SM.  Most sequences of more than 256 rows of 128
-// channels (in_pairs) are taken by pairs of CTAs, clusters of two: each has its own
+// channels (kv_in_pairs) are taken by pairs of CTAs, clusters of two: each has its own
 // 256 rows, converts half of a tile - half of the tokens for K, half of the
 // channels for V - and every MMA runs over both CTAs' rows with the two halves as
 // its second operand, issued by the first.  Roles, each its own warps:
@@ -801,11 +801,12 @@ cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_kv_prefill<D, PAIR>), bytes, &ready);
   if (e != cudaSuccess) return e;
-  const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + rows - 1) / rows;
-  if (tiles > 65535u) return cudaErrorInvalidConfiguration;
+  const uint64_t tiles = (static_cast<uint64_t>(a.max_new) * a.group + rows - 1) / rows;   // at most 65535: kv_route
   return launch_clustered(k_kv_prefill<D, PAIR>, dim3(PAIR * kv.heads, a.n_seqs, static_cast<uint32_t>(tiles)),
                           Sh::kThreads, bytes, st, PAIR, kv, a);
 }
+
+}  // namespace
 
 // Whether pairs serve a call's sequences of 128 channels.  Per token tile a pair's CTA
 // takes 97 us / 47 where a single one takes 110 (8 x 4 heads over 6000 tokens), but a
@@ -815,22 +816,20 @@ cudaError_t prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
 // 6000 tokens 109 : 119 us, 8 of up to 260 108 : 121, 8 of up to 768 210 : 232; but with
 // a round more, 32 of up to 260 over 1024 114 : 83, 32 of up to 768 207 : 159.  Over few
 // tokens, which the host does not know, a pair's start shows: 8 of 512 rows over 512 29 : 26.
-bool in_pairs(const KvDev& kv, const KvQuery& a) {
+bool kv_in_pairs(const KvDev& kv, const KvQuery& a, uint32_t sms) {
   const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.group, most = static_cast<uint64_t>(a.max_new) * a.group;
   if (most <= 256) return false;
   // as many sequences alike as the rows make; short ones beside long ones do not count
   const uint64_t seqs = std::max<uint64_t>(1, std::min<uint64_t>(a.n_seqs, 2 * rows / most));
-  const uint64_t each = std::min(most, (rows + seqs - 1) / seqs), sms = sm_count();
+  const uint64_t each = std::min(most, (rows + seqs - 1) / seqs);
   auto rounds = [&](uint64_t ctas) { return (ctas * seqs * kv.heads + sms - 1) / sms; };
   return rounds((each + 511) / 512 * 2) <= rounds((each + 255) / 256);
 }
 
-}  // namespace
-
-cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& a, cudaStream_t st) {
+cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& a, KvRoute route, cudaStream_t st) {
   switch (kv.dim) {
     case 64: return prefill<64, 1>(kv, a, st);
-    case 128: return in_pairs(kv, a) ? prefill<128, 2>(kv, a, st) : prefill<128, 1>(kv, a, st);
+    case 128: return route == KvRoute::kPairs ? prefill<128, 2>(kv, a, st) : prefill<128, 1>(kv, a, st);
     default: return prefill<256, 1>(kv, a, st);
   }
 }

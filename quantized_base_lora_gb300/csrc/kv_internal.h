@@ -152,7 +152,12 @@ cudaError_t launch_kv_append(const KvDev& kv, uint32_t layer, const int32_t* seq
 cudaError_t launch_kv_read(const KvDev& kv, uint32_t layer, const int32_t* seqs, const int32_t* off, uint32_t n,
                            uint32_t n_tokens, float* k, float* v, cudaStream_t st);
 cudaError_t launch_kv_attention(const KvDev& kv, const KvQuery& q, cudaStream_t st);
-cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& q, cudaStream_t st);
+// Which kernels serve a call of these sizes on a device of `sms` SMs: the one for few
+// rows alone, or beside it the one for many, in single CTAs or in pairs.
+enum class KvRoute : uint32_t { kFewRows, kSingle, kPairs };
+KvRoute kv_route(const KvDev& kv, const KvQuery& q, uint32_t sms);
+bool kv_in_pairs(const KvDev& kv, const KvQuery& q, uint32_t sms);
+cudaError_t launch_kv_prefill(const KvDev& kv, const KvQuery& q, KvRoute route, cudaStream_t st);
 enum class KvPages { kExtend, kFork, kCompact, kRelease };
 cudaError_t launch_kv_pages(const KvDev& kv, KvPages what, const int32_t* src, const int32_t* dst, const int32_t* keep,
                             const int32_t* off, uint32_t n, uint32_t n_keep, cudaStream_t st);

@@ -238,6 +238,25 @@ ovl_status ovl_kv_attention(const ovl_kv* kv, uint32_t layer, const int32_t* seq
   return done(launch_kv_attention(d, a, static_cast<cudaStream_t>(stream)));
 }
 
+ovl_status ovl_debug_kv_route(const ovl_kv* kv, uint32_t n_seqs, uint32_t n_tokens, uint32_t max_new, uint32_t dtype,
+                              uint32_t n_heads, uint32_t n_sms, uint32_t* out) {
+  const ovl_status st = check_dims(kv);
+  if (st != OVL_OK) return st;
+  if (!out || !n_sms || (dtype != OVL_F32 && dtype != OVL_BF16)) return fail(OVL_E_ARG, "out, n_sms or dtype");
+  if (!n_heads || n_heads % kv->n_kv_heads) return fail(OVL_E_SHAPE, "n_heads must be a multiple of n_kv_heads");
+  KvDev d{};
+  d.dim = kv->head_dim;
+  d.heads = kv->n_kv_heads;
+  KvQuery a{};
+  a.n_seqs = n_seqs;
+  a.n_tokens = n_tokens;
+  a.max_new = max_new < n_tokens ? max_new : n_tokens;
+  a.group = n_heads / kv->n_kv_heads;
+  a.bf16 = dtype == OVL_BF16;
+  *out = static_cast<uint32_t>(kv_route(d, a, n_sms));
+  return OVL_OK;
+}
+
 ovl_status ovl_kv_check(const ovl_kv* kv, void* stream) {
   KvDev d;
   const ovl_status st = check_kv(kv, &d);

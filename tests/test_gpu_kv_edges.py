@@ -130,3 +130,24 @@ def test_a_tail_of_small_weights_at_any_size_of_values(dim, most, size):
     w, spread, top = K.attention(x.double().cpu().numpy(), kk, vv, [n - 1], scale)
     assert (np.abs(got - w) <= (2 ** -17 * spread + 2 ** -10) * top + 2 ** -8 * np.abs(w)).all(), \
         float(np.abs(got - w).max() / size)
+
+
+# ---------------------------------------------------------------- sizes
+
+def test_more_row_tiles_than_the_grid_of_the_kernel_for_many_rows():
+    """16.8 million rows of one sequence.  A window of one token: every row returns its own token's values."""
+    rng = np.random.default_rng(0)
+    n, group = 16400, 1024
+    assert n * group > 65535 * 256
+    c = make(n_pages=n // 256 + 1, page=256, kv=1, dim=64, rows=1, cols=n // 256 + 1, garbage=False)
+    rows, off = dev([0]), dev([0, n])
+    c.extend(rows, off)
+    k, v = draw(rng, (n, 1, 64), True), draw(rng, (n, 1, 64), True)
+    c.append(0, rows, off, k, v)
+    x = torch.ones((n, group, 64), device="cuda", dtype=torch.bfloat16)
+    out = c.attention(0, rows, off, x, n, window=1)
+    c.check()
+    want = c.read(0, rows, off, n)[1]
+    for i in range(0, n, 1024):
+        w = want[i:i + 1024]
+        assert ((out[i:i + 1024].float() - w).abs() <= 2 ** -8 * w.abs()).all()

@@ -93,3 +93,48 @@ def test_the_device_is_restored_when_a_call_is_refused(stand_in):
     with pytest.raises(OvlError):
         c.release(ints(0))
     assert where["device"] == 0
+
+
+# ---------------------------------------------------------------- which kernel
+
+FEW, SINGLE, PAIRS = range(3)
+
+
+def route(n_seqs, n_tokens, max_new, heads, kv=8, dim=128, bf16=True, sms=152):
+    q = pytest.importorskip("quantized_base_lora_gb300")
+    d = q.ovl_kv()
+    for name, value in dict(n_pages=9, page_tokens=64, n_layers=1, n_kv_heads=kv, head_dim=dim, max_seqs=9,
+                            max_pages=9).items():
+        setattr(d, name, value)
+    st, r = q.ovl_debug_kv_route(d, n_seqs, n_tokens, max_new, q.OVL_BF16 if bf16 else q.OVL_F32, heads, sms)
+    assert st == q.OVL_OK
+    return r
+
+
+def test_which_kernel_serves_a_call():
+    assert route(32, 32, 1, 32) == FEW                                   # decode steps
+    assert route(2, 4096, 2048, 32) == PAIRS                             # chunks of prompts
+    assert route(2, 4096, 2048, 32, bf16=False) == FEW                   # which f32 calls have no other kernel for
+    assert route(4, 3108, 777, 24, kv=3, dim=64) == SINGLE
+    assert route(2, 4096, 2048, 32, dim=256) == SINGLE
+
+
+@pytest.mark.parametrize("dim,rows", [(64, 256), (128, 256), (256, 128)])
+def test_row_tiles_beyond_the_grid_stay_with_the_kernel_for_few_rows(dim, rows):
+    group, most = 8, 65535 * rows // 8
+    assert route(1, most, most, 8 * group, dim=dim) != FEW
+    assert route(1, most + 1, most + 1, 8 * group, dim=dim) == FEW
+    assert route(1, 2 ** 31 - 1, 2 ** 31 - 1, 8 * 1024, dim=dim) == FEW
+
+
+def test_refusals_of_the_route():
+    q = pytest.importorskip("quantized_base_lora_gb300")
+    d = q.ovl_kv()
+    assert q.ovl_debug_kv_route(d, 1, 1, 1, q.OVL_BF16, 8, 152)[0] == q.OVL_E_SHAPE
+    for name, value in dict(n_pages=9, page_tokens=64, n_layers=1, n_kv_heads=8, head_dim=64, max_seqs=9,
+                            max_pages=9).items():
+        setattr(d, name, value)
+    assert q.ovl_debug_kv_route(d, 1, 1, 1, 77, 8, 152)[0] == q.OVL_E_ARG
+    assert q.ovl_debug_kv_route(d, 1, 1, 1, q.OVL_BF16, 8, 0)[0] == q.OVL_E_ARG
+    assert q.ovl_debug_kv_route(d, 1, 1, 1, q.OVL_BF16, 12, 152)[0] == q.OVL_E_SHAPE
+    assert q.lib.ovl_debug_kv_route(ctypes.byref(d), 1, 1, 1, q.OVL_BF16, 8, 152, None) == q.OVL_E_ARG
