@@ -34,6 +34,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+_U32 = 1 << 32      # numbers go to the library as 32 bits without a sign, where -1 would be the largest
+
+
 class KvCache:
     """codes uint8 [pages][layers][2][kv heads][page tokens * D / 2], scales float16 [pages][layers][2][kv heads]
     [page tokens][D / 32], table int32 [rows][columns], length int32 [rows], refs int32 [pages]: contiguous, on one
@@ -126,6 +129,8 @@ class KvCache:
 
     def append(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
         """Write the last tokens of the rows: k, v [tokens][kv heads][head_dim] float32 or bfloat16."""
+        if not 0 <= layer < _U32:
+            raise ValueError(f"layer {layer} is out of range")
         n = seqs.shape[0]
         kp, tokens, _, code, ks = self._tokens("k", k, self.n_kv_heads)
         vp, v_tokens, _, v_code, vs = self._tokens("v", v, self.n_kv_heads)
@@ -136,6 +141,8 @@ class KvCache:
 
     def read(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, n_tokens: int):
         """The values of the rows' last tokens: float32 (k, v), each [n_tokens][kv heads][head_dim]."""
+        if not (0 <= layer < _U32 and 0 <= n_tokens < _U32):
+            raise ValueError(f"layer {layer} or n_tokens {n_tokens} is out of range")
         n = seqs.shape[0]
         k = torch.empty((n_tokens, self.n_kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
         v = torch.empty_like(k)
@@ -150,6 +157,8 @@ class KvCache:
                   out: torch.Tensor | None = None) -> torch.Tensor:
         """Attention of the rows' last tokens over the cache: q [tokens][heads][head_dim] -> the same shape and type.
         max_new: upper bound of the new tokens of one row; scale: 1 / sqrt(head_dim) unless given."""
+        if not (0 <= layer < _U32 and 0 <= max_new < _U32 and 0 <= window < _U32 and 0 <= sinks < _U32):
+            raise ValueError(f"layer {layer}, max_new {max_new}, window {window} or sinks {sinks} is out of range")
         n = seqs.shape[0]
         qp, tokens, heads, code, qs = self._tokens("q", q)
         if out is None:

@@ -138,3 +138,23 @@ def test_refusals_of_the_route():
     assert q.ovl_debug_kv_route(d, 1, 1, 1, q.OVL_BF16, 8, 0)[0] == q.OVL_E_ARG
     assert q.ovl_debug_kv_route(d, 1, 1, 1, q.OVL_BF16, 12, 152)[0] == q.OVL_E_SHAPE
     assert q.lib.ovl_debug_kv_route(ctypes.byref(d), 1, 1, 1, q.OVL_BF16, 8, 152, None) == q.OVL_E_ARG
+
+
+# ---------------------------------------------------------------- numbers beyond 32 bits
+
+@pytest.mark.parametrize("bad", [-1, 1 << 32, (1 << 32) + 4])
+def test_numbers_that_32_bits_would_change_are_refused(stand_in, bad):
+    """-1 sinks would be 2^32 - 1 and make every token visible; 2^32 + 4 would be 4."""
+    c, lib, _ = stand_in
+    one, off, x = ints(0), ints(0, 1), torch.zeros((1, 2, 64))
+    for kw in (dict(sinks=bad), dict(window=bad), dict(window=8, sinks=bad)):
+        with pytest.raises(ValueError):
+            c.attention(0, one, off, x, 1, **kw)
+    for call in (lambda: c.attention(bad, one, off, x, 1), lambda: c.attention(0, one, off, x, bad),
+                 lambda: c.append(bad, one, off, x, x), lambda: c.read(bad, one, off, 1),
+                 lambda: c.read(0, one, off, bad)):
+        with pytest.raises(ValueError):
+            call()
+    assert not lib.calls
+    c.attention(0, one, off, x, 1, window=(1 << 32) - 1, sinks=(1 << 32) - 1)
+    assert lib.calls[0][2][-5:-3] == ((1 << 32) - 1, (1 << 32) - 1)
