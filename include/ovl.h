@@ -567,8 +567,10 @@ ovl_status ovl_kv_extend(const ovl_kv* kv, const int32_t* seqs, const int32_t* t
  * channels contiguous; base and stride multiples of 16 bytes).  Per block of 32
  * channels d = binary16(min(max|x| / 8, 65504)) and
  * code = clamp(round_half_away(x / d), -8, 7) + 8, the base weights' q4_0 (code 8
- * where d = 0); NaN counts as 0, infinities are clipped.  No counterpart in the
- * source pages. */
+ * where d = 0); NaN counts as 0, infinities are clipped.  Quotient and rounding
+ * (trunc(t +- 0.5)) are 32-bit, as the base weights' are.  A token whose page
+ * other rows hold too (the row was forked between ovl_kv_extend and this call) is
+ * not written and latched as OVL_E_STATE.  No counterpart in the source pages. */
 ovl_status ovl_kv_append(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,
                          uint32_t n_seqs, uint32_t n_tokens, const void* k, const void* v, uint32_t dtype,
                          uint64_t k_stride, uint64_t v_stride, void* stream);

@@ -78,10 +78,11 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float
 // a channel) with the arithmetic close behind: most blocks are tame - finite and
 // neither so small nor so large that d is subnormal or saturated - and need no
 // care for single channels.  Measured: 26600 tokens of 8 heads of 128 in fp32 (218
-// MB in, 31 MB out), and reading their values back (218 MB out), 95 us together;
+// MB in, 31 MB out), and reading their values back (218 MB out), 97 us together;
 // 162 us with one head a thread and a division a channel, 115 with four heads and
-// one reciprocal a block, 101 without the care (two heads 104, eight 122).  8 tokens: 5 us each, of
-// which the launch and six dependent loads are all.
+// one reciprocal a block, 101 without the care (two heads 104, eight 122), 95 with
+// streaming loads, 97 with a look at the page's readers.  8 tokens: 5 us each, of which
+// the launch and seven dependent loads are all.
 constexpr uint32_t kHeadsMany = 4;
 
 template <int D, bool BF16, uint32_t HT>
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t
   }
   KvPlace at{-1, 0};
   if (live) at = kv_place(kv, seqs, off, n, static_cast<int32_t>(token));
+  const int32_t readers = at.page >= 0 ? kv.refs[at.page] : 0;      // asked for here, looked at before the stores
   const uint64_t u0 = kv_unit(kv, at.page < 0 ? 0 : at.page, layer, values, h0);
   uint8_t* const codes = kv.codes + u0 * kv.unit_codes + word_offset<D>(values, at.slot, j);
   __half* const scales = kv.scales + u0 * kv.unit_scales + at.slot * (D / 32) + (j >> 2);
@@ -129,10 +131,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvDev kv, uint32_t
     if (__all_sync(0xffffffffu, tame)) w = codes_of<true>(x[h], s, inv);
     else w = codes_of<false>(x[h], s, inv);
     if (values) w = transpose8(w, j & 7);
-    if (at.page < 0 || h0 + h >= kv.heads) continue;
+    if (at.page < 0 || readers > 1 || h0 + h >= kv.heads) continue;
     *reinterpret_cast<uint32_t*>(codes + static_cast<uint64_t>(h) * kv.unit_codes) = w;
     if ((j & 3) == 0) scales[static_cast<uint64_t>(h) * kv.unit_scales] = d;
   }
+  if (readers > 1) kv_latch(kv, OVL_E_STATE);      // another row's page as well: its tokens would change under it
 }
 
 template <int D, uint32_t HT>

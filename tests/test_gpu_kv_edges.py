@@ -151,3 +151,34 @@ def test_more_row_tiles_than_the_grid_of_the_kernel_for_many_rows():
     for i in range(0, n, 1024):
         w = want[i:i + 1024]
         assert ((out[i:i + 1024].float() - w).abs() <= 2 ** -8 * w.abs()).all()
+
+
+# ---------------------------------------------------------------- pages of more than one row
+
+@pytest.mark.parametrize("kv,bf16", [(1, False), (2, True), (64, True)])       # 64: several heads a thread
+def test_tokens_are_not_written_into_pages_that_another_row_holds(kv, bf16):
+    """A fork between extend and append: the new tokens' full pages are shared by then."""
+    rng = np.random.default_rng(kv)
+    new = 100 if kv == 64 else 20                                    # tokens 40 ..: 40 .. 47 in the third page
+    c = make(n_pages=20, page=16, kv=kv, dim=128, rows=3, cols=12)
+    held = fill(c, [0], [40], rng, bf16=bf16)[0]
+    row, off = dev([0]), dev([0, new])
+    c.extend(row, off)
+    c.fork(row, dev([1]))
+    before = c.codes.clone(), c.scales.view(torch.int16).clone()
+    k, v = draw(rng, (new, kv, 128), bf16), draw(rng, (new, kv, 128), bf16)
+    c.append(0, row, off, k, v)
+    latched(c, q.OVL_E_STATE)
+    shared = c.refs > 1
+    assert int(shared.sum()) == (40 + new) // 16
+    assert torch.equal(c.codes[shared], before[0][shared])
+    assert torch.equal(c.scales.view(torch.int16)[shared], before[1][shared])
+    for got, x in zip(c.read(0, row, dev([0, (40 + new) % 16]), (40 + new) % 16), (k, v)):   # the open page is its own
+        own = K.values_of(*K.quantize(x[new - (40 + new) % 16:].float().cpu().numpy()))
+        np.testing.assert_array_equal(got.cpu().numpy(), own.astype(np.float32))
+    c.release(dev([1]))
+    c.append(0, row, off, k, v)
+    c.check()
+    for got, x, old in zip(c.read(0, row, dev([0, 40 + new]), 40 + new), (k, v), held):
+        want = np.concatenate([old, K.values_of(*K.quantize(x.float().cpu().numpy()))])
+        np.testing.assert_array_equal(got.cpu().numpy(), want.astype(np.float32))
