@@ -777,10 +777,12 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
           __syncwarp();
         }
       }
-      // nothing of this CTA may still run when its tensor memory goes
+      // nothing of this CTA may still run when its tensor memory goes: waited for, within the
+      // same limit, where another wait has run out as well
       if (tl.count) {
         if (elect_one()) commit<PAIR>(&bar.o_done[x]);
         __syncwarp();
+        dead = false;
         wait(&bar.o_done[x], 0);
       }
       tc_fence_before();
