@@ -522,11 +522,11 @@ ovl_status ovl_debug_inject(ovl_ctx* ctx, uint32_t phase, ovl_status code);
  * the host and every call can be captured in a CUDA graph.  What only the
  * device can see is checked there: a row, page, length or index out of range,
  * a row listed twice, a token that tok_off gives to no sequence, or too few free
- * pages is latched as a status code that
- * ovl_kv_check returns and clears; ovl_kv_extend, _fork, _compact and _release
- * then change nothing, ovl_kv_append writes and ovl_kv_read and
- * ovl_kv_attention return the rest (zeros for a token that cannot be reached;
- * where a page of the context is missing, outputs that need it mean nothing).
+ * pages is latched as a status code that ovl_kv_check returns and clears;
+ * ovl_kv_extend, _fork, _compact and _release then change nothing, ovl_kv_append
+ * writes and ovl_kv_read and ovl_kv_attention return the rest (zeros for a token
+ * that cannot be reached; where a page of the context is missing, outputs that
+ * need it mean nothing).
  * Calls on one cache must be stream-ordered: they share its workspace.  They
  * run on the current device, on `stream`, and allocate nothing.
  * Errors of every entry point: OVL_E_ARG (null pointer, unknown dtype, layer or
@@ -593,10 +593,18 @@ ovl_status ovl_kv_read(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, co
  * n_kv_heads; query head h reads kv head h / (n_heads / n_kv_heads).
  * max_new: an upper bound of the new tokens of any one sequence (the kernel is
  * chosen by it); more than that is latched as OVL_E_SHAPE, and the tokens
- * beyond are zeros.  Scores, softmax and sums are 32-bit.  With OVL_F32 every
- * product is exact to 24 bits; with OVL_BF16 the weights of the values are
- * rounded to 11 bits, 3 more than the output keeps.  The same inputs give the
- * same bits.  No counterpart in the source pages. */
+ * beyond are zeros.  Scores, softmax and sums are 32-bit.  What is rounded:
+ *   OVL_F32   queries, and weights times value scales, to two 11-bit parts each:
+ *             2^-23 of the number, or 2^-34 of the largest of its row (tokens so
+ *             far) where that is more;
+ *   OVL_BF16  weights to 11 bits, and to 11 again with a value scale; in calls with
+ *             many rows (new tokens x query heads) also every key and value, d *
+ *             (code - 8), to 11 bits.  The output's rounding is to 8.  Blocks whose
+ *             scale is below 2^-14 of the largest that the head's keys (values) have
+ *             within 128 tokens keep fewer bits, below 2^-24 none.
+ * The kernel is chosen by the sizes of the whole call, so a sequence's last bits
+ * can depend on what it is batched with; the same call gives the same bits.
+ * No counterpart in the source pages. */
 ovl_status ovl_kv_attention(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,
                             uint32_t n_seqs, uint32_t n_tokens, uint32_t max_new, const void* q, uint32_t dtype,
                             uint32_t n_heads, uint64_t q_stride, float scale, uint32_t window, uint32_t sinks,

@@ -32,7 +32,10 @@
 // Range.  Keys and values of a tile are multiplied by 2^-E, 2^E above the tile's
 // largest scale, before they are rounded to f16 (|x| <= 8); the factor goes back
 // into the scores, and into P for the values.  Rows of q are scaled by a power of
-// two.  So f16's 11 bits hold whatever the size of the data is.
+// two.  So f16's 11 bits hold whatever the size of the data is; within a tile, they
+// hold down to 2^-14 of the largest scale: smaller blocks end in f16's subnormals.
+// Keys, values and P are rounded to them (q is exact): the sums' operands are what
+// the tensor cores take, and the output keeps 8 bits.
 //
 // Measured (GB300, 8 kv heads of 128, 32 query heads): 2 x 2048 new tokens over
 // 6000 to 8192, 405 us = 963 TFLOP/s, 0.50 of the measured bf16 burst rate (452 us

@@ -182,3 +182,28 @@ def test_tokens_are_not_written_into_pages_that_another_row_holds(kv, bf16):
     for got, x, old in zip(c.read(0, row, dev([0, 40 + new]), 40 + new), (k, v), held):
         want = np.concatenate([old, K.values_of(*K.quantize(x.float().cpu().numpy()))])
         np.testing.assert_array_equal(got.cpu().numpy(), want.astype(np.float32))
+
+
+@pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -8])
+@pytest.mark.parametrize("dim,kv,new", [(128, 1, 1), (64, 2, 4), (128, 40, 60), (64, 40, 60), (256, 40, 60)])
+def test_blocks_of_very_different_size(dim, kv, new, small):
+    """Within 2^-14 of a tile's largest scale every block of channels keeps its bits: small values beside large ones."""
+    rng = np.random.default_rng(dim + new)
+    n = 300
+    c = make(n_pages=20, page=16, kv=kv, dim=dim, rows=1, cols=20)
+    rows, off = dev([0]), dev([0, n])
+    c.extend(rows, off)
+    k, v = draw(rng, (n, kv, dim)), draw(rng, (n, kv, dim))
+    k[..., :32] *= small
+    v[..., 32:64] *= small
+    k, v = k.bfloat16(), v.bfloat16()
+    c.append(0, rows, off, k, v)
+    c.check()
+    x = draw(rng, (new, 8 * kv, dim), True)
+    got = c.attention(0, rows, dev([0, new]), x, new).double().cpu().numpy()
+    c.check()
+    kk, vv = (K.values_of(*K.quantize(t.float().cpu().numpy())) for t in (k, v))
+    w, spread, top = K.attention(x.double().cpu().numpy(), kk, vv, np.arange(n - new, n), dim ** -0.5)
+    assert (np.abs(got - w) <= K.allowed(w, spread, top, True)).all()
+    block = np.s_[..., 32:64]
+    assert np.sqrt(((got - w)[block] ** 2).mean()) <= 2 ** -8 * np.sqrt((w[block] ** 2).mean())
