@@ -590,7 +590,8 @@ ovl_status ovl_kv_read(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, co
  * q, out: device [n_tokens][n_heads][head_dim] of `dtype` (OVL_F32 or OVL_BF16),
  * q_stride and out_stride elements from token to token, base and strides
  * multiples of 16 bytes; out must not overlap q.  n_heads is a multiple of
- * n_kv_heads; query head h reads kv head h / (n_heads / n_kv_heads).
+ * n_kv_heads, at most 1024 times it and below 2^32 / head_dim; query head h reads
+ * kv head h / (n_heads / n_kv_heads).
  * max_new: an upper bound of the new tokens of any one sequence (the kernel is
  * chosen by it); more than that is latched as OVL_E_SHAPE, and the tokens
  * beyond are zeros.  Scores, softmax and sums are 32-bit.  What is rounded:

@@ -210,6 +210,8 @@ ovl_status ovl_kv_attention(const ovl_kv* kv, uint32_t layer, const int32_t* seq
   if (!std::isfinite(scale)) return fail(OVL_E_ARG, "scale is not finite");
   if (!n_heads || n_heads % d.heads) return fail(OVL_E_SHAPE, "n_heads must be a multiple of n_kv_heads");
   if (n_heads / d.heads > 1024) return fail(OVL_E_SHAPE, "more than 1024 query heads to a kv head");
+  if (static_cast<uint64_t>(n_heads) * d.dim >= (1ull << 32))      // offsets inside a token are 32-bit
+    return fail(OVL_E_SHAPE, "a token's query heads must be below 2^32 elements");
   if (n_seqs == 0 || n_tokens == 0) return OVL_OK;
   if (n_tokens > 0x7fffffffu || !max_new) return fail(OVL_E_ARG, "n_tokens or max_new out of range");
   if (!q || !out) return fail(OVL_E_ARG, "q or out is null");

@@ -158,3 +158,21 @@ def test_numbers_that_32_bits_would_change_are_refused(stand_in, bad):
     assert not lib.calls
     c.attention(0, one, off, x, 1, window=(1 << 32) - 1, sinks=(1 << 32) - 1)
     assert lib.calls[0][2][-5:-3] == ((1 << 32) - 1, (1 << 32) - 1)
+
+
+def test_query_heads_beyond_32_bit_offsets_are_refused():
+    """Offsets of a token's heads are 32-bit in the kernels; judged before anything touches a device."""
+    q = pytest.importorskip("quantized_base_lora_gb300")
+    d = q.ovl_kv()
+    for name, value in dict(n_pages=9, page_tokens=16, n_layers=1, n_kv_heads=65535, head_dim=256, max_seqs=9,
+                            max_pages=9, codes=4096, scales=4096, table=4096, length=4096, refs=4096, workspace=4096,
+                            workspace_bytes=1 << 40).items():
+        setattr(d, name, value)
+    heads = 65535 * 1024
+
+    def attend(heads, tokens=1):
+        return q.ovl_kv_attention(d, 0, 16, 16, 1, tokens, 1, 16, q.OVL_BF16, heads, heads * 256, 1.0, 0, 0, 16,
+                                  heads * 256)
+
+    assert attend(heads, tokens=0) == q.OVL_E_SHAPE and "2^32" in q.ovl_last_error(None)
+    assert attend(65535 * 256, tokens=0) == q.OVL_OK                     # just below: no tokens, so no call either
