@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       for (int b = 0; b < NB; ++b) {
         if constexpr (BF16) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (on) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qa + 32 * b + 8 * t));
+          if (on) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qa + 32 * b + 8 * t);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           float4 u = make_float4(0, 0, 0, 0), v = u;
           if (on) {
             const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qa + 32 * b + 8 * t);
-            u = __ldg(p), v = __ldg(p + 1);
+            u = p[0], v = p[1];
           }
           x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
           x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;

@@ -82,9 +82,8 @@ __device__ __forceinline__ void add_refs(const KvDev& kv, int32_t page, int32_t 
   if (static_cast<uint32_t>(page) < kv.n_pages) atomicAdd(kv.refs + page, by);
 }
 
-__global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what, const int32_t* __restrict__ src,
-                                                    const int32_t* __restrict__ dst, const int32_t* __restrict__ keep,
-                                                    const int32_t* __restrict__ off, uint32_t n, uint32_t n_keep) {
+__global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what, const int32_t* src, const int32_t* dst,
+                                                    const int32_t* keep, const int32_t* off, uint32_t n, uint32_t n_keep) {
   __shared__ BookShared s;
   const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const bool two = what == KvPages::kFork || what == KvPages::kCompact;
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kBook) k_kv_pages(const KvDev kv, KvPages what
     for (int64_t j0 = t; j0 < total; j0 += 8 * kBook) {
       int32_t p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = j0 + i * kBook < total ? __ldg(keep + j0 + i * kBook) : 0;
+      for (int i = 0; i < 8; ++i) p[i] = j0 + i * kBook < total ? keep[j0 + i * kBook] : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t j = j0 + i * kBook;
@@ -335,7 +334,7 @@ __device__ __forceinline__ void copy_heads(uint8_t* pool, uint64_t from, uint64_
 // Bound by memory; a value unit is 4 to 16 bytes, so scattered tokens read whole
 // sectors of values for a part of them.
 template <int D>
-__global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* __restrict__ keep,
+__global__ void __launch_bounds__(kCopy, 4) k_kv_gather(const KvDev kv, const int32_t* keep,
                                                         uint32_t layers_each) {
   __shared__ int32_t from_page[256], from_slot[256];
   griddep_launch_dependents();

@@ -258,7 +258,7 @@ __device__ __forceinline__ void tile_pages(const KvDev& kv, const int32_t* row, 
   for (int k = 0; k < N; ++k) {
     const uint32_t t = tok + 32 * k + lane;
     p[k] = -1;
-    if (t < length) p[k] = __ldg(row + (t >> kv.page_shift));
+    if (t < length) p[k] = row[t >> kv.page_shift];
   }
 }
 
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
       if (on) {
 #pragma unroll 8
         for (uint32_t c = 0; c < D / 8; ++c) {
-          const uint4 v = __ldg(src + c);
+          const uint4 v = src[c];
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
 #pragma unroll 8
       for (uint32_t c = 0; c < D / 8; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = __ldg(src + c);
+        if (on) v = src[c];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float f[8];
 #pragma unroll
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
         }
 #pragma unroll
         for (uint32_t i = 0; i < NW; ++i) sc[k * NW + i] = 0;
-        if (pages[k] >= 0) ldg<NW>(scales + wide(pages[k], page_scales) + (t & (kv.page - 1)) * NB, &sc[k * NW]);
+        if (pages[k] >= 0) load_words<NW>(scales + wide(pages[k], page_scales) + (t & (kv.page - 1)) * NB, &sc[k * NW]);
       }
     };
     // The exponent above the tile's scales, which are multiplied by 2^-it.
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
           const int32_t p = __shfl_sync(0xffffffffu, PAIR == 2 && rank ? pages[(PAIR - 1) * KI + k] : pages[k], from);
 #pragma unroll
           for (uint32_t i = 0; i < NB; ++i) kw[k][i] = 0x88888888u;
-          if (p >= 0) ldg<NB>(codes + wide(p, page_codes) + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), kw[k]);
+          if (p >= 0) load_words<NB>(codes + wide(p, page_codes) + (u & (kv.page - 1)) * (D / 2) + part * (D / 8), kw[k]);
         }
       };
       first(load);
@@ -674,10 +674,10 @@ __global__ void __launch_bounds__(Shape<D, PAIR>::kThreads, 1) k_kv_prefill(cons
                                     half * (4 * WT);
           if constexpr (kSplit) {
 #pragma unroll
-            for (uint32_t t = 0; t < 8; ++t) ldg<WT>(at + t * (D / 16), vw[t]);
+            for (uint32_t t = 0; t < 8; ++t) load_words<WT>(at + t * (D / 16), vw[t]);
           } else {
             uint32_t w[8 * WT];
-            ldg<8 * WT>(at, w);
+            load_words<8 * WT>(at, w);
 #pragma unroll
             for (uint32_t t = 0; t < 8; ++t)
 #pragma unroll

@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t kv_owner(const int32_t* off, uint32_t n, int
   uint32_t lo = 0, hi = n;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) >> 1;
-    if (__ldg(off + mid) <= t) lo = mid;
+    if (off[mid] <= t) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -70,7 +70,7 @@ struct KvPlace {
 __device__ __forceinline__ KvPlace kv_place(const KvDev& kv, const int32_t* seqs, const int32_t* off, uint32_t n,
                                             int32_t t) {
   const uint32_t i = kv_owner(off, n, t);
-  const int32_t s = __ldg(seqs + i), after = __ldg(off + i + 1) - t;
+  const int32_t s = seqs[i], after = off[i + 1] - t;
   if (static_cast<uint32_t>(s) >= kv.max_seqs || after <= 0) {
     kv_latch(kv, OVL_E_ARG);
     return {-1, 0};
@@ -121,7 +121,10 @@ inline cudaError_t allow_smem(const void* f, uint32_t bytes, std::atomic<uint64_
 // Launches f in the stream's programmatic chain: its CTAs may be scheduled while
 // the kernel before it still runs, so f calls griddep_wait() before it reads or
 // writes anything, and griddep_launch_dependents() as early as that is sound for
-// the next one (at once: every kernel here waits first).
+// the next one (at once: every kernel here waits first).  What a kernel before it may
+// write - any argument, and the whole cache - is therefore read by ordinary loads, never
+// through the read-only path (__ldg, const __restrict__), which promises that nothing
+// changes while the kernel is resident.
 // `cluster`: CTAs of a cluster, along x.
 template <class... P, class... A>
 cudaError_t launch_clustered(void (*f)(P...), dim3 grid, uint32_t block, uint32_t smem, cudaStream_t st, uint32_t cluster,

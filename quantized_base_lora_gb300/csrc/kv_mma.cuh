@@ -116,16 +116,16 @@ __device__ __forceinline__ float2 halves(uint32_t w) {
 
 // N consecutive 32-bit words from global memory, in loads of up to 16 bytes.
 template <int N>
-__device__ __forceinline__ void ldg(const void* p, uint32_t* w) {
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
   if constexpr (N == 1) {
-    w[0] = __ldg(static_cast<const uint32_t*>(p));
+    w[0] = *static_cast<const uint32_t*>(p);
   } else if constexpr (N == 2) {
-    const uint2 v = __ldg(static_cast<const uint2*>(p));
+    const uint2 v = *static_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
+      const uint4 v = static_cast<const uint4*>(p)[i];
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }

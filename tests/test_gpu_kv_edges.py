@@ -207,3 +207,33 @@ def test_blocks_of_very_different_size(dim, kv, new, small):
     assert (np.abs(got - w) <= K.allowed(w, spread, top, True)).all()
     block = np.s_[..., 32:64]
     assert np.sqrt(((got - w)[block] ** 2).mean()) <= 2 ** -8 * np.sqrt((w[block] ** 2).mean())
+
+
+# ---------------------------------------------------------------- kernels that overlap their launches
+
+@pytest.mark.parametrize("kv,new", [(2, 1), (40, 30)], ids=["few rows", "many rows"])
+def test_steps_without_a_pause_give_what_steps_with_pauses_give(kv, new):
+    """Each kernel is resident while the one before still runs: pages, tokens and queries written just before."""
+    def run(pause):
+        g = torch.Generator("cuda").manual_seed(3)
+        c = make(n_pages=160, page=16, layers=2, kv=kv, dim=128, rows=4, cols=60, garbage=False)
+        c.scales.fill_(float("nan"))
+        rows, off = dev([2, 0]), dev([0, new, 2 * new])
+        outs = []
+        for step in range(24):
+            calls = [lambda: c.extend(rows, off)]
+            for layer in range(2):
+                k, v, x = (torch.randn((2 * new, h, 128), generator=g, device="cuda").bfloat16()
+                           for h in (kv, kv, 4 * kv))
+                calls += [lambda layer=layer, k=k, v=v: c.append(layer, rows, off, k, v),
+                          lambda layer=layer, x=x: outs.append(c.attention(layer, rows, off, x, new))]
+            calls += [lambda: c.fork(dev([2]), dev([1]))] if step % 5 == 4 else []
+            for call in calls:
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        c.check()
+        return torch.cat(outs)
+
+    a, b = run(False), run(True)
+    assert torch.isfinite(a).all() and torch.equal(a, b)

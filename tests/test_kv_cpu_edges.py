@@ -176,3 +176,18 @@ def test_query_heads_beyond_32_bit_offsets_are_refused():
 
     assert attend(heads, tokens=0) == q.OVL_E_SHAPE and "2^32" in q.ovl_last_error(None)
     assert attend(65535 * 256, tokens=0) == q.OVL_OK                     # just below: no tokens, so no call either
+
+
+def test_kernels_of_the_cache_read_by_ordinary_loads():
+    """Each is resident while the kernel before it may still write what it will read, so nothing of it may go through
+    the read-only path."""
+    import glob
+    import os
+    import re
+    root = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_base_lora_gb300", "csrc")
+    files = glob.glob(os.path.join(root, "k_kv_*.cu")) + glob.glob(os.path.join(root, "kv_*"))
+    assert len(files) >= 6
+    for f in files:
+        with open(f) as t:
+            code = re.sub(r"//.*", "", t.read())
+        assert not re.search(r"__ldg\(|__restrict__|ld\.global\.nc", code), f
