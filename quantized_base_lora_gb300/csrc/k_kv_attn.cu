@@ -44,16 +44,17 @@
 // Measured (GB300, 8 kv heads of 128, 32 query heads, bf16): 16 sequences of
 // 60001 to 131072 tokens, 292 us = 5.7 TB/s, 0.85 of the measured copy rate; 32
 // sequences of 500 to 8000 tokens, 32 us (0.39: starting, joining and the first
-// loads are two thirds of it); 64 sequences, window 2048 and 4 sinks, 43 us
+// loads are two thirds of it); 64 sequences, window 2048 and 4 sinks, 44 us
 // (0.50).  The copies alone take 241 us of the first, the arithmetic alone
-// about 280: a tile of 32 tokens is some 620 instructions of a warp, 128 of them
+// about 280: a tile of 32 tokens is some 640 instructions of a warp, 128 of them
 // the masks that take the codes apart, at 0.6 to 0.7 of the issue slots with
 // four warps a scheduler (128 registers).  What brought it there, in order, on
 // that case: 489 us with keys in bf16 and two instructions a mask; 356 with f16
 // codes and one; 314 with asynchronous copies by the whole warp in place of bulk
 // copies by four lanes (whose operands went through uniform registers one lane
 // after the other) and a reference that trails; 291 with a shorter loop; 289 with
-// rings of two tiles (three: the 32 sequences 33, the windows 45 us).  Not
+// rings of two tiles (three: the 32 sequences 33, the windows 45 us); 292 with value
+// scales far from 1 seen to.  Not
 // adopted: eight warps a CTA (280, but 36 and 49), two (331, 38, 50), the next
 // part's first tiles requested before a part is joined (291, 36, 48: registers).
 #include <math_constants.h>

@@ -38,7 +38,7 @@
 // the tensor cores take, and the output keeps 8 bits.
 //
 // Measured (GB300, 8 kv heads of 128, 32 query heads): 2 x 2048 new tokens over
-// 6000 to 8192, 405 us = 963 TFLOP/s, 0.50 of the measured bf16 burst rate (452 us
+// 6000 to 8192, 403 us = 967 TFLOP/s, 0.50 of the measured bf16 burst rate (452 us
 // without pairs); 4 chunks of up to 777 tokens, 3 kv heads of 64, window 1024, 62 us
 // (267 CTAs of 4 to 11 tiles on 152 SMs: two rounds, each with its prologue).
 // Bound by the chain from scores to P and back: of 4800 clocks a tile (timed inside,

@@ -10,7 +10,7 @@
 
 namespace ovl {
 
-constexpr uint32_t kKvMaxSeqs = 65536;       // rows: two bits each in shared memory of the page kernel
+constexpr uint32_t kKvMaxSeqs = 65536;       // rows: a bit each in shared memory of the page kernel
 constexpr uint32_t kKvMaxCtas = 640;         // CTAs of an attention launch that may leave partial results
 constexpr uint32_t kKvPartialRows = 16;      // query rows of one partial result
 
