@@ -257,8 +257,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
 
   uint8_t* const my_ring = ring + warp * St::kWarpBytes;
   uint32_t slot = 0;                          // of the ring, in bytes, across segments
-  // the sign goes into q; the key codes of bf16 calls stand for 2^-24 of themselves
-  const float scale2 = fabsf(a.scale) * kLog2e * (BF16 ? 0x1p24f : 1.f);
+  const float scale2 = fabsf(a.scale) * kLog2e;   // the sign goes into q
   uint32_t magic;
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
@@ -417,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
       // 2^ex <= top < 2^(ex + 1), biased; the row is multiplied by 2^(kUp - ex): as far up
       // as f16 goes for a bf16 number, and for two parts so that both keep their small end.
       constexpr uint32_t kUp = BF16 ? 15 : 9;
-      const uint32_t ex = min(max(__float_as_uint(top) >> 23, kUp + 1), 253u);
+      const uint32_t ex = min(max(__float_as_uint(top) >> 23, kUp + 1), 254u);
       const float up = copysignf(__uint_as_float((254u + kUp - ex) << 23), a.scale), down = __uint_as_float((ex - kUp) << 23);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -457,9 +456,11 @@ __global__ void __launch_bounds__(kThreads, (D <= 128 && BF16 && NT == 1) ? 4 : 
           if (NB == 8 ? t == i : t == i + NB / 2) qs[nt][NB == 8] = rest[i];
         }
       }
-      // finite, so that a score of 0 stays one: above 2^128 only one token counts anyway
-      to_log2[nt][0] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t), 0x1.fffffep127f);
-      to_log2[nt][1] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4), 0x1.fffffep127f);
+      // the key codes of bf16 calls stand for 2^-24 of themselves; multiplied last, and kept
+      // finite, so that sizes of q and scale that make up for one another do so
+      constexpr float kCodes = BF16 ? 0x1p24f : 1.f;
+      to_log2[nt][0] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t) * kCodes, 0x1.fffffep127f);
+      to_log2[nt][1] = fminf(scale2 * __shfl_sync(0xffffffffu, down, 8 * t + 4) * kCodes, 0x1.fffffep127f);
     }
     // tiles that every row sees whole need no mask
     const uint32_t i0 = r0 / rows_group, i1 = (r0 + n_rows - 1) / rows_group;

@@ -237,3 +237,23 @@ def test_steps_without_a_pause_give_what_steps_with_pauses_give(kv, new):
 
     a, b = run(False), run(True)
     assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- queries of any size
+
+@pytest.mark.parametrize("size", [-118, 0, 119, 125, 127])
+@pytest.mark.parametrize("kv,new,bf16", [(1, 1, False), (1, 1, True), (2, 4, True), (40, 60, True)],
+                         ids=["f32", "bf16", "bf16-2", "many rows"])
+def test_queries_of_any_size(size, kv, new, bf16):
+    """Queries up to the type's end and down to where their scale makes up for it."""
+    rng = np.random.default_rng(size & 0xff)
+    c = make(n_pages=20, page=16, kv=kv, dim=64, rows=1, cols=20)
+    held = fill(c, [0], [200], rng, bf16=bf16)
+    x = draw(rng, (new, 8 * kv, 64), bf16).clamp(-1.9, 1.9) * 2.0 ** size
+    assert torch.isfinite(x).all()
+    x[:, 0, 0] = 1.9 * 2.0 ** size                                   # the size is reached in some row
+    scale = max(0.125 * 2.0 ** -size, 2.0 ** -126)                   # a normal number
+    got = c.attention(0, dev([0]), dev([0, new]), x, new, scale=scale).double().cpu().numpy()
+    c.check()
+    w, spread, top = K.attention(x.double().cpu().numpy(), *held[0], np.arange(200 - new, 200), scale)
+    assert (np.abs(got - w) <= K.allowed(w, spread, top, bf16)).all()
