@@ -647,9 +647,184 @@ ovl_status ovl_kv_check(const ovl_kv* kv, void* stream);
 ovl_status ovl_debug_kv_route(const ovl_kv* kv, uint32_t n_seqs, uint32_t n_tokens, uint32_t max_new, uint32_t dtype,
                               uint32_t n_heads, uint32_t n_sms, uint32_t* route);
 
+/* ---- between the projections -----------------------------------------------
+ * What a decoder block computes between the linear layers above and the cache's
+ * attention: rotary positions, the norms around a block with its gate and
+ * residual, the gated activation of its feed-forward part, and a
+ * mixture-of-experts layer whose experts are held in the base's formats.  The
+ * source pages stop at the linear layers; every entry point of this part has no
+ * counterpart in them.
+ *
+ * The library keeps nothing between calls; structs are read during the call only.
+ * Tensors are device memory of OVL_F32 or OVL_BF16, a token's elements contiguous,
+ * with strides in elements from token to token; "16-byte rows" below means base and
+ * stride multiples of 16 bytes.  Sums, statistics, angles and activations are in 32
+ * bits or more and each output is rounded once.  Calls run on the current device, on
+ * `stream`, allocate nothing, never wait for the host and can be captured in a CUDA
+ * graph.  Errors of every entry point: OVL_E_ARG (null pointer, unknown dtype or
+ * kind, number out of range), OVL_E_SHAPE (dimensions, strides or alignment),
+ * OVL_E_OOM (workspace too small), OVL_E_CUDA; the message is ovl_last_error(NULL).
+ * No tokens are a no-op. */
+
+enum { OVL_ROPE_HALF = 1, OVL_ROPE_PAIRS = 2 };   /* channel i rotates with i + rot_dim / 2, or 2 i with 2 i + 1 */
+enum {                                             /* long contexts */
+  OVL_ROPE_PLAIN = 0, OVL_ROPE_LINEAR = 1, OVL_ROPE_BASE = 2, OVL_ROPE_BANDS = 3, OVL_ROPE_RAMP = 4
+};
+enum { OVL_ROPE_MAX_DIM = 512 };
+
+/* A rotation as the kernel takes it (made by ovl_rope_plan, kept by the caller, host memory). */
+typedef struct {
+  uint32_t head_dim, rot_dim, layout;
+  float magnitude;                            /* factor of both cosine and sine */
+  uint64_t turn[OVL_ROPE_MAX_DIM / 2];        /* turns a position of pair i, in units of 2^-64 */
+} ovl_rope;
+
+/* Host utility (no device needed): the rotation of the first rot_dim channels of
+ * heads of head_dim.  Pair i < rot_dim / 2 turns by w_i radians a position,
+ * w_i = base^(-2 i / rot_dim), changed for long contexts by `scaling`:
+ *   OVL_ROPE_PLAIN   nothing (factor, original, low and high are not looked at);
+ *   OVL_ROPE_LINEAR  w_i / factor;
+ *   OVL_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in the place of base;
+ *   OVL_ROPE_BANDS   with n = original w_i / 2 pi turns within the original length:
+ *                    w_i for n >= high, w_i / factor for n <= low, and in between
+ *                    s w_i + (1 - s) w_i / factor, s = (n - low) / (high - low);
+ *   OVL_ROPE_RAMP    w_i (1 - r_i) + r_i w_i / factor, r_i = (i - a) / (b - a) within 0
+ *                    .. 1, a = max(0, floor(c(high))), b = min(rot_dim - 1, ceil(c(low))),
+ *                    c(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), b - a at least 0.001.
+ * magnitude: 0 = the scaling's own (0.1 ln(factor) + 1 for OVL_ROPE_RAMP, else 1).
+ * Frequencies are computed in 64 bits and held as fractions of a turn in 64-bit
+ * fixed point, so that pos * turn is reduced exactly: the angle is off by less than
+ * 2^-50 pos w_i, at any position.  OVL_E_SHAPE: head_dim not even or outside 2 ..
+ * OVL_ROPE_MAX_DIM, rot_dim not even or outside 2 .. head_dim.  OVL_E_ARG: base <= 1,
+ * factor < 1, original 0 where it is used, low >= high or low <= 0, non-finite numbers.
+ * No counterpart in the source pages. */
+ovl_status ovl_rope_plan(uint32_t head_dim, uint32_t rot_dim, uint32_t layout, double base, uint32_t scaling,
+                         double factor, uint32_t original, double low, double high, double magnitude, ovl_rope* out);
+
+/* Rotate q and k to their positions: with the angle f = pos[token] * w_i, the pair
+ * (a, b) becomes (a cos f - b sin f, a sin f + b cos f) * magnitude; channels from
+ * rot_dim on are passed through.  pos: device int32 [n_tokens], any sign.  q: device
+ * [n_tokens][q_heads][head_dim] of `dtype`, k the same with k_heads (0: no k), heads
+ * contiguous.  q_out, k_out: the same shape in out_dtype; each may be its input where
+ * type and stride agree, and overlaps nothing else.  16-byte rows and dimensions that
+ * are multiples of 8 are served by wide loads, others element by element.  No
+ * counterpart in the source pages. */
+ovl_status ovl_rope_apply(const ovl_rope* rope, uint32_t n_tokens, const int32_t* pos, const void* q, uint32_t q_heads,
+                          uint64_t q_stride, const void* k, uint32_t k_heads, uint64_t k_stride, uint32_t dtype,
+                          void* q_out, uint64_t q_out_stride, void* k_out, uint64_t k_out_stride, uint32_t out_dtype,
+                          void* stream);
+
+/* Positions of a batch's new tokens in a cache (see above): pos[t], device int32
+ * [n_tokens], is the place of packed token t in its sequence, counted by length;
+ * -1 for a token that tok_off gives to no sequence or whose row is out of range
+ * (latched as OVL_E_ARG).  One call a step serves every layer's ovl_rope_apply.  No
+ * counterpart in the source pages. */
+ovl_status ovl_kv_positions(const ovl_kv* kv, const int32_t* seqs, const int32_t* tok_off, uint32_t n_seqs,
+                            uint32_t n_tokens, int32_t* pos, void* stream);
+
+enum { OVL_NORM_NONE = 0, OVL_NORM_RMS = 1, OVL_NORM_LAYER = 2 };
+enum { OVL_NORM_MAX_HIDDEN = 32768 };
+
+/* One norm over a token's channels:
+ *   OVL_NORM_RMS    v / sqrt(mean(v^2) + eps) * (weight + offset) + bias
+ *   OVL_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (weight + offset) + bias
+ * weight, bias: device [hidden] of w_dtype; NULL: ones (offset is not added), zeros. */
+typedef struct {
+  uint32_t kind, w_dtype;
+  const void* weight;
+  const void* bias;
+  float eps, offset;
+} ovl_norm;
+
+/* What joins two blocks; host memory. */
+typedef struct {
+  uint32_t hidden;       /* 1 .. OVL_NORM_MAX_HIDDEN */
+  float alpha, beta;     /* scales of the residual and of the block's output */
+  ovl_norm post, pre;    /* of the block's output; of the next block's input */
+} ovl_block_norm;
+
+/* The end of one block and the beginning of the next:
+ *   x' = alpha x + beta gate * post(y),    h = pre(x')
+ * x: device [n_tokens][hidden], the residual stream; y: the block's output, NULL for
+ * none (x' = alpha x).  gate: device [n_gates][hidden] with gate_stride elements from
+ * row to row, NULL for ones; token t takes row gate_row[t] (device int32), or, without
+ * gate_row, row t where n_gates = n_tokens and row 0 where n_gates = 1.  A row outside 0 .. n_gates - 1
+ * leaves the block's output out: x' = alpha x.  x_out: x' in x_dtype (may be x with x's
+ * stride; NULL: not wanted).  h: in h_dtype, computed from x' before x' is rounded
+ * (NULL where pre.kind is OVL_NORM_NONE).  Outputs overlap nothing else.  No counterpart
+ * in the source pages. */
+ovl_status ovl_block_norm_apply(const ovl_block_norm* norm, uint32_t n_tokens, const void* x, uint32_t x_dtype,
+                                uint64_t x_stride, const void* y, uint32_t y_dtype, uint64_t y_stride,
+                                const void* gate, uint32_t gate_dtype, uint64_t gate_stride, const int32_t* gate_row,
+                                uint32_t n_gates, void* x_out, uint64_t x_out_stride, void* h, uint32_t h_dtype,
+                                uint64_t h_stride, void* stream);
+
+enum { OVL_ACT_SILU = 1, OVL_ACT_GELU = 2, OVL_ACT_GELU_TANH = 3, OVL_ACT_RELU = 4 };
+
+/* out = act(gate) * up, element by element: device [n_tokens][width], gate and up of
+ * `dtype`.  OVL_ACT_SILU v / (1 + e^-v), OVL_ACT_GELU v (1 + erf(v / sqrt 2)) / 2,
+ * OVL_ACT_GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2, OVL_ACT_RELU
+ * max(v, 0).  out may be gate or up where type and stride agree.  No counterpart in the
+ * source pages. */
+ovl_status ovl_glu(uint32_t act, uint32_t n_tokens, uint32_t width, const void* gate, uint64_t gate_stride,
+                   const void* up, uint64_t up_stride, uint32_t dtype, void* out, uint64_t out_stride,
+                   uint32_t out_dtype, void* stream);
+
+enum { OVL_MOE_SOFTMAX = 1, OVL_MOE_SIGMOID = 2 };
+enum { OVL_MOE_MAX_EXPERTS = 512, OVL_MOE_MAX_TOP = 16, OVL_MOE_MAX_HIDDEN = 32768 };
+
+/* A mixture-of-experts layer: caller-owned device memory and its dimensions.
+ *   gate, up   [n_experts * ffn] rows of hidden weights, down [n_experts * hidden]
+ *              rows of ffn weights, expert after expert, in the base's layout of `quant`
+ *              (a qs and a d plane each, as one tensor of a base buffer; 16-byte aligned)
+ *   router     [n_experts][hidden] of router_dtype, 16-byte aligned, or NULL where every
+ *              call brings its own choice
+ *   bias       float32 [n_experts], added to the scores for the choice only; NULL: none
+ *   workspace  ovl_moe_workspace_bytes bytes, 256-byte aligned, zero-filled by the caller
+ *              before the first call, then left to the library
+ * hidden and ffn: multiples of 32 (of 256 for OVL_Q4_K) up to OVL_MOE_MAX_HIDDEN.  The
+ * planes are like the base: not written while calls that read them are in flight (copies
+ * of them start before the kernel in front has ended).  Overlays are not applied to
+ * experts. */
+typedef struct {
+  uint32_t quant, n_experts, top_k, hidden, ffn, act;
+  uint32_t score, renormalize;     /* OVL_MOE_SOFTMAX or _SIGMOID; weights of a token divided by their sum */
+  float scale;                     /* of the router's weights */
+  uint32_t router_dtype, max_tokens;
+  const void *gate_qs, *gate_d, *up_qs, *up_d, *down_qs, *down_d;
+  const void* router;
+  const float* bias;
+  void* workspace;
+  size_t workspace_bytes;
+} ovl_moe;
+
+/* Size of the workspace for the dimensions of `moe` (its pointers are not looked at).
+ * No counterpart in the source pages. */
+ovl_status ovl_moe_workspace_bytes(const ovl_moe* moe, size_t* out);
+
+/* The layer for up to max_tokens (at most OVL_MAX_T) tokens:
+ *   y = sum_s weight_s down_e (act(gate_e x) * (up_e x)),   e = choice_s, s < top_k
+ * With choice NULL the router chooses: scores are the softmax or the sigmoid of
+ * router x, the top_k experts of the largest score + bias are taken (the lowest index
+ * where they are equal; NaN counts as the least), a chosen expert's weight is its score,
+ * divided by the sum of the chosen ones' where renormalize is set, times scale; choice_out
+ * int32 and weight_out float32 [n_tokens][top_k] receive them, in falling order
+ * (NULL: not wanted).  Otherwise choice int32 and weight float32 [n_tokens][top_k] are
+ * the caller's: an index outside 0 .. n_experts - 1 is no expert and adds nothing, an
+ * expert listed twice adds twice.  x: device [n_tokens][hidden] of `dtype`, y the same;
+ * 16-byte rows.  What is rounded: OVL_F32 x and the activations to three bf16 parts each
+ * (2^-24 of each number); OVL_BF16 activations to two (2^-16).  Dot products are sums over
+ * 32-weight blocks of exact products with the codes, in 32 bits, times the block's scale.
+ * The result depends on the call's inputs alone: the same call gives the same bits.
+ * Calls on one workspace must be stream-ordered.  No counterpart in the source pages. */
+ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, uint32_t n_tokens, uint64_t x_stride,
+                           const int32_t* choice, const float* weight, int32_t* choice_out, float* weight_out, void* y,
+                           uint64_t y_stride, void* stream);
+
 /* Message of the last failed call on ctx (static storage owned by ctx; "" after
  * success).  ctx NULL returns the message of the last failed call that has no
- * context on this thread (ovl_create, ovl_manifest_parse, ovl_kv_*).
+ * context on this thread (ovl_create, ovl_manifest_parse, ovl_kv_*, and the part
+ * between the projections).
  * ([MODELD] §"Observability": why an adapter failed to load.) */
 const char* ovl_last_error(ovl_ctx* ctx);
 

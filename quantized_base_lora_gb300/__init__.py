@@ -99,6 +99,42 @@ class ovl_kv(C.Structure):
 
 OVL_KV_MAX_BATCH = 1024
 
+OVL_ROPE_HALF, OVL_ROPE_PAIRS = 1, 2
+OVL_ROPE_PLAIN, OVL_ROPE_LINEAR, OVL_ROPE_BASE, OVL_ROPE_BANDS, OVL_ROPE_RAMP = 0, 1, 2, 3, 4
+OVL_ROPE_MAX_DIM = 512
+OVL_NORM_NONE, OVL_NORM_RMS, OVL_NORM_LAYER = 0, 1, 2
+OVL_NORM_MAX_HIDDEN = 32768
+OVL_ACT_SILU, OVL_ACT_GELU, OVL_ACT_GELU_TANH, OVL_ACT_RELU = 1, 2, 3, 4
+OVL_MOE_SOFTMAX, OVL_MOE_SIGMOID = 1, 2
+OVL_MOE_MAX_EXPERTS, OVL_MOE_MAX_TOP, OVL_MOE_MAX_HIDDEN = 512, 16, 32768
+
+
+class ovl_rope(C.Structure):
+    """A rotation of heads (host memory), made by ovl_rope_plan."""
+    _fields_ = [("head_dim", C.c_uint32), ("rot_dim", C.c_uint32), ("layout", C.c_uint32), ("magnitude", C.c_float),
+                ("turn", C.c_uint64 * (OVL_ROPE_MAX_DIM // 2))]
+
+
+class ovl_norm(C.Structure):
+    _fields_ = [("kind", C.c_uint32), ("w_dtype", C.c_uint32), ("weight", C.c_void_p), ("bias", C.c_void_p),
+                ("eps", C.c_float), ("offset", C.c_float)]
+
+
+class ovl_block_norm(C.Structure):
+    """What joins two blocks (host memory)."""
+    _fields_ = [("hidden", C.c_uint32), ("alpha", C.c_float), ("beta", C.c_float), ("post", ovl_norm),
+                ("pre", ovl_norm)]
+
+
+class ovl_moe(C.Structure):
+    """A mixture-of-experts layer: caller-owned device memory and its dimensions."""
+    _fields_ = [("quant", C.c_uint32), ("n_experts", C.c_uint32), ("top_k", C.c_uint32), ("hidden", C.c_uint32),
+                ("ffn", C.c_uint32), ("act", C.c_uint32), ("score", C.c_uint32), ("renormalize", C.c_uint32),
+                ("scale", C.c_float), ("router_dtype", C.c_uint32), ("max_tokens", C.c_uint32),
+                ("gate_qs", C.c_void_p), ("gate_d", C.c_void_p), ("up_qs", C.c_void_p), ("up_d", C.c_void_p),
+                ("down_qs", C.c_void_p), ("down_d", C.c_void_p), ("router", C.c_void_p), ("bias", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
 
 def _load():
     if not os.path.exists(LIB_PATH):
@@ -144,6 +180,13 @@ def _load():
         "ovl_kv_compact": ([P, P, P, P, P, U32, U32, P], I32),
         "ovl_kv_release": ([P, P, U32, P], I32),
         "ovl_kv_check": ([P, P], I32),
+        "ovl_kv_positions": ([P, P, P, U32, U32, P, P], I32),
+        "ovl_rope_plan": ([U32, U32, U32, C.c_double, U32, C.c_double, U32, C.c_double, C.c_double, C.c_double, P], I32),
+        "ovl_rope_apply": ([P, U32, P, P, U32, U64, P, U32, U64, U32, P, U64, P, U64, U32, P], I32),
+        "ovl_block_norm_apply": ([P, U32, P, U32, U64, P, U32, U64, P, U32, U64, P, U32, P, U64, P, U32, U64, P], I32),
+        "ovl_glu": ([U32, U32, U32, P, U64, P, U64, U32, P, U64, U32, P], I32),
+        "ovl_moe_workspace_bytes": ([P, C.POINTER(SZ)], I32),
+        "ovl_moe_forward": ([P, P, U32, U32, U64, P, P, P, P, P, U64, P], I32),
         "ovl_debug_kv_route": ([P, U32, U32, U32, U32, U32, U32, C.POINTER(U32)], I32),
     }
     for name, (args, res) in sig.items():
@@ -161,7 +204,8 @@ EXPORTED = ("ovl_create", "ovl_destroy", "ovl_load_base", "ovl_stage_adapter", "
             "ovl_content_digest", "ovl_version", "ovl_dualpath_forward_noalloc", "ovl_stage_activations",
             "ovl_manifest_parse", "ovl_activate_manifest", "ovl_kv_workspace_bytes", "ovl_kv_init", "ovl_kv_extend",
             "ovl_kv_append", "ovl_kv_read", "ovl_kv_attention", "ovl_kv_fork", "ovl_kv_compact", "ovl_kv_release",
-            "ovl_kv_check", "ovl_debug_kv_route")
+            "ovl_kv_check", "ovl_debug_kv_route", "ovl_kv_positions", "ovl_rope_plan", "ovl_rope_apply", "ovl_block_norm_apply",
+            "ovl_glu", "ovl_moe_workspace_bytes", "ovl_moe_forward")
 
 
 class OvlError(RuntimeError):
@@ -404,6 +448,10 @@ def ovl_kv_extend(kv, seqs: int, tok_off: int, n_seqs: int, stream: int = 0) -> 
     return lib.ovl_kv_extend(_kv(kv), seqs, tok_off, n_seqs, stream)
 
 
+def ovl_kv_positions(kv, seqs: int, tok_off: int, n_seqs: int, n_tokens: int, pos: int, stream: int = 0) -> int:
+    return lib.ovl_kv_positions(_kv(kv), seqs, tok_off, n_seqs, n_tokens, pos, stream)
+
+
 def ovl_kv_append(kv, layer: int, seqs: int, tok_off: int, n_seqs: int, n_tokens: int, k: int, v: int, dtype: int,
                   k_stride: int, v_stride: int, stream: int = 0) -> int:
     return lib.ovl_kv_append(_kv(kv), layer, seqs, tok_off, n_seqs, n_tokens, k, v, dtype, k_stride, v_stride, stream)
@@ -442,3 +490,50 @@ def ovl_debug_kv_route(kv, n_seqs: int, n_tokens: int, max_new: int, dtype: int,
     out = C.c_uint32(0)
     st = lib.ovl_debug_kv_route(_kv(kv), n_seqs, n_tokens, max_new, dtype, n_heads, n_sms, C.byref(out))
     return st, int(out.value)
+
+
+# ---- between the projections (see include/ovl.h).  Structs or their addresses;
+# the rest device addresses, strides in elements and sizes.
+
+def _struct(s):
+    return C.byref(s) if isinstance(s, C.Structure) else s
+
+
+def ovl_rope_plan(head_dim: int, rot_dim: int, layout: int, base: float, scaling: int = OVL_ROPE_PLAIN,
+                  factor: float = 1.0, original: int = 0, low: float = 1.0, high: float = 4.0, magnitude: float = 0.0):
+    out = ovl_rope()
+    st = lib.ovl_rope_plan(head_dim, rot_dim, layout, base, scaling, factor, original, low, high, magnitude,
+                           C.byref(out))
+    return st, out
+
+
+def ovl_rope_apply(rope, n_tokens: int, pos: int, q: int, q_heads: int, q_stride: int, k: int, k_heads: int,
+                   k_stride: int, dtype: int, q_out: int, q_out_stride: int, k_out: int, k_out_stride: int,
+                   out_dtype: int, stream: int = 0) -> int:
+    return lib.ovl_rope_apply(_struct(rope), n_tokens, pos, q, q_heads, q_stride, k, k_heads, k_stride, dtype, q_out,
+                              q_out_stride, k_out, k_out_stride, out_dtype, stream)
+
+
+def ovl_block_norm_apply(norm, n_tokens: int, x: int, x_dtype: int, x_stride: int, y: int, y_dtype: int, y_stride: int,
+                         gate: int, gate_dtype: int, gate_stride: int, gate_row: int, n_gates: int, x_out: int,
+                         x_out_stride: int, h: int, h_dtype: int, h_stride: int, stream: int = 0) -> int:
+    return lib.ovl_block_norm_apply(_struct(norm), n_tokens, x, x_dtype, x_stride, y, y_dtype, y_stride, gate,
+                                    gate_dtype, gate_stride, gate_row, n_gates, x_out, x_out_stride, h, h_dtype, h_stride,
+                                    stream)
+
+
+def ovl_glu(act: int, n_tokens: int, width: int, gate: int, gate_stride: int, up: int, up_stride: int, dtype: int,
+            out: int, out_stride: int, out_dtype: int, stream: int = 0) -> int:
+    return lib.ovl_glu(act, n_tokens, width, gate, gate_stride, up, up_stride, dtype, out, out_stride, out_dtype, stream)
+
+
+def ovl_moe_workspace_bytes(moe):
+    out = C.c_size_t(0)
+    st = lib.ovl_moe_workspace_bytes(_struct(moe), C.byref(out))
+    return st, int(out.value)
+
+
+def ovl_moe_forward(moe, x: int, dtype: int, n_tokens: int, x_stride: int, choice: int, weight: int, choice_out: int,
+                    weight_out: int, y: int, y_stride: int, stream: int = 0) -> int:
+    return lib.ovl_moe_forward(_struct(moe), x, dtype, n_tokens, x_stride, choice, weight, choice_out, weight_out, y,
+                               y_stride, stream)

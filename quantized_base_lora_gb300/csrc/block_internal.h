@@ -1,0 +1,149 @@
+// Shared by the translation units of what a decoder block computes between its
+// projections (ovl_rope_apply, ovl_block_norm_apply, ovl_glu, ovl_moe_forward).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ovl.h"
+#include "kv_internal.h"
+#include "ptx.cuh"
+
+namespace ovl {
+
+// A tensor of tokens: element c of token t lies at ptr + (t * stride + c) elements.
+struct Rows {
+  void* ptr;
+  uint64_t stride;
+  bool bf16;
+};
+
+// N consecutive elements from element `at` of a float32 or bfloat16 array, as
+// fp32.  N > 1: the address is a multiple of N elements or of 16 bytes, whichever is less.
+template <int N>
+__device__ __forceinline__ void load_f32(const void* base, bool bf16, uint64_t at, float (&v)[N]) {
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if constexpr (N == 1) {
+      v[0] = __uint_as_float(static_cast<uint32_t>(*p) << 16);
+    } else {
+      uint32_t w[N / 2];
+      if constexpr (N == 8) {
+        const uint4 r = *reinterpret_cast<const uint4*>(p);
+        w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+      } else {
+        static_assert(N == 4, "1, 4 or 8 elements");
+        const uint2 r = *reinterpret_cast<const uint2*>(p);
+        w[0] = r.x, w[1] = r.y;
+      }
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+    const float* p = static_cast<const float*>(base) + at;
+    if constexpr (N == 1) {
+      v[0] = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(p + i);
+        v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The same way back, rounded to nearest.
+template <int N>
+__device__ __forceinline__ void store_f32(void* base, bool bf16, uint64_t at, const float (&v)[N]) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    if constexpr (N == 1) *p = static_cast<uint16_t>(two_bf16(v[0], v[0]));
+    else if constexpr (N == 4)
+      *reinterpret_cast<uint2*>(p) = make_uint2(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]));
+    else
+      *reinterpret_cast<uint4*>(p) = make_uint4(two_bf16(v[0], v[1]), two_bf16(v[2], v[3]), two_bf16(v[4], v[5]),
+                                                two_bf16(v[6], v[7]));
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if constexpr (N == 1) {
+      *p = v[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+  }
+}
+
+// act(v) of OVL_ACT_*, in fp32.  The tanh of the last but one is written as
+// (1 + tanh u) / 2 = 1 / (1 + e^(-2u)).
+__device__ __forceinline__ float activated(float v, uint32_t act) {
+  switch (act) {
+    case OVL_ACT_SILU: return __fdividef(v, 1.f + expf(-v));
+    case OVL_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    case OVL_ACT_GELU_TANH:
+      return __fdividef(v, 1.f + expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
+    default: return fmaxf(v, 0.f);
+  }
+}
+
+cudaError_t launch_rope(const ovl_rope& rope, uint32_t n_tokens, const int32_t* pos, Rows q, uint32_t q_heads, Rows k,
+                        uint32_t k_heads, Rows q_out, Rows k_out, cudaStream_t st);
+cudaError_t launch_kv_positions(const KvDev& kv, const int32_t* seqs, const int32_t* off, uint32_t n, uint32_t n_tokens,
+                                int32_t* pos, cudaStream_t st);
+
+// Gate of ovl_block_norm_apply; ptr null: ones.
+struct Gate {
+  Rows rows;
+  const int32_t* row;
+  uint32_t n;
+};
+cudaError_t launch_block_norm(const ovl_block_norm& norm, uint32_t n_tokens, Rows x, Rows y, Gate gate, Rows x_out,
+                              Rows h, cudaStream_t st);
+cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gate, Rows up, Rows out, cudaStream_t st);
+
+// A mixture-of-experts call as its kernels take it.
+constexpr uint32_t kMoeTokens = 32;      // tokens of one expert that one pass over its weights serves
+constexpr uint32_t kMoeMaxUnits = OVL_MOE_MAX_EXPERTS + OVL_MAX_T * OVL_MOE_MAX_TOP / kMoeTokens;
+struct MoeUnit {
+  uint32_t expert_n;       // expert << 8 | pairs (1 .. kMoeTokens)
+  uint32_t first;          // of its pairs in `order`
+};
+struct MoeDev {
+  const uint8_t *gate_qs, *up_qs, *down_qs, *gate_d, *up_d, *down_d;
+  const void* router;
+  const float* bias;
+  uint32_t quant, experts, top, hidden, ffn, act, score, renormalize;
+  float scale;
+  bool router_bf16, bf16, given;
+  uint32_t tokens, pairs;
+  Rows x, y;
+  const int32_t* given_choice;
+  const float* given_weight;
+  int32_t* choice_out;
+  float* weight_out;
+  // workspace
+  uint32_t* arrived;       // [0] groups of 8 tokens whose choice is made, [1 + i] CTAs of group i: 0 between calls
+  uint32_t* n_units;
+  float* logits;           // [tokens][experts]
+  int32_t* choice;         // [tokens][top], -1 = none
+  float* weight;           // [tokens][top]
+  int32_t* order;          // pairs (token * top + place) by expert
+  MoeUnit* units;          // [kMoeMaxUnits]
+  uint16_t* xp;            // [parts][tokens][hidden] bf16, in the order of the MMA fragments
+  uint16_t* hp;            // [parts][pairs][ffn], the same of the activations
+  float* part;             // [pairs][hidden]: weighted outputs
+};
+cudaError_t launch_moe(const MoeDev& m, cudaStream_t st);
+
+}  // namespace ovl

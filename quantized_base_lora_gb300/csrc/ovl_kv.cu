@@ -4,6 +4,7 @@
 #include <cstring>
 #include <string>
 
+#include "block_internal.h"
 #include "kv_internal.h"
 #include "ovl_internal.h"
 
@@ -196,6 +197,19 @@ ovl_status ovl_kv_read(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, co
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(OVL_E_SHAPE, "k_out and v_out need 16-byte alignment");
   return done(launch_kv_read(d, layer, seqs, tok_off, n_seqs, n_tokens, k_out, v_out,
                              static_cast<cudaStream_t>(stream)));
+}
+
+ovl_status ovl_kv_positions(const ovl_kv* kv, const int32_t* seqs, const int32_t* tok_off, uint32_t n_seqs,
+                            uint32_t n_tokens, int32_t* pos, void* stream) {
+  KvDev d;
+  ovl_status st = check_kv(kv, &d);
+  if (st == OVL_OK) st = check_batch(d, 0, seqs, tok_off, n_seqs);
+  if (st != OVL_OK) return st;
+  if (n_seqs == 0 || n_tokens == 0) return OVL_OK;
+  if (n_tokens > 0x7fffffffu) return fail(OVL_E_ARG, "too many tokens");
+  if (!pos) return fail(OVL_E_ARG, "pos is null");
+  if (!aligned(pos, 4)) return fail(OVL_E_SHAPE, "pos needs 4-byte alignment");
+  return done(launch_kv_positions(d, seqs, tok_off, n_seqs, n_tokens, pos, static_cast<cudaStream_t>(stream)));
 }
 
 ovl_status ovl_kv_attention(const ovl_kv* kv, uint32_t layer, const int32_t* seqs, const int32_t* tok_off,

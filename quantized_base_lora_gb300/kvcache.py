@@ -127,6 +127,18 @@ class KvCache:
         n = seqs.shape[0]
         self._call(lib.ovl_kv_extend, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n)
 
+    def positions(self, seqs: torch.Tensor, tok_off: torch.Tensor, n_tokens: int) -> torch.Tensor:
+        """int32 [n_tokens]: where the rows' last tokens stand in their sequences, for every layer of a step."""
+        if not 0 <= n_tokens < _U32:
+            raise ValueError(f"n_tokens {n_tokens} is out of range")
+        n = seqs.shape[0]
+        pos = torch.empty(n_tokens, dtype=torch.int32, device=self.device)
+        if n == 0:                                   # no sequence, so no call: tokens that no one owns
+            return pos.fill_(-1)
+        self._call(lib.ovl_kv_positions, self._ints("seqs", seqs, n), self._ints("tok_off", tok_off, n + 1), n, n_tokens,
+                   pos.data_ptr())
+        return pos
+
     def append(self, layer: int, seqs: torch.Tensor, tok_off: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
         """Write the last tokens of the rows: k, v [tokens][kv heads][head_dim] float32 or bfloat16."""
         if not 0 <= layer < _U32:

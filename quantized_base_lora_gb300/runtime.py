@@ -46,6 +46,7 @@ class Runtime:
         rotate among them."""
         self.base = torch.from_numpy(np.ascontiguousarray(buf)).to(self.device)
         self.base_copies = [self.base] + [self.base.clone() for _ in range(copies - 1)]
+        self.quant = int(quant)
         self.tensors = [tuple(int(v) for v in t) for t in tensors]
         return ovl_load_base(self.ctx, quant, self.tensors, self.base.data_ptr(), self.base.numel(), digest,
                              stream_handle())
