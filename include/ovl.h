@@ -771,7 +771,7 @@ ovl_status ovl_glu(uint32_t act, uint32_t n_tokens, uint32_t width, const void* 
                    uint32_t out_dtype, void* stream);
 
 enum { OVL_MOE_SOFTMAX = 1, OVL_MOE_SIGMOID = 2 };
-enum { OVL_MOE_MAX_EXPERTS = 512, OVL_MOE_MAX_TOP = 16, OVL_MOE_MAX_HIDDEN = 32768 };
+enum { OVL_MOE_MAX_TOKENS = 128, OVL_MOE_MAX_EXPERTS = 512, OVL_MOE_MAX_TOP = 16, OVL_MOE_MAX_HIDDEN = 32768 };
 
 /* A mixture-of-experts layer: caller-owned device memory and its dimensions.
  *   gate, up   [n_experts * ffn] rows of hidden weights, down [n_experts * hidden]
@@ -802,19 +802,21 @@ typedef struct {
  * No counterpart in the source pages. */
 ovl_status ovl_moe_workspace_bytes(const ovl_moe* moe, size_t* out);
 
-/* The layer for up to max_tokens (at most OVL_MAX_T) tokens:
+/* The layer for up to max_tokens (at most OVL_MOE_MAX_TOKENS) tokens:
  *   y = sum_s weight_s down_e (act(gate_e x) * (up_e x)),   e = choice_s, s < top_k
  * With choice NULL the router chooses: scores are the softmax or the sigmoid of
  * router x, the top_k experts of the largest score + bias are taken (the lowest index
  * where they are equal; NaN counts as the least), a chosen expert's weight is its score,
  * divided by the sum of the chosen ones' where renormalize is set, times scale; choice_out
  * int32 and weight_out float32 [n_tokens][top_k] receive them, in falling order
- * (NULL: not wanted).  Otherwise choice int32 and weight float32 [n_tokens][top_k] are
+ * (NULL: not wanted; with a caller's choice they have to be).  Otherwise choice int32 and weight float32 [n_tokens][top_k] are
  * the caller's: an index outside 0 .. n_experts - 1 is no expert and adds nothing, an
  * expert listed twice adds twice.  x: device [n_tokens][hidden] of `dtype`, y the same;
  * 16-byte rows.  What is rounded: OVL_F32 x and the activations to three bf16 parts each
  * (2^-24 of each number); OVL_BF16 activations to two (2^-16).  Dot products are sums over
- * 32-weight blocks of exact products with the codes, in 32 bits, times the block's scale.
+ * 32-weight blocks of exact products with the codes, in 32 bits, times the block's scale;
+ * activations below 2^-20 of the square of their token's largest |x| keep fewer bits.  A
+ * token with a NaN or an infinity gives outputs that mean nothing, the others are not touched.
  * The result depends on the call's inputs alone: the same call gives the same bits.
  * Calls on one workspace must be stream-ordered.  No counterpart in the source pages. */
 ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, uint32_t n_tokens, uint64_t x_stride,

@@ -106,7 +106,7 @@ OVL_NORM_NONE, OVL_NORM_RMS, OVL_NORM_LAYER = 0, 1, 2
 OVL_NORM_MAX_HIDDEN = 32768
 OVL_ACT_SILU, OVL_ACT_GELU, OVL_ACT_GELU_TANH, OVL_ACT_RELU = 1, 2, 3, 4
 OVL_MOE_SOFTMAX, OVL_MOE_SIGMOID = 1, 2
-OVL_MOE_MAX_EXPERTS, OVL_MOE_MAX_TOP, OVL_MOE_MAX_HIDDEN = 512, 16, 32768
+OVL_MOE_MAX_TOKENS, OVL_MOE_MAX_EXPERTS, OVL_MOE_MAX_TOP, OVL_MOE_MAX_HIDDEN = 128, 512, 16, 32768
 
 
 class ovl_rope(C.Structure):

@@ -284,7 +284,7 @@ def glu(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", dtype: torch.dt
 
 
 class Moe:
-    """A mixture-of-experts layer over quantized experts, for up to max_tokens (at most 512) tokens a call.
+    """A mixture-of-experts layer over quantized experts, for up to max_tokens (at most 128) tokens a call.
 
     gate, up: (qs, d) of [n_experts * ffn] rows of hidden weights, down: of [n_experts * hidden] rows of ffn weights, in
     the base's layout of `quant`: qs int8 or uint8 and d float16 (q4_K: uint8) tensors, contiguous, of any shape with
@@ -367,6 +367,8 @@ class Moe:
                     or weight.get_device() != index:
                 raise ValueError(f"weight must be contiguous float32 {shape} on cuda:{index}")
             wp = weight.data_ptr()
+            if routing:
+                raise ValueError("routing returns the router's choice, and the choice is given")
         if routing:
             choice_out = torch.empty(shape, dtype=torch.int32, device=x.device)
             weight_out = torch.empty(shape, dtype=torch.float32, device=x.device)

@@ -113,12 +113,27 @@ cudaError_t launch_block_norm(const ovl_block_norm& norm, uint32_t n_tokens, Row
 cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gate, Rows up, Rows out, cudaStream_t st);
 
 // A mixture-of-experts call as its kernels take it.
-constexpr uint32_t kMoeTokens = 32;      // tokens of one expert that one pass over its weights serves
-constexpr uint32_t kMoeMaxUnits = OVL_MOE_MAX_EXPERTS + OVL_MAX_T * OVL_MOE_MAX_TOP / kMoeTokens;
+constexpr uint32_t kMoeTokens = 8;       // tokens of one expert that one pass over its weights serves
+constexpr uint32_t kMoeMaxPairs = OVL_MOE_MAX_TOKENS * OVL_MOE_MAX_TOP;
+constexpr uint32_t kMoeMaxUnits = OVL_MOE_MAX_EXPERTS + kMoeMaxPairs / kMoeTokens;
+// Up to kMoeTokens pairs of one expert, in 41 bits.
 struct MoeUnit {
-  uint32_t expert_n;       // expert << 8 | pairs (1 .. kMoeTokens)
-  uint32_t first;          // of its pairs in `order`
+  uint16_t first_pairs;    // first of its pairs in the order by experts: 11 bits; pairs - 1: 3
+  uint16_t expert_groups;  // expert: 9 bits; units of the expert - 1: the lower 7 of 8
+  uint16_t group_groups;   // the expert's first unit: 10 bits; the rest of the 8
+  static __device__ MoeUnit make(uint32_t expert, uint32_t pairs, uint32_t group, uint32_t groups, uint32_t first) {
+    return {static_cast<uint16_t>(first | (pairs - 1) << 11), static_cast<uint16_t>(expert | ((groups - 1) & 127) << 9),
+            static_cast<uint16_t>(group | (groups - 1) >> 7 << 10)};
+  }
+  __device__ uint32_t expert() const { return expert_groups & 511; }
+  __device__ uint32_t groups() const { return (expert_groups >> 9 | (group_groups >> 10 << 7)) + 1; }
+  __device__ uint32_t group() const { return group_groups & 1023; }
+  __device__ uint32_t pairs() const { return (first_pairs >> 11) + 1; }
+  __device__ uint32_t first() const { return first_pairs & 2047; }
 };
+static_assert(OVL_MOE_MAX_EXPERTS <= 512 && kMoeMaxPairs <= 2048 && kMoeTokens <= 8 && kMoeMaxPairs / kMoeTokens <= 256 &&
+                  kMoeMaxUnits <= 1024,
+              "fields of a unit");
 struct MoeDev {
   const uint8_t *gate_qs, *up_qs, *down_qs, *gate_d, *up_d, *down_d;
   const void* router;
@@ -133,14 +148,12 @@ struct MoeDev {
   int32_t* choice_out;
   float* weight_out;
   // workspace
-  uint32_t* arrived;       // [0] groups of 8 tokens whose choice is made, [1 + i] CTAs of group i: 0 between calls
-  uint32_t* n_units;
+  uint32_t* arrived;       // router CTAs of each group of 8 tokens: 0 between calls
   float* logits;           // [tokens][experts]
-  int32_t* choice;         // [tokens][top], -1 = none
-  float* weight;           // [tokens][top]
-  int32_t* order;          // pairs (token * top + place) by expert
-  MoeUnit* units;          // [kMoeMaxUnits]
-  uint16_t* xp;            // [parts][tokens][hidden] bf16, in the order of the MMA fragments
+  int32_t* choice;         // [tokens][top] (the caller's stay where they are)
+  float* weight;
+  float* power;            // [tokens]: 2^e of the largest |x|
+  uint16_t* xp;            // [parts][tokens][hidden] bf16, scaled, in the order of the MMA fragments
   uint16_t* hp;            // [parts][pairs][ffn], the same of the activations
   float* part;             // [pairs][hidden]: weighted outputs
 };

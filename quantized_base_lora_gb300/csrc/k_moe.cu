@@ -1,10 +1,9 @@
-// The router of a mixture-of-experts layer, what it hands to the experts' products
-// (moe_rows.cuh), and the sum of the experts' outputs.
+// The router of a mixture-of-experts layer, the tokens as its products (moe_rows.cuh) take
+// them, and the sum of the experts' outputs.
 //
-// Scores are plain fp32 dot products: a warp has one expert and up to 8 tokens.  The last
-// CTA of 8 tokens chooses their experts, a warp a token, and the last of those sorts the
-// chosen (token, expert) pairs by expert: the products then read an expert's weights once for all its tokens.
-// Beside that, further CTAs split the tokens into the bf16 parts that the products multiply.
+// Scores are plain fp32 dot products: a CTA has 8 experts and up to 8 tokens, two warps an
+// expert.  The last CTA of 8 tokens chooses their experts, a warp a token.  Beside that,
+// further CTAs split the tokens into scaled bf16 parts.
 #include <type_traits>
 
 #include "moe_rows.cuh"
@@ -13,8 +12,8 @@ namespace ovl {
 namespace {
 
 using namespace moe;
-constexpr int kThreads = 256;
-constexpr uint32_t kGroup = 8;           // tokens of a router CTA, experts of it as well: one a warp
+constexpr uint32_t kThreads = 512;
+constexpr uint32_t kGroup = 8;           // tokens of a router CTA, and its experts
 
 // Order-preserving bits of a score; NaN is the least.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -28,36 +27,42 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// logits[token][expert] of up to 8 tokens from t0 and the warp's expert.
-__device__ void scores(const MoeDev& m, uint32_t expert, uint32_t t0, uint32_t n) {
+// Scores of N tokens from t0 (places behind the last token take it once more) and an
+// expert over every other piece of the row, added up over the warp.
+template <int N>
+__device__ __forceinline__ void scores(const MoeDev& m, uint32_t expert, uint32_t t0, uint32_t odd, float (&acc)[N]) {
+  constexpr int kAhead = N == 1 ? 8 : 2;           // pieces in flight
   const uint32_t lane = threadIdx.x & 31;
-  float acc[kGroup];
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(kGroup); ++i) acc[i] = 0.f;
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
   const uint64_t row = static_cast<uint64_t>(expert) * m.hidden;
-#pragma unroll 4
-  for (uint32_t c = lane * 4; c < m.hidden; c += 128) {
-    float w[4];
-    load_f32<4>(m.router, m.router_bf16, row + c, w);
+  for (uint32_t c0 = odd * 128 + lane * 4; c0 < m.hidden; c0 += 256 * kAhead) {
+    float w[kAhead][4], x[kAhead][N][4];
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(kGroup); ++i) {
-      if (i >= static_cast<int>(n)) break;
-      float x[4];
-      load_f32<4>(m.x.ptr, m.x.bf16, (t0 + i) * m.x.stride + c, x);
+    for (int a = 0; a < kAhead; ++a) {
+      const uint32_t c = c0 + 256 * a, at = min(c, m.hidden - 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i] = fmaf(w[j], x[j], acc[i]);
+      for (int j = 0; j < 4; ++j) w[a][j] = 0.f;
+      if (c < m.hidden) load_f32<4>(m.router, m.router_bf16, row + c, w[a]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) load_f32<4>(m.x.ptr, m.x.bf16, min(t0 + i, m.tokens - 1) * m.x.stride + at, x[a][i]);
     }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (c0 + 256 * a < m.hidden) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i] = fmaf(w[a][j], x[a][i][j], acc[i]);
+      }
   }
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(kGroup); ++i) {
-    const float v = warp_sum(acc[i]);
-    if (i < static_cast<int>(n) && lane == 0) m.logits[static_cast<uint64_t>(t0 + i) * m.experts + expert] = v;
-  }
+  for (int i = 0; i < N; ++i) acc[i] = warp_sum(acc[i]);
 }
 
-// The token's top_k experts and their weights, by one warp.
+// The token's top_k experts and their weights, by one warp; 32 kMost experts at most.
+template <int kMost>
 __device__ void choose(const MoeDev& m, uint32_t token) {
-  constexpr int kMost = OVL_MOE_MAX_EXPERTS / 32;
   const uint32_t lane = threadIdx.x & 31;
   const bool softmax = m.score == OVL_MOE_SOFTMAX;
   float z[kMost];
@@ -118,113 +123,51 @@ __device__ void choose(const MoeDev& m, uint32_t token) {
   }
 }
 
-// Pairs sorted by expert, in pair order within one, and cut into units; by one CTA.
-__device__ void sort_pairs(const MoeDev& m, bool given) {
-  constexpr uint32_t kW = kThreads / 32;
-  __shared__ uint32_t count[kW][OVL_MOE_MAX_EXPERTS];
-  __shared__ uint32_t sums[2][kW];
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  for (uint32_t i = threadIdx.x; i < kW * OVL_MOE_MAX_EXPERTS; i += kThreads) (&count[0][0])[i] = 0;
+// A token as scaled bf16 parts, by one CTA.
+template <uint32_t Q, int PARTS>
+__device__ void split_token(const MoeDev& m, uint32_t token) {
+  __shared__ float most[kThreads / 32];
+  const uint64_t row = token * m.x.stride;
+  float top = 0.f;
+  for (uint32_t c = threadIdx.x * 8; c < m.hidden; c += kThreads * 8) {
+    float x[8];
+    load_f32<8>(m.x.ptr, m.x.bf16, row + c, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x / 32] = top;
   __syncthreads();
-  const uint32_t per = (m.pairs + kW * 32 - 1) / (kW * 32);          // rounds of 32 pairs a warp
-  const uint32_t first = warp * per * 32;
-  auto expert_of = [&](uint32_t p) {
-    int32_t e = -1;
-    if (p < m.pairs) {
-      e = given ? m.given_choice[p] : __ldcg(&m.choice[p]);
-      if (static_cast<uint32_t>(e) >= m.experts) e = -1;
-    }
-    return e;
-  };
-  for (uint32_t r = 0; r < per; ++r) {
-    const uint32_t p = first + r * 32 + lane;
-    const int32_t e = expert_of(p);
-    if (given && p < m.pairs) {
-      m.choice[p] = e;
-      m.weight[p] = m.given_weight[p];
-      if (m.choice_out) m.choice_out[p] = e;
-      if (m.weight_out) m.weight_out[p] = m.given_weight[p];
-    }
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) count[warp][e] += __popc(same);
-    __syncwarp();
-  }
-  __syncthreads();
-  // Thread t has experts 2 t and 2 t + 1: pairs and units before them.
-  uint32_t n[2], before_pairs = 0, before_units = 0, pairs = 0, units = 0;
-  static_assert(OVL_MOE_MAX_EXPERTS == 2 * kThreads, "two experts a thread");
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t e = 2 * threadIdx.x + i;
-    n[i] = 0;
-    for (uint32_t w = 0; w < kW; ++w) n[i] += count[w][e];
-    pairs += n[i];
-    units += (n[i] + kMoeTokens - 1) / kMoeTokens;
-  }
-  uint32_t a = pairs, b = units;
+  for (uint32_t w = 0; w < kThreads / 32; ++w) top = fmaxf(top, most[w]);
+  // 2^e <= top < 2^(e + 1) within the normal range, whose inverse is a number too
+  const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 2), 253) - 127;
+  if (threadIdx.x == 0) m.power[token] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const float once = __uint_as_float(static_cast<uint32_t>((kTokenExponent - e) / 2 + 127) << 23);       // (100 - e) / 2 is -13 .. 112
+  const float twice = __uint_as_float(static_cast<uint32_t>(kTokenExponent - e - (kTokenExponent - e) / 2 + 127) << 23);
+  for (uint32_t c = threadIdx.x * 8; c < m.hidden; c += kThreads * 8) {
+    float x[8];
+    load_f32<8>(m.x.ptr, m.x.bf16, row + c, x);
+    uint16_t v[8][PARTS];
 #pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, a, s), v = __shfl_up_sync(0xffffffffu, b, s);
-    if (static_cast<int>(lane) >= s) a += u, b += v;
-  }
-  if (lane == 31) sums[0][warp] = a, sums[1][warp] = b;
-  __syncthreads();
-  for (uint32_t w = 0; w < warp; ++w) before_pairs += sums[0][w], before_units += sums[1][w];
-  before_pairs += a - pairs;
-  before_units += b - units;
-  if (threadIdx.x == kThreads - 1) *m.n_units = before_units + units;
+    for (int j = 0; j < 8; ++j) parts_of<PARTS>(x[j] * once * twice * share_of<Q>(j), v[j]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t e = 2 * threadIdx.x + i;
-    for (uint32_t at = 0; at < n[i]; at += kMoeTokens)
-      m.units[before_units++] = MoeUnit{e << 8 | min(n[i] - at, kMoeTokens), before_pairs + at};
-    uint32_t at = before_pairs;
-    for (uint32_t w = 0; w < kW; ++w) {
-      const uint32_t c = count[w][e];
-      count[w][e] = at;
-      at += c;
-    }
-    before_pairs += n[i];
-  }
-  __syncthreads();
-  for (uint32_t r = 0; r < per; ++r) {
-    const uint32_t p = first + r * 32 + lane;
-    const int32_t e = expert_of(p);
-    const uint32_t same = __match_any_sync(0xffffffffu, e), below = __popc(same & ((1u << lane) - 1));
-    uint32_t at = 0;
-    if (e >= 0) at = count[warp][e] + below;
-    __syncwarp();
-    if (e >= 0 && below == 0) count[warp][e] += __popc(same);
-    __syncwarp();
-    if (e >= 0) m.order[at] = static_cast<int32_t>(p);
-  }
-}
-
-// The tokens as bf16 parts, 8 channels a thread.
-template <uint32_t Q>
-__device__ void split_tokens(const MoeDev& m, uint32_t block) {
-  const uint32_t per = m.hidden / 8;
-  const uint64_t i = static_cast<uint64_t>(block) * kThreads + threadIdx.x;
-  const uint32_t token = static_cast<uint32_t>(i / per), c = static_cast<uint32_t>(i % per) * 8;
-  if (token >= m.tokens) return;
-  float x[8];
-  load_f32<8>(m.x.ptr, m.x.bf16, token * m.x.stride + c, x);
-  auto put = [&](auto parts) {
-    constexpr int kParts = decltype(parts)::value;
-    uint16_t v[8][kParts];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) parts_of<kParts>(x[j], v[j]);
-#pragma unroll
-    for (int q = 0; q < kParts; ++q) {
+    for (int q = 0; q < PARTS; ++q) {
+      uint16_t* out = m.xp + (static_cast<uint64_t>(q) * m.tokens + token) * m.hidden + (c & ~31u);
       uint32_t w[4];
+      if constexpr (Q == OVL_Q8_0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = Q == OVL_Q8_0 ? v[2 * j][q] | static_cast<uint32_t>(v[2 * j + 1][q]) << 16 : v[j][q] | static_cast<uint32_t>(v[j + 4][q]) << 16;
-      *reinterpret_cast<uint4*>(m.xp + (static_cast<uint64_t>(q) * m.tokens + token) * m.hidden + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) w[j] = v[2 * j][q] | static_cast<uint32_t>(v[2 * j + 1][q]) << 16;
+        *reinterpret_cast<uint2*>(out + place_of<Q>(c & 31)) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(out + place_of<Q>((c & 31) + 4)) = make_uint2(w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = v[j][q] | static_cast<uint32_t>(v[j + 4][q]) << 16;
+        *reinterpret_cast<uint4*>(out + (c & 31)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-  };
-  if (m.bf16) put(std::integral_constant<int, 1>{});
-  else put(std::integral_constant<int, 3>{});
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ MoeDev m, uint32_t routers) {
@@ -232,51 +175,63 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ 
   griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x >= routers) {
-    if (m.quant == OVL_Q8_0) split_tokens<OVL_Q8_0>(m, blockIdx.x - routers);
-    else split_tokens<OVL_Q4_0>(m, blockIdx.x - routers);
+    const uint32_t token = blockIdx.x - routers;
+    if (m.quant == OVL_Q8_0) m.bf16 ? split_token<OVL_Q8_0, 1>(m, token) : split_token<OVL_Q8_0, 3>(m, token);
+    else m.bf16 ? split_token<OVL_Q4_0, 1>(m, token) : split_token<OVL_Q4_0, 3>(m, token);
     return;
   }
-  if (m.given) {
-    sort_pairs(m, true);
-    return;
+  __shared__ float part[kGroup][kGroup];           // expert, token: of the odd pieces
+  const uint32_t wide = (m.experts + kGroup - 1) / kGroup;
+  const uint32_t group = blockIdx.x / wide, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const uint32_t e = warp % kGroup, odd = warp / kGroup;
+  const uint32_t expert = blockIdx.x % wide * kGroup + e, t0 = group * kGroup, n = min(m.tokens - t0, kGroup);
+  float mine = 0.f;                                // lane i: of token i
+  if (expert < m.experts) {
+    if (n == 1) {
+      float acc[1];
+      scores(m, expert, t0, odd, acc);
+      mine = acc[0];
+    } else {
+      float acc[kGroup];
+      scores(m, expert, t0, odd, acc);
+#pragma unroll
+      for (uint32_t i = 0; i < kGroup; ++i)
+        if (lane == i) mine = acc[i];
+    }
   }
-  const uint32_t wide = (m.experts + kGroup - 1) / kGroup, groups = (m.tokens + kGroup - 1) / kGroup;
-  const uint32_t group = blockIdx.x / wide, warp = threadIdx.x / 32;
-  const uint32_t expert = blockIdx.x % wide * kGroup + warp, t0 = group * kGroup, n = min(m.tokens - t0, kGroup);
-  if (expert < m.experts) scores(m, expert, t0, n);
-  __threadfence();
+  if (odd && lane < kGroup) part[e][lane] = mine;
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&m.arrived[1 + group], 1u) + 1 == wide;
+  if (!odd && expert < m.experts && lane < n) {
+    m.logits[static_cast<uint64_t>(t0 + lane) * m.experts + expert] = mine + part[e][lane];
+    __threadfence();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(&m.arrived[group], 1u) + 1 == wide;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  if (warp < n) choose(m, t0 + warp);
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    m.arrived[1 + group] = 0;
-    last = atomicAdd(&m.arrived[0], 1u) + 1 == groups;
+  if (warp < n) {
+    if (m.experts <= 128) choose<4>(m, t0 + warp);
+    else choose<OVL_MOE_MAX_EXPERTS / 32>(m, t0 + warp);
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  if (threadIdx.x == 0) m.arrived[0] = 0;
-  sort_pairs(m, false);
+  if (threadIdx.x == 0) m.arrived[group] = 0;
 }
 
 // y of a token: its experts' weighted outputs, in the order of the choice.
-__global__ void __launch_bounds__(kThreads) k_moe_sum(const __grid_constant__ MoeDev m) {
+constexpr uint32_t kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) k_moe_sum(const __grid_constant__ MoeDev m) {
   griddep_launch_dependents();
+  const int32_t* choice = m.given ? m.given_choice : m.choice;
   griddep_wait();
   const uint32_t per = m.hidden / 4;
-  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
   const uint32_t token = static_cast<uint32_t>(i / per), c = static_cast<uint32_t>(i % per) * 4;
   if (token >= m.tokens) return;
   float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (uint32_t s = 0; s < m.top; ++s) {
     const uint32_t p = token * m.top + s;
-    if (m.choice[p] < 0) continue;
+    if (static_cast<uint32_t>(choice[p]) >= m.experts) continue;
     float v[4];
     load_f32<4>(m.part, false, static_cast<uint64_t>(p) * m.hidden + c, v);
 #pragma unroll
@@ -289,13 +244,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_sum(const __grid_constant__ Mo
 
 cudaError_t launch_moe(const MoeDev& m, cudaStream_t st) {
   const uint32_t wide = (m.experts + kGroup - 1) / kGroup, groups = (m.tokens + kGroup - 1) / kGroup;
-  const uint32_t routers = m.given ? 1 : wide * groups;
-  const uint32_t splitters = (m.tokens * (m.hidden / 8) + kThreads - 1) / kThreads;
-  cudaError_t e = launch_chained(k_moe_route, dim3(routers + splitters), kThreads, 0, st, m, routers);
+  const uint32_t routers = m.given ? 0 : wide * groups;
+  cudaError_t e = launch_chained(k_moe_route, dim3(routers + m.tokens), kThreads, 0, st, m, routers);
   if (e == cudaSuccess)
     e = m.quant == OVL_Q8_0 ? launch_products_q8_0(m, st) : m.quant == OVL_Q4_0 ? launch_products_q4_0(m, st) : launch_products_q4_k(m, st);
   if (e != cudaSuccess) return e;
-  return launch_chained(k_moe_sum, dim3((m.tokens * (m.hidden / 4) + kThreads - 1) / kThreads), kThreads, 0, st, m);
+  return launch_chained(k_moe_sum, dim3((m.tokens * (m.hidden / 4) + kSumThreads - 1) / kSumThreads), kSumThreads, 0, st, m);
 }
 
 }  // namespace ovl

@@ -26,65 +26,104 @@
 namespace ovl {
 namespace moe {
 
-constexpr int kWarps = 8;
-constexpr int kStages = 4;
-constexpr uint32_t kRowBytes = 128;                       // of a row in one stage
+constexpr uint32_t kWarps = 12;
+constexpr int kStages = 2;
+constexpr uint32_t kRowBytes = 128;                       // of a row in one stage: 8 pieces of 16
 constexpr uint32_t kScaleBytes = 20;                      // of a row in one stage: 16, or five words around 16 bytes
 constexpr uint32_t kStageBytes = 32 * (kRowBytes + kScaleBytes);
-constexpr uint32_t kTableBytes = 2 * 8 * 32 * 4;          // a warp's scales (and minimums) of a stage
-constexpr uint32_t kJoinBytes = 32 * 32 * 4;              // a warp's sums
-constexpr uint32_t kSmem = kWarps * (kStages * kStageBytes + kTableBytes + kJoinBytes);
+constexpr uint32_t kJoinBytes = kMoeTokens * 32 * 4;      // a warp's sums
+
+// Shared memory of a CTA.  It stays within 131 KB (q4_K: 163), so that the rest of the
+// SM's 256 KB is cache for the inputs, which every warp reads: with 16 warps and 206 KB,
+// 20 to 57 percent of those loads hit, and one token over two experts of 14336 took 110
+// us instead of 90.
+template <uint32_t Q>
+struct Shape {
+  static constexpr uint32_t kTableBytes = Q == OVL_Q4_K ? 2 * 8 * 32 * 4 : 0;         // a warp's scales and minimums of a stage
+  static constexpr uint32_t kTables = kWarps * kStages * kStageBytes, kJoins = kTables + kWarps * kTableBytes,
+                            kUnits = kJoins + (kWarps - 1) * kJoinBytes, kOrder = kUnits + kMoeMaxUnits * sizeof(MoeUnit),
+                            kSmem = kOrder + kMoeMaxPairs * 2;
+  static_assert(kStageBytes % 128 == 0, "slots begin on 128 bytes");
+  static_assert(kSmem <= (Q == OVL_Q4_K ? 163 : 131) * 1024, "what is left to the cache");
+};
 
 __device__ __forceinline__ void cp_async4_if(uint32_t dst, const void* src, bool on) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst),
                "l"(src), "r"(static_cast<uint32_t>(on))
                : "memory");
 }
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
-               "l"(src), "r"(static_cast<uint32_t>(on))
-               : "memory");
+// OFF: added to the address in shared memory.
+template <int BYTES, int OFF>
+__device__ __forceinline__ void cp_async_at(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1], %3;" ::"r"(dst), "l"(src), "n"(OFF), "n"(BYTES) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float* c) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// 8x8 16-bit matrices of four groups of 8 rows of 16 bytes: lane l gives the address of row
+// l and gets word l % 4 of rows l / 4 + 8 i.
+__device__ __forceinline__ void load_rows(uint32_t (&w)[4], uint32_t address) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(address)
+               : "memory");
 }
 
+// A word of codes as bf16 pairs, exactly and without any arithmetic: the integer n <= 255 in
+// the low bits of a bf16 is n 2^-133 (below 128 a subnormal, from there on the first
+// binade, which goes on in the same steps).
+//   4 bits: pair 0 is codes 0 and 4, pair 1 16 times codes 1 and 5, and so on: the inputs
+//   of odd channels are stored a 16th as large.
+//   8 bits: code + 128; pairs 0 and 1 of a word.
+// What the codes are too large by (8 and 128) is, in bf16 calls, a product with the same
+// constant in every place, from which the MMAs of the block start.  In fp32 calls it is
+// subtracted from every code: the sums then are no larger than they have to be, which their
+// 24 bits are needed for, and three parts would be six more MMAs a block.
+constexpr int kCodeExponent = 133;
+__device__ __forceinline__ void pairs_of_4(uint32_t w, uint32_t (&p)[4]) {
+  const uint32_t h = w >> 8;
+  p[0] = w & 0x000f000fu, p[1] = w & 0x00f000f0u, p[2] = h & 0x000f000fu, p[3] = h & 0x00f000f0u;
+}
+__device__ __forceinline__ void pairs_of_8(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  w ^= 0x80808080u;
+  p0 = __byte_perm(w, 0, 0x4140), p1 = __byte_perm(w, 0, 0x4342);
+}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Place of channel c of a block of 32 in the order in which lanes take them.
+template <uint32_t Q>
+__device__ __forceinline__ uint32_t place_of(uint32_t c) {
+  if constexpr (Q == OVL_Q8_0) return (c & 12) * 2 + (c >> 4) * 4 + (c & 3);
+  else return (c & 24) + ((c & 4) ? 2 * (c & 7) - 7 : 2 * (c & 7));
+}
+// What its input is multiplied by.
+template <uint32_t Q>
+__device__ __forceinline__ float share_of(uint32_t c) {
+  return Q != OVL_Q8_0 && (c & 1) ? 0.0625f : 1.f;
 }
 
-// Eight consecutive codes of a row as four bf16 pairs, exactly.
-//   4 bits: 0x4300 | c is 128 + c in bf16; pair i is codes i and i + 4 of the word.
-//   8 bits: with the sign bit s and the other seven m, 0x4300 | m is 128 + m and 0x4300 |
-//   s is 128 or 256: their difference is m - s.  Pair i is codes 2 i and 2 i + 1.
-template <uint32_t Q>
-__device__ __forceinline__ void pairs_of(uint2 w, uint32_t (&p)[4]) {
-  if constexpr (Q == OVL_Q8_0) {
-    const uint32_t b[4] = {__byte_perm(w.x, 0, 0x4140), __byte_perm(w.x, 0, 0x4342), __byte_perm(w.y, 0, 0x4140),
-                           __byte_perm(w.y, 0, 0x4342)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p[i] = sub_bf16x2((b[i] & 0x007f007fu) | 0x43004300u, (b[i] & 0x00800080u) | 0x43004300u);
-  } else {
-    const uint32_t zero = Q == OVL_Q4_K ? 0x43004300u : 0x43084308u;      // 128, or 128 + 8
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = sub_bf16x2(((w.x >> (4 * i)) & 0x000f000fu) | 0x43004300u, zero);
-  }
-}
-// Place of channel c of a group of 8 in the order of the pairs.
-template <uint32_t Q>
-__device__ __forceinline__ uint32_t pair_place(uint32_t c) {
-  return Q == OVL_Q8_0 ? c : c < 4 ? 2 * c : 2 * c - 7;
-}
+// Inputs are scaled by powers of two, so that the products stay in fp32's range: a token's
+// largest |x| to 2^kTokenExponent and up to twice that, with 2^e the power of two below it;
+// the activations by 2^(kActExponent - 2 e), since they go with the square of x.  At
+// 2^kActExponent, activations 2^77 times and 2^-20 times max|x|^2 are within range, with all of
+// the sums' 24 bits.
+__host__ __device__ constexpr float pow2(int e) { return e == 0 ? 1.f : e > 0 ? 2.f * pow2(e - 1) : 0.5f * pow2(e + 1); }
+constexpr int kTokenExponent = 100;
+constexpr int kActExponent = 50;
 
 // v as bf16 parts: the upper bits cut off, exactly, so that three parts are all 24 bits.
 // The last of two is rounded to nearest instead.
@@ -103,9 +142,101 @@ __device__ __forceinline__ void parts_of(float v, uint16_t (&p)[PARTS]) {
   }
 }
 
+// The chosen pairs sorted by expert, in pair order within one, and cut into units: by every
+// CTA for itself, in shared memory (less work than to wait for one to do it).  Returns the
+// number of units.
+template <uint32_t Q>
+__device__ __forceinline__ uint32_t sort_pairs(const MoeDev& m, uint8_t* smem) {
+  MoeUnit* units = reinterpret_cast<MoeUnit*>(smem + Shape<Q>::kUnits);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + Shape<Q>::kOrder);
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int32_t* choice = m.given ? m.given_choice : m.choice;
+  if (m.tokens == 1 && !m.given) {                        // distinct experts with one pair each
+    if (threadIdx.x < m.top) {
+      units[threadIdx.x] = MoeUnit::make(choice[threadIdx.x], 1, threadIdx.x, 1, threadIdx.x);
+      order[threadIdx.x] = static_cast<uint16_t>(threadIdx.x);
+    }
+    __syncthreads();
+    return m.top;
+  }
+  // scratch where the ring will be: pairs of each expert in each warp's share, first pairs
+  uint16_t* count = reinterpret_cast<uint16_t*>(smem);           // [kWarps][OVL_MOE_MAX_EXPERTS]
+  uint16_t* first = count + kWarps * OVL_MOE_MAX_EXPERTS;
+  uint32_t* sums = reinterpret_cast<uint32_t*>(first + OVL_MOE_MAX_EXPERTS);      // [2][kWarps]
+  static_assert(kWarps * 32 >= OVL_MOE_MAX_EXPERTS / 2, "two experts a thread");
+  constexpr uint32_t kRounds = (kMoeMaxPairs + kWarps * 32 - 1) / (kWarps * 32);
+  const uint32_t per = (m.pairs + kWarps * 32 - 1) / (kWarps * 32), from = warp * per * 32 + lane;
+  int32_t e[kRounds];
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    e[r] = -1;
+    if (r < per && from + r * 32 < m.pairs) e[r] = choice[from + r * 32];
+    if (static_cast<uint32_t>(e[r]) >= m.experts) e[r] = -1;
+  }
+  const uint32_t own = 2 * threadIdx.x;                   // the thread's experts: own and own + 1
+  if (own < m.experts) {
+#pragma unroll
+    for (uint32_t w = 0; w < kWarps; ++w) *reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own) = 0;
+  }
+  __syncthreads();
+  uint32_t rank[kRounds];
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    rank[r] = 0;
+    if (r < per) {
+      const uint32_t same = __match_any_sync(0xffffffffu, e[r]), below = __popc(same & ((1u << lane) - 1));
+      uint16_t* c = count + warp * OVL_MOE_MAX_EXPERTS + e[r];
+      if (e[r] >= 0) rank[r] = *c + below;
+      __syncwarp();
+      if (e[r] >= 0 && below == 0) *c = static_cast<uint16_t>(*c + __popc(same));
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  uint32_t n[2] = {0, 0};                                 // their pairs
+  if (own < m.experts) {
+#pragma unroll
+    for (uint32_t w = 0; w < kWarps; ++w) {
+      uint32_t* c = reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own);
+      const uint32_t some = *c;
+      *c = n[0] | n[1] << 16;
+      n[0] += some & 0xffff, n[1] += some >> 16;
+    }
+  }
+  const uint32_t groups[2] = {(n[0] + kMoeTokens - 1) / kMoeTokens, (n[1] + kMoeTokens - 1) / kMoeTokens};
+  uint32_t a = n[0] + n[1], b = groups[0] + groups[1];    // pairs and units up to them
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, a, s), v = __shfl_up_sync(0xffffffffu, b, s);
+    if (static_cast<int>(lane) >= s) a += u, b += v;
+  }
+  if (lane == 31) sums[warp] = a, sums[kWarps + warp] = b;
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kWarps; ++w) {
+    if (w < warp) a += sums[w], b += sums[kWarps + w];
+    all += sums[kWarps + w];
+  }
+  a -= n[0] + n[1], b -= groups[0] + groups[1];
+#pragma unroll
+  for (uint32_t j = 0; j < 2; ++j) {
+    if (own + j < m.experts) first[own + j] = static_cast<uint16_t>(a);
+    for (uint32_t i = 0; i < groups[j]; ++i)
+      units[b + i] = MoeUnit::make(own + j, min(n[j] - i * kMoeTokens, kMoeTokens), b, groups[j], a + i * kMoeTokens);
+    a += n[j], b += groups[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r)
+    if (e[r] >= 0) order[first[e[r]] + count[warp * OVL_MOE_MAX_EXPERTS + e[r]] + rank[r]] = static_cast<uint16_t>(from + r * 32);
+  __syncthreads();
+  return all;
+}
+
 // Where a warp's copies are: an item (32 rows of a unit) and the stage inside it.
 struct Cursor {
-  const uint8_t* row[2];       // the lane's first row and piece: of the first and of the last 16 rows
+  const uint8_t* row[2];       // the lane's next piece: of the first and of the last 16 rows
   const uint8_t* scale;        // the lane's row of scales
   uint32_t item, stage;
 };
@@ -114,16 +245,21 @@ struct Cursor {
 template <uint32_t Q, bool DOWN, int PARTS>
 struct Rows32 {
   static constexpr uint32_t kBlocks = Q == OVL_Q8_0 ? 4 : 8;            // 32-weight blocks of a stage
-  static constexpr uint32_t kScales = Q == OVL_Q8_0 ? 8 : 16;           // bytes of a row's scales in a stage
+  static constexpr bool kSigned = PARTS == 3;
+  static constexpr int kScales = Q == OVL_Q8_0 ? 8 : 16;                // bytes of a row's scales in a stage
 
   const MoeDev& m;
+  const MoeUnit* units;        // in shared memory
   uint8_t* ring;               // the warp's
   float* table;
   uint32_t lane, k, pitch, scale_pitch, tiles;
   bool scales_aligned;
 
-  __device__ Rows32(const MoeDev& dev, uint8_t* r, float* t) : m(dev), ring(r), table(t) {
+  __device__ Rows32(const MoeDev& dev, uint8_t* smem)
+      : m(dev), units(reinterpret_cast<const MoeUnit*>(smem + Shape<Q>::kUnits)) {
     lane = threadIdx.x & 31;
+    ring = smem + threadIdx.x / 32 * kStages * kStageBytes;
+    table = reinterpret_cast<float*>(smem + Shape<Q>::kTables + threadIdx.x / 32 * Shape<Q>::kTableBytes);
     k = DOWN ? m.ffn : m.hidden;
     pitch = Q == OVL_Q8_0 ? k : k / 2;
     scale_pitch = k / 16;                                               // 2 bytes a block; 16 bytes of 256 weights
@@ -131,175 +267,267 @@ struct Rows32 {
     tiles = DOWN ? m.hidden / 32 : m.ffn / 16;
   }
 
+  // Unit and tile of an item: an expert's units side by side for each tile, so that its
+  // weights are in L2 for the second and later ones.
+  __device__ MoeUnit unit_of(uint32_t item, uint32_t* tile) const {
+    const MoeUnit any = units[item / tiles];
+    const uint32_t r = item - any.group() * tiles, n = any.groups();
+    if (n == 1) {
+      *tile = r;
+      return any;
+    }
+    *tile = r / n;
+    return units[any.group() + r % n];
+  }
+
   __device__ void at(Cursor& c, uint32_t item, uint32_t stage) const {
     c.item = item;
     c.stage = stage;
-    const uint32_t unit = item / tiles, tile = item % tiles, expert = m.units[unit].expert_n >> 8;
-    const uint32_t r = lane >> 3;
-    const uint64_t piece = (lane & 7) * 16;
+    uint32_t tile;
+    const uint32_t expert = unit_of(item, &tile).expert(), r = lane / 8;
+    const uint64_t piece = lane % 8 * 16 + stage * kRowBytes;
     if constexpr (DOWN) {
       const uint64_t first = static_cast<uint64_t>(expert) * m.hidden + tile * 32;
       c.row[0] = m.down_qs + (first + r) * pitch + piece;
       c.row[1] = c.row[0] + 16ull * pitch;
-      c.scale = m.down_d + (first + lane) * scale_pitch;
+      c.scale = m.down_d + (first + lane) * scale_pitch + stage * kScales;
     } else {
       const uint64_t first = static_cast<uint64_t>(expert) * m.ffn + tile * 16;
       c.row[0] = m.gate_qs + (first + r) * pitch + piece;
       c.row[1] = m.up_qs + (first + r) * pitch + piece;
-      c.scale = (lane < 16 ? m.gate_d : m.up_d) + (first + (lane & 15)) * scale_pitch;
+      c.scale = (lane < 16 ? m.gate_d : m.up_d) + (first + (lane & 15)) * scale_pitch + stage * kScales;
     }
   }
 
-  // Asks for stage c.stage of the item.  Piece p of row r lies at piece p ^ swizzle(r), so
-  // that the 8 rows of a fragment load meet different banks.
-  __device__ void fill(const Cursor& c, uint32_t slot) const {
-    const uint32_t dst = smem_u32(ring + slot * kStageBytes);
-    const uint32_t r0 = lane >> 3, piece = lane & 7;
-    const bool on = c.stage * kRowBytes + piece * 16 < pitch;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t r = r0 + 4 * i, swizzle = Q == OVL_Q8_0 ? (r & 3) << 1 : r & 7;
-      const uint8_t* src = c.row[i / 4] + static_cast<uint64_t>(4 * (i & 3)) * pitch + c.stage * kRowBytes;
-      cp_async16_if(dst + r * kRowBytes + ((piece ^ swizzle) << 4), src, on);
+  // Asks for stage c.stage of the item and goes on to the next.  Piece p of row r lies at
+  // piece p ^ (r % 8), so that the 8 rows of a matrix meet different banks.
+  __device__ __forceinline__ void fill(Cursor& c, uint32_t slot) const {
+    const uint32_t at = smem_u32(ring) + slot * kStageBytes, r = lane / 8, piece = lane % 8;
+    if (c.stage * kRowBytes + piece * 16 < pitch) {
+      const uint32_t even = at + r * kRowBytes + ((piece ^ r) << 4), odd = even ^ 64;      // rows r + 8 i, r + 4 + 8 i
+      const uint8_t *p = c.row[0], *q = c.row[1];
+      const uint64_t step = 4 * pitch;
+      cp_async_at<16, 0>(even, p);
+      cp_async_at<16, 4 * kRowBytes>(odd, p += step);
+      cp_async_at<16, 8 * kRowBytes>(even, p += step);
+      cp_async_at<16, 12 * kRowBytes>(odd, p += step);
+      cp_async_at<16, 16 * kRowBytes>(even, q);
+      cp_async_at<16, 20 * kRowBytes>(odd, q += step);
+      cp_async_at<16, 24 * kRowBytes>(even, q += step);
+      cp_async_at<16, 28 * kRowBytes>(odd, q += step);
     }
-    const uint32_t raw = dst + 32 * kRowBytes;
-    const uint8_t* s = c.scale + c.stage * kScales;
     if (Q == OVL_Q4_K || scales_aligned) {
-      if constexpr (kScales == 16) {
-        cp_async16_if(raw + lane * 16, s, true);
-      } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(raw + lane * 8), "l"(s) : "memory");
-      }
+      cp_async_at<kScales, 32 * kRowBytes>(at + lane * kScales, c.scale);
     } else {                                                            // rows of scales begin at any even address
-      const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s)) & 2;
-      const uint32_t have = min(kScales, scale_pitch - c.stage * kScales) + shift;
+      const uint32_t shift = (lane & 1) * (scale_pitch & 2);            // a tile begins at an even row
+      const uint32_t have = min(static_cast<uint32_t>(kScales), scale_pitch - c.stage * kScales) + shift;
 #pragma unroll
-      for (uint32_t i = 0; i < kScales / 4 + 1; ++i) cp_async4_if(raw + lane * kScaleBytes + 4 * i, s - shift + 4 * i, 4 * i < have);
+      for (uint32_t i = 0; i < kScales / 4 + 1; ++i)
+        cp_async4_if(at + 32 * kRowBytes + lane * kScaleBytes + 4 * i, c.scale - shift + 4 * i, 4 * i < have);
     }
+    c.row[0] += kRowBytes, c.row[1] += kRowBytes, c.scale += kScales;
+    ++c.stage;
   }
 
-  // A stage's scales as fp32: table[block][row], and for Q4_K the minimums behind them.
-  __device__ void decode(uint32_t slot, uint32_t stage, const uint8_t* scale_row) const {
+  // A stage's scales of row r.
+  __device__ const uint16_t* scales_of(uint32_t slot, uint32_t r) const {
     const uint8_t* raw = ring + slot * kStageBytes + 32 * kRowBytes;
-    if constexpr (Q == OVL_Q4_K) {
-      const uint4 h = *reinterpret_cast<const uint4*>(raw + lane * 16);
-      const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-      const uint64_t sc = h.y | (static_cast<uint64_t>(h.z & 0xffffu) << 32), mn = (h.z >> 16) | (static_cast<uint64_t>(h.w) << 16);
+    return reinterpret_cast<const uint16_t*>(scales_aligned ? raw + r * kScales : raw + r * kScaleBytes + (r & 1) * (scale_pitch & 2));
+  }
+
+  // Q4_K: a stage's scales and minimums as fp32: table[block][row % 8][row / 8], minimums behind.
+  __device__ void decode(uint32_t slot) const {
+    const uint4 h = *reinterpret_cast<const uint4*>(ring + slot * kStageBytes + 32 * kRowBytes + lane * 16);
+    const uint32_t place = (lane & 7) * 4 + (lane >> 3);
+    const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+    const uint64_t sc = h.y | (static_cast<uint64_t>(h.z & 0xffffu) << 32), mn = (h.z >> 16) | (static_cast<uint64_t>(h.w) << 16);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        table[b * 32 + lane] = d.x * static_cast<float>(static_cast<uint32_t>(sc >> (6 * b)) & 63u);
-        table[256 + b * 32 + lane] = -d.y * static_cast<float>(static_cast<uint32_t>(mn >> (6 * b)) & 63u);
-      }
-    } else {
-      const __half* s;
-      if (scales_aligned) s = reinterpret_cast<const __half*>(raw + lane * kScales);
-      else s = reinterpret_cast<const __half*>(raw + lane * kScaleBytes +
-                                               (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(scale_row + stage * kScales)) & 2));
-#pragma unroll
-      for (uint32_t b = 0; b < kBlocks; ++b) table[b * 32 + lane] = __half2float(s[b]);
+    for (uint32_t b = 0; b < 8; ++b) {
+      const float scale = d.x * static_cast<float>(static_cast<uint32_t>(sc >> (6 * b)) & 63u);
+      const float least = -d.y * static_cast<float>(static_cast<uint32_t>(mn >> (6 * b)) & 63u);
+      table[b * 32 + place] = scale;
+      table[(8 + b) * 32 + place] = 0x1p-7f * (kSigned ? fmaf(8.f, scale, least) : least);
     }
   }
 
-  // One stage's products: acc[half of the rows][8 tokens each][fragment] += scale * codes x.
-  template <int NT>
-  __device__ void multiply(uint32_t slot, uint32_t stage, const uint16_t* const (&x)[NT], uint64_t part,
-                           float (&acc)[2][NT][4]) const {
-    const uint8_t* rows = ring + slot * kStageBytes;
-    const uint32_t g = lane >> 2, t = lane & 3;
-    const uint32_t blocks = min(kBlocks, k / 32 - stage * kBlocks);
-#pragma unroll 2
-    for (uint32_t b = 0; b < blocks; ++b) {
-      uint4 xs[NT][PARTS];
+  // The inputs of a block: `at` is the lane's byte in the first part.  The blocks behind a
+  // row's last one lie in the workspace too.
+  __device__ void inputs(uint32_t at, uint32_t part, uint4 (&v)[PARTS]) const {
+    const char* base = reinterpret_cast<const char*>(DOWN ? m.hp : m.xp);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int q = 0; q < PARTS; ++q) v[q] = *reinterpret_cast<const uint4*>(base + (at + q * part));
+  }
+
+  // One stage's products: acc[half of the rows][fragment] += scale * codes x.  `next` holds
+  // the inputs of the two blocks to come (for three parts there is no room).
+  static constexpr bool kAhead = PARTS < 3;
+  __device__ __forceinline__ void multiply(uint32_t slot, uint32_t stage, uint32_t x, uint32_t part, uint4 (&next)[2][PARTS],
+                                           float (&acc)[2][4]) const {
+    const uint32_t first = stage * kBlocks, blocks = min(kBlocks, k / 32 - first);
+    if (blocks == kBlocks) {
+      uint32_t packed[4][kBlocks / 2];           // scales of rows g + 8 i, two blocks a word
+      if constexpr (Q != OVL_Q4_K) {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          xs[n][q] = x[n] ? *reinterpret_cast<const uint4*>(x[n] + q * part + (stage * kBlocks + b) * 32) : make_uint4(0, 0, 0, 0);
-      uint32_t a[2][2][4];                       // half, k16 step, fragment
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint16_t* s = scales_of(slot, (lane >> 2) + 8 * i);
+          if (scales_aligned) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t r = h * 16 + e * 8 + g;
-          uint2 w;
-          if constexpr (Q == OVL_Q8_0) {
-            const uint32_t piece = (2 * b + (t >> 1)) ^ ((r & 3) << 1);
-            w = *reinterpret_cast<const uint2*>(rows + r * kRowBytes + piece * 16 + (t & 1) * 8);
+            for (uint32_t b = 0; b < kBlocks / 2; ++b) packed[i][b] = reinterpret_cast<const uint32_t*>(s)[b];
           } else {
-            w.x = *reinterpret_cast<const uint32_t*>(rows + r * kRowBytes + ((b ^ (r & 7)) << 4) + t * 4);
-            w.y = 0;
-          }
-          if (e == 0) pairs_of<Q>(w, lo);
-          else pairs_of<Q>(w, hi);
-        }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) a[h][s][0] = lo[2 * s], a[h][s][1] = hi[2 * s], a[h][s][2] = lo[2 * s + 1], a[h][s][3] = hi[2 * s + 1];
-      }
-      float scale[4], least[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        scale[r] = table[b * 32 + r * 8 + g];
-        if constexpr (Q == OVL_Q4_K) least[r] = table[256 + b * 32 + r * 8 + g];
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (Q == OVL_Q4_K) {           // the block's inputs summed up, in every row: codes of one
-          const uint32_t one[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q) {
-            mma_bf16(sum, one, xs[n][q].x, xs[n][q].y);
-            mma_bf16(sum, one, xs[n][q].z, xs[n][q].w);
+            for (uint32_t b = 0; b < kBlocks / 2; ++b) packed[i][b] = s[2 * b] | static_cast<uint32_t>(s[2 * b + 1]) << 16;
           }
         }
+      }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float p[4] = {0.f, 0.f, 0.f, 0.f};     // small parts first: the MMAs cut off their sums
-#pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q) {
-            mma_bf16(p, a[h][0], xs[n][q].x, xs[n][q].y);
-            mma_bf16(p, a[h][1], xs[n][q].z, xs[n][q].w);
-          }
+      for (uint32_t b = 0; b < kBlocks; b += 2) {
+        float scale[2][4], least[2][4];
+        if constexpr (Q == OVL_Q4_K) {
+          from_table(b, scale[0], least[0]);
+          from_table(b + 1, scale[1], least[1]);
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            acc[h][n][i] = fmaf(scale[2 * h + (i >> 1)], p[i], acc[h][n][i]);
-            if constexpr (Q == OVL_Q4_K) acc[h][n][i] = fmaf(least[2 * h + (i >> 1)], sum[i], acc[h][n][i]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed[i][b / 2]));
+            scale[0][i] = f.x, scale[1][i] = f.y;
           }
+        }
+        multiply_blocks<2>(slot, b, first + b, x, part, scale, least, next, acc);
+      }
+    } else {                                     // the row's last stage
+#pragma unroll 1
+      for (uint32_t b = 0; b < blocks; ++b) {
+        float scale[1][4], least[1][4];
+        if constexpr (Q == OVL_Q4_K) {
+          from_table(b, scale[0], least[0]);
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i)
+            scale[0][i] = __half2float(__ushort_as_half(scales_of(slot, (lane >> 2) + 8 * i)[b]));
+        }
+        multiply_blocks<1>(slot, b, first + b, x, part, scale, least, next, acc);
+      }
+    }
+  }
+  __device__ __forceinline__ void from_table(uint32_t b, float (&scale)[4], float (&least)[4]) const {
+    const float4 u = *reinterpret_cast<const float4*>(table + b * 32 + (lane >> 2) * 4);
+    const float4 v = *reinterpret_cast<const float4*>(table + (8 + b) * 32 + (lane >> 2) * 4);
+    scale[0] = u.x, scale[1] = u.y, scale[2] = u.z, scale[3] = u.w;
+    least[0] = v.x, least[1] = v.y, least[2] = v.z, least[3] = v.w;
+  }
+
+  // N blocks beside one another, so that their chains of MMAs fill each other's waits.
+  template <int N>
+  __device__ __forceinline__ void multiply_blocks(uint32_t slot, uint32_t b, uint32_t block, uint32_t x, uint32_t part,
+                                                  const float (&scale)[N][4], const float (&least)[N][4],
+                                                  uint4 (&next)[2][PARTS], float (&acc)[2][4]) const {
+    uint4 xs[N][PARTS];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if constexpr (kAhead && N == 2) {
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) xs[n][q] = next[n][q];
+        inputs(x + (block + 2 + n) * 64, part, next[n]);
+      } else {
+        inputs(x + (block + n) * 64, part, xs[n]);
+      }
+    }
+    uint32_t a[N][2][2][4];                      // block, half of the rows, k16 step, fragment
+    const uint32_t row = smem_u32(ring) + slot * kStageBytes + lane * kRowBytes;
+#pragma unroll
+    for (uint32_t n = 0; n < N; ++n) {
+      if constexpr (Q == OVL_Q8_0) {
+#pragma unroll
+        for (uint32_t s = 0; s < 2; ++s) {
+          uint32_t w[4];
+          load_rows(w, row + (((2 * (b + n) + s) ^ (lane & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pairs_of_8(w[i], a[n][i / 2][s][i % 2], a[n][i / 2][s][2 + i % 2]);
+        }
+      } else {
+        uint32_t w[4], p[4];
+        load_rows(w, row + (((b + n) ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pairs_of_4(w[i], p);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) a[n][i / 2][s][i % 2] = p[2 * s], a[n][i / 2][s][2 + i % 2] = p[2 * s + 1];
         }
       }
     }
+    if constexpr (kSigned) {
+      constexpr uint32_t even = Q == OVL_Q8_0 ? 0x00800080u : 0x00080008u, odd = 0x00800080u;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[n][i / 8][i / 4 % 2][i % 4] = sub_bf16x2(a[n][i / 8][i / 4 % 2][i % 4], i % 4 < 2 ? even : odd);
+    }
+    // The block's inputs added up, in every row: times -8, 128 (Q4_K) or -128 2^-133.  (Of a
+    // subnormal, the bits in front of its first one are lost to the product: hence not 1.)
+    constexpr bool kSum = Q == OVL_Q4_K || !kSigned;
+    constexpr uint32_t one = Q == OVL_Q8_0 ? 0x80808080u : Q == OVL_Q4_0 ? 0x80088008u : 0x00800080u;
+    constexpr uint32_t odd = Q == OVL_Q8_0 ? one : Q == OVL_Q4_0 ? 0x80808080u : 0x02800280u;
+    const uint32_t same[4] = {one, one, odd, odd};
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum[N][4], p[N][2][4];
+    // small parts first: the MMAs cut off their sums
+#pragma unroll
+    for (int q = kSum ? PARTS - 1 : -1; q >= 0; --q)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          mma_bf16(sum[n], same, s ? xs[n][q].z : xs[n][q].x, s ? xs[n][q].w : xs[n][q].y, q == PARTS - 1 && s == 0 ? zero : sum[n]);
+#pragma unroll
+    for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma_bf16(p[n][h], a[n][h][s], s ? xs[n][q].z : xs[n][q].x, s ? xs[n][q].w : xs[n][q].y,
+                     q < PARTS - 1 || s ? p[n][h] : Q == OVL_Q4_K || kSigned ? zero : sum[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[h][i] = fmaf(scale[n][2 * h + (i >> 1)], p[n][h][i], acc[h][i]);
+          if constexpr (Q == OVL_Q4_K) acc[h][i] = fmaf(least[n][2 * h + (i >> 1)], sum[n][i], acc[h][i]);
+        }
   }
 
   // What an item's sums become.
-  template <int NT>
-  __device__ void finish(uint32_t item, uint32_t n_pairs, int32_t pair, const float (&acc)[2][NT][4]) const {
-    const uint32_t tile = item % tiles, g = lane >> 2, t = lane & 3;
-    const float w = DOWN && lane < n_pairs ? m.weight[pair] : 0.f;
+  // `w`: the lane's pair's weight, power: its token's 2^e.
+  __device__ void finish(uint32_t tile, uint32_t n_pairs, int32_t pair, float w, float power, const float (&acc)[2][4]) const {
+    const uint32_t g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t column = 2 * t + j;
+      const int32_t p = __shfl_sync(0xffffffffu, pair, column);
+      const float weight = __shfl_sync(0xffffffffu, w, column), up = __shfl_sync(0xffffffffu, power, column);
+      if (column >= n_pairs) continue;
+      if constexpr (DOWN) {
+        float* out = m.part + static_cast<uint64_t>(p) * m.hidden + tile * 32 + g;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t column = n * 8 + 2 * t + j;
-        const int32_t p = __shfl_sync(0xffffffffu, pair, column);
-        const float weight = __shfl_sync(0xffffffffu, w, column);
-        if (column >= n_pairs) continue;
-        if constexpr (DOWN) {
-          float* out = m.part + static_cast<uint64_t>(p) * m.hidden + tile * 32 + g;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int e = 0; e < 2; ++e) out[h * 16 + e * 8] = weight * (acc[h][2 * e + j] * pow2(kCodeExponent - kActExponent) * up * up);
+      } else {
+        constexpr int kParts = PARTS == 1 ? 2 : 3;
+        constexpr float back = pow2(kCodeExponent - kTokenExponent);
+        const float down = 1.f / up;             // a power of two
 #pragma unroll
-            for (int e = 0; e < 2; ++e) out[h * 16 + e * 8] = weight * acc[h][n][2 * e + j];
-        } else {
-          constexpr int kParts = PARTS == 1 ? 2 : 3;
+        for (int e = 0; e < 2; ++e) {
+          const float gate = activated(acc[0][2 * e + j] * back * up, m.act) * down;
+          const uint32_t c = (tile & 1) * 16 + e * 8 + g;
+          uint16_t v[kParts];
+          parts_of<kParts>(gate * share_of<Q>(c) * (acc[1][2 * e + j] * back) * pow2(kActExponent), v);
+          uint16_t* out = m.hp + static_cast<uint64_t>(p) * m.ffn + (tile >> 1) * 32 + place_of<Q>(c);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint16_t v[kParts];
-            parts_of<kParts>(activated(acc[0][n][2 * e + j], m.act) * acc[1][n][2 * e + j], v);
-            uint16_t* out = m.hp + static_cast<uint64_t>(p) * m.ffn + tile * 16 + e * 8 + pair_place<Q>(g);
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) out[q * static_cast<uint64_t>(m.pairs) * m.ffn] = v[q];
-          }
+          for (int q = 0; q < kParts; ++q) out[q * static_cast<uint64_t>(m.pairs) * m.ffn] = v[q];
         }
       }
     }
@@ -310,40 +538,31 @@ template <uint32_t Q, bool DOWN, int PARTS>
 __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_constant__ MoeDev m) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * kStages * kStageBytes;
-  float* table = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes + warp * kTableBytes);
-  float* join = reinterpret_cast<float*>(smem + kWarps * (kStages * kStageBytes + kTableBytes));
   // The first product waits for the router before it lets the second start, so that the
   // second may read the router's results and ask for weights before the first has ended.
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();
   }
-  const Rows32<Q, DOWN, PARTS> op(m, ring, table);
-  // Items in equal runs to the CTAs.  Where a CTA has fewer items than warps, `split`
-  // warps share an item's stages and add up through shared memory.
-  const uint64_t items = static_cast<uint64_t>(*m.n_units) * op.tiles;
-  const uint32_t begin = static_cast<uint32_t>(items * blockIdx.x / gridDim.x), end = static_cast<uint32_t>(items * (blockIdx.x + 1) / gridDim.x);
-  const uint32_t most = static_cast<uint32_t>((items + gridDim.x - 1) / gridDim.x);
-  const uint32_t stages = (op.pitch + kRowBytes - 1) / kRowBytes;
-  uint32_t split = kWarps;
-  while (split > 1 && (most * split > kWarps || split > stages)) split /= 2;
-  const uint32_t slots = kWarps / split, sub = warp % split;
-  const uint32_t s0 = stages * sub / split, s1 = stages * (sub + 1) / split;
-  const uint32_t rounds = (end - begin + slots - 1) / slots;
+  const uint32_t n_units = sort_pairs<Q>(m, smem);
+  const uint16_t* order = reinterpret_cast<const uint16_t*>(smem + Shape<Q>::kOrder);
+  const Rows32<Q, DOWN, PARTS> op(m, smem);
+  // Items in equal runs to the CTAs; inside a CTA, their stages in equal runs to the warps.
+  // An item whose stages are divided is finished by the warp that has its first ones, last
+  // thing; the others come to it first thing and leave their sums in shared memory.
+  const uint32_t items = n_units * op.tiles, per = items / gridDim.x, more = items % gridDim.x;
+  const uint32_t begin = per * blockIdx.x + more * blockIdx.x / gridDim.x;
+  const uint32_t end = per * (blockIdx.x + 1) + more * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t stages = (op.pitch + kRowBytes - 1) / kRowBytes, total = (end - begin) * stages;
+  auto start_of = [&](uint32_t w) { return total / kWarps * w + total % kWarps * w / kWarps; };
+  const uint32_t p0 = start_of(warp), p1 = start_of(warp + 1);
   Cursor c{};
-  uint32_t ahead = 0;                                     // round of the copies
-  c.item = begin + warp / split;
-  if (c.item < end) op.at(c, c.item, s0);
-  uint32_t slot_in = 0;
+  uint32_t asked = p0, slot_in = 0;
+  if (p0 < p1) op.at(c, begin + p0 / stages, p0 % stages);
   auto ask = [&]() {
-    if (c.item < end) {
+    if (asked < p1) {
       op.fill(c, slot_in);
-      if (++c.stage == s1) {
-        ++ahead;
-        c.item += slots;
-        if (c.item < end) op.at(c, c.item, s0);
-      }
+      if (++asked < p1 && c.stage == stages) op.at(c, c.item + 1, 0);
     }
     cp_async_commit();
     slot_in = slot_in + 1 == kStages ? 0 : slot_in + 1;
@@ -354,63 +573,64 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
     griddep_wait();
     griddep_launch_dependents();
   }
+  const uint32_t part = (DOWN ? m.pairs : m.tokens) * op.k * 2;
+  const float* weights = m.given ? m.given_weight : m.weight;
+  float* mine = reinterpret_cast<float*>(smem + Shape<Q>::kJoins) + (static_cast<int>(warp) - 1) * static_cast<int>(kJoinBytes / 4) + lane;    // not of warp 0
   uint32_t slot = 0;
-  auto run = [&](auto tokens, uint32_t item, uint32_t n_pairs, int32_t pair) {
-    constexpr int NT = decltype(tokens)::value;
-    const uint16_t* x[NT];
-    const uint64_t part = static_cast<uint64_t>(DOWN ? m.pairs : m.tokens) * op.k;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t column = n * 8 + (lane >> 2);
-      const uint32_t p = static_cast<uint32_t>(__shfl_sync(0xffffffffu, pair, column));
-      x[n] = column < n_pairs ? (DOWN ? m.hp + static_cast<uint64_t>(p) * op.k : m.xp + static_cast<uint64_t>(p / m.top) * op.k) + (lane & 3) * 8
-                              : nullptr;
+  bool divided = false;                                   // whether others have stages of the last item
+  uint32_t item = 0, tile = 0, n_pairs = 0;
+  int32_t pair = 0;
+  float w = 0.f, power = 1.f, acc[2][4];
+  for (uint32_t p = p0; p < p1;) {
+    item = begin + p / stages;
+    const uint32_t s0 = p % stages, s1 = min(stages, s0 + (p1 - p));
+    p += s1 - s0;
+    const MoeUnit unit = op.unit_of(item, &tile);
+    n_pairs = unit.pairs();
+    // the lane's pair; places behind the last repeat it, and no one reads their sums
+    pair = order[unit.first() + min(lane, n_pairs - 1)];
+    const uint32_t column = static_cast<uint32_t>(__shfl_sync(0xffffffffu, pair, lane >> 2));
+    const uint32_t x = (DOWN ? column : column / m.top) * op.k * 2 + (lane & 3) * 16;    // bytes, below 2^32
+    uint4 next[2][PARTS];
+    if constexpr (op.kAhead) {
+      op.inputs(x + s0 * op.kBlocks * 64, part, next[0]);
+      op.inputs(x + (s0 * op.kBlocks + 1) * 64, part, next[1]);
     }
-    float acc[2][NT][4];
+    if constexpr (DOWN) w = weights[pair];
+    power = m.power[pair / m.top];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[h][n][i] = 0.f;
-    const uint32_t tile = item % op.tiles, expert = m.units[item / op.tiles].expert_n >> 8;
-    const uint8_t* scale_row;
-    if constexpr (DOWN) scale_row = m.down_d + (static_cast<uint64_t>(expert) * m.hidden + tile * 32 + lane) * op.scale_pitch;
-    else scale_row = (lane < 16 ? m.gate_d : m.up_d) + (static_cast<uint64_t>(expert) * m.ffn + tile * 16 + (lane & 15)) * op.scale_pitch;
+    for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = 0.f;
     for (uint32_t s = s0; s < s1; ++s) {
       cp_async_wait<kStages - 2>();
       __syncwarp();                                       // everyone's copies are there, and everyone is done with the stage before
       ask();
-      op.decode(slot, s, scale_row);
-      __syncwarp();
-      op.template multiply<NT>(slot, s, x, part, acc);
+      if constexpr (Q == OVL_Q4_K) {
+        op.decode(slot);
+        __syncwarp();
+      }
+      op.multiply(slot, s, x, part, next, acc);
       slot = slot + 1 == kStages ? 0 : slot + 1;
     }
-    if (split > 1) {
-      float* mine = join + warp * 1024 + lane;
-      if (sub) {
+    if (s0) {
 #pragma unroll
-        for (int i = 0; i < 8 * NT; ++i) mine[i * 32] = acc[i / (4 * NT)][i / 4 % NT][i % 4];
-      }
-      named_bar(1 + warp / split, split * 32);
-      if (!sub) {
-        for (uint32_t o = 1; o < split; ++o)
-#pragma unroll
-          for (int i = 0; i < 8 * NT; ++i) acc[i / (4 * NT)][i / 4 % NT][i % 4] += mine[o * 1024 + i * 32];
-      }
-      named_bar(1 + warp / split, split * 32);
+      for (int i = 0; i < 8; ++i) mine[i * 32] = acc[i / 4][i % 4];
+    } else if (s1 < stages) {
+      divided = true;
+      break;
+    } else {
+      op.finish(tile, n_pairs, pair, w, power, acc);
     }
-    if (!sub) op.template finish<NT>(item, n_pairs, pair, acc);
-  };
-  for (uint32_t r = 0; r < rounds; ++r) {
-    const uint32_t item = begin + r * slots + warp / split;
-    if (item >= end) break;                               // the same for the warps of an item
-    const MoeUnit u = m.units[item / op.tiles];
-    const uint32_t n_pairs = u.expert_n & 255;
-    const int32_t pair = lane < n_pairs ? m.order[u.first + lane] : 0;
-    if (n_pairs <= 8) run(std::integral_constant<int, 1>{}, item, n_pairs, pair);
-    else if (n_pairs <= 16) run(std::integral_constant<int, 2>{}, item, n_pairs, pair);
-    else run(std::integral_constant<int, 4>{}, item, n_pairs, pair);
+  }
+  __syncthreads();
+  if (divided) {
+    const uint32_t behind = (item - begin + 1) * stages;
+    for (uint32_t o = warp + 1; o < kWarps && start_of(o) < behind; ++o) {
+      if (start_of(o) == start_of(o + 1)) continue;
+      const float* theirs = mine + kJoinBytes / 4 * (o - warp);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] += theirs[i * 32];
+    }
+    op.finish(tile, n_pairs, pair, w, power, acc);
   }
   cp_async_wait<0>();
 }
@@ -418,9 +638,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
 template <uint32_t Q, bool DOWN, int PARTS>
 cudaError_t launch_rows(const MoeDev& m, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_rows<Q, DOWN, PARTS>), kSmem, &allowed);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_rows<Q, DOWN, PARTS>), Shape<Q>::kSmem, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_chained(k_moe_rows<Q, DOWN, PARTS>, dim3(sm_count()), kWarps * 32, kSmem, st, m);
+  return launch_chained(k_moe_rows<Q, DOWN, PARTS>, dim3(sm_count()), kWarps * 32, Shape<Q>::kSmem, st, m);
 }
 
 // Both products, one behind the other.

@@ -55,9 +55,9 @@ ovl_status check_norm(const ovl_norm& n) {
 
 // Offsets of a mixture of experts' workspace.
 struct MoeLayout {
-  uint64_t logits, choice, weight, order, units, xp, hp, part, total;
+  uint64_t logits, choice, weight, power, xp, hp, part, total;
 };
-constexpr uint32_t kMoeHead = 512;               // counters: n_units, arrivals
+constexpr uint32_t kMoeHead = 256;               // counters of arrivals
 
 ovl_status check_moe_dims(const ovl_moe* m) {
   if (!m) return fail(OVL_E_ARG, "moe is null");
@@ -69,7 +69,7 @@ ovl_status check_moe_dims(const ovl_moe* m) {
       m->ffn > OVL_MOE_MAX_HIDDEN)
     return fail(OVL_E_SHAPE, "hidden and ffn must be multiples of the format's block up to OVL_MOE_MAX_HIDDEN");
   if (m->act < OVL_ACT_SILU || m->act > OVL_ACT_RELU) return fail(OVL_E_ARG, "unknown act");
-  if (!m->max_tokens || m->max_tokens > OVL_MAX_T) return fail(OVL_E_ARG, "max_tokens must be 1..OVL_MAX_T");
+  if (!m->max_tokens || m->max_tokens > OVL_MOE_MAX_TOKENS) return fail(OVL_E_ARG, "max_tokens must be 1..OVL_MOE_MAX_TOKENS");
   return OVL_OK;
 }
 
@@ -79,9 +79,8 @@ MoeLayout moe_layout(const ovl_moe* m) {
   l.logits = kMoeHead;
   l.choice = l.logits + up256(4 * t * m->n_experts);
   l.weight = l.choice + up256(4 * p);
-  l.order = l.weight + up256(4 * p);
-  l.units = l.order + up256(4 * p);
-  l.xp = l.units + up256(sizeof(MoeUnit) * kMoeMaxUnits);
+  l.power = l.weight + up256(4 * p);
+  l.xp = l.power + up256(4 * t);
   l.hp = l.xp + up256(6 * t * m->hidden);
   l.part = l.hp + up256(6 * p * m->ffn);
   l.total = l.part + up256(4 * p * m->hidden);
@@ -252,6 +251,7 @@ ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, ui
   const MoeLayout l = moe_layout(moe);
   if (moe->workspace_bytes < l.total) return fail(OVL_E_OOM, "the workspace is smaller than ovl_moe_workspace_bytes");
   if (!choice != !weight) return fail(OVL_E_ARG, "choice and weight come together");
+  if (choice && (choice_out || weight_out)) return fail(OVL_E_ARG, "choice_out and weight_out are the router's");
   if (!choice) {
     if (!moe->router) return fail(OVL_E_ARG, "neither a router nor a choice is given");
     if (moe->score != OVL_MOE_SOFTMAX && moe->score != OVL_MOE_SIGMOID) return fail(OVL_E_ARG, "unknown score");
@@ -296,13 +296,11 @@ ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, ui
   m.given_weight = weight;
   m.choice_out = choice_out;
   m.weight_out = weight_out;
-  m.n_units = reinterpret_cast<uint32_t*>(w);
-  m.arrived = reinterpret_cast<uint32_t*>(w + 128);
+  m.arrived = reinterpret_cast<uint32_t*>(w);
   m.logits = reinterpret_cast<float*>(w + l.logits);
   m.choice = reinterpret_cast<int32_t*>(w + l.choice);
   m.weight = reinterpret_cast<float*>(w + l.weight);
-  m.order = reinterpret_cast<int32_t*>(w + l.order);
-  m.units = reinterpret_cast<MoeUnit*>(w + l.units);
+  m.power = reinterpret_cast<float*>(w + l.power);
   m.xp = reinterpret_cast<uint16_t*>(w + l.xp);
   m.hp = reinterpret_cast<uint16_t*>(w + l.hp);
   m.part = reinterpret_cast<float*>(w + l.part);
