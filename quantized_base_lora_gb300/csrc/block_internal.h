@@ -18,42 +18,63 @@ struct Rows {
   bool bf16;
 };
 
-// N consecutive elements from element `at` of a float32 or bfloat16 array, as
-// fp32.  N > 1: the address is a multiple of N elements or of 16 bytes, whichever is less.
+// N consecutive elements of a float32 or bfloat16 array as they lie.  Loading and
+// converting are apart, so that a thread's loads are all under way before the first one is
+// waited for: a conversion behind its load, in the branch of its type, had them one by one.
 template <int N>
-__device__ __forceinline__ void load_f32(const void* base, bool bf16, uint64_t at, float (&v)[N]) {
+struct Raw {
+  uint32_t w[N];
+};
+// From element `at`.  N > 1: its address is a multiple of N elements or of 16 bytes, whichever is less.
+template <int N>
+__device__ __forceinline__ void load_raw(const void* base, bool bf16, uint64_t at, Raw<N>& r) {
+  static_assert(N == 1 || N == 4 || N == 8, "1, 4 or 8 elements");
   if (bf16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
     if constexpr (N == 1) {
-      v[0] = __uint_as_float(static_cast<uint32_t>(*p) << 16);
+      r.w[0] = *p;
+    } else if constexpr (N == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      r.w[0] = v.x, r.w[1] = v.y;
     } else {
-      uint32_t w[N / 2];
-      if constexpr (N == 8) {
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
-        w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
-      } else {
-        static_assert(N == 4, "1, 4 or 8 elements");
-        const uint2 r = *reinterpret_cast<const uint2*>(p);
-        w[0] = r.x, w[1] = r.y;
-      }
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
     }
   } else {
-    const float* p = static_cast<const float*>(base) + at;
+    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
     if constexpr (N == 1) {
-      v[0] = *p;
+      r.w[0] = *p;
     } else {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(p + i);
-        v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+        const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+        r.w[i] = v.x, r.w[i + 1] = v.y, r.w[i + 2] = v.z, r.w[i + 3] = v.w;
       }
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void to_f32(const Raw<N>& r, bool bf16, float (&v)[N]) {
+  if (bf16) {
+    if constexpr (N == 1) {
+      v[0] = __uint_as_float(r.w[0] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        v[2 * i] = __uint_as_float(r.w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r.w[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_f32(const void* base, bool bf16, uint64_t at, float (&v)[N]) {
+  Raw<N> r;
+  load_raw(base, bf16, at, r);
+  to_f32(r, bf16, v);
 }
 
 __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {

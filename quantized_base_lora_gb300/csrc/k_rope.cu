@@ -46,7 +46,10 @@ struct RopeArgs {
 // HT heads, for which the angles' sines are computed once.
 template <int P, int HT>
 __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeArgs a) {
+  __shared__ uint64_t turn[OVL_ROPE_MAX_DIM / 2];         // as a kernel argument, each lane's place would be read in turn
   griddep_launch_dependents();
+  for (uint32_t j = threadIdx.x; j < a.rope.rot_dim / 2; j += kThreads) turn[j] = a.rope.turn[j];
+  __syncthreads();
   griddep_wait();
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const uint32_t slot = static_cast<uint32_t>(i % a.slots);
@@ -58,14 +61,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
   const bool turns = first < half, halves = a.rope.layout == OVL_ROPE_HALF;
   // channels c0 .. and c1 ..: both halves of the pairs, or 2 P consecutive channels
   const uint32_t c0 = turns && halves ? first : 2 * first, c1 = turns && halves ? half + first : c0 + P;
-  float cosine[P], sine[P];
-  if (turns) {
-    const int64_t p = a.pos[token];
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-      turned(static_cast<uint64_t>(p) * a.rope.turn[first + j], a.rope.magnitude, &cosine[j], &sine[j]);
-  }
-  float u[HT][P], v[HT][P];
+  const int64_t p = a.pos[token];
+  Raw<P> ur[HT], vr[HT];
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     const uint32_t head = chunk * HT + h;
@@ -73,25 +70,34 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     const bool is_k = head >= a.q_heads;
     const Rows& in = is_k ? a.k : a.q;
     const uint64_t at = token * in.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    load_f32<P>(in.ptr, in.bf16, at + c0, u[h]);
-    load_f32<P>(in.ptr, in.bf16, at + c1, v[h]);
+    load_raw<P>(in.ptr, a.q.bf16, at + c0, ur[h]);
+    load_raw<P>(in.ptr, a.q.bf16, at + c1, vr[h]);
+  }
+  float cosine[P], sine[P];
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+      turned(static_cast<uint64_t>(p) * turn[first + j], a.rope.magnitude, &cosine[j], &sine[j]);
   }
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     const uint32_t head = chunk * HT + h;
     if (head >= a.heads) break;
+    float u[P], v[P];
+    to_f32<P>(ur[h], a.q.bf16, u);
+    to_f32<P>(vr[h], a.q.bf16, v);
     if (turns) {
       if (halves) {
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const float x = u[h][j], y = v[h][j];
-          u[h][j] = x * cosine[j] - y * sine[j];
-          v[h][j] = x * sine[j] + y * cosine[j];
+          const float x = u[j], y = v[j];
+          u[j] = x * cosine[j] - y * sine[j];
+          v[j] = x * sine[j] + y * cosine[j];
         }
       } else {
         float w[2 * P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) w[j] = u[h][j], w[P + j] = v[h][j];
+        for (int j = 0; j < P; ++j) w[j] = u[j], w[P + j] = v[j];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           const float x = w[2 * j], y = w[2 * j + 1];
@@ -99,14 +105,14 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
           w[2 * j + 1] = x * sine[j] + y * cosine[j];
         }
 #pragma unroll
-        for (int j = 0; j < P; ++j) u[h][j] = w[j], v[h][j] = w[P + j];
+        for (int j = 0; j < P; ++j) u[j] = w[j], v[j] = w[P + j];
       }
     }
     const bool is_k = head >= a.q_heads;
     const Rows& out = is_k ? a.k_out : a.q_out;
     const uint64_t at = token * out.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    store_f32<P>(out.ptr, out.bf16, at + c0, u[h]);
-    store_f32<P>(out.ptr, out.bf16, at + c1, v[h]);
+    store_f32<P>(out.ptr, a.q_out.bf16, at + c0, u);
+    store_f32<P>(out.ptr, a.q_out.bf16, at + c1, v);
   }
 }
 
