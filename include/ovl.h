@@ -707,8 +707,8 @@ ovl_status ovl_rope_plan(uint32_t head_dim, uint32_t rot_dim, uint32_t layout, d
  * [n_tokens][q_heads][head_dim] of `dtype`, k the same with k_heads (0: no k), heads
  * contiguous.  q_out, k_out: the same shape in out_dtype; each may be its input where
  * type and stride agree, and overlaps nothing else.  16-byte rows and dimensions that
- * are multiples of 8 are served by wide loads, others element by element.  No
- * counterpart in the source pages. */
+ * are multiples of 8 are served by wide loads, others element by element.
+ * No counterpart in the source pages. */
 ovl_status ovl_rope_apply(const ovl_rope* rope, uint32_t n_tokens, const int32_t* pos, const void* q, uint32_t q_heads,
                           uint64_t q_stride, const void* k, uint32_t k_heads, uint64_t k_stride, uint32_t dtype,
                           void* q_out, uint64_t q_out_stride, void* k_out, uint64_t k_out_stride, uint32_t out_dtype,
@@ -717,8 +717,8 @@ ovl_status ovl_rope_apply(const ovl_rope* rope, uint32_t n_tokens, const int32_t
 /* Positions of a batch's new tokens in a cache (see above): pos[t], device int32
  * [n_tokens], is the place of packed token t in its sequence, counted by length;
  * -1 for a token that tok_off gives to no sequence or whose row is out of range
- * (latched as OVL_E_ARG).  One call a step serves every layer's ovl_rope_apply.  No
- * counterpart in the source pages. */
+ * (latched as OVL_E_ARG).  One call a step serves every layer's ovl_rope_apply.
+ * No counterpart in the source pages. */
 ovl_status ovl_kv_positions(const ovl_kv* kv, const int32_t* seqs, const int32_t* tok_off, uint32_t n_seqs,
                             uint32_t n_tokens, int32_t* pos, void* stream);
 
@@ -811,8 +811,8 @@ ovl_status ovl_moe_workspace_bytes(const ovl_moe* moe, size_t* out);
  * int32 and weight_out float32 [n_tokens][top_k] receive them, in falling order
  * (NULL: not wanted; with a caller's choice they have to be).  Otherwise choice int32 and weight float32 [n_tokens][top_k] are
  * the caller's: an index outside 0 .. n_experts - 1 is no expert and adds nothing, an
- * expert listed twice adds twice.  x: device [n_tokens][hidden] of `dtype`, y the same;
- * 16-byte rows.  What is rounded: OVL_F32 x and the activations to three bf16 parts each
+ * expert listed twice adds twice.  x: device [n_tokens][hidden] of `dtype`, y the same
+ * (it may be x with x's stride); 16-byte rows.  What is rounded: OVL_F32 x and the activations to three bf16 parts each
  * (2^-24 of each number); OVL_BF16 activations to two (2^-16).  Dot products are sums over
  * 32-weight blocks of exact products with the codes, in 32 bits, times the block's scale;
  * activations below 2^-20 of the square of their token's largest |x| keep fewer bits.  A

@@ -33,6 +33,7 @@ _NORM = {None: OVL_NORM_NONE, "rms": OVL_NORM_RMS, "layer": OVL_NORM_LAYER}
 _ACT = {"silu": OVL_ACT_SILU, "gelu": OVL_ACT_GELU, "gelu_tanh": OVL_ACT_GELU_TANH, "relu": OVL_ACT_RELU}
 _SCORE = {"softmax": OVL_MOE_SOFTMAX, "sigmoid": OVL_MOE_SIGMOID}
 _MOST = (1 << 31) - 1
+_FLAT = torch.contiguous_format
 
 
 def _check(st: int):
@@ -136,7 +137,7 @@ class Rope:
         if out_code is None:
             raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = torch.empty_like(q, dtype=dtype, memory_format=_FLAT)
             qop, qos = q_out.data_ptr(), qh * self.head_dim
         else:
             qop, m, h, c, qos = self._heads("q_out", q_out, index)
@@ -148,7 +149,7 @@ class Rope:
             if m != n or c != code:
                 raise ValueError("q and k must have one type and length")
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+                k_out = torch.empty_like(k, dtype=dtype, memory_format=_FLAT)
                 kop, kos = k_out.data_ptr(), kh * self.head_dim
             else:
                 kop, m, h, c, kos = self._heads("k_out", k_out, index)
@@ -233,7 +234,7 @@ class BlockNorm:
         elif gate_row is not None:
             raise ValueError("gate_row without gate")
         if x_out is None:
-            x_out = torch.empty((n, hidden), dtype=x.dtype, device=x.device)
+            x_out = torch.empty_like(x, memory_format=_FLAT)
             xop, xos = x_out.data_ptr(), hidden
         else:
             xop, xos = _out("x_out", x_out, n, hidden, x_code, index)
@@ -246,7 +247,7 @@ class BlockNorm:
             if h_out is not None:
                 raise ValueError("h_out without a pre norm")
         elif h_out is None:
-            h_out = torch.empty((n, hidden), dtype=dtype, device=x.device)
+            h_out = torch.empty_like(x, dtype=dtype, memory_format=_FLAT)
             hp, hs = h_out.data_ptr(), hidden
         else:
             hp, hs = _out("h_out", h_out, n, hidden, h_code, index)
@@ -273,7 +274,7 @@ def glu(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", dtype: torch.dt
     if out_code is None:
         raise ValueError(f"dtype must be float32 or bfloat16, not {dtype}")
     if out is None:
-        out = torch.empty((n, width), dtype=dtype, device=gate.device)
+        out = torch.empty_like(gate, dtype=dtype, memory_format=_FLAT)
         op, os_ = out.data_ptr(), width
     else:
         op, os_ = _out("out", out, n, width, out_code, index)
@@ -353,7 +354,7 @@ class Moe:
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens, max_tokens is {self.max_tokens}")
         if out is None:
-            out = torch.empty((n, self.hidden), dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x, memory_format=_FLAT)
             op, os_ = out.data_ptr(), self.hidden
         else:
             op, os_ = _out("out", out, n, self.hidden, code, index)

@@ -44,7 +44,7 @@ struct RopeArgs {
 
 // A thread has P pairs of one token (or 2 P channels that are passed through) and
 // HT heads, for which the angles' sines are computed once.
-template <int P, int HT>
+template <int P, int HT, bool XB, bool OB>
 __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeArgs a) {
   __shared__ uint64_t turn[OVL_ROPE_MAX_DIM / 2];         // as a kernel argument, each lane's place would be read in turn
   griddep_launch_dependents();
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     const bool is_k = head >= a.q_heads;
     const Rows& in = is_k ? a.k : a.q;
     const uint64_t at = token * in.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    load_raw<P>(in.ptr, a.q.bf16, at + c0, ur[h]);
-    load_raw<P>(in.ptr, a.q.bf16, at + c1, vr[h]);
+    load_raw<P>(in.ptr, XB, at + c0, ur[h]);
+    load_raw<P>(in.ptr, XB, at + c1, vr[h]);
   }
   float cosine[P], sine[P];
   if (turns) {
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     const uint32_t head = chunk * HT + h;
     if (head >= a.heads) break;
     float u[P], v[P];
-    to_f32<P>(ur[h], a.q.bf16, u);
-    to_f32<P>(vr[h], a.q.bf16, v);
+    to_f32<P>(ur[h], XB, u);
+    to_f32<P>(vr[h], XB, v);
     if (turns) {
       if (halves) {
 #pragma unroll
@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
     const bool is_k = head >= a.q_heads;
     const Rows& out = is_k ? a.k_out : a.q_out;
     const uint64_t at = token * out.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    store_f32<P>(out.ptr, a.q_out.bf16, at + c0, u);
-    store_f32<P>(out.ptr, a.q_out.bf16, at + c1, v);
+    store_f32<P>(out.ptr, OB, at + c0, u);
+    store_f32<P>(out.ptr, OB, at + c1, v);
   }
 }
 
@@ -135,13 +135,18 @@ bool wide(const Rows& r) {
   return !r.ptr || ((reinterpret_cast<uintptr_t>(r.ptr) & 15) == 0 && r.stride % lanes == 0);
 }
 
-template <int P, int HT>
+template <int P, int HT, bool XB, bool OB>
 cudaError_t launch_as(RopeArgs& a, cudaStream_t st) {
   a.slots = a.rope.head_dim / 2 / P;
   a.chunks = (a.heads + HT - 1) / HT;
   const uint64_t threads = static_cast<uint64_t>(a.n_tokens) * a.slots * a.chunks;
-  return launch_chained(k_rope<P, HT>, dim3(static_cast<uint32_t>((threads + kThreads - 1) / kThreads)), kThreads, 0, st,
-                        a);
+  return launch_chained(k_rope<P, HT, XB, OB>, dim3(static_cast<uint32_t>((threads + kThreads - 1) / kThreads)), kThreads, 0,
+                        st, a);
+}
+template <int P, int HT>
+cudaError_t launch_of(RopeArgs& a, cudaStream_t st) {
+  if (a.q.bf16) return a.q_out.bf16 ? launch_as<P, HT, true, true>(a, st) : launch_as<P, HT, true, false>(a, st);
+  return a.q_out.bf16 ? launch_as<P, HT, false, true>(a, st) : launch_as<P, HT, false, false>(a, st);
 }
 
 }  // namespace
@@ -160,8 +165,8 @@ cudaError_t launch_rope(const ovl_rope& rope, uint32_t n_tokens, const int32_t* 
   // sines, where there is work for all of them.
   const uint64_t singles = static_cast<uint64_t>(n_tokens) * a.heads * rope.head_dim / (vec ? 8 : 2);
   const bool few = singles <= static_cast<uint64_t>(sm_count()) * 2048;
-  if (vec) return few ? launch_as<4, 1>(a, st) : launch_as<4, 4>(a, st);
-  return few ? launch_as<1, 1>(a, st) : launch_as<1, 4>(a, st);
+  if (vec) return few ? launch_of<4, 1>(a, st) : launch_of<4, 4>(a, st);
+  return few ? launch_of<1, 1>(a, st) : launch_of<1, 4>(a, st);
 }
 
 cudaError_t launch_kv_positions(const KvDev& kv, const int32_t* seqs, const int32_t* off, uint32_t n, uint32_t n_tokens,

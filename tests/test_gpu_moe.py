@@ -1,0 +1,262 @@
+"""The mixture-of-experts layer on the GPU, against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import block_plain as P  # noqa: E402
+import oracle as O  # noqa: E402
+import synth as S  # noqa: E402
+
+if torch.cuda.is_available():
+    import quantized_base_lora_gb300 as q
+    from quantized_base_lora_gb300 import block as B
+
+F32, BF16 = torch.float32, torch.bfloat16
+QUANTS = [O.Q8_0, O.Q4_0, O.Q4_K]
+
+
+def rand(seed, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype).cuda()
+
+
+class Layer:
+    def __init__(self, quant, n, hidden, ffn, top, seed=0, router=True, **kw):
+        rng = np.random.default_rng(seed)
+        made = [P.experts(rng, quant, n, r, c) for r, c in ((ffn, hidden), (ffn, hidden), (hidden, ffn))]
+        self.w = [w for _, w in made]
+        planes = [tuple(torch.from_numpy(p).cuda() for p in planes) for planes, _ in made]
+        self.router = rand(seed + 1, n, hidden, scale=2 / math.sqrt(hidden), dtype=kw.pop("router_dtype", F32)) if router else None
+        self.act = kw.get("act", "silu")
+        self.moe = B.Moe(quant, n, hidden, ffn, *planes, top_k=top, router=self.router, **kw)
+
+    def check(self, x, y, choice, weight):
+        f32 = x.dtype == F32
+        want, room = P.moe(x.double().cpu(), *self.w, choice.cpu(), weight.double().cpu(), self.act, f32)
+        got = y.double().cpu()
+        assert y.dtype == x.dtype and torch.isfinite(got).all()
+        off = (got - want).abs()
+        room = room + want.abs() * P.HALF[x.dtype] * 1.001
+        assert (off <= room).all(), float((off / room.clamp(min=1e-300)).max())
+        # and in the mean square, where the roundings do not add up: 2^-18 of an fp32 output, half a step of a bf16 one
+        mean = want.square().mean(-1).sqrt()
+        assert (off.square().mean(-1).sqrt() <= mean * (2.0 ** -18 if f32 else 2.0 ** -8) + 1e-300).all()
+
+
+@pytest.mark.parametrize("quant", QUANTS, ids=["q8_0", "q4_0", "q4_K"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,top,hidden,ffn,tokens", [
+    (8, 2, 256, 512, 1), (8, 2, 512, 256, 2), (4, 4, 256, 256, 9), (16, 3, 768, 256, 40), (1, 1, 256, 256, 17),
+    (512, 16, 256, 256, 3), (60, 5, 1280, 512, 64), (3, 2, 256, 1024, 128)])
+def test_layers(quant, dtype, n, top, hidden, ffn, tokens):
+    L = Layer(quant, n, hidden, ffn, top, seed=n, max_tokens=tokens)
+    x = rand(7, tokens, hidden, dtype=dtype)
+    y, choice, weight = L.moe(x, routing=True)
+    c, w, gap = P.route(x.cpu(), L.router.cpu(), None, "softmax", top, True, 1.0)
+    assert gap > 1e-5                                    # 2^-19 of scores of a few units; no choice is that close here
+    assert torch.equal(choice.cpu(), c)
+    assert (weight.cpu().double() - w).abs().max() < 2.0 ** -18
+    L.check(x, y, c, w)
+    assert torch.equal(L.moe(x), y)                      # the same call, the same bits
+
+
+@pytest.mark.parametrize("quant", [O.Q8_0, O.Q4_0], ids=["q8_0", "q4_0"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("hidden,ffn", [(32, 32), (64, 96), (96, 64), (160, 32), (288, 224), (544, 800), (1056, 352)])
+def test_odd_sizes(quant, dtype, hidden, ffn):
+    """Rows whose scales begin at any even address, last stages of 1 to 7 blocks, tiles of half a block."""
+    L = Layer(quant, 5, hidden, ffn, 2, seed=hidden, router=False, max_tokens=20)
+    for tokens in (1, 20):
+        x = rand(3, tokens, hidden, dtype=dtype)
+        choice = torch.stack([torch.randperm(5, generator=torch.Generator().manual_seed(t))[:2] for t in range(tokens)]).int()
+        weight = torch.rand((tokens, 2), generator=torch.Generator().manual_seed(1))
+        L.check(x, L.moe(x, choice.cuda(), weight.cuda()), choice, weight)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("rd", [F32, BF16], ids=["f32", "bf16"])
+def test_routers(score, renormalize, biased, rd):
+    bias = rand(4, 40) if biased else None
+    L = Layer(O.Q4_0, 40, 128, 64, 6, router_dtype=rd, score=score, renormalize=renormalize, scale=2.5, bias=bias,
+              act="gelu_tanh")
+    x = rand(5, 21, 128, dtype=BF16)
+    y, choice, weight = L.moe(x, routing=True)
+    c, w, gap = P.route(x.cpu(), L.router.cpu(), bias.cpu() if biased else None, score, 6, renormalize, 2.5)
+    assert gap > 1e-6
+    assert torch.equal(choice.cpu(), c) and (weight.cpu().double() - w).abs().max() < 2.0 ** -17
+    L.check(x, y, c, w)
+
+
+def test_equal_scores_take_the_lowest_index_and_nan_is_the_least():
+    L = Layer(O.Q4_0, 70, 64, 64, 5)
+    L.router.zero_()
+    x = rand(1, 3, 64)
+    _, choice, weight = L.moe(x, routing=True)
+    assert choice.tolist() == [[0, 1, 2, 3, 4]] * 3 and torch.allclose(weight, torch.full_like(weight, 0.2))
+    L.router[[0, 2, 33]] = math.nan                      # their scores, for any token
+    L.router[40, 0] = math.inf
+    x[:, 0] = 1.0
+    assert L.moe(x, routing=True)[1].tolist() == [[40, 1, 3, 4, 5]] * 3
+
+
+def test_choices_of_the_caller():
+    """No expert, an index out of range, an expert twice, a token with none at all."""
+    L = Layer(O.Q4_K, 6, 256, 256, 4, router=False, max_tokens=8)
+    x = rand(2, 5, 256)
+    choice = torch.tensor([[0, -1, 5, 6], [3, 3, 3, 3], [-1, -1, -7, 1 << 30], [5, 4, 5, 0], [1, 0, 2, -(1 << 31)]], dtype=torch.int32)
+    weight = torch.rand((5, 4), generator=torch.Generator().manual_seed(3)) - 0.3
+    weight[2] = math.nan                                 # of no expert: not looked at
+    y = L.moe(x, choice.cuda(), weight.cuda())
+    assert (y[2] == 0).all()
+    L.check(x, y, choice, weight)
+    assert (L.moe(x, torch.full_like(choice, -1).cuda(), weight.cuda()) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_every_token_to_the_same_expert(dtype):
+    """128 tokens of one expert are 16 passes over its weights; the others have none."""
+    L = Layer(O.Q8_0, 9, 128, 96, 1, router=False, max_tokens=128)
+    for tokens in (8, 9, 127, 128):
+        x = rand(tokens, tokens, 128, dtype=dtype)
+        choice, weight = torch.full((tokens, 1), 8, dtype=torch.int32), torch.rand((tokens, 1)) + 0.5
+        L.check(x, L.moe(x, choice.cuda(), weight.cuda()), choice, weight)
+
+
+def test_one_token_sixteen_times_to_one_expert_of_512():
+    L = Layer(O.Q4_0, 512, 64, 64, 16, router=False, max_tokens=128)
+    x = rand(1, 128, 64, dtype=BF16)
+    choice = torch.full((128, 16), 511, dtype=torch.int32)          # 2048 pairs, 256 units of one expert
+    weight = torch.full((128, 16), 1 / 16)
+    L.check(x, L.moe(x, choice.cuda(), weight.cuda()), choice, weight)
+
+
+@pytest.mark.parametrize("quant", QUANTS, ids=["q8_0", "q4_0", "q4_K"])
+@pytest.mark.parametrize("dtype,sizes", [(F32, (1e-12, 1e-3, 1.0, 1e5, 3e12)), (BF16, (1e-12, 1e-3, 1.0, 1e5, 3e12))],
+                         ids=["f32", "bf16"])
+def test_tokens_of_any_size_beside_one_another(quant, dtype, sizes):
+    """relu goes with the square of x, as the scales of the kernels do; a zero token; one channel far above the rest."""
+    L = Layer(quant, 4, 256, 256, 2, router=False, act="relu")
+    x = rand(5, len(sizes) + 2, 256, dtype=F32)
+    for i, s in enumerate(sizes):
+        x[i] *= s
+    x[-2] = 0
+    x[-1, 77] = 4e4
+    x = x.to(dtype)
+    choice = torch.tensor([[i % 4, (i + 1) % 4] for i in range(len(x))], dtype=torch.int32)
+    weight = torch.full((len(x), 2), 0.5)
+    y = L.moe(x, choice.cuda(), weight.cuda())
+    assert (y[-2] == 0).all()
+    L.check(x, y, choice, weight)
+
+
+def test_a_token_that_is_not_finite_touches_no_other():
+    L = Layer(O.Q4_0, 4, 256, 128, 2)
+    x = rand(6, 12, 256, dtype=BF16)
+    want = L.moe(x)
+    bad = x.clone()
+    bad[3, 5], bad[7, 0] = math.nan, math.inf
+    got = L.moe(bad)
+    keep = [i for i in range(12) if i not in (3, 7)]
+    # the others' experts and places may share passes with other tokens, but not their numbers
+    L.check(x[keep], got[keep], *L.moe(x[keep], routing=True)[1:])
+    assert not torch.isfinite(got[3]).any() and torch.equal(L.moe(x), want)
+
+
+def test_strided_tokens_and_what_is_behind_them():
+    L = Layer(O.Q8_0, 4, 64, 64, 2, max_tokens=16)
+    wide = rand(7, 11, 160, dtype=BF16)
+    x = wide[:, 32:96]
+    out = torch.full((14, 80), 9.0, device="cuda", dtype=BF16)
+    y = L.moe(x, out=out[:11, :64])
+    assert torch.equal(y, L.moe(x.contiguous()))
+    assert (out[11:] == 9).all() and (out[:, 64:] == 9).all()
+    L.moe(x, out=x)                                      # over its own input: read before it is written
+    assert torch.equal(x, y)
+    assert L.moe(x[:0]).shape == (0, 64)
+    L.check(wide[:1, 96:], L.moe(wide[:1, 96:]), *L.moe(wide[:1, 96:], routing=True)[1:])
+
+
+def test_graphs_that_share_a_workspace_and_other_streams():
+    L = Layer(O.Q4_0, 32, 256, 128, 4, max_tokens=64)
+    a, b = rand(1, 50, 256, dtype=BF16), rand(2, 1, 256, dtype=F32)
+    wa, wb = L.moe(a), L.moe(b)
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(ga):
+        oa = L.moe(a)
+    with torch.cuda.graph(gb):
+        ob = L.moe(b)
+    for _ in range(5):                                   # in turn, on one stream
+        ga.replay()
+        gb.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(oa, wa) and torch.equal(ob, wb)
+    a.copy_(rand(9, 50, 256))
+    ga.replay()
+    assert torch.equal(oa, L.moe(a))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = L.moe(b)
+    side.synchronize()
+    assert torch.equal(out, wb)
+
+
+def test_two_layers_in_one_stream():
+    """Calls one behind the other, each with a workspace of its own, chained without a wait between them."""
+    A, C = Layer(O.Q4_0, 16, 256, 128, 4, seed=3), Layer(O.Q8_0, 8, 256, 64, 2, seed=4)
+    x = rand(1, 33, 256, dtype=BF16)
+    one = A.moe(x)
+    torch.cuda.synchronize()
+    two = C.moe(one)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = C.moe(A.moe(x))
+    assert torch.equal(got, two)
+
+
+def test_experts_of_a_loaded_base():
+    from quantized_base_lora_gb300.runtime import Runtime
+    rng = np.random.default_rng(2)
+    n, hidden, ffn = 4, 256, 512
+    shapes = [(n * ffn, hidden), (n * ffn, hidden), (n * hidden, ffn)]
+    for quant in QUANTS:
+        base = S.build_base(quant, [(0, i, S.gaussian(rng, s, 0.05)) for i, s in enumerate(shapes)])
+        rt = Runtime(arena_bytes=32 << 20)
+        tensors = [(t.layer, t.proj, t.d_out, t.d_in, t.qs_off, t.d_off) for t in base.tensors]
+        q.check(rt.load_base(base.quant, tensors, base.buf, S.content_digest(base.buf)), rt.ctx)
+        w = []
+        for (qs, d), (rows, cols) in zip(base.planes, shapes):
+            w.append(torch.from_numpy(np.asarray(O.dequantize(quant, qs, d), np.float64)).reshape(n, -1, cols))
+        router = rand(3, n, hidden, scale=0.2)
+        moe = B.Moe.from_base(rt, 0, 1, 2, n, 2, router=router)
+        x = rand(4, 6, hidden, dtype=BF16)
+        y, choice, weight = moe(x, routing=True)
+        L = Layer.__new__(Layer)
+        L.w, L.act = w, "silu"
+        L.check(x, y, choice.cpu(), weight.cpu())
+        with pytest.raises(ValueError):
+            B.Moe.from_base(rt, 0, 2, 1, n, 2, router=router)
+        rt.close()
+
+
+def test_what_the_torch_side_refuses():
+    L = Layer(O.Q4_0, 4, 64, 64, 2, max_tokens=4)
+    x = rand(1, 3, 64)
+    c, w = torch.zeros((3, 2), dtype=torch.int32, device="cuda"), torch.zeros((3, 2), device="cuda")
+    for call in (lambda: L.moe(rand(1, 5, 64)), lambda: L.moe(x.half()), lambda: L.moe(x[:, :32]), lambda: L.moe(x.cpu()),
+                 lambda: L.moe(x, c), lambda: L.moe(x, weight=w), lambda: L.moe(x, c.long(), w), lambda: L.moe(x, c, w.double()),
+                 lambda: L.moe(x, c[:2], w), lambda: L.moe(x, c, w[:, :1]), lambda: L.moe(x, c, w, routing=True),
+                 lambda: L.moe(x, out=x[:2]), lambda: L.moe(x, out=x.bfloat16())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(q.OvlError):
+        Layer(O.Q4_0, 4, 64, 64, 2, router=False).moe(x)
+    planes = L.moe._held[:3]
+    for n, kw in ((4, dict(router=rand(1, 4, 32))), (4, dict(bias=rand(1, 5))), (3, {}), (4, dict(score="top")), (4, dict(act="no"))):
+        with pytest.raises(ValueError):
+            B.Moe(O.Q4_0, n, 64, 64, *planes, top_k=2, **kw)
