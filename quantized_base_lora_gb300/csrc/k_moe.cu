@@ -13,7 +13,7 @@ namespace {
 
 using namespace moe;
 constexpr uint32_t kThreads = 512;
-constexpr uint32_t kGroup = 8;           // tokens of a router CTA, and its experts
+constexpr int kGroup = 8;                // tokens of a router CTA, and its experts
 
 // Order-preserving bits of a score; NaN is the least.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -29,31 +29,33 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Scores of N tokens from t0 (places behind the last token take it once more) and an
 // expert over every other piece of the row, added up over the warp.
-template <int N>
+template <int N, bool XB, bool RB>
 __device__ __forceinline__ void scores(const MoeDev& m, uint32_t expert, uint32_t t0, uint32_t odd, float (&acc)[N]) {
-  constexpr int kAhead = N == 1 ? 8 : 2;           // pieces in flight
+  constexpr int kAhead = N == 1 ? 8 : XB ? 4 : 2;  // pieces in flight
   const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
   const uint64_t row = static_cast<uint64_t>(expert) * m.hidden;
   for (uint32_t c0 = odd * 128 + lane * 4; c0 < m.hidden; c0 += 256 * kAhead) {
-    float w[kAhead][4], x[kAhead][N][4];
+    Raw<4> w[kAhead], x[kAhead][N];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const uint32_t c = c0 + 256 * a, at = min(c, m.hidden - 4);
+      const uint32_t c = min(c0 + 256 * a, m.hidden - 4);
+      load_raw<4>(m.router, RB, row + c, w[a]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[a][j] = 0.f;
-      if (c < m.hidden) load_f32<4>(m.router, m.router_bf16, row + c, w[a]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) load_f32<4>(m.x.ptr, m.x.bf16, min(t0 + i, m.tokens - 1) * m.x.stride + at, x[a][i]);
+      for (int i = 0; i < N; ++i) load_raw<4>(m.x.ptr, XB, min(t0 + i, m.tokens - 1) * m.x.stride + c, x[a][i]);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
       if (c0 + 256 * a < m.hidden) {
+        float u[4], v[4];
+        to_f32<4>(w[a], RB, u);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+          to_f32<4>(x[a][i], XB, v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i] = fmaf(w[a][j], x[a][i][j], acc[i]);
+          for (int j = 0; j < 4; ++j) acc[i] = fmaf(u[j], v[j], acc[i]);
+        }
       }
   }
 #pragma unroll
@@ -131,7 +133,7 @@ __device__ void split_token(const MoeDev& m, uint32_t token) {
   float top = 0.f;
   for (uint32_t c = threadIdx.x * 8; c < m.hidden; c += kThreads * 8) {
     float x[8];
-    load_f32<8>(m.x.ptr, m.x.bf16, row + c, x);
+    load_f32<8>(m.x.ptr, PARTS == 1, row + c, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
   }
@@ -148,7 +150,7 @@ __device__ void split_token(const MoeDev& m, uint32_t token) {
   const float twice = __uint_as_float(static_cast<uint32_t>(kTokenExponent - e - (kTokenExponent - e) / 2 + 127) << 23);
   for (uint32_t c = threadIdx.x * 8; c < m.hidden; c += kThreads * 8) {
     float x[8];
-    load_f32<8>(m.x.ptr, m.x.bf16, row + c, x);
+    load_f32<8>(m.x.ptr, PARTS == 1, row + c, x);
     uint16_t v[8][PARTS];
 #pragma unroll
     for (int j = 0; j < 8; ++j) parts_of<PARTS>(x[j] * once * twice * share_of<Q>(j), v[j]);
@@ -170,14 +172,15 @@ __device__ void split_token(const MoeDev& m, uint32_t token) {
   }
 }
 
+template <bool XB, bool RB>
 __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ MoeDev m, uint32_t routers) {
   __shared__ uint32_t last;
   griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x >= routers) {
     const uint32_t token = blockIdx.x - routers;
-    if (m.quant == OVL_Q8_0) m.bf16 ? split_token<OVL_Q8_0, 1>(m, token) : split_token<OVL_Q8_0, 3>(m, token);
-    else m.bf16 ? split_token<OVL_Q4_0, 1>(m, token) : split_token<OVL_Q4_0, 3>(m, token);
+    if (m.quant == OVL_Q8_0) split_token<OVL_Q8_0, XB ? 1 : 3>(m, token);
+    else split_token<OVL_Q4_0, XB ? 1 : 3>(m, token);
     return;
   }
   __shared__ float part[kGroup][kGroup];           // expert, token: of the odd pieces
@@ -189,11 +192,11 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ 
   if (expert < m.experts) {
     if (n == 1) {
       float acc[1];
-      scores(m, expert, t0, odd, acc);
+      scores<1, XB, RB>(m, expert, t0, odd, acc);
       mine = acc[0];
     } else {
       float acc[kGroup];
-      scores(m, expert, t0, odd, acc);
+      scores<kGroup, XB, RB>(m, expert, t0, odd, acc);
 #pragma unroll
       for (uint32_t i = 0; i < kGroup; ++i)
         if (lane == i) mine = acc[i];
@@ -221,19 +224,23 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ 
 constexpr uint32_t kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) k_moe_sum(const __grid_constant__ MoeDev m) {
   griddep_launch_dependents();
+  // The choice was made before the products began: which places have an expert.
   const int32_t* choice = m.given ? m.given_choice : m.choice;
-  griddep_wait();
   const uint32_t per = m.hidden / 4;
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
   const uint32_t token = static_cast<uint32_t>(i / per), c = static_cast<uint32_t>(i % per) * 4;
+  uint32_t some = 0;
+  if (token < m.tokens)
+    for (uint32_t s = 0; s < m.top; ++s)
+      if (static_cast<uint32_t>(choice[token * m.top + s]) < m.experts) some |= 1u << s;
+  griddep_wait();
   if (token >= m.tokens) return;
   float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (uint32_t s = 0; s < m.top; ++s) {
-    const uint32_t p = token * m.top + s;
-    if (static_cast<uint32_t>(choice[p]) >= m.experts) continue;
+    if (!(some >> s & 1)) continue;
     float v[4];
-    load_f32<4>(m.part, false, static_cast<uint64_t>(p) * m.hidden + c, v);
+    load_f32<4>(m.part, false, static_cast<uint64_t>(token * m.top + s) * m.hidden + c, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] += v[j];
   }
@@ -245,7 +252,9 @@ __global__ void __launch_bounds__(kSumThreads) k_moe_sum(const __grid_constant__
 cudaError_t launch_moe(const MoeDev& m, cudaStream_t st) {
   const uint32_t wide = (m.experts + kGroup - 1) / kGroup, groups = (m.tokens + kGroup - 1) / kGroup;
   const uint32_t routers = m.given ? 0 : wide * groups;
-  cudaError_t e = launch_chained(k_moe_route, dim3(routers + m.tokens), kThreads, 0, st, m, routers);
+  const auto route = m.bf16 ? (m.router_bf16 ? k_moe_route<true, true> : k_moe_route<true, false>)
+                            : (m.router_bf16 ? k_moe_route<false, true> : k_moe_route<false, false>);
+  cudaError_t e = launch_chained(route, dim3(routers + m.tokens), kThreads, 0, st, m, routers);
   if (e == cudaSuccess)
     e = m.quant == OVL_Q8_0 ? launch_products_q8_0(m, st) : m.quant == OVL_Q4_0 ? launch_products_q4_0(m, st) : launch_products_q4_k(m, st);
   if (e != cudaSuccess) return e;

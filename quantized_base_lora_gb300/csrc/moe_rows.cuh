@@ -16,7 +16,9 @@
 //
 // Inputs are bf16 parts (one: bf16 tokens; two: activations of bf16 calls; three: all 24
 // bits of fp32) in the order of the fragments: lane t of a quad takes 8 consecutive
-// channels of a block in one load, stored as the pairs in which a word's codes unpack.
+// channels of a block in one load, stored as the pairs in which a word's codes unpack.  A
+// unit of so few tokens that all their parts find room in the 8 columns has the parts
+// beside one another, added up at the end (one fp32 token: a third of the MMAs and loads).
 #pragma once
 #include <atomic>
 #include <type_traits>
@@ -44,7 +46,7 @@ struct Shape {
                             kUnits = kJoins + (kWarps - 1) * kJoinBytes, kOrder = kUnits + kMoeMaxUnits * sizeof(MoeUnit),
                             kSmem = kOrder + kMoeMaxPairs * 2;
   static_assert(kStageBytes % 128 == 0, "slots begin on 128 bytes");
-  static_assert(kSmem <= (Q == OVL_Q4_K ? 163 : 131) * 1024, "what is left to the cache");
+  static_assert(kSmem + 64 <= (Q == OVL_Q4_K ? 163 : 131) * 1024, "what is left to the cache");
 };
 
 __device__ __forceinline__ void cp_async4_if(uint32_t dst, const void* src, bool on) {
@@ -142,11 +144,17 @@ __device__ __forceinline__ void parts_of(float v, uint16_t (&p)[PARTS]) {
   }
 }
 
+// Where the share of CTA `cta` begins, of n.
+__device__ __forceinline__ uint32_t share(uint32_t n, uint32_t cta) {
+  return n / gridDim.x * cta + n % gridDim.x * cta / gridDim.x;
+}
+
 // The chosen pairs sorted by expert, in pair order within one, and cut into units: by every
-// CTA for itself, in shared memory (less work than to wait for one to do it).  Returns the
-// number of units.
-template <uint32_t Q>
-__device__ __forceinline__ uint32_t sort_pairs(const MoeDev& m, uint8_t* smem) {
+// CTA for itself, in shared memory (less work than to wait for one to do it).  The CTA's
+// items go to range[0] .. range[1] - 1: runs of tiles of equal cost, where a unit whose parts
+// do not fit beside one another counts half as much again.
+template <uint32_t Q, int PARTS>
+__device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint32_t tiles, uint32_t (&range)[2]) {
   MoeUnit* units = reinterpret_cast<MoeUnit*>(smem + Shape<Q>::kUnits);
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + Shape<Q>::kOrder);
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -156,46 +164,42 @@ __device__ __forceinline__ uint32_t sort_pairs(const MoeDev& m, uint8_t* smem) {
       units[threadIdx.x] = MoeUnit::make(choice[threadIdx.x], 1, threadIdx.x, 1, threadIdx.x);
       order[threadIdx.x] = static_cast<uint16_t>(threadIdx.x);
     }
+    if (threadIdx.x < 2) range[threadIdx.x] = share(m.top * tiles, blockIdx.x + threadIdx.x);
     __syncthreads();
-    return m.top;
+    return;
   }
-  // scratch where the ring will be: pairs of each expert in each warp's share, first pairs
-  uint16_t* count = reinterpret_cast<uint16_t*>(smem);           // [kWarps][OVL_MOE_MAX_EXPERTS]
+  // scratch where the ring will be: pairs of each expert in each warp's share, first pairs,
+  // sums, the pairs' experts and their places in their warp's share.  Loops are not unrolled:
+  // each line of instructions comes from L2 here.
+  uint16_t* count = reinterpret_cast<uint16_t*>(smem);                   // [kWarps][OVL_MOE_MAX_EXPERTS]
   uint16_t* first = count + kWarps * OVL_MOE_MAX_EXPERTS;
-  uint32_t* sums = reinterpret_cast<uint32_t*>(first + OVL_MOE_MAX_EXPERTS);      // [2][kWarps]
+  uint32_t* sums = reinterpret_cast<uint32_t*>(first + OVL_MOE_MAX_EXPERTS);      // [3][kWarps]
+  uint32_t* expert_rank = sums + 3 * kWarps;              // [kMoeMaxPairs], of a warp's own pairs
   static_assert(kWarps * 32 >= OVL_MOE_MAX_EXPERTS / 2, "two experts a thread");
-  constexpr uint32_t kRounds = (kMoeMaxPairs + kWarps * 32 - 1) / (kWarps * 32);
   const uint32_t per = (m.pairs + kWarps * 32 - 1) / (kWarps * 32), from = warp * per * 32 + lane;
-  int32_t e[kRounds];
-#pragma unroll
-  for (uint32_t r = 0; r < kRounds; ++r) {
-    e[r] = -1;
-    if (r < per && from + r * 32 < m.pairs) e[r] = choice[from + r * 32];
-    if (static_cast<uint32_t>(e[r]) >= m.experts) e[r] = -1;
-  }
   const uint32_t own = 2 * threadIdx.x;                   // the thread's experts: own and own + 1
   if (own < m.experts) {
-#pragma unroll
+#pragma unroll 1
     for (uint32_t w = 0; w < kWarps; ++w) *reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own) = 0;
   }
   __syncthreads();
-  uint32_t rank[kRounds];
-#pragma unroll
-  for (uint32_t r = 0; r < kRounds; ++r) {
-    rank[r] = 0;
-    if (r < per) {
-      const uint32_t same = __match_any_sync(0xffffffffu, e[r]), below = __popc(same & ((1u << lane) - 1));
-      uint16_t* c = count + warp * OVL_MOE_MAX_EXPERTS + e[r];
-      if (e[r] >= 0) rank[r] = *c + below;
-      __syncwarp();
-      if (e[r] >= 0 && below == 0) *c = static_cast<uint16_t>(*c + __popc(same));
-      __syncwarp();
-    }
+#pragma unroll 1
+  for (uint32_t r = 0; r < per; ++r) {
+    const uint32_t p = from + r * 32;
+    uint32_t e = p < m.pairs ? static_cast<uint32_t>(choice[p]) : m.experts;
+    if (e >= m.experts) e = OVL_MOE_MAX_EXPERTS;          // none
+    const uint32_t same = __match_any_sync(0xffffffffu, e), below = __popc(same & ((1u << lane) - 1));
+    uint16_t* c = count + warp * OVL_MOE_MAX_EXPERTS + e;
+    const bool some = e < OVL_MOE_MAX_EXPERTS;
+    if (p < m.pairs) expert_rank[p] = e << 16 | (some ? *c + below : 0);
+    __syncwarp();
+    if (some && below == 0) *c = static_cast<uint16_t>(*c + __popc(same));
+    __syncwarp();
   }
   __syncthreads();
   uint32_t n[2] = {0, 0};                                 // their pairs
   if (own < m.experts) {
-#pragma unroll
+#pragma unroll 1
     for (uint32_t w = 0; w < kWarps; ++w) {
       uint32_t* c = reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own);
       const uint32_t some = *c;
@@ -204,34 +208,52 @@ __device__ __forceinline__ uint32_t sort_pairs(const MoeDev& m, uint8_t* smem) {
     }
   }
   const uint32_t groups[2] = {(n[0] + kMoeTokens - 1) / kMoeTokens, (n[1] + kMoeTokens - 1) / kMoeTokens};
-  uint32_t a = n[0] + n[1], b = groups[0] + groups[1];    // pairs and units up to them
+  auto cost_of = [](uint32_t pairs) { return !pairs ? 0u : pairs * PARTS <= 8 ? 2u : 3u; };
+  uint32_t cost[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) cost[j] = n[j] / kMoeTokens * cost_of(kMoeTokens) + cost_of(n[j] % kMoeTokens);
+  uint32_t a = n[0] + n[1], b = groups[0] + groups[1], c = cost[0] + cost[1];    // pairs, units and costs up to them
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, a, s), v = __shfl_up_sync(0xffffffffu, b, s);
-    if (static_cast<int>(lane) >= s) a += u, b += v;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, a, s), v = __shfl_up_sync(0xffffffffu, b, s), w = __shfl_up_sync(0xffffffffu, c, s);
+    if (static_cast<int>(lane) >= s) a += u, b += v, c += w;
   }
-  if (lane == 31) sums[warp] = a, sums[kWarps + warp] = b;
+  if (lane == 31) sums[warp] = a, sums[kWarps + warp] = b, sums[2 * kWarps + warp] = c;
   __syncthreads();
-  uint32_t all = 0;
-#pragma unroll
+  uint32_t all = 0, whole = 0;
+#pragma unroll 1
   for (uint32_t w = 0; w < kWarps; ++w) {
-    if (w < warp) a += sums[w], b += sums[kWarps + w];
-    all += sums[kWarps + w];
+    if (w < warp) a += sums[w], b += sums[kWarps + w], c += sums[2 * kWarps + w];
+    all += sums[kWarps + w], whole += sums[2 * kWarps + w];
   }
-  a -= n[0] + n[1], b -= groups[0] + groups[1];
+  a -= n[0] + n[1], b -= groups[0] + groups[1], c -= cost[0] + cost[1];
+  uint32_t from_cost[2];                                  // below 768 units * 3 * 2048 tiles
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k) {
+    from_cost[k] = share(whole * tiles, blockIdx.x + k);
+    if (threadIdx.x == 0 && from_cost[k] == whole * tiles) range[k] = all * tiles;
+  }
 #pragma unroll
   for (uint32_t j = 0; j < 2; ++j) {
     if (own + j < m.experts) first[own + j] = static_cast<uint16_t>(a);
     for (uint32_t i = 0; i < groups[j]; ++i)
       units[b + i] = MoeUnit::make(own + j, min(n[j] - i * kMoeTokens, kMoeTokens), b, groups[j], a + i * kMoeTokens);
-    a += n[j], b += groups[j];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {                    // the first tile that begins there or behind it
+      const uint32_t at = from_cost[k] - c * tiles;
+      if (from_cost[k] >= c * tiles && at < cost[j] * tiles) range[k] = b * tiles + (at + cost[j] - 1) / cost[j] * groups[j];
+    }
+    a += n[j], b += groups[j], c += cost[j];
   }
   __syncthreads();
-#pragma unroll
-  for (uint32_t r = 0; r < kRounds; ++r)
-    if (e[r] >= 0) order[first[e[r]] + count[warp * OVL_MOE_MAX_EXPERTS + e[r]] + rank[r]] = static_cast<uint16_t>(from + r * 32);
+#pragma unroll 1
+  for (uint32_t r = 0; r < per; ++r) {
+    const uint32_t p = from + r * 32;
+    if (p >= m.pairs) break;
+    const uint32_t e = expert_rank[p] >> 16, rank = expert_rank[p] & 0xffff;
+    if (e < OVL_MOE_MAX_EXPERTS) order[first[e] + count[warp * OVL_MOE_MAX_EXPERTS + e] + rank] = static_cast<uint16_t>(p);
+  }
   __syncthreads();
-  return all;
 }
 
 // Where a warp's copies are: an item (32 rows of a unit) and the stage inside it.
@@ -352,47 +374,54 @@ struct Rows32 {
 
   // The inputs of a block: `at` is the lane's byte in the first part.  The blocks behind a
   // row's last one lie in the workspace too.
-  __device__ void inputs(uint32_t at, uint32_t part, uint4 (&v)[PARTS]) const {
+  template <int P>
+  __device__ void inputs(uint32_t at, uint32_t part, uint4 (&v)[P]) const {
     const char* base = reinterpret_cast<const char*>(DOWN ? m.hp : m.xp);
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q) v[q] = *reinterpret_cast<const uint4*>(base + (at + q * part));
+    for (int q = 0; q < P; ++q) v[q] = *reinterpret_cast<const uint4*>(base + (at + q * part));
   }
 
-  // One stage's products: acc[half of the rows][fragment] += scale * codes x.  `next` holds
-  // the inputs of the two blocks to come (for three parts there is no room).
-  static constexpr bool kAhead = PARTS < 3;
-  __device__ __forceinline__ void multiply(uint32_t slot, uint32_t stage, uint32_t x, uint32_t part, uint4 (&next)[2][PARTS],
+  // One stage's products: acc[half of the rows][fragment] += scale * codes x, x in P parts
+  // one behind the other.  `next` holds the inputs of the two blocks to come (for three parts
+  // there is no room).
+  template <int P>
+  static constexpr bool kAhead = P < 3;
+  template <int P>
+  __device__ __forceinline__ void multiply(uint32_t slot, uint32_t stage, uint32_t x, uint32_t part, uint4 (&next)[2][P],
                                            float (&acc)[2][4]) const {
     const uint32_t first = stage * kBlocks, blocks = min(kBlocks, k / 32 - first);
     if (blocks == kBlocks) {
-      uint32_t packed[4][kBlocks / 2];           // scales of rows g + 8 i, two blocks a word
-      if constexpr (Q != OVL_Q4_K) {
+      // Four blocks a round, not more: instructions come from L2 when a kernel begins, and
+      // unrolled over the stage its first microseconds went there.
+#pragma unroll 1
+      for (uint32_t b = 0; b < kBlocks; b += 4) {
+        uint2 packed[4];                         // scales of rows g + 8 i
+        if constexpr (Q != OVL_Q4_K) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint16_t* s = scales_of(slot, (lane >> 2) + 8 * i);
-          if (scales_aligned) {
+          for (uint32_t i = 0; i < 4; ++i) {
+            const uint16_t* s = scales_of(slot, (lane >> 2) + 8 * i) + b;
+            if (scales_aligned) packed[i] = *reinterpret_cast<const uint2*>(s);
+            else packed[i] = make_uint2(s[0] | static_cast<uint32_t>(s[1]) << 16, s[2] | static_cast<uint32_t>(s[3]) << 16);
+          }
+        }
 #pragma unroll
-            for (uint32_t b = 0; b < kBlocks / 2; ++b) packed[i][b] = reinterpret_cast<const uint32_t*>(s)[b];
+        for (uint32_t c = 0; c < 4; c += 2) {
+          float scale[2][4], least[2][4];
+          if constexpr (Q == OVL_Q4_K) {
+            from_table(b + c, scale[0], least[0]);
+            from_table(b + c + 1, scale[1], least[1]);
           } else {
 #pragma unroll
-            for (uint32_t b = 0; b < kBlocks / 2; ++b) packed[i][b] = s[2 * b] | static_cast<uint32_t>(s[2 * b + 1]) << 16;
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(c ? &packed[i].y : &packed[i].x));
+              scale[0][i] = f.x, scale[1][i] = f.y;
+            }
           }
+          uint32_t codes[2][kWords][4];
+          codes_of(slot, b + c, codes[0]);
+          codes_of(slot, b + c + 1, codes[1]);
+          multiply_blocks<2, P>(codes, first + b + c, x, part, scale, least, next, acc);
         }
-      }
-#pragma unroll
-      for (uint32_t b = 0; b < kBlocks; b += 2) {
-        float scale[2][4], least[2][4];
-        if constexpr (Q == OVL_Q4_K) {
-          from_table(b, scale[0], least[0]);
-          from_table(b + 1, scale[1], least[1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed[i][b / 2]));
-            scale[0][i] = f.x, scale[1][i] = f.y;
-          }
-        }
-        multiply_blocks<2>(slot, b, first + b, x, part, scale, least, next, acc);
       }
     } else {                                     // the row's last stage
 #pragma unroll 1
@@ -405,7 +434,9 @@ struct Rows32 {
           for (uint32_t i = 0; i < 4; ++i)
             scale[0][i] = __half2float(__ushort_as_half(scales_of(slot, (lane >> 2) + 8 * i)[b]));
         }
-        multiply_blocks<1>(slot, b, first + b, x, part, scale, least, next, acc);
+        uint32_t codes[1][kWords][4];
+        codes_of(slot, b, codes[0]);
+        multiply_blocks<1, P>(codes, first + b, x, part, scale, least, next, acc);
       }
     }
   }
@@ -416,40 +447,43 @@ struct Rows32 {
     least[0] = v.x, least[1] = v.y, least[2] = v.z, least[3] = v.w;
   }
 
+  // The lane's words of block b, rows of both halves.
+  static constexpr int kWords = Q == OVL_Q8_0 ? 2 : 1;
+  __device__ __forceinline__ void codes_of(uint32_t slot, uint32_t b, uint32_t (&w)[kWords][4]) const {
+    const uint32_t row = smem_u32(ring) + slot * kStageBytes + lane * kRowBytes;
+#pragma unroll
+    for (uint32_t s = 0; s < kWords; ++s) load_rows(w[s], row + (((kWords * b + s) ^ (lane & 7)) << 4));
+  }
+
   // N blocks beside one another, so that their chains of MMAs fill each other's waits.
-  template <int N>
-  __device__ __forceinline__ void multiply_blocks(uint32_t slot, uint32_t b, uint32_t block, uint32_t x, uint32_t part,
+  template <int N, int P>
+  __device__ __forceinline__ void multiply_blocks(const uint32_t (&codes)[N][kWords][4], uint32_t block, uint32_t x, uint32_t part,
                                                   const float (&scale)[N][4], const float (&least)[N][4],
-                                                  uint4 (&next)[2][PARTS], float (&acc)[2][4]) const {
-    uint4 xs[N][PARTS];
+                                                  uint4 (&next)[2][P], float (&acc)[2][4]) const {
+    uint4 xs[N][P];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      if constexpr (kAhead && N == 2) {
+      if constexpr (kAhead<P> && N == 2) {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) xs[n][q] = next[n][q];
+        for (int q = 0; q < P; ++q) xs[n][q] = next[n][q];
         inputs(x + (block + 2 + n) * 64, part, next[n]);
       } else {
         inputs(x + (block + n) * 64, part, xs[n]);
       }
     }
     uint32_t a[N][2][2][4];                      // block, half of the rows, k16 step, fragment
-    const uint32_t row = smem_u32(ring) + slot * kStageBytes + lane * kRowBytes;
 #pragma unroll
     for (uint32_t n = 0; n < N; ++n) {
       if constexpr (Q == OVL_Q8_0) {
 #pragma unroll
-        for (uint32_t s = 0; s < 2; ++s) {
-          uint32_t w[4];
-          load_rows(w, row + (((2 * (b + n) + s) ^ (lane & 7)) << 4));
+        for (uint32_t s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pairs_of_8(w[i], a[n][i / 2][s][i % 2], a[n][i / 2][s][2 + i % 2]);
-        }
+          for (int i = 0; i < 4; ++i) pairs_of_8(codes[n][s][i], a[n][i / 2][s][i % 2], a[n][i / 2][s][2 + i % 2]);
       } else {
-        uint32_t w[4], p[4];
-        load_rows(w, row + (((b + n) ^ (lane & 7)) << 4));
+        uint32_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          pairs_of_4(w[i], p);
+          pairs_of_4(codes[n][0][i], p);
 #pragma unroll
           for (int s = 0; s < 2; ++s) a[n][i / 2][s][i % 2] = p[2 * s], a[n][i / 2][s][2 + i % 2] = p[2 * s + 1];
         }
@@ -472,14 +506,14 @@ struct Rows32 {
     float sum[N][4], p[N][2][4];
     // small parts first: the MMAs cut off their sums
 #pragma unroll
-    for (int q = kSum ? PARTS - 1 : -1; q >= 0; --q)
+    for (int q = kSum ? P - 1 : -1; q >= 0; --q)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          mma_bf16(sum[n], same, s ? xs[n][q].z : xs[n][q].x, s ? xs[n][q].w : xs[n][q].y, q == PARTS - 1 && s == 0 ? zero : sum[n]);
+          mma_bf16(sum[n], same, s ? xs[n][q].z : xs[n][q].x, s ? xs[n][q].w : xs[n][q].y, q == P - 1 && s == 0 ? zero : sum[n]);
 #pragma unroll
-    for (int q = PARTS - 1; q >= 0; --q)
+    for (int q = P - 1; q >= 0; --q)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -487,7 +521,7 @@ struct Rows32 {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             mma_bf16(p[n][h], a[n][h][s], s ? xs[n][q].z : xs[n][q].x, s ? xs[n][q].w : xs[n][q].y,
-                     q < PARTS - 1 || s ? p[n][h] : Q == OVL_Q4_K || kSigned ? zero : sum[n]);
+                     q < P - 1 || s ? p[n][h] : Q == OVL_Q4_K || kSigned ? zero : sum[n]);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -501,8 +535,28 @@ struct Rows32 {
 
   // What an item's sums become.
   // `w`: the lane's pair's weight, power: its token's 2^e.
-  __device__ void finish(uint32_t tile, uint32_t n_pairs, int32_t pair, float w, float power, const float (&acc)[2][4]) const {
+  __device__ void finish(uint32_t tile, uint32_t n_pairs, int32_t pair, float w, float power, bool beside, float (&acc)[2][4]) const {
     const uint32_t g = lane >> 2, t = lane & 3;
+    if (beside) {                                // column c's parts are columns c + n, c + 2 n: the small ones first
+      float all[2][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all[i / 4][i % 4] = 0.f;
+#pragma unroll
+      for (int q = PARTS - 1; q >= 0; --q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t from = (2 * t + j + q * n_pairs) & 7, source = (lane & 28) + from / 2;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float even = __shfl_sync(0xffffffffu, acc[h][2 * e], source), odd = __shfl_sync(0xffffffffu, acc[h][2 * e + 1], source);
+              all[h][2 * e + j] += (from & 1) ? odd : even;
+            }
+        }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = all[i / 4][i % 4];
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t column = 2 * t + j;
@@ -540,19 +594,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   // The first product waits for the router before it lets the second start, so that the
   // second may read the router's results and ask for weights before the first has ended.
+  __shared__ uint32_t range[2];
+  const Rows32<Q, DOWN, PARTS> op(m, smem);
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();
   }
-  const uint32_t n_units = sort_pairs<Q>(m, smem);
+  sort_pairs<Q, PARTS>(m, smem, op.tiles, range);
   const uint16_t* order = reinterpret_cast<const uint16_t*>(smem + Shape<Q>::kOrder);
-  const Rows32<Q, DOWN, PARTS> op(m, smem);
-  // Items in equal runs to the CTAs; inside a CTA, their stages in equal runs to the warps.
-  // An item whose stages are divided is finished by the warp that has its first ones, last
-  // thing; the others come to it first thing and leave their sums in shared memory.
-  const uint32_t items = n_units * op.tiles, per = items / gridDim.x, more = items % gridDim.x;
-  const uint32_t begin = per * blockIdx.x + more * blockIdx.x / gridDim.x;
-  const uint32_t end = per * (blockIdx.x + 1) + more * (blockIdx.x + 1) / gridDim.x;
+  // Items in runs of equal cost to the CTAs; inside a CTA, their stages in equal runs to the
+  // warps.  An item whose stages are divided is finished by the warp that has its first
+  // ones, last thing; the others come to it first thing and leave their sums in shared memory.
+  const uint32_t begin = range[0], end = range[1];
   const uint32_t stages = (op.pitch + kRowBytes - 1) / kRowBytes, total = (end - begin) * stages;
   auto start_of = [&](uint32_t w) { return total / kWarps * w + total % kWarps * w / kWarps; };
   const uint32_t p0 = start_of(warp), p1 = start_of(warp + 1);
@@ -577,7 +630,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   const float* weights = m.given ? m.given_weight : m.weight;
   float* mine = reinterpret_cast<float*>(smem + Shape<Q>::kJoins) + (static_cast<int>(warp) - 1) * static_cast<int>(kJoinBytes / 4) + lane;    // not of warp 0
   uint32_t slot = 0;
-  bool divided = false;                                   // whether others have stages of the last item
+  bool divided = false, beside = false;                   // whether others have stages of the last item; parts in columns
   uint32_t item = 0, tile = 0, n_pairs = 0;
   int32_t pair = 0;
   float w = 0.f, power = 1.f, acc[2][4];
@@ -589,28 +642,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
     n_pairs = unit.pairs();
     // the lane's pair; places behind the last repeat it, and no one reads their sums
     pair = order[unit.first() + min(lane, n_pairs - 1)];
-    const uint32_t column = static_cast<uint32_t>(__shfl_sync(0xffffffffu, pair, lane >> 2));
-    const uint32_t x = (DOWN ? column : column / m.top) * op.k * 2 + (lane & 3) * 16;    // bytes, below 2^32
-    uint4 next[2][PARTS];
-    if constexpr (op.kAhead) {
-      op.inputs(x + s0 * op.kBlocks * 64, part, next[0]);
-      op.inputs(x + (s0 * op.kBlocks + 1) * 64, part, next[1]);
-    }
+    beside = PARTS > 1 && n_pairs * PARTS <= 8;
+    const uint32_t column = lane >> 2, which = beside ? column / n_pairs : 0;
+    const uint32_t p_of = static_cast<uint32_t>(__shfl_sync(0xffffffffu, pair, column - which * n_pairs));
+    const uint32_t x = (DOWN ? p_of : p_of / m.top) * op.k * 2 + (which < PARTS ? which : 0) * part + (lane & 3) * 16;    // bytes, below 2^32
     if constexpr (DOWN) w = weights[pair];
     power = m.power[pair / m.top];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = 0.f;
-    for (uint32_t s = s0; s < s1; ++s) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();                                       // everyone's copies are there, and everyone is done with the stage before
-      ask();
-      if constexpr (Q == OVL_Q4_K) {
-        op.decode(slot);
-        __syncwarp();
+    auto stages_in = [&](auto parts) {
+      constexpr int P = decltype(parts)::value;
+      uint4 next[2][P];
+      if constexpr (op.template kAhead<P>) {
+        op.template inputs<P>(x + s0 * op.kBlocks * 64, part, next[0]);
+        op.template inputs<P>(x + (s0 * op.kBlocks + 1) * 64, part, next[1]);
       }
-      op.multiply(slot, s, x, part, next, acc);
-      slot = slot + 1 == kStages ? 0 : slot + 1;
-    }
+      for (uint32_t s = s0; s < s1; ++s) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();                                     // everyone's copies are there, and everyone is done with the stage before
+        ask();
+        if constexpr (Q == OVL_Q4_K) {
+          op.decode(slot);
+          __syncwarp();
+        }
+        op.template multiply<P>(slot, s, x, part, next, acc);
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+      }
+    };
+    if (beside || PARTS == 1) stages_in(std::integral_constant<int, 1>{});
+    else stages_in(std::integral_constant<int, PARTS>{});
     if (s0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) mine[i * 32] = acc[i / 4][i % 4];
@@ -618,7 +678,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
       divided = true;
       break;
     } else {
-      op.finish(tile, n_pairs, pair, w, power, acc);
+      op.finish(tile, n_pairs, pair, w, power, beside, acc);
     }
   }
   __syncthreads();
@@ -630,7 +690,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] += theirs[i * 32];
     }
-    op.finish(tile, n_pairs, pair, w, power, acc);
+    op.finish(tile, n_pairs, pair, w, power, beside, acc);
   }
   cp_async_wait<0>();
 }
