@@ -41,15 +41,10 @@ def _check(st: int):
         raise OvlError(st, ovl_last_error(None))
 
 
-def _call(index: int, fn, *args):
-    """fn(*args, stream) on device `index` (the library launches on the current one)."""
-    if _current_device() == index:
-        st = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index))
-    if st:
-        _check(st)
+def _elsewhere(index: int, fn, *args):
+    """fn(*args, stream) on device `index`, which is not the current one (the library launches on that)."""
+    with torch.cuda.device(index):
+        _check(fn(*args, _raw_stream(index)))
 
 
 def _named(table: dict, name: str, value):
@@ -59,17 +54,20 @@ def _named(table: dict, name: str, value):
     return code
 
 
+# The checks below run at every call, for every tensor: they read each property once.
+
 def _rows(name: str, t: torch.Tensor, width: int, index: int):
     """(address, tokens, dtype code, stride) of [tokens][width]."""
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} {tuple(t.shape)} is not [tokens][{width}]")
-    n = t.shape[0]
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} {tuple(shape)} is not [tokens][{width}]")
     step, by_channel = t.stride()
     code = _DTYPE.get(t.dtype)
     if code is None or t.get_device() != index:
         raise ValueError(f"{name} must be float32 or bfloat16 on cuda:{index}, not {t.dtype} on {t.device}")
     if by_channel != 1 and width > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
+    n = shape[0]
     return t.data_ptr(), n, code, (step if n > 1 else width)
 
 
@@ -82,9 +80,10 @@ def _out(name: str, t: torch.Tensor, n: int, width: int, code: int, index: int):
 
 
 def _index_of(name: str, t: torch.Tensor) -> int:
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
-    return t.get_device()
+    return index
 
 
 def _ints(name: str, t: torch.Tensor, shape: tuple, index: int) -> int:
@@ -114,9 +113,10 @@ class Rope:
 
     def _heads(self, name: str, t: torch.Tensor, index: int):
         """(address, tokens, heads, dtype code, stride) of [tokens][heads][head_dim]."""
-        if t.dim() != 3 or t.shape[2] != self.head_dim:
-            raise ValueError(f"{name} {tuple(t.shape)} is not [tokens][heads][{self.head_dim}]")
-        n, h, d = t.shape
+        shape, d = t.shape, self.head_dim
+        if len(shape) != 3 or shape[2] != d:
+            raise ValueError(f"{name} {tuple(shape)} is not [tokens][heads][{d}]")
+        n, h, _ = shape
         step, by_head, by_channel = t.stride()
         code = _DTYPE.get(t.dtype)
         if code is None or t.get_device() != index:
@@ -159,8 +159,11 @@ class Rope:
             raise ValueError("k_out without k")
         if n > _MOST:
             raise ValueError("too many tokens")
-        _call(index, lib.ovl_rope_apply, self._at, n, _ints("pos", pos, (n,), index), qp, qh, qs, kp, kh, ks, code, qop,
-              qos, kop, kos, out_code)
+        args = (self._at, n, _ints("pos", pos, (n,), index), qp, qh, qs, kp, kh, ks, code, qop, qos, kop, kos, out_code)
+        if _current_device() != index:
+            _elsewhere(index, lib.ovl_rope_apply, *args)
+        elif st := lib.ovl_rope_apply(*args, _raw_stream(index)):
+            _check(st)
         return q_out if k is None else (q_out, k_out)
 
 
@@ -255,8 +258,11 @@ class BlockNorm:
             return x_out, h_out
         if n > _MOST or rows > _MOST:
             raise ValueError("too many tokens or gates")
-        _call(index, lib.ovl_block_norm_apply, self._at, n, xp, x_code, xs, yp, y_code, ys, gp, g_code, gs, rp, rows, xop,
-              xos, hp, h_code, hs)
+        args = (self._at, n, xp, x_code, xs, yp, y_code, ys, gp, g_code, gs, rp, rows, xop, xos, hp, h_code, hs)
+        if _current_device() != index:
+            _elsewhere(index, lib.ovl_block_norm_apply, *args)
+        elif st := lib.ovl_block_norm_apply(*args, _raw_stream(index)):
+            _check(st)
         return x_out, h_out
 
 
@@ -280,7 +286,11 @@ def glu(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", dtype: torch.dt
         op, os_ = _out("out", out, n, width, out_code, index)
     if n > _MOST or width > _MOST:
         raise ValueError("too many tokens or channels")
-    _call(index, lib.ovl_glu, _named(_ACT, "act", act), n, width, gp, gs, up_, us, code, op, os_, out_code)
+    args = (_named(_ACT, "act", act), n, width, gp, gs, up_, us, code, op, os_, out_code)
+    if _current_device() != index:
+        _elsewhere(index, lib.ovl_glu, *args)
+    elif st := lib.ovl_glu(*args, _raw_stream(index)):
+        _check(st)
     return out
 
 
@@ -299,8 +309,8 @@ class Moe:
                         ("max_tokens", max_tokens)):
             if not 0 <= v <= _MOST:
                 raise ValueError(f"{name} {v} is out of range")
-        self.moe = ovl_moe(quant, n_experts, top_k, hidden, ffn, _named(_ACT, "act", act), _named(_SCORE, "score", score),
-                           bool(renormalize), scale, OVL_F32, max_tokens)
+        self.moe = ovl_moe(quant, n_experts, top_k, hidden, ffn, _named(_ACT, "act", act),
+                           _named(_SCORE, "score", score), bool(renormalize), scale, OVL_F32, max_tokens)
         st, nbytes = ovl_moe_workspace_bytes(self.moe)
         _check(st)
         self._index = _index_of("gate", gate[0])
@@ -375,5 +385,9 @@ class Moe:
             weight_out = torch.empty(shape, dtype=torch.float32, device=x.device)
             cop, wop = choice_out.data_ptr(), weight_out.data_ptr()
         if n:
-            _call(index, lib.ovl_moe_forward, self._at, xp, code, n, xs, cp, wp, cop, wop, op, os_)
+            args = (self._at, xp, code, n, xs, cp, wp, cop, wop, op, os_)
+            if _current_device() != index:
+                _elsewhere(index, lib.ovl_moe_forward, *args)
+            elif st := lib.ovl_moe_forward(*args, _raw_stream(index)):
+                _check(st)
         return (out, choice_out, weight_out) if routing else out

@@ -114,7 +114,7 @@ __device__ __forceinline__ float activated(float v, uint32_t act) {
     case OVL_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
     case OVL_ACT_GELU_TANH:
       return __fdividef(v, 1.f + expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
-    default: return fmaxf(v, 0.f);
+    default: return v < 0.f ? 0.f : v;            // a NaN stays one
   }
 }
 

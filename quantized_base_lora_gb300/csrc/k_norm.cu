@@ -275,6 +275,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
     }
   };
   if constexpr (SLOTS == 0) load(token);
+  auto gate_of = [&](uint64_t t) -> uint32_t {            // the token's row of the gates; none: outside
+    if (!a.gate.rows.ptr || t >= a.n_tokens) return 0;
+    return a.gate.row ? static_cast<uint32_t>(a.gate.row[t]) : a.gate.n == 1 ? 0u : static_cast<uint32_t>(t);
+  };
+  uint32_t row_then = gate_of(token);
+  constexpr bool kGateEarly = VEC * NV <= 8;             // asked for before the first norm, where registers are left
   uint32_t slot = 0;
   int turn = 0;
   // as many rounds for every thread of the block
@@ -292,20 +298,24 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
       for (int i = 0; i < NV; ++i) to_f32<VEC>(xr[i], XB, x[i]), to_f32<VEC>(yr[i], YB, z[i]);
       load(token + step);
     }
-    uint32_t row = 0;
-    bool joins = live && yp;
-    if (joins && a.gate.rows.ptr) {
-      row = a.gate.row ? static_cast<uint32_t>(a.gate.row[token]) : a.gate.n == 1 ? 0u : static_cast<uint32_t>(token);
-      joins = row < a.gate.n;
+    const uint32_t row = row_then;
+    row_then = gate_of(token + step);
+    const bool gated = live && yp && a.gate.rows.ptr && row < a.gate.n, joins = live && yp && (gated || !a.gate.rows.ptr);
+    [[maybe_unused]] Raw<VEC> gr[NV];
+    const uint64_t g0 = row * a.gate.rows.stride + c0;
+    if constexpr (kGateEarly) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (gated && in[i]) load_raw<VEC>(a.gate.rows.ptr, a.gate.rows.bf16, g0 + i * RT * VEC, gr[i]);
     }
     if (yp && a.norm.post.kind != OVL_NORM_NONE) normed_by<VEC, NV, RT>(a.norm.post, z, wy, in, inv, c0, red, turn);
-    if (joins && a.gate.rows.ptr) {
-      const uint64_t g0 = row * a.gate.rows.stride + c0;
+    if (gated) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
         float g[VEC];
-        load_f32<VEC>(a.gate.rows.ptr, a.gate.rows.bf16, g0 + i * RT * VEC, g);
+        if constexpr (kGateEarly) to_f32<VEC>(gr[i], a.gate.rows.bf16, g);
+        else load_f32<VEC>(a.gate.rows.ptr, a.gate.rows.bf16, g0 + i * RT * VEC, g);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) z[i][j] *= g[j];
       }
