@@ -823,6 +823,16 @@ ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, ui
                            const int32_t* choice, const float* weight, int32_t* choice_out, float* weight_out, void* y,
                            uint64_t y_stride, void* stream);
 
+enum { OVL_PACKED_ROPE = 1, OVL_PACKED_BLOCK_NORM = 2, OVL_PACKED_GLU = 3, OVL_PACKED_MOE = 4 };
+
+/* One of ovl_rope_apply, ovl_block_norm_apply, ovl_glu and ovl_moe_forward, with all
+ * its arguments but the stream as 64-bit words in their order (pointers and numbers,
+ * widened without a sign): for bindings that pay for each argument of a call, where a
+ * step's calls are a few microseconds each.  n_words must be the call's own number (15, 18,
+ * 11 and 11) and words of 32-bit arguments below 2^32 (OVL_E_ARG).  No counterpart in the
+ * source pages. */
+ovl_status ovl_packed(uint32_t call, const uint64_t* words, uint32_t n_words, void* stream);
+
 /* Message of the last failed call on ctx (static storage owned by ctx; "" after
  * success).  ctx NULL returns the message of the last failed call that has no
  * context on this thread (ovl_create, ovl_manifest_parse, ovl_kv_*, and the part

@@ -106,6 +106,7 @@ OVL_NORM_NONE, OVL_NORM_RMS, OVL_NORM_LAYER = 0, 1, 2
 OVL_NORM_MAX_HIDDEN = 32768
 OVL_ACT_SILU, OVL_ACT_GELU, OVL_ACT_GELU_TANH, OVL_ACT_RELU = 1, 2, 3, 4
 OVL_MOE_SOFTMAX, OVL_MOE_SIGMOID = 1, 2
+OVL_PACKED_ROPE, OVL_PACKED_BLOCK_NORM, OVL_PACKED_GLU, OVL_PACKED_MOE = 1, 2, 3, 4
 OVL_MOE_MAX_TOKENS, OVL_MOE_MAX_EXPERTS, OVL_MOE_MAX_TOP, OVL_MOE_MAX_HIDDEN = 128, 512, 16, 32768
 
 
@@ -187,6 +188,7 @@ def _load():
         "ovl_glu": ([U32, U32, U32, P, U64, P, U64, U32, P, U64, U32, P], I32),
         "ovl_moe_workspace_bytes": ([P, C.POINTER(SZ)], I32),
         "ovl_moe_forward": ([P, P, U32, U32, U64, P, P, P, P, P, U64, P], I32),
+        "ovl_packed": ([U32, C.c_char_p, U32, P], I32),
         "ovl_debug_kv_route": ([P, U32, U32, U32, U32, U32, U32, C.POINTER(U32)], I32),
     }
     for name, (args, res) in sig.items():
@@ -205,7 +207,7 @@ EXPORTED = ("ovl_create", "ovl_destroy", "ovl_load_base", "ovl_stage_adapter", "
             "ovl_manifest_parse", "ovl_activate_manifest", "ovl_kv_workspace_bytes", "ovl_kv_init", "ovl_kv_extend",
             "ovl_kv_append", "ovl_kv_read", "ovl_kv_attention", "ovl_kv_fork", "ovl_kv_compact", "ovl_kv_release",
             "ovl_kv_check", "ovl_debug_kv_route", "ovl_kv_positions", "ovl_rope_plan", "ovl_rope_apply", "ovl_block_norm_apply",
-            "ovl_glu", "ovl_moe_workspace_bytes", "ovl_moe_forward")
+            "ovl_glu", "ovl_moe_workspace_bytes", "ovl_moe_forward", "ovl_packed")
 
 
 class OvlError(RuntimeError):
@@ -537,3 +539,8 @@ def ovl_moe_forward(moe, x: int, dtype: int, n_tokens: int, x_stride: int, choic
                     weight_out: int, y: int, y_stride: int, stream: int = 0) -> int:
     return lib.ovl_moe_forward(_struct(moe), x, dtype, n_tokens, x_stride, choice, weight, choice_out, weight_out, y,
                                y_stride, stream)
+
+
+def ovl_packed(call: int, words: bytes, n_words: int, stream: int = 0) -> int:
+    """words: n_words 64-bit words, in this machine's order."""
+    return lib.ovl_packed(call, words, n_words, stream)

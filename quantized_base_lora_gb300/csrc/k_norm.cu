@@ -472,7 +472,6 @@ cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gat
     a.n_tokens = 1;
   }
   const bool vec = a.width % 8 == 0 && wide(gate) && wide(up) && wide(out);
-  if (a.n_tokens == 1 && vec) return glu_as<8>(act, a, st);
   return vec ? glu_as<8>(act, a, st) : glu_as<1>(act, a, st);
 }
 

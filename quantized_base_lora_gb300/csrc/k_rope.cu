@@ -162,10 +162,11 @@ cudaError_t launch_rope(const ovl_rope& rope, uint32_t n_tokens, const int32_t* 
   a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out;
   const bool vec = rope.rot_dim % 8 == 0 && rope.head_dim % 8 == 0 && wide(q) && wide(k) && wide(q_out) && wide(k_out);
   // One head a thread while that leaves the SMs room for more; four, which share the
-  // sines, where there is work for all of them.
+  // sines, where there is work for all of them; eight of many heads (8192 tokens of 40 heads
+  // of 128: two 38, four 30, eight 27 us; of 12 heads of 96, four 8.4 and eight 9.1).
   const uint64_t singles = static_cast<uint64_t>(n_tokens) * a.heads * rope.head_dim / (vec ? 8 : 2);
   const bool few = singles <= static_cast<uint64_t>(sm_count()) * 2048;
-  if (vec) return few ? launch_of<4, 1>(a, st) : launch_of<4, 4>(a, st);
+  if (vec) return few ? launch_of<4, 1>(a, st) : a.heads >= 32 ? launch_of<4, 8>(a, st) : launch_of<4, 4>(a, st);
   return few ? launch_of<1, 1>(a, st) : launch_of<1, 4>(a, st);
 }
 

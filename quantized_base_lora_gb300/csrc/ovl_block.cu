@@ -307,4 +307,47 @@ ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, ui
   return done(launch_moe(m, static_cast<cudaStream_t>(stream)));
 }
 
+ovl_status ovl_packed(uint32_t call, const uint64_t* words, uint32_t n_words, void* stream) {
+  if (!words) return fail(OVL_E_ARG, "words is null");
+  bool narrow = true;
+  auto ptr = [&](uint32_t i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(words[i])); };
+  auto num = [&](uint32_t i) {
+    narrow &= words[i] < (1ull << 32);
+    return static_cast<uint32_t>(words[i]);
+  };
+  const auto ints = [&](uint32_t i) { return static_cast<const int32_t*>(ptr(i)); };
+  switch (call) {
+    case OVL_PACKED_ROPE: {
+      if (n_words != 15) break;
+      const uint32_t n = num(1), qh = num(4), kh = num(7), dt = num(9), od = num(14);
+      if (!narrow) break;
+      return ovl_rope_apply(static_cast<const ovl_rope*>(ptr(0)), n, ints(2), ptr(3), qh, words[5], ptr(6), kh, words[8], dt,
+                            ptr(10), words[11], ptr(12), words[13], od, stream);
+    }
+    case OVL_PACKED_BLOCK_NORM: {
+      if (n_words != 18) break;
+      const uint32_t n = num(1), xd = num(3), yd = num(6), gd = num(9), ng = num(12), hd = num(16);
+      if (!narrow) break;
+      return ovl_block_norm_apply(static_cast<const ovl_block_norm*>(ptr(0)), n, ptr(2), xd, words[4], ptr(5), yd, words[7],
+                                  ptr(8), gd, words[10], ints(11), ng, ptr(13), words[14], ptr(15), hd, words[17], stream);
+    }
+    case OVL_PACKED_GLU: {
+      if (n_words != 11) break;
+      const uint32_t act = num(0), n = num(1), width = num(2), dt = num(7), od = num(10);
+      if (!narrow) break;
+      return ovl_glu(act, n, width, ptr(3), words[4], ptr(5), words[6], dt, ptr(8), words[9], od, stream);
+    }
+    case OVL_PACKED_MOE: {
+      if (n_words != 11) break;
+      const uint32_t dt = num(2), n = num(3);
+      if (!narrow) break;
+      return ovl_moe_forward(static_cast<const ovl_moe*>(ptr(0)), ptr(1), dt, n, words[4], ints(5),
+                             static_cast<const float*>(ptr(6)), static_cast<int32_t*>(ptr(7)), static_cast<float*>(ptr(8)),
+                             ptr(9), words[10], stream);
+    }
+    default: return fail(OVL_E_ARG, "unknown call");
+  }
+  return fail(OVL_E_ARG, "not the call's number of words, or a word above 32 bits");
+}
+
 }  // extern "C"

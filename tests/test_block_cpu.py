@@ -223,12 +223,51 @@ def test_positions_that_are_refused(q):
     assert q.ovl_kv_positions(kv, AT, AT, 0, 4, AT) == 0
 
 
+def test_packed_calls(q):
+    import struct
+
+    def call(which, *words):
+        return q.ovl_packed(which, struct.pack(f"={len(words)}Q", *words), len(words))
+
+    plan, norm, moe = q.ovl_rope_plan(8, 8, 1, 1e4)[1], q.ovl_block_norm(8, 1.0, 1.0), layer(q)
+    norm.pre.kind = 1
+    at = ctypes.addressof
+    rope = [at(plan), 0, AT, AT, 2, 16, AT, 1, 8, 1, 2 * AT, 16, 2 * AT, 8, 1]
+    block = [at(norm), 0, AT, 1, 8, AT, 1, 8, 0, 1, 0, 0, 0, AT, 8, 2 * AT, 1, 8]
+    glu = [1, 0, 8, AT, 8, AT, 8, 1, AT, 8, 1]
+    experts = [at(moe), AT, 1, 0, 64, 0, 0, 0, 0, 2 * AT, 64]
+    calls = [(q.OVL_PACKED_ROPE, rope), (q.OVL_PACKED_BLOCK_NORM, block), (q.OVL_PACKED_GLU, glu), (q.OVL_PACKED_MOE, experts)]
+    for which, words in calls:
+        assert call(which, *words) == 0                  # no tokens: checked, and nothing to do
+        assert call(which, *words, 0) == q.OVL_E_ARG and call(which, *words[:-1]) == q.OVL_E_ARG
+    # every argument is in its place: what each refuses is refused
+    for which, words, i, v, status in (
+            (1, rope, 0, 0, "ARG"), (1, rope, 4, 0, "SHAPE"), (1, rope, 7, 70000, "SHAPE"), (1, rope, 9, 5, "ARG"),
+            (1, rope, 14, 0, "ARG"), (1, rope, 1, 1 << 32, "ARG"), (2, block, 0, 0, "ARG"), (2, block, 3, 0, "ARG"),
+            (2, block, 6, 9, "ARG"), (2, block, 15, 0, "ARG"), (2, block, 16, 4, "ARG"), (2, block, 9, 1 << 40, "ARG"),
+            (3, glu, 0, 7, "ARG"), (3, glu, 2, 0, "SHAPE"), (3, glu, 7, 0, "ARG"), (3, glu, 10, 3, "ARG"),
+            (4, experts, 0, 0, "ARG"), (4, experts, 2, 0, "ARG"), (4, experts, 3, 17, "ARG"), (4, experts, 5, AT, "ARG"),
+            (4, experts, 3, 1 << 32, "ARG")):
+        assert call(which, *(words[:i] + [v] + words[i + 1:])) == getattr(q, f"OVL_E_{status}"), (which, i)
+    # and where there are tokens, of the tensors
+    for which, words, n, bad in ((1, rope, 1, (2, 3, 6, 10, 12)), (2, block, 1, (2,)), (3, glu, 1, (3, 5, 8)), (4, experts, 3, (1, 9))):
+        some = words[:n] + [4] + words[n + 1:]
+        for i in bad:
+            assert call(which, *(some[:i] + [0] + some[i + 1:])) == q.OVL_E_ARG, (which, i)
+    for which, words, n, strides in ((1, rope, 1, (5, 8, 11, 13)), (2, block, 1, (4, 7, 14, 17)), (3, glu, 1, (4, 6, 9)),
+                                     (4, experts, 3, (4, 10))):
+        some = words[:n] + [4] + words[n + 1:]
+        for i in strides:
+            assert call(which, *(some[:i] + [1] + some[i + 1:])) == q.OVL_E_SHAPE, (which, i)
+    assert call(0) == call(5, *glu) == q.OVL_E_ARG and q.lib.ovl_packed(1, None, 15, None) == q.OVL_E_ARG
+
+
 def test_constants_match_the_header(q):
     import os
     import re
     with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ovl.h")) as f:
         text = f.read()
-    found = re.findall(r"\b(OVL_(?:ROPE|NORM|ACT|MOE)_[A-Z_0-9]+) = (\d+)", text)
+    found = re.findall(r"\b(OVL_(?:ROPE|NORM|ACT|MOE|PACKED)_[A-Z_0-9]+) = (\d+)", text)
     assert len(found) >= 20
     for name, value in found:
         assert getattr(q, name) == int(value), name

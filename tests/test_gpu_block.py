@@ -342,3 +342,12 @@ def test_what_the_torch_side_refuses():
             call()
     with pytest.raises(q.OvlError):                      # tokens that overlap
         rope(ints(0, 1, 2, 3), h, q_out=torch.as_strided(torch.zeros(64, device="cuda"), (4, 1, 64), (0, 64, 1)))
+
+
+def test_rotations_of_many_heads_and_tokens():
+    rope = B.Rope(64, 48, "pairs")
+    pos = torch.arange(4001, device="cuda", dtype=torch.int32) * 31
+    qk = rand(4, 4001, 45, 64, dtype=BF16)
+    q2, k2 = rope(pos, qk[:, :36], qk[:, 36:], dtype=F32)
+    for a, b in ((qk[:, :36], q2), (qk[:, 36:], k2)):
+        check_rope("pairs", P.frequencies(48), pos, a, b)
