@@ -33,8 +33,16 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int turn) {
     __syncthreads();
     const float* mine = red[turn] + warp / kWarps * kWarps;
     float part[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kWarps % 4 == 0) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) part[w & 3] += mine[w];
+      for (int w = 0; w < kWarps; w += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(mine + w);
+        part[0] += f.x, part[1] += f.y, part[2] += f.z, part[3] += f.w;
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) part[w & 3] += mine[w];
+    }
     v = (part[0] + part[1]) + (part[2] + part[3]);
   }
   return v;
@@ -232,7 +240,7 @@ __device__ __forceinline__ void normed_by(const ovl_norm& n, float (&v)[NV][VEC]
 template <int VEC, int NV, int RT, int THREADS, int SLOTS, int BLOCKS, bool XB, bool YB, bool HB>
 __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   using X = Ahead<NV, RT, XB>;
   using Y = Ahead<NV, RT, YB>;
   constexpr uint32_t kRows = THREADS / RT, kSlot = X::kBytes + Y::kBytes;
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
 // Wide rows, of any type: a block of RT threads has one at a time.
 template <int VEC, int NV, int RT, int BLOCKS>
 __global__ void __launch_bounds__(RT, BLOCKS) k_block_norm_any(const __grid_constant__ NormArgs a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t hidden = a.norm.hidden, c0 = threadIdx.x * VEC;
