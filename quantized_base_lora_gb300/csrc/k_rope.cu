@@ -7,7 +7,9 @@
 // leave an angle within 2^-32 of a turn.  The nearest quarter turn comes off as an
 // integer as well, so that Taylor's series are needed for |angle| <= pi / 4 only, where
 // nine terms of both together end below 2e-9.
-// Bound by memory: each element is read once and written once.
+// Bound by memory: each element is read once and written once.  8192 tokens of 40 heads of
+// 128 in bf16 (168 MB): 27 us, 0.92 of the copy bandwidth; 51 us while loads were converted one
+// by one, 33 while the frequencies were kernel arguments that each lane read at its own place.
 #include "block_internal.h"
 
 namespace ovl {
