@@ -158,11 +158,12 @@ __device__ __forceinline__ uint32_t share(uint32_t n, uint32_t cta) {
 }
 
 // The chosen pairs sorted by expert, in pair order within one, and cut into units: by every
-// CTA for itself, in shared memory (less work than to wait for one to do it).  The CTA's
-// items go to range[0] .. range[1] - 1: runs of tiles of equal cost, where a unit whose parts
-// do not fit beside one another counts half as much again.
+// CTA for itself, in shared memory (less work than to wait for one to do it).  An entry of
+// the order is token << 4 | place, which saves the divisions behind it.  The CTA's items are
+// range[0] .. range[1] - 1, of range[2] units: runs of tiles of equal cost, where a unit
+// whose parts do not fit beside one another counts half as much again.
 template <uint32_t Q, int PARTS>
-__device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint32_t tiles, uint32_t (&range)[2]) {
+__device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint32_t tiles, uint32_t (&range)[3]) {
   MoeUnit* units = reinterpret_cast<MoeUnit*>(smem + Shape<Q>::kUnits);
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + Shape<Q>::kOrder);
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -170,9 +171,10 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
   if (m.tokens == 1 && !m.given) {                        // distinct experts with one pair each
     if (threadIdx.x < m.top) {
       units[threadIdx.x] = MoeUnit::make(choice[threadIdx.x], 1, threadIdx.x, 1, threadIdx.x);
-      order[threadIdx.x] = static_cast<uint16_t>(threadIdx.x);
+      order[threadIdx.x] = static_cast<uint16_t>(threadIdx.x);       // place threadIdx.x of token 0
     }
     if (threadIdx.x < 2) range[threadIdx.x] = share(m.top * tiles, blockIdx.x + threadIdx.x);
+    if (threadIdx.x == 2) range[2] = m.top;
     __syncthreads();
     return;
   }
@@ -183,7 +185,7 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
   uint16_t* first = count + kWarps * OVL_MOE_MAX_EXPERTS;
   uint32_t* sums = reinterpret_cast<uint32_t*>(first + OVL_MOE_MAX_EXPERTS);      // [3][kWarps]
   uint32_t* expert_rank = sums + 3 * kWarps;              // [kMoeMaxPairs], of a warp's own pairs
-  static_assert(kWarps * 32 >= OVL_MOE_MAX_EXPERTS / 2, "two experts a thread");
+  static_assert(kWarps * 32 >= OVL_MOE_MAX_EXPERTS / 2 && OVL_MOE_MAX_TOP <= 16, "two experts a thread; an entry's fields");
   const uint32_t per = (m.pairs + kWarps * 32 - 1) / (kWarps * 32), from = warp * per * 32 + lane;
   const uint32_t own = 2 * threadIdx.x;                   // the thread's experts: own and own + 1
   if (own < m.experts) {
@@ -235,6 +237,7 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
     all += sums[kWarps + w], whole += sums[2 * kWarps + w];
   }
   a -= n[0] + n[1], b -= groups[0] + groups[1], c -= cost[0] + cost[1];
+  if (threadIdx.x == 0) range[2] = all;
   uint32_t from_cost[2];                                  // below 768 units * 3 * 2048 tiles
 #pragma unroll
   for (uint32_t k = 0; k < 2; ++k) {
@@ -259,16 +262,51 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
     const uint32_t p = from + r * 32;
     if (p >= m.pairs) break;
     const uint32_t e = expert_rank[p] >> 16, rank = expert_rank[p] & 0xffff;
-    if (e < OVL_MOE_MAX_EXPERTS) order[first[e] + count[warp * OVL_MOE_MAX_EXPERTS + e] + rank] = static_cast<uint16_t>(p);
+    const uint32_t token = p / m.top;
+    if (e < OVL_MOE_MAX_EXPERTS)
+      order[first[e] + count[warp * OVL_MOE_MAX_EXPERTS + e] + rank] = static_cast<uint16_t>(token << 4 | (p - token * m.top));
   }
   __syncthreads();
 }
 
-// Where a warp's copies are: an item (32 rows of a unit) and the stage inside it.
+// An item: 32 rows of a unit.  An expert's units lie side by side for each tile, so that its
+// weights are in L2 for the second and later ones.
+struct Item {
+  MoeUnit unit;
+  uint32_t tile, place, next;  // tile; the unit's place in its group; the first unit behind the group
+  __device__ void find(const MoeUnit* units, uint32_t tiles, uint32_t item) {
+    const MoeUnit any = units[item / tiles];
+    const uint32_t g = any.group(), n = any.groups(), r = item - g * tiles;
+    tile = n == 1 ? r : r / n;
+    place = r - tile * n;
+    next = g + n;
+    unit = units[g + place];
+  }
+  // The one behind it; none behind the last unit's last.
+  __device__ void advance(const MoeUnit* units, uint32_t tiles, uint32_t n_units) {
+    const uint32_t n = unit.groups();
+    if (++place < n) {
+      unit = units[next - n + place];
+      return;
+    }
+    place = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (next == n_units) return;
+      unit = units[next];
+      next += unit.groups();
+    } else if (n > 1) {
+      unit = units[next - n];
+    }
+  }
+};
+
+// Where a warp's copies are.
 struct Cursor {
   const uint8_t* row[2];       // the lane's next piece: of the first and of the last 16 rows
   const uint8_t* scale;        // the lane's row of scales
-  uint32_t item, stage;
+  uint32_t stage;
+  Item item;
 };
 
 // DOWN: the second product.  PARTS: of its input.
@@ -297,24 +335,10 @@ struct Rows32 {
     tiles = DOWN ? m.hidden / 32 : m.ffn / 16;
   }
 
-  // Unit and tile of an item: an expert's units side by side for each tile, so that its
-  // weights are in L2 for the second and later ones.
-  __device__ MoeUnit unit_of(uint32_t item, uint32_t* tile) const {
-    const MoeUnit any = units[item / tiles];
-    const uint32_t r = item - any.group() * tiles, n = any.groups();
-    if (n == 1) {
-      *tile = r;
-      return any;
-    }
-    *tile = r / n;
-    return units[any.group() + r % n];
-  }
-
-  __device__ void at(Cursor& c, uint32_t item, uint32_t stage) const {
-    c.item = item;
+  // To stage `stage` of the cursor's item.
+  __device__ void at(Cursor& c, uint32_t stage) const {
     c.stage = stage;
-    uint32_t tile;
-    const uint32_t expert = unit_of(item, &tile).expert(), r = lane / 8;
+    const uint32_t expert = c.item.unit.expert(), tile = c.item.tile, r = lane / 8;
     const uint64_t piece = lane % 8 * 16 + stage * kRowBytes;
     if constexpr (DOWN) {
       const uint64_t first = static_cast<uint64_t>(expert) * m.hidden + tile * 32;
@@ -546,24 +570,19 @@ struct Rows32 {
   __device__ void finish(uint32_t tile, uint32_t n_pairs, int32_t pair, float w, float power, bool beside, float (&acc)[2][4]) const {
     const uint32_t g = lane >> 2, t = lane & 3;
     if (beside) {                                // column c's parts are columns c + n, c + 2 n: the small ones first
-      float all[2][4];
+      float all[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) all[i / 4][i % 4] = 0.f;
+      for (int q = PARTS - 1; q >= 0; --q) {
+        const uint32_t by = q * n_pairs;         // odd: the other one of a lane's two columns
 #pragma unroll
-      for (int q = PARTS - 1; q >= 0; --q)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t from = (2 * t + j + q * n_pairs) & 7, source = (lane & 28) + from / 2;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float even = __shfl_sync(0xffffffffu, acc[h][2 * e], source), odd = __shfl_sync(0xffffffffu, acc[h][2 * e + 1], source);
-              all[h][2 * e + j] += (from & 1) ? odd : even;
-            }
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t from = (2 * t + (i & 1) + by) & 7;
+          const float v = __shfl_sync(0xffffffffu, (by & 1) ? acc[i / 4][(i & 3) ^ 1] : acc[i / 4][i & 3], (lane & 28) + from / 2);
+          all[i] = q == PARTS - 1 ? v : all[i] + v;
         }
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = all[i / 4][i % 4];
+      for (int i = 0; i < 8; ++i) acc[i / 4][i & 3] = all[i];
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -572,21 +591,22 @@ struct Rows32 {
       const float weight = __shfl_sync(0xffffffffu, w, column), up = __shfl_sync(0xffffffffu, power, column);
       if (column >= n_pairs) continue;
       if constexpr (DOWN) {
+        constexpr float back = pow2(kCodeExponent - kActExponent);
         float* out = m.part + static_cast<uint64_t>(p) * m.hidden + tile * 32 + g;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) out[h * 16 + e * 8] = weight * (acc[h][2 * e + j] * pow2(kCodeExponent - kActExponent) * up * up);
+          for (int e = 0; e < 2; ++e) out[h * 16 + e * 8] = weight * (acc[h][2 * e + j] * back * up * up);
       } else {
         constexpr int kParts = PARTS == 1 ? 2 : 3;
-        constexpr float back = pow2(kCodeExponent - kTokenExponent);
+        constexpr float back = pow2(kCodeExponent - kTokenExponent), scaled = pow2(kActExponent);
         const float down = 1.f / up;             // a power of two
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float gate = activated(acc[0][2 * e + j] * back * up, m.act) * down;
           const uint32_t c = (tile & 1) * 16 + e * 8 + g;
           uint16_t v[kParts];
-          parts_of<kParts>(gate * share_of<Q>(c) * (acc[1][2 * e + j] * back) * pow2(kActExponent), v);
+          parts_of<kParts>(gate * share_of<Q>(c) * (acc[1][2 * e + j] * back) * scaled, v);
           uint16_t* out = m.hp + static_cast<uint64_t>(p) * m.ffn + (tile >> 1) * 32 + place_of<Q>(c);
 #pragma unroll
           for (int q = 0; q < kParts; ++q) out[q * static_cast<uint64_t>(m.pairs) * m.ffn] = v[q];
@@ -602,7 +622,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   // The first product waits for the router before it lets the second start, so that the
   // second may read the router's results and ask for weights before the first has ended.
-  __shared__ uint32_t range[2];
+  __shared__ uint32_t range[3];
   const Rows32<Q, DOWN, PARTS> op(m, smem);
   if constexpr (!DOWN) {
     griddep_wait();
@@ -619,11 +639,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   const uint32_t p0 = start_of(warp), p1 = start_of(warp + 1);
   Cursor c{};
   uint32_t asked = p0, slot_in = 0;
-  if (p0 < p1) op.at(c, begin + p0 / stages, p0 % stages);
+  if (p0 < p1) {
+    c.item.find(op.units, op.tiles, begin + p0 / stages);
+    op.at(c, p0 % stages);
+  }
+  Item now = c.item;
+  const uint32_t n_units = range[2];
   auto ask = [&]() {
     if (asked < p1) {
       op.fill(c, slot_in);
-      if (++asked < p1 && c.stage == stages) op.at(c, c.item + 1, 0);
+      if (++asked < p1 && c.stage == stages) {
+        c.item.advance(op.units, op.tiles, n_units);
+        op.at(c, 0);
+      }
     }
     cp_async_commit();
     slot_in = slot_in + 1 == kStages ? 0 : slot_in + 1;
@@ -639,23 +667,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   float* mine = reinterpret_cast<float*>(smem + Shape<Q>::kJoins) + (static_cast<int>(warp) - 1) * static_cast<int>(kJoinBytes / 4) + lane;    // not of warp 0
   uint32_t slot = 0;
   bool divided = false, beside = false;                   // whether others have stages of the last item; parts in columns
-  uint32_t item = 0, tile = 0, n_pairs = 0;
+  uint32_t n_pairs = 0, s0 = p0 % stages;
   int32_t pair = 0;
   float w = 0.f, power = 1.f, acc[2][4];
-  for (uint32_t p = p0; p < p1;) {
-    item = begin + p / stages;
-    const uint32_t s0 = p % stages, s1 = min(stages, s0 + (p1 - p));
+  uint32_t p = p0;
+  while (p < p1) {
+    const uint32_t s1 = min(stages, s0 + (p1 - p));
     p += s1 - s0;
-    const MoeUnit unit = op.unit_of(item, &tile);
-    n_pairs = unit.pairs();
+    n_pairs = now.unit.pairs();
     // the lane's pair; places behind the last repeat it, and no one reads their sums
-    pair = order[unit.first() + min(lane, n_pairs - 1)];
+    const uint32_t entry = order[now.unit.first() + min(lane, n_pairs - 1)];
+    pair = static_cast<int32_t>((entry >> 4) * m.top + (entry & 15));
     beside = PARTS > 1 && n_pairs * PARTS <= 8;
-    const uint32_t column = lane >> 2, which = beside ? column / n_pairs : 0;
-    const uint32_t p_of = static_cast<uint32_t>(__shfl_sync(0xffffffffu, pair, column - which * n_pairs));
-    const uint32_t x = (DOWN ? p_of : p_of / m.top) * op.k * 2 + (which < PARTS ? which : 0) * part + (lane & 3) * 16;    // bytes, below 2^32
+    const uint32_t column = lane >> 2;
+    uint32_t which = 0;
+#pragma unroll
+    for (int q = 1; q < PARTS; ++q) which += beside && column >= q * n_pairs;
+    const uint32_t source = static_cast<uint32_t>(__shfl_sync(0xffffffffu, DOWN ? pair : static_cast<int32_t>(entry >> 4), column - which * n_pairs));
+    const uint32_t x = source * op.k * 2 + which * part + (lane & 3) * 16;               // bytes, below 2^32
     if constexpr (DOWN) w = weights[pair];
-    power = m.power[pair / m.top];
+    power = m.power[entry >> 4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] = 0.f;
     auto stages_in = [&](auto parts) {
@@ -686,19 +717,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
       divided = true;
       break;
     } else {
-      op.finish(tile, n_pairs, pair, w, power, beside, acc);
+      op.finish(now.tile, n_pairs, pair, w, power, beside, acc);
     }
+    s0 = 0;
+    now.advance(op.units, op.tiles, n_units);
   }
   __syncthreads();
   if (divided) {
-    const uint32_t behind = (item - begin + 1) * stages;
+    const uint32_t behind = p - p % stages + stages;      // where the item ends: p is inside it
     for (uint32_t o = warp + 1; o < kWarps && start_of(o) < behind; ++o) {
       if (start_of(o) == start_of(o + 1)) continue;
       const float* theirs = mine + kJoinBytes / 4 * (o - warp);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i / 4][i % 4] += theirs[i * 32];
     }
-    op.finish(tile, n_pairs, pair, w, power, beside, acc);
+    op.finish(now.tile, n_pairs, pair, w, power, beside, acc);
   }
   cp_async_wait<0>();
 }
