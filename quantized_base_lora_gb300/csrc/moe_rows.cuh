@@ -15,12 +15,11 @@
 // mma.sync is idle most of the time as it is.
 //
 // Measured (graph of calls, the whole layer): one fp32 token over two q8_0 experts of 4096 x
-// 14336 (375 MB) 87 us; one bf16 token over 8 of 128 q4_0 experts of 2048 x 768 (22 MB) 20; 64
-// tokens over the same experts (336 MB) 100; 19 over 64 q4_K experts of 2048 x 1280 (240 MB) 70.
+// 14336 (375 MB) 82 us; one bf16 token over 8 of 128 q4_0 experts of 2048 x 768 (22 MB) 20; 64
+// tokens over the same experts (336 MB) 99; 19 over 64 q4_K experts of 2048 x 1280 (240 MB) 69.
 // The copies alone take 0.7 of a product's time, the arithmetic alone as much: 72
-// instructions a 1024 weights on 12 warps, half of the issue slots, waits for fixed latencies
-// between them.  More warps at the cost of the cache or of registers were slower (16: 106 for
-// 100 us), fewer as well (8: 104).
+// instructions a 1024 weights, half of the issue slots, waits for fixed latencies between
+// them.
 //
 // Inputs are bf16 parts (one: bf16 tokens; two: activations of bf16 calls; three: all 24
 // bits of fp32) in the order of the fragments: lane t of a quad takes 8 consecutive
@@ -36,25 +35,31 @@
 namespace ovl {
 namespace moe {
 
-constexpr uint32_t kWarps = 12;
+// Warps of a CTA.  16 have 128 registers each and leave less of the SM to the cache, 12 have
+// 168; q4_K holds the most in both, then the fp32 calls.  12 against 16, the whole layer in us:
+//                                             q8_0 bf16   fp32       q4_0 bf16   fp32       q4_K bf16   fp32
+//   1 token, 2 experts of 4096 x 14336        84.7/81.5   86.7/82.7  62.2/55.9   60.6/61.6  60.6/62.4   68.3/70.5
+//   1 token, 8 of 128 experts of 2048 x 768   21.2/22.0   22.2/22.6  19.7/20.3   20.1/22.3  20.0/21.9   21.2/24.7
+//   64 tokens over the same                   144/143     183/180    103/99.2    140/146    103/106     169/181
+template <uint32_t Q, int PARTS>
+constexpr uint32_t kWarps = Q == OVL_Q4_K || (Q == OVL_Q4_0 && PARTS == 3) ? 12 : 16;
 constexpr int kStages = 2;
 constexpr uint32_t kRowBytes = 128;                       // of a row in one stage: 8 pieces of 16
 constexpr uint32_t kScaleBytes = 20;                      // of a row in one stage: 16, or five words around 16 bytes
 constexpr uint32_t kStageBytes = 32 * (kRowBytes + kScaleBytes);
 constexpr uint32_t kJoinBytes = kMoeTokens * 32 * 4;      // a warp's sums
 
-// Shared memory of a CTA.  It stays within 131 KB (q4_K: 163), so that the rest of the
-// SM's 256 KB is cache for the inputs, which every warp reads: with 16 warps and 206 KB,
-// 20 to 57 percent of those loads hit, and one token over two experts of 14336 took 110
-// us instead of 90.
-template <uint32_t Q>
+// Shared memory of a CTA.  It stays within 175 KB, so that the rest of the SM's 256 KB is
+// cache for the inputs, which every warp reads: at 206 KB, 20 to 57 percent of those loads
+// hit, and one token over two experts of 14336 took 110 us instead of 90.
+template <uint32_t Q, int PARTS>
 struct Shape {
   static constexpr uint32_t kTableBytes = Q == OVL_Q4_K ? 2 * 8 * 32 * 4 : 0;         // a warp's scales and minimums of a stage
-  static constexpr uint32_t kTables = kWarps * kStages * kStageBytes, kJoins = kTables + kWarps * kTableBytes,
-                            kUnits = kJoins + (kWarps - 1) * kJoinBytes, kOrder = kUnits + kMoeMaxUnits * sizeof(MoeUnit),
+  static constexpr uint32_t kTables = kWarps<Q, PARTS> * kStages * kStageBytes, kJoins = kTables + kWarps<Q, PARTS> * kTableBytes,
+                            kUnits = kJoins + (kWarps<Q, PARTS> - 1) * kJoinBytes, kOrder = kUnits + kMoeMaxUnits * sizeof(MoeUnit),
                             kSmem = kOrder + kMoeMaxPairs * 2;
   static_assert(kStageBytes % 128 == 0, "slots begin on 128 bytes");
-  static_assert(kSmem + 64 <= (Q == OVL_Q4_K ? 163 : 131) * 1024, "what is left to the cache");
+  static_assert(kSmem + 64 <= 175 * 1024, "what is left to the cache");
 };
 
 __device__ __forceinline__ void cp_async4_if(uint32_t dst, const void* src, bool on) {
@@ -164,8 +169,8 @@ __device__ __forceinline__ uint32_t share(uint32_t n, uint32_t cta) {
 // whose parts do not fit beside one another counts half as much again.
 template <uint32_t Q, int PARTS>
 __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint32_t tiles, uint32_t (&range)[3]) {
-  MoeUnit* units = reinterpret_cast<MoeUnit*>(smem + Shape<Q>::kUnits);
-  uint16_t* order = reinterpret_cast<uint16_t*>(smem + Shape<Q>::kOrder);
+  MoeUnit* units = reinterpret_cast<MoeUnit*>(smem + Shape<Q, PARTS>::kUnits);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + Shape<Q, PARTS>::kOrder);
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int32_t* choice = m.given ? m.given_choice : m.choice;
   if (m.tokens == 1 && !m.given) {                        // distinct experts with one pair each
@@ -182,15 +187,15 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
   // sums, the pairs' experts and their places in their warp's share.  Loops are not unrolled:
   // each line of instructions comes from L2 here.
   uint16_t* count = reinterpret_cast<uint16_t*>(smem);                   // [kWarps][OVL_MOE_MAX_EXPERTS]
-  uint16_t* first = count + kWarps * OVL_MOE_MAX_EXPERTS;
+  uint16_t* first = count + kWarps<Q, PARTS> * OVL_MOE_MAX_EXPERTS;
   uint32_t* sums = reinterpret_cast<uint32_t*>(first + OVL_MOE_MAX_EXPERTS);      // [3][kWarps]
-  uint32_t* expert_rank = sums + 3 * kWarps;              // [kMoeMaxPairs], of a warp's own pairs
-  static_assert(kWarps * 32 >= OVL_MOE_MAX_EXPERTS / 2 && OVL_MOE_MAX_TOP <= 16, "two experts a thread; an entry's fields");
-  const uint32_t per = (m.pairs + kWarps * 32 - 1) / (kWarps * 32), from = warp * per * 32 + lane;
+  uint32_t* expert_rank = sums + 3 * kWarps<Q, PARTS>;              // [kMoeMaxPairs], of a warp's own pairs
+  static_assert(kWarps<Q, PARTS> * 32 >= OVL_MOE_MAX_EXPERTS / 2 && OVL_MOE_MAX_TOP <= 16, "two experts a thread; an entry's fields");
+  const uint32_t per = (m.pairs + kWarps<Q, PARTS> * 32 - 1) / (kWarps<Q, PARTS> * 32), from = warp * per * 32 + lane;
   const uint32_t own = 2 * threadIdx.x;                   // the thread's experts: own and own + 1
   if (own < m.experts) {
 #pragma unroll 1
-    for (uint32_t w = 0; w < kWarps; ++w) *reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own) = 0;
+    for (uint32_t w = 0; w < kWarps<Q, PARTS>; ++w) *reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own) = 0;
   }
   __syncthreads();
 #pragma unroll 1
@@ -210,7 +215,7 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
   uint32_t n[2] = {0, 0};                                 // their pairs
   if (own < m.experts) {
 #pragma unroll 1
-    for (uint32_t w = 0; w < kWarps; ++w) {
+    for (uint32_t w = 0; w < kWarps<Q, PARTS>; ++w) {
       uint32_t* c = reinterpret_cast<uint32_t*>(count + w * OVL_MOE_MAX_EXPERTS + own);
       const uint32_t some = *c;
       *c = n[0] | n[1] << 16;
@@ -228,13 +233,13 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
     const uint32_t u = __shfl_up_sync(0xffffffffu, a, s), v = __shfl_up_sync(0xffffffffu, b, s), w = __shfl_up_sync(0xffffffffu, c, s);
     if (static_cast<int>(lane) >= s) a += u, b += v, c += w;
   }
-  if (lane == 31) sums[warp] = a, sums[kWarps + warp] = b, sums[2 * kWarps + warp] = c;
+  if (lane == 31) sums[warp] = a, sums[kWarps<Q, PARTS> + warp] = b, sums[2 * kWarps<Q, PARTS> + warp] = c;
   __syncthreads();
   uint32_t all = 0, whole = 0;
 #pragma unroll 1
-  for (uint32_t w = 0; w < kWarps; ++w) {
-    if (w < warp) a += sums[w], b += sums[kWarps + w], c += sums[2 * kWarps + w];
-    all += sums[kWarps + w], whole += sums[2 * kWarps + w];
+  for (uint32_t w = 0; w < kWarps<Q, PARTS>; ++w) {
+    if (w < warp) a += sums[w], b += sums[kWarps<Q, PARTS> + w], c += sums[2 * kWarps<Q, PARTS> + w];
+    all += sums[kWarps<Q, PARTS> + w], whole += sums[2 * kWarps<Q, PARTS> + w];
   }
   a -= n[0] + n[1], b -= groups[0] + groups[1], c -= cost[0] + cost[1];
   if (threadIdx.x == 0) range[2] = all;
@@ -324,10 +329,10 @@ struct Rows32 {
   bool scales_aligned;
 
   __device__ Rows32(const MoeDev& dev, uint8_t* smem)
-      : m(dev), units(reinterpret_cast<const MoeUnit*>(smem + Shape<Q>::kUnits)) {
+      : m(dev), units(reinterpret_cast<const MoeUnit*>(smem + Shape<Q, PARTS>::kUnits)) {
     lane = threadIdx.x & 31;
     ring = smem + threadIdx.x / 32 * kStages * kStageBytes;
-    table = reinterpret_cast<float*>(smem + Shape<Q>::kTables + threadIdx.x / 32 * Shape<Q>::kTableBytes);
+    table = reinterpret_cast<float*>(smem + Shape<Q, PARTS>::kTables + threadIdx.x / 32 * Shape<Q, PARTS>::kTableBytes);
     k = DOWN ? m.ffn : m.hidden;
     pitch = Q == OVL_Q8_0 ? k : k / 2;
     scale_pitch = k / 16;                                               // 2 bytes a block; 16 bytes of 256 weights
@@ -617,7 +622,7 @@ struct Rows32 {
 };
 
 template <uint32_t Q, bool DOWN, int PARTS>
-__global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_constant__ MoeDev m) {
+__global__ void __launch_bounds__(kWarps<Q, PARTS> * 32, 1) k_moe_rows(const __grid_constant__ MoeDev m) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   // The first product waits for the router before it lets the second start, so that the
@@ -629,13 +634,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
     griddep_launch_dependents();
   }
   sort_pairs<Q, PARTS>(m, smem, op.tiles, range);
-  const uint16_t* order = reinterpret_cast<const uint16_t*>(smem + Shape<Q>::kOrder);
+  const uint16_t* order = reinterpret_cast<const uint16_t*>(smem + Shape<Q, PARTS>::kOrder);
   // Items in runs of equal cost to the CTAs; inside a CTA, their stages in equal runs to the
   // warps.  An item whose stages are divided is finished by the warp that has its first
   // ones, last thing; the others come to it first thing and leave their sums in shared memory.
   const uint32_t begin = range[0], end = range[1];
   const uint32_t stages = (op.pitch + kRowBytes - 1) / kRowBytes, total = (end - begin) * stages;
-  auto start_of = [&](uint32_t w) { return total / kWarps * w + total % kWarps * w / kWarps; };
+  auto start_of = [&](uint32_t w) { return total / kWarps<Q, PARTS> * w + total % kWarps<Q, PARTS> * w / kWarps<Q, PARTS>; };
   const uint32_t p0 = start_of(warp), p1 = start_of(warp + 1);
   Cursor c{};
   uint32_t asked = p0, slot_in = 0;
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   }
   const uint32_t part = (DOWN ? m.pairs : m.tokens) * op.k * 2;
   const float* weights = m.given ? m.given_weight : m.weight;
-  float* mine = reinterpret_cast<float*>(smem + Shape<Q>::kJoins) + (static_cast<int>(warp) - 1) * static_cast<int>(kJoinBytes / 4) + lane;    // not of warp 0
+  float* mine = reinterpret_cast<float*>(smem + Shape<Q, PARTS>::kJoins) + (static_cast<int>(warp) - 1) * static_cast<int>(kJoinBytes / 4) + lane;    // not of warp 0
   uint32_t slot = 0;
   bool divided = false, beside = false;                   // whether others have stages of the last item; parts in columns
   uint32_t n_pairs = 0, s0 = p0 % stages;
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
   __syncthreads();
   if (divided) {
     const uint32_t behind = p - p % stages + stages;      // where the item ends: p is inside it
-    for (uint32_t o = warp + 1; o < kWarps && start_of(o) < behind; ++o) {
+    for (uint32_t o = warp + 1; o < kWarps<Q, PARTS> && start_of(o) < behind; ++o) {
       if (start_of(o) == start_of(o + 1)) continue;
       const float* theirs = mine + kJoinBytes / 4 * (o - warp);
 #pragma unroll
@@ -739,9 +744,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_moe_rows(const __grid_consta
 template <uint32_t Q, bool DOWN, int PARTS>
 cudaError_t launch_rows(const MoeDev& m, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_rows<Q, DOWN, PARTS>), Shape<Q>::kSmem, &allowed);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_moe_rows<Q, DOWN, PARTS>), Shape<Q, PARTS>::kSmem, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_chained(k_moe_rows<Q, DOWN, PARTS>, dim3(sm_count()), kWarps * 32, Shape<Q>::kSmem, st, m);
+  return launch_chained(k_moe_rows<Q, DOWN, PARTS>, dim3(sm_count()), kWarps<Q, PARTS> * 32, Shape<Q, PARTS>::kSmem, st, m);
 }
 
 // Both products, one behind the other.
