@@ -206,18 +206,20 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ 
   __syncthreads();
   if (!odd && expert < m.experts && lane < n) {
     m.logits[static_cast<uint64_t>(t0 + lane) * m.experts + expert] = mine + part[e][lane];
-    __threadfence();
+    if (wide > 1) __threadfence();
   }
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&m.arrived[group], 1u) + 1 == wide;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+  if (wide > 1) {                                  // else all scores are the CTA's own: one token's choice 1 us sooner
+    if (threadIdx.x == 0) last = atomicAdd(&m.arrived[group], 1u) + 1 == wide;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+  }
   if (warp < n) {
     if (m.experts <= 128) choose<4>(m, t0 + warp);
     else choose<OVL_MOE_MAX_EXPERTS / 32>(m, t0 + warp);
   }
-  if (threadIdx.x == 0) m.arrived[group] = 0;
+  if (wide > 1 && threadIdx.x == 0) m.arrived[group] = 0;
 }
 
 // y of a token: its experts' weighted outputs, in the order of the choice.
