@@ -76,6 +76,22 @@ def test_odd_sizes(quant, dtype, hidden, ffn):
         L.check(x, L.moe(x, choice.cuda(), weight.cuda()), choice, weight)
 
 
+@pytest.mark.parametrize("quant", QUANTS, ids=["q8_0", "q4_0", "q4_K"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,top,hidden,ffn", [
+    (1, 1, 256, 256), (3, 1, 256, 8192), (4, 2, 2048, 1024), (16, 16, 256, 768), (5, 3, 1280, 2816), (2, 1, 4096, 256),
+    (2, 2, 4864, 512), (1, 1, 512, 20480), (16, 16, 1792, 256)])
+def test_one_routed_token(quant, dtype, n, top, hidden, ffn):
+    """Fewer tiles than CTAs, a few more, rows of 1 to 160 stages; routed and with the same choice given."""
+    L = Layer(quant, n, hidden, ffn, top, seed=ffn, max_tokens=1)
+    x = rand(9, 1, hidden, dtype=dtype)
+    y, choice, weight = L.moe(x, routing=True)
+    assert sorted(choice[0].tolist()) == sorted(set(choice[0].tolist())) and choice.max() < n
+    L.check(x, y, choice, weight)
+    L.check(x, L.moe(x, choice, weight), choice, weight)
+    assert torch.equal(L.moe(x), y)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
