@@ -179,23 +179,71 @@ __device__ __forceinline__ void rest_of_row(const NormArgs& a, float (&x)[NV][VE
     if (live && c0 + i * RT * VEC < hidden) store_f32<VEC>(a.h.ptr, h_bf16, h0 + i * RT * VEC, x[i]);
 }
 
+// A thread's pieces of a row that begins at `at`; the type is looked at once.
+template <int VEC, int NV, int RT>
+__device__ __forceinline__ void load_row(const void* base, bool bf16, uint64_t at, const bool (&in)[NV], Raw<VEC> (&r)[NV]) {
+  if (bf16) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) load_raw<VEC>(base, true, at + i * RT * VEC, r[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) load_raw<VEC>(base, false, at + i * RT * VEC, r[i]);
+  }
+}
+template <int VEC, int NV>
+__device__ __forceinline__ void row_f32(const Raw<VEC> (&r)[NV], bool bf16, float (&v)[NV][VEC]) {
+  if (bf16) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to_f32<VEC>(r[i], true, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to_f32<VEC>(r[i], false, v[i]);
+  }
+}
+
+template <int VEC, int NV, int RT>
+__device__ __forceinline__ void store_row(void* base, bool bf16, uint64_t at, const bool (&in)[NV], const float (&v)[NV][VEC]) {
+  if (bf16) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) store_f32<VEC>(base, true, at + i * RT * VEC, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in[i]) store_f32<VEC>(base, false, at + i * RT * VEC, v[i]);
+  }
+}
+
 // A norm's weights of a thread, ready to multiply with.
 template <int VEC, int NV, int RT>
 __device__ __forceinline__ void weights_of(const ovl_norm& n, const bool (&in)[NV], uint32_t c0, float (&w)[NV][VEC]) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) w[i][j] = 1.f;
-    if (n.kind == OVL_NORM_NONE || !n.weight || !in[i]) continue;
-    load_f32<VEC>(n.weight, n.w_dtype == OVL_BF16, c0 + i * RT * VEC, w[i]);
+  if (n.kind == OVL_NORM_NONE || !n.weight) return;
+  Raw<VEC> r[NV] = {};
+  load_row<VEC, NV, RT>(n.weight, n.w_dtype == OVL_BF16, c0, in, r);
+  row_f32<VEC, NV>(r, n.w_dtype == OVL_BF16, w);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) w[i][j] += n.offset;
-  }
+}
+// And its biases; none are zeros.
+template <int VEC, int NV, int RT>
+__device__ __forceinline__ void biases_of(const ovl_norm& n, const bool (&in)[NV], uint32_t c0, float (&b)[NV][VEC]) {
+  Raw<VEC> r[NV] = {};
+  if (n.kind != OVL_NORM_NONE && n.bias) load_row<VEC, NV, RT>(n.bias, n.w_dtype == OVL_BF16, c0, in, r);
+  row_f32<VEC, NV>(r, n.w_dtype == OVL_BF16, b);
 }
 
-// v becomes its norm, with the weights at hand.
-template <int VEC, int NV, int RT>
-__device__ __forceinline__ void normed_by(const ovl_norm& n, float (&v)[NV][VEC], const float (&w)[NV][VEC], const bool (&in)[NV],
+// v becomes its norm, with the weights at hand (KEEP: and the biases `b`).
+template <int VEC, int NV, int RT, bool KEEP>
+__device__ __forceinline__ void normed_by(const ovl_norm& n, float (&v)[NV][VEC], const float (&w)[NV][VEC],
+                                          const float (&b)[KEEP ? NV : 1][VEC], const bool (&in)[NV],
                                           float inv, uint32_t c0, float (*red)[32], int& turn) {
   if (n.kind == OVL_NORM_LAYER) {
     float s = 0.f;
@@ -220,23 +268,23 @@ __device__ __forceinline__ void normed_by(const ovl_norm& n, float (&v)[NV][VEC]
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[i][j] = v[i][j] * r * w[i][j];
-  if (n.bias) {
+    for (int j = 0; j < VEC; ++j) v[i][j] = KEEP ? fmaf(v[i][j] * r, w[i][j], b[KEEP ? i : 0][j]) : v[i][j] * r * w[i][j];
+  if (!KEEP && n.bias) {
+    Raw<VEC> raw[NV] = {};
+    float bias[NV][VEC];
+    load_row<VEC, NV, RT>(n.bias, n.w_dtype == OVL_BF16, c0, in, raw);
+    row_f32<VEC, NV>(raw, n.w_dtype == OVL_BF16, bias);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
-      float b[VEC];
-      load_f32<VEC>(n.bias, n.w_dtype == OVL_BF16, c0 + i * RT * VEC, b);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] += b[j];
-    }
+      for (int j = 0; j < VEC; ++j) v[i][j] += bias[i][j];
   }
 }
 
 // RT threads have a row of NV * VEC * RT channels at most; a block has THREADS / RT rows at a
 // time and goes on to others.  The weights stay in registers.  SLOTS > 0 (pieces of 16
 // bytes): that many rows, the one at work included, are under way in shared memory; else
-// the next one in registers.
+// the next one in registers, and types are looked at once a row and not XB, YB and HB.
 template <int VEC, int NV, int RT, int THREADS, int SLOTS, int BLOCKS, bool XB, bool YB, bool HB>
 __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -247,6 +295,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t hidden = a.norm.hidden, c0 = threadIdx.x % RT * VEC;
+  const bool xb = SLOTS > 0 ? XB : a.x.bf16, yb = SLOTS > 0 ? YB : a.y.bf16, hb = SLOTS > 0 ? HB : a.h.bf16;
   const float inv = 1.f / static_cast<float>(hidden);
   uint64_t token = static_cast<uint64_t>(blockIdx.x) * kRows + threadIdx.x / RT;
   const uint64_t step = static_cast<uint64_t>(gridDim.x) * kRows;
@@ -269,6 +318,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
   float wy[NV][VEC], wx[NV][VEC];
   weights_of<VEC, NV, RT>(a.norm.post, in, c0, wy);
   weights_of<VEC, NV, RT>(a.norm.pre, in, c0, wx);
+  constexpr bool kKeep = VEC * NV <= 10;                 // where registers are left: the biases too, and gates early
+  float by[kKeep ? NV : 1][VEC], bx[kKeep ? NV : 1][VEC];
+  if constexpr (kKeep) {
+    biases_of<VEC, NV, RT>(a.norm.post, in, c0, by);
+    biases_of<VEC, NV, RT>(a.norm.pre, in, c0, bx);
+  }
   [[maybe_unused]] Raw<VEC> xr[NV], yr[NV];             // SLOTS = 0: the next row
   [[maybe_unused]] auto load = [&](uint64_t t) {
     const uint64_t x0 = t * a.x.stride + c0, y0 = t * a.y.stride + c0;
@@ -276,10 +331,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) xr[i].w[j] = yr[i].w[j] = 0;
-      if (in[i] && t < a.n_tokens) {
-        load_raw<VEC>(xp, XB, x0 + i * RT * VEC, xr[i]);
-        if (yp) load_raw<VEC>(yp, YB, y0 + i * RT * VEC, yr[i]);
-      }
+    }
+    if (t < a.n_tokens) {
+      load_row<VEC, NV, RT>(xp, xb, x0, in, xr);
+      if (yp) load_row<VEC, NV, RT>(yp, yb, y0, in, yr);
     }
   };
   if constexpr (SLOTS == 0) load(token);
@@ -288,7 +343,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
     return a.gate.row ? static_cast<uint32_t>(a.gate.row[t]) : a.gate.n == 1 ? 0u : static_cast<uint32_t>(t);
   };
   uint32_t row_then = gate_of(token);
-  constexpr bool kGateEarly = VEC * NV <= 8;             // asked for before the first norm, where registers are left
   uint32_t slot = 0;
   int turn = 0;
   // as many rounds for every thread of the block
@@ -302,50 +356,34 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_block_norm(const __grid_con
       X::take(mine + slot * kSlot, c0, live ? hidden : 0, x);
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
     } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) to_f32<VEC>(xr[i], XB, x[i]), to_f32<VEC>(yr[i], YB, z[i]);
+      row_f32<VEC, NV>(xr, xb, x);
+      row_f32<VEC, NV>(yr, yb, z);
       load(token + step);
     }
     const uint32_t row = row_then;
     row_then = gate_of(token + step);
     const bool gated = live && yp && a.gate.rows.ptr && row < a.gate.n, joins = live && yp && (gated || !a.gate.rows.ptr);
-    [[maybe_unused]] Raw<VEC> gr[NV];
+    Raw<VEC> gr[NV] = {};
     const uint64_t g0 = row * a.gate.rows.stride + c0;
-    if constexpr (kGateEarly) {
+    if (kKeep && gated) load_row<VEC, NV, RT>(a.gate.rows.ptr, a.gate.rows.bf16, g0, in, gr);
+    if (yp && a.norm.post.kind != OVL_NORM_NONE) normed_by<VEC, NV, RT, kKeep>(a.norm.post, z, wy, by, in, inv, c0, red, turn);
+    if (gated) {
+      float g[NV][VEC];
+      if (!kKeep) load_row<VEC, NV, RT>(a.gate.rows.ptr, a.gate.rows.bf16, g0, in, gr);
+      row_f32<VEC, NV>(gr, a.gate.rows.bf16, g);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (gated && in[i]) load_raw<VEC>(a.gate.rows.ptr, a.gate.rows.bf16, g0 + i * RT * VEC, gr[i]);
-    }
-    if (yp && a.norm.post.kind != OVL_NORM_NONE) normed_by<VEC, NV, RT>(a.norm.post, z, wy, in, inv, c0, red, turn);
-    if (gated) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (!in[i]) continue;
-        float g[VEC];
-        if constexpr (kGateEarly) to_f32<VEC>(gr[i], a.gate.rows.bf16, g);
-        else load_f32<VEC>(a.gate.rows.ptr, a.gate.rows.bf16, g0 + i * RT * VEC, g);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) z[i][j] *= g[j];
-      }
+        for (int j = 0; j < VEC; ++j) z[i][j] = in[i] ? z[i][j] * g[i][j] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) x[i][j] = a.norm.alpha * x[i][j] + (joins ? a.norm.beta * z[i][j] : 0.f);
-    if (live && a.x_out.ptr) {
-      const uint64_t at = token * a.x_out.stride + c0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i]) store_f32<VEC>(a.x_out.ptr, XB, at + i * RT * VEC, x[i]);
-    }
+    if (live && a.x_out.ptr) store_row<VEC, NV, RT>(a.x_out.ptr, xb, token * a.x_out.stride + c0, in, x);
     if (!a.h.ptr) continue;
-    normed_by<VEC, NV, RT>(a.norm.pre, x, wx, in, inv, c0, red, turn);
-    if (live) {
-      const uint64_t at = token * a.h.stride + c0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i]) store_f32<VEC>(a.h.ptr, HB, at + i * RT * VEC, x[i]);
-    }
+    normed_by<VEC, NV, RT, kKeep>(a.norm.pre, x, wx, bx, in, inv, c0, red, turn);
+    if (live) store_row<VEC, NV, RT>(a.h.ptr, hb, token * a.h.stride + c0, in, x);
   }
   if constexpr (SLOTS > 0) cp_async_wait_all();
 }
@@ -431,6 +469,10 @@ cudaError_t norm_of(const NormArgs& a, cudaStream_t st) {
     default: return norm_as<VEC, NV, RT, THREADS, SLOTS, BLOCKS, true, true, true>(a, st);
   }
 }
+template <int NV, int RT, int THREADS, int BLOCKS>
+cudaError_t norm_odd(const NormArgs& a, cudaStream_t st) {
+  return norm_as<1, NV, RT, THREADS, 0, BLOCKS, false, false, false>(a, st);
+}
 template <int VEC, int NV, int RT, int BLOCKS>
 cudaError_t norm_any(const NormArgs& a, cudaStream_t st) {
   const uint32_t fit = sm_count() * BLOCKS;
@@ -460,21 +502,32 @@ cudaError_t launch_block_norm(const ovl_block_norm& norm, uint32_t n_tokens, Row
   const bool vec = norm.hidden % 8 == 0 && wide(x) && wide(y) && wide(x_out) && wide(h) && wide(gate.rows) &&
                    aligned16(norm.post.weight) && aligned16(norm.post.bias) && aligned16(norm.pre.weight) &&
                    aligned16(norm.pre.bias);
-  // 8 channels a piece where rows and widths allow it, 16 a thread; the threads of a row follow
-  // from the width.  8192 rows of 4096, x bf16, y fp32, both norms (336 MB): 64 us, 0.79 of
-  // the copy bandwidth; with 8 channels a thread and 512 threads 80, three blocks an SM
-  // (80 registers) 76, 32 channels and 128 threads 111, and 91 before types and row lengths were
-  // template arguments.  Element by element, 3001 rows of 1155 in fp32 with gates, layer
-  // norms and biases (56 MB): 19 us; its bound is the chain of four reductions a row.
+  // 8 channels a piece where rows and widths allow it, 16 a thread, so that the fewest warps
+  // share a row; one warp alone needs no barrier.  8192 rows of 4096, x bf16, y fp32, both norms
+  // (336 MB): 64 us, 0.79 of the copy bandwidth; with 8 channels a thread and 512 threads 80, three
+  // blocks an SM (80 registers) 76, 32 channels and 128 threads 111, and 91 before types and row
+  // lengths were template arguments.  20001 rows of 128 like these: a warp a row 9 us, two 22; 5001
+  // of 2048: four warps 21.6, eight 27.
+  // Element by element for other rows, 5 to 20 channels a thread and types looked at once a row: these
+  // are bound by instructions and by the exchanges of a row's sums.  fp32 rows with gates, layer
+  // norms and biases: 20001 of 299, a warp a row 19 us (eight warps 87); 3001 of 1155, four
+  // warps 12 (eight 15); 2003 of 4095, eight warps 37 (sixteen 67).
   if (vec) {
+    if (norm.hidden <= 256) return norm_of<8, 1, 32, 256, 3, 2>(a, st);
+    if (norm.hidden <= 512) return norm_of<8, 2, 32, 256, 3, 2>(a, st);
     if (norm.hidden <= 1024) return norm_of<8, 2, 64, 256, 3, 2>(a, st);
+    if (norm.hidden <= 2048) return norm_of<8, 2, 128, 256, 3, 2>(a, st);
     if (norm.hidden <= 4096) return norm_of<8, 2, 256, 256, 3, 2>(a, st);
     if (norm.hidden <= 8192) return norm_of<8, 2, 512, 512, 3, 1>(a, st);
     return norm_any<8, 4, 1024, 1>(a, st);
   }
-  if (norm.hidden <= 1280) return norm_of<1, 5, 256, 256, 0, 4>(a, st);
-  if (norm.hidden <= 2048) return norm_of<1, 8, 256, 256, 0, 3>(a, st);
-  if (norm.hidden <= 8192) return norm_of<1, 16, 512, 512, 0, 1>(a, st);
+  if (norm.hidden <= 160) return norm_odd<5, 32, 256, 3>(a, st);
+  if (norm.hidden <= 320) return norm_odd<10, 32, 128, 4>(a, st);
+  if (norm.hidden <= 640) return norm_odd<20, 32, 128, 3>(a, st);
+  if (norm.hidden <= 1280) return norm_odd<10, 128, 128, 4>(a, st);
+  if (norm.hidden <= 2048) return norm_odd<16, 128, 128, 4>(a, st);
+  if (norm.hidden <= 4096) return norm_odd<16, 256, 256, 2>(a, st);
+  if (norm.hidden <= 8192) return norm_odd<16, 512, 512, 1>(a, st);
   return norm_any<1, 32, 1024, 1>(a, st);
 }
 
