@@ -203,6 +203,25 @@ def test_norm_types_over_more_rows_than_fit_at_once(xd, yd, hd, hidden):
     assert torch.equal(one[0][0], xs[-1]) and torch.equal(one[1][0], h[-1])
 
 
+@pytest.mark.parametrize("xd", [F32, BF16])
+@pytest.mark.parametrize("hidden", [3, 100, 160, 161, 320, 333, 640, 641, 1283, 2049, 4099,           # element by element, but for 160, 320, 640
+                                    8, 128, 256, 264, 512, 520, 1032, 1536, 2048, 2056])
+def test_gated_rows_of_every_width(xd, hidden):
+    """Several rounds of rows, the last one not full; layer norms, biases and a gate for each of five sequences."""
+    tokens = 5003 if hidden < 700 else 1301
+    yd, wd = (BF16, F32) if xd == F32 else (F32, BF16)
+    x, y, gate = rand(1, tokens, hidden, dtype=xd), rand(2, tokens, hidden, dtype=yd), rand(3, 5, hidden, dtype=wd)
+    row = torch.randint(0, 5, (tokens,), generator=torch.Generator().manual_seed(4)).int().cuda()
+    pre = B.Norm("layer", rand(5, hidden, dtype=wd), rand(6, hidden, dtype=wd))
+    post = B.Norm("layer", rand(7, hidden, dtype=wd), rand(8, hidden, dtype=wd), 1e-3, 1.0)
+    n = B.BlockNorm(hidden, pre, post, alpha=0.5, beta=2.0)
+    xs, h = n(x, y, gate=gate, gate_row=row, dtype=xd)
+    check_norm(x, y, pre, post, gate, row, 0.5, 2.0, (xs, h), xd)
+    for t in (0, tokens - 1):                            # alone, the same bits
+        one = n(x[t:t + 1], y[t:t + 1], gate=gate, gate_row=row[t:t + 1], dtype=xd)
+        assert torch.equal(one[0][0], xs[t]) and torch.equal(one[1][0], h[t])
+
+
 @pytest.mark.parametrize("hidden", [256, 255, 12288])
 def test_gates_of_rows(hidden):
     """A row of -1 (or beyond the gates) leaves the block's output out, whatever it holds."""
