@@ -422,6 +422,31 @@ struct GluArgs {
   Rows gate, up, out;
 };
 
+// Rows that begin at odd addresses, element by element: a thread has PER of them, 256 apart,
+// with all loads under way before the first is looked at, and types looked at once for all.
+// bf16, 4095 rows of 14335 (352 MB): 86 us with 8, 94 with 4, 82 with 16, 239 with one; 3333 rows of
+// 333, fp32 to bf16: 2.7 with 2, 3.0 with 4, 3.4 with one.
+template <int PER, uint32_t ACT>
+__global__ void __launch_bounds__(256) k_glu_odd(const __grid_constant__ GluArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint64_t c = static_cast<uint64_t>(blockIdx.x) * (256 * PER) + threadIdx.x;
+  bool in[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) in[i] = c + i * 256 < a.width;
+  for (uint64_t t = blockIdx.y; t < a.n_tokens; t += gridDim.y) {
+    Raw<1> gr[PER] = {}, ur[PER] = {};
+    float g[PER][1], u[PER][1];
+    load_row<1, PER, 256>(a.gate.ptr, a.gate.bf16, t * a.gate.stride + c, in, gr);
+    load_row<1, PER, 256>(a.up.ptr, a.up.bf16, t * a.up.stride + c, in, ur);
+    row_f32<1, PER>(gr, a.gate.bf16, g);
+    row_f32<1, PER>(ur, a.up.bf16, u);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) g[i][0] = activated(g[i][0], ACT) * u[i][0];
+    store_row<1, PER, 256>(a.out.ptr, a.out.bf16, t * a.out.stride + c, in, g);
+  }
+}
+
 template <int VEC, uint32_t ACT>
 __global__ void __launch_bounds__(256) k_glu(const __grid_constant__ GluArgs a) {
   griddep_launch_dependents();
@@ -479,6 +504,16 @@ cudaError_t norm_any(const NormArgs& a, cudaStream_t st) {
   return launch_chained(k_block_norm_any<VEC, NV, RT, BLOCKS>, dim3(a.n_tokens < fit ? a.n_tokens : fit), RT, 0, st, a);
 }
 
+template <int PER>
+cudaError_t glu_odd(uint32_t act, const GluArgs& a, cudaStream_t st) {
+  const dim3 grid(static_cast<uint32_t>((a.width + 256 * PER - 1) / (256 * PER)), a.n_tokens < 65535 ? a.n_tokens : 65535);
+  switch (act) {
+    case OVL_ACT_SILU: return launch_chained(k_glu_odd<PER, OVL_ACT_SILU>, grid, 256, 0, st, a);
+    case OVL_ACT_GELU: return launch_chained(k_glu_odd<PER, OVL_ACT_GELU>, grid, 256, 0, st, a);
+    case OVL_ACT_GELU_TANH: return launch_chained(k_glu_odd<PER, OVL_ACT_GELU_TANH>, grid, 256, 0, st, a);
+    default: return launch_chained(k_glu_odd<PER, OVL_ACT_RELU>, grid, 256, 0, st, a);
+  }
+}
 template <int VEC>
 cudaError_t glu_as(uint32_t act, const GluArgs& a, cudaStream_t st) {
   const dim3 grid(static_cast<uint32_t>((a.width + 256 * VEC - 1) / (256 * VEC)), a.n_tokens < 65535 ? a.n_tokens : 65535);
@@ -538,7 +573,8 @@ cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gat
     a.n_tokens = 1;
   }
   const bool vec = a.width % 8 == 0 && wide(gate) && wide(up) && wide(out);
-  return vec ? glu_as<8>(act, a, st) : glu_as<1>(act, a, st);
+  if (vec) return glu_as<8>(act, a, st);
+  return a.width > 1024 ? glu_odd<8>(act, a, st) : glu_odd<2>(act, a, st);
 }
 
 }  // namespace ovl

@@ -8,8 +8,10 @@
 // integer as well, so that Taylor's series are needed for |angle| <= pi / 4 only, where
 // nine terms of both together end below 2e-9.
 // Bound by memory: each element is read once and written once.  8192 tokens of 40 heads of
-// 128 in bf16 (168 MB): 27 us, 0.92 of the copy bandwidth; 51 us while loads were converted one
+// 128 in bf16 (168 MB): 26 us, 0.96 of the copy bandwidth; 51 us while loads were converted one
 // by one, 33 while the frequencies were kernel arguments that each lane read at its own place.
+// Where halves or rows begin at odd places, pair by pair, it is bound by instructions: 37 us
+// for 34 channels of the same heads, 60 while places were divided and heads addressed in 64 bits.
 #include "block_internal.h"
 
 namespace ovl {
@@ -54,26 +56,44 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
   __syncthreads();
   griddep_wait();
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t slot = static_cast<uint32_t>(i % a.slots);
-  const uint64_t rest = i / a.slots;
-  const uint32_t chunk = static_cast<uint32_t>(rest % a.chunks);
-  const uint64_t token = rest / a.chunks;
+  uint32_t slot, chunk;
+  uint64_t token;
+  if (blockIdx.x < (1u << 24)) {                          // i < 2^32
+    const uint32_t rest = static_cast<uint32_t>(i) / a.slots;
+    slot = static_cast<uint32_t>(i) - rest * a.slots;
+    token = rest / a.chunks;
+    chunk = rest - static_cast<uint32_t>(token) * a.chunks;
+  } else {
+    const uint64_t rest = i / a.slots;
+    slot = static_cast<uint32_t>(i - rest * a.slots);
+    token = rest / a.chunks;
+    chunk = static_cast<uint32_t>(rest - token * a.chunks);
+  }
+  static_assert(kThreads == 256, "2^24 blocks");
   if (token >= a.n_tokens) return;
   const uint32_t first = slot * P, half = a.rope.rot_dim / 2;
   const bool turns = first < half, halves = a.rope.layout == OVL_ROPE_HALF;
   // channels c0 .. and c1 ..: both halves of the pairs, or 2 P consecutive channels
   const uint32_t c0 = turns && halves ? first : 2 * first, c1 = turns && halves ? half + first : c0 + P;
   const int64_t p = a.pos[token];
+  // where head 0 of the queries would begin, and of heads counted on into the keys
+  auto rows = [&](const Rows& q, const Rows& k, uint32_t size, uint64_t (&at)[2]) {
+    at[0] = reinterpret_cast<uint64_t>(q.ptr) + (token * q.stride + c0) * size;
+    at[1] = reinterpret_cast<uint64_t>(k.ptr) + (token * k.stride + c0 - static_cast<uint64_t>(a.q_heads) * a.rope.head_dim) * size;
+  };
+  constexpr uint32_t kIn = XB ? 2 : 4, kOut = OB ? 2 : 4;
+  const uint32_t apart = c1 - c0;
+  uint64_t in[2], out[2];
+  rows(a.q, a.k, kIn, in);
+  rows(a.q_out, a.k_out, kOut, out);
   Raw<P> ur[HT], vr[HT];
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     const uint32_t head = chunk * HT + h;
     if (head >= a.heads) break;
-    const bool is_k = head >= a.q_heads;
-    const Rows& in = is_k ? a.k : a.q;
-    const uint64_t at = token * in.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    load_raw<P>(in.ptr, XB, at + c0, ur[h]);
-    load_raw<P>(in.ptr, XB, at + c1, vr[h]);
+    const void* from = reinterpret_cast<const void*>((head < a.q_heads ? in[0] : in[1]) + static_cast<uint64_t>(head) * (a.rope.head_dim * kIn));
+    load_raw<P>(from, XB, 0, ur[h]);
+    load_raw<P>(from, XB, apart, vr[h]);
   }
   float cosine[P], sine[P];
   if (turns) {
@@ -110,11 +130,9 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeA
         for (int j = 0; j < P; ++j) u[j] = w[j], v[j] = w[P + j];
       }
     }
-    const bool is_k = head >= a.q_heads;
-    const Rows& out = is_k ? a.k_out : a.q_out;
-    const uint64_t at = token * out.stride + static_cast<uint64_t>(is_k ? head - a.q_heads : head) * a.rope.head_dim;
-    store_f32<P>(out.ptr, OB, at + c0, u);
-    store_f32<P>(out.ptr, OB, at + c1, v);
+    void* to = reinterpret_cast<void*>((head < a.q_heads ? out[0] : out[1]) + static_cast<uint64_t>(head) * (a.rope.head_dim * kOut));
+    store_f32<P>(to, OB, 0, u);
+    store_f32<P>(to, OB, apart, v);
   }
 }
 
@@ -165,11 +183,12 @@ cudaError_t launch_rope(const ovl_rope& rope, uint32_t n_tokens, const int32_t* 
   const bool vec = rope.rot_dim % 8 == 0 && rope.head_dim % 8 == 0 && wide(q) && wide(k) && wide(q_out) && wide(k_out);
   // One head a thread while that leaves the SMs room for more; four, which share the
   // sines, where there is work for all of them; eight of many heads (8192 tokens of 40 heads
-  // of 128: two 38, four 30, eight 27 us; of 12 heads of 96, four 8.4 and eight 9.1).
+  // of 128: two 38, four 30, eight 27 us; of 12 heads of 96, four 8.4 and eight 9.1; pair by pair
+  // 34 of 40 x 128 channels, four 55, eight and sixteen 51).
   const uint64_t singles = static_cast<uint64_t>(n_tokens) * a.heads * rope.head_dim / (vec ? 8 : 2);
   const bool few = singles <= static_cast<uint64_t>(sm_count()) * 2048;
   if (vec) return few ? launch_of<4, 1>(a, st) : a.heads >= 32 ? launch_of<4, 8>(a, st) : launch_of<4, 4>(a, st);
-  return few ? launch_of<1, 1>(a, st) : launch_of<1, 4>(a, st);
+  return few ? launch_of<1, 1>(a, st) : a.heads >= 32 ? launch_of<1, 8>(a, st) : launch_of<1, 4>(a, st);
 }
 
 cudaError_t launch_kv_positions(const KvDev& kv, const int32_t* seqs, const int32_t* off, uint32_t n, uint32_t n_tokens,

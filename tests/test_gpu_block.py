@@ -59,6 +59,19 @@ def test_rotations(layout, dim, rot, heads, kv, tokens, dtype, out):
         check_rope(layout, P.frequencies(rot, 500000.0), pos, src, have)
 
 
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F32, F32), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("dim,rot,heads,kv", [(80, 34, 30, 3), (80, 80, 35, 1), (66, 66, 9, 2), (64, 64, 5, 0)])
+def test_rotations_of_many_tokens(layout, dtype, out, dim, rot, heads, kv):
+    """Several heads a thread, the last of them not full; queries and keys in tensors of their own."""
+    rope, tokens = B.Rope(dim, rot, layout), 2503
+    pos = torch.randint(0, 1 << 17, (tokens,), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(dim))
+    x, k = rand(1, tokens, heads, dim, dtype=dtype), rand(2, tokens, kv, dim, dtype=dtype)
+    got = rope(pos, x, k if kv else None, dtype=out)
+    for have, src in zip(got if kv else (got,), (x, k)):
+        check_rope(layout, P.frequencies(rot, 10000.0), pos, src, have)
+
+
 @pytest.mark.parametrize("scaling,factor,original,magnitude", [
     ("linear", 4.0, 0, None), ("base", 8.0, 0, None), ("bands", 8.0, 8192, None), ("ramp", 16.0, 4096, None),
     ("ramp", 16.0, 4096, 1.0), (None, 1.0, 0, 0.25)])
@@ -292,6 +305,21 @@ def test_activations(act, tokens, width, dtype, out):
     # e^-v and erf to 2 ulp, of an argument that is off by up to 5 roundings of 2^-24 (a tenth of 100 at the most where
     # what follows is not below 2^-24 of v), a quotient to 2 ulp: 2^-20 of |v u|
     close(got, P.activated(g, act) * u, 2.0 ** -20 * (g * u).abs(), out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,width", [(70000, 3), (301, 1023), (301, 1025), (77, 5001)])
+def test_activations_of_odd_halves(dtype, tokens, width):
+    """Gate and up side by side at an odd width: rows begin at any address."""
+    both = rand(width, tokens, 2 * width, dtype=dtype)
+    gate, up = both[:, :width], both[:, width:]
+    back = torch.full((tokens, width + 2), 3.0, device="cuda", dtype=dtype)
+    B.glu(gate, up, act="gelu_tanh", out=back[:, :width])
+    g, u = gate.double(), up.double()
+    close(back[:, :width], P.activated(g, "gelu_tanh") * u, 2.0 ** -20 * (g * u).abs(), dtype)
+    assert (back[:, width:] == 3).all()
+    B.glu(gate, up, act="gelu_tanh", out=gate)           # in place
+    assert torch.equal(gate, back[:, :width])
 
 
 def test_activations_in_place_strided_and_of_large_values():
