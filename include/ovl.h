@@ -812,8 +812,8 @@ ovl_status ovl_moe_workspace_bytes(const ovl_moe* moe, size_t* out);
  * (NULL: not wanted; with a caller's choice they have to be).  Otherwise choice int32 and weight float32 [n_tokens][top_k] are
  * the caller's: an index outside 0 .. n_experts - 1 is no expert and adds nothing, an
  * expert listed twice adds twice.  x: device [n_tokens][hidden] of `dtype`, y the same
- * (it may be x with x's stride); 16-byte rows.  What is rounded: OVL_F32 x and the activations to three bf16 parts each
- * (2^-24 of each number); OVL_BF16 activations to two (2^-16).  Dot products are sums over
+ * (it may be x with x's stride); 16-byte rows.  What is rounded: OVL_F32 x, and the activations of
+ * either type's calls, to three bf16 parts each (2^-24 of each number).  Dot products are sums over
  * 32-weight blocks of exact products with the codes, in 32 bits, times the block's scale;
  * activations below 2^-20 of the square of their token's largest |x| keep fewer bits.  A
  * token with a NaN or an infinity gives outputs that mean nothing, the others are not touched.

@@ -21,9 +21,12 @@
 // instructions a 1024 weights, half of the issue slots, waits for fixed latencies between
 // them.
 //
-// Inputs are bf16 parts (one: bf16 tokens; two: activations of bf16 calls; three: all 24
-// bits of fp32) in the order of the fragments: lane t of a quad takes 8 consecutive
-// channels of a block in one load, stored as the pairs in which a word's codes unpack.  A
+// Inputs are bf16 parts (one: bf16 tokens; three: all 24 bits of fp32 tokens, and of the
+// activations of either call) in the order of the fragments: lane t of a quad takes 8
+// consecutive channels of a block in one load, stored as the pairs in which a word's codes
+// unpack.  Activations of bf16 calls in two parts, 2^-17 of each, took 100 us instead of 111
+// over 64 tokens and 69 instead of 76 over 19, and no less over one; but outputs that cancel
+// showed it, and one bf16 output in 700 was rounded otherwise for it.  A
 // unit of so few tokens that all their parts find room in the 8 columns has the parts
 // beside one another, added up at the end (one fp32 token: a third of the MMAs and loads).
 #pragma once
@@ -101,10 +104,12 @@ __device__ __forceinline__ void load_rows(uint32_t (&w)[4], uint32_t address) {
 //   4 bits: pair 0 is codes 0 and 4, pair 1 16 times codes 1 and 5, and so on: the inputs
 //   of odd channels are stored a 16th as large.
 //   8 bits: code + 128; pairs 0 and 1 of a word.
-// What the codes are too large by (8 and 128) is, in bf16 calls, a product with the same
-// constant in every place, from which the MMAs of the block start.  In fp32 calls it is
-// subtracted from every code: the sums then are no larger than they have to be, which their
-// 24 bits are needed for, and three parts would be six more MMAs a block.
+// What the codes are too large by (8 and 128) is, for inputs in one part, a product with the
+// same constant in every place, from which the MMAs of the block start: an MMA then cuts its
+// sums as for codes of 128, 4 bits more than 4-bit codes need, which bf16 inputs have to
+// spare (signed codes gave outputs no nearer to the plain form's, and took 4 % longer).  For
+// three parts it is subtracted from every code: the sums then are no larger than they have to
+// be, which their 24 bits are needed for, and three parts would be six more MMAs a block.
 constexpr int kCodeExponent = 133;
 __device__ __forceinline__ void pairs_of_4(uint32_t w, uint32_t (&p)[4]) {
   const uint32_t h = w >> 8;
@@ -141,12 +146,12 @@ constexpr int kTokenExponent = 100;
 constexpr int kActExponent = 50;
 
 // v as bf16 parts: the upper bits cut off, exactly, so that three parts are all 24 bits.
-// The last of two is rounded to nearest instead.
+// One part is for values that are bf16 as they are.
 template <int PARTS>
 __device__ __forceinline__ void parts_of(float v, uint16_t (&p)[PARTS]) {
 #pragma unroll
   for (int i = 0; i < PARTS; ++i) {
-    if (PARTS < 3 && i == PARTS - 1) {
+    if (PARTS == 1) {
       p[i] = static_cast<uint16_t>(two_bf16(v, v));
       break;
     }
@@ -603,7 +608,7 @@ struct Rows32 {
 #pragma unroll
           for (int e = 0; e < 2; ++e) out[h * 16 + e * 8] = weight * (acc[h][2 * e + j] * back * up * up);
       } else {
-        constexpr int kParts = PARTS == 1 ? 2 : 3;
+        constexpr int kParts = 3;                // of the second product's input
         constexpr float back = pow2(kCodeExponent - kTokenExponent), scaled = pow2(kActExponent);
         const float down = 1.f / up;             // a power of two
 #pragma unroll
@@ -753,7 +758,7 @@ cudaError_t launch_rows(const MoeDev& m, cudaStream_t st) {
 template <uint32_t Q>
 cudaError_t launch_products(const MoeDev& m, cudaStream_t st) {
   cudaError_t e = m.bf16 ? launch_rows<Q, false, 1>(m, st) : launch_rows<Q, false, 3>(m, st);
-  if (e == cudaSuccess) e = m.bf16 ? launch_rows<Q, true, 2>(m, st) : launch_rows<Q, true, 3>(m, st);
+  if (e == cudaSuccess) e = launch_rows<Q, true, 3>(m, st);
   return e;
 }
 

@@ -276,3 +276,31 @@ def test_what_the_torch_side_refuses():
     for n, kw in ((4, dict(router=rand(1, 4, 32))), (4, dict(bias=rand(1, 5))), (3, {}), (4, dict(score="top")), (4, dict(act="no"))):
         with pytest.raises(ValueError):
             B.Moe(O.Q4_0, n, 64, 64, *planes, top_k=2, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 3, 11])
+def test_activations_keep_their_bits_between_the_products(dtype, tokens):
+    """Outputs that are the difference of two activations, of up to 19 bits each: what is cut off them shows in full.
+
+    x is one channel, so that g = 1 and u = 127 d x come out of their products exactly but for a rounding or two, and a
+    down row has the codes 127 and -127 (the 7 bits that an MMA holds).  Three parts are all 24 bits of an activation;
+    six MMAs cut their sums at 2^-23 of the larger product and a handful of steps round by 2^-24: below 2^-20 of both."""
+    rng = np.random.default_rng(tokens)
+    hidden, ffn = 256, 256
+    gate, up = np.zeros((ffn, hidden), np.int8), np.zeros((ffn, hidden), np.int8)
+    gate[:, 0], up[:, 0] = 64, 127
+    gd = np.full((ffn, hidden // 32), 1 / 64, np.float16)
+    ud = np.broadcast_to((1 + rng.integers(0, 1024, (ffn, 1)) / 1024).astype(np.float16), gd.shape)
+    down, one, two = np.zeros((hidden, ffn), np.int8), np.arange(hidden), (np.arange(hidden) + rng.integers(1, ffn, hidden)) % ffn
+    down[one, one], down[one, two] = 127, -127
+    dd = np.full((hidden, ffn // 32), 1 / 128, np.float16)
+    planes = [tuple(torch.from_numpy(np.ascontiguousarray(p)).cuda() for p in pl) for pl in ((gate, gd), (up, ud), (down, dd))]
+    moe = B.Moe(O.Q8_0, 1, hidden, ffn, *planes, top_k=1, act="relu")
+    x = torch.zeros((tokens, hidden))
+    x[:, 0] = 1 + torch.arange(tokens) / 128                 # bf16 values
+    y = moe(x.to(dtype).cuda(), torch.zeros((tokens, 1), dtype=torch.int32, device="cuda"), torch.ones((tokens, 1), device="cuda"))
+    h = x[:, :1].double() ** 2 * 127 * torch.from_numpy(ud[:, 0].astype(np.float64))
+    a, b = h[:, one] * 127 / 128, h[:, two] * 127 / 128
+    off = (y.double().cpu() - (a - b)).abs()
+    assert (off <= 2.0 ** -20 * (a + b) + P.HALF[dtype] * (a - b).abs() * 1.001).all(), float((off / (a + b)).max() * 2 ** 20)
