@@ -26,7 +26,7 @@
 // consecutive channels of a block in one load, stored as the pairs in which a word's codes
 // unpack.  Activations of bf16 calls in two parts, 2^-17 of each, took 100 us instead of 111
 // over 64 tokens and 69 instead of 76 over 19, and no less over one; but outputs that cancel
-// showed it, and one bf16 output in 700 was rounded otherwise for it.  A
+// showed it, and one output in about 1500 was rounded otherwise for it.  A
 // unit of so few tokens that all their parts find room in the 8 columns has the parts
 // beside one another, added up at the end (one fp32 token: a third of the MMAs and loads).
 #pragma once
