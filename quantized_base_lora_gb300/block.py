@@ -35,6 +35,7 @@ _ACT = {"silu": OVL_ACT_SILU, "gelu": OVL_ACT_GELU, "gelu_tanh": OVL_ACT_GELU_TA
 _SCORE = {"softmax": OVL_MOE_SOFTMAX, "sigmoid": OVL_MOE_SIGMOID}
 _MOST = (1 << 31) - 1
 _packed = lib.ovl_packed
+_address = ctypes.addressof
 _FLAT = torch.contiguous_format
 
 
@@ -121,7 +122,6 @@ class Rope:
         _check(lib.ovl_rope_plan(head_dim, rot_dim, _named(_LAYOUT, "layout", layout), base, kind, factor, original,
                                  turns[0] if low is None else low, turns[1] if high is None else high,
                                  0.0 if magnitude is None else magnitude, ctypes.byref(self.plan)))
-        self._at = ctypes.addressof(self.plan)
 
     def _heads(self, name: str, t: torch.Tensor, index: int):
         """(address, tokens, heads, dtype code, stride) of [tokens][heads][head_dim]."""
@@ -171,8 +171,9 @@ class Rope:
             raise ValueError("k_out without k")
         if n > _MOST:
             raise ValueError("too many tokens")
-        _call(index, OVL_PACKED_ROPE, _words15(self._at, n, _ints("pos", pos, (n,), index), qp, qh, qs, kp, kh, ks,
-                                               code, qop, qos, kop, kos, out_code))
+        # the plan's address is taken here: a copy of this object has a plan of its own
+        _call(index, OVL_PACKED_ROPE, _words15(_address(self.plan), n, _ints("pos", pos, (n,), index), qp, qh, qs, kp, kh,
+                                               ks, code, qop, qos, kop, kos, out_code))
         return q_out if k is None else (q_out, k_out)
 
 

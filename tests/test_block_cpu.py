@@ -294,3 +294,28 @@ def test_torch_side_refuses_what_is_not_on_a_device(q):
     with pytest.raises(q.OvlError):
         B.Rope(63)
     assert ctypes.sizeof(q.ovl_rope) == 16 + 8 * 256
+
+
+# ---------------------------------------------------------------- what the torch side keeps
+
+def test_a_copied_or_pickled_rope_has_a_plan_of_its_own(q, monkeypatch):
+    """The plan that a call hands to the library is the object's own, also after the one it was copied from is gone."""
+    import copy
+    import pickle
+    import struct
+
+    from quantized_base_lora_gb300 import block as B
+    seen = []
+    monkeypatch.setattr(B, "_call", lambda index, which, words: seen.append(struct.unpack("=15Q", words)[0]))
+    monkeypatch.setattr(B, "_index_of", lambda name, t: t.get_device())
+    monkeypatch.setattr(B, "_ints", lambda name, t, shape, index: t.data_ptr())
+    pos, x = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 1, 64))
+    rope = B.Rope(64, 48, base=500000.0)
+    want = bytes(rope.plan)
+    for made in (rope, copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+        made(pos, x)
+        assert seen.pop() == ctypes.addressof(made.plan) and bytes(made.plan) == want
+    far = copy.deepcopy(rope)
+    del rope, made
+    far(pos, x)
+    assert bytes((ctypes.c_char * len(want)).from_address(seen.pop())) == want
