@@ -818,7 +818,8 @@ ovl_status ovl_moe_workspace_bytes(const ovl_moe* moe, size_t* out);
  * activations below 2^-20 of the square of their token's largest |x| keep fewer bits.  A
  * token with a NaN or an infinity gives outputs that mean nothing, the others are not touched.
  * The result depends on the call's inputs alone: the same call gives the same bits.
- * Calls on one workspace must be stream-ordered.  No counterpart in the source pages. */
+ * Calls on one workspace must be stream-ordered; those that were not have outputs that mean
+ * nothing, and later ones are right again.  No counterpart in the source pages. */
 ovl_status ovl_moe_forward(const ovl_moe* moe, const void* x, uint32_t dtype, uint32_t n_tokens, uint64_t x_stride,
                            const int32_t* choice, const float* weight, int32_t* choice_out, float* weight_out, void* y,
                            uint64_t y_stride, void* stream);

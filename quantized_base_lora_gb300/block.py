@@ -9,7 +9,8 @@ PyTorch provides device memory and streams only; all computation is libovl's.
     a = glu(gate, up, dtype=torch.bfloat16)
     y = moe(h)                                         # Moe(...): router, chosen experts, weighted sum
 
-Calls go to the current stream of the tensors' device, whichever device is current.  Tensors are float32 or
+Calls go to the current stream of the tensors' device, whichever device is current; those of one Moe must be
+ordered by streams or events, since they share its workspace.  Tensors are float32 or
 bfloat16 with contiguous channels; tokens may have any stride.  Nothing is differentiated."""
 from __future__ import annotations
 
@@ -303,7 +304,10 @@ class Moe:
     gate, up: (qs, d) of [n_experts * ffn] rows of hidden weights, down: of [n_experts * hidden] rows of ffn weights, in
     the base's layout of `quant`: qs int8 or uint8 and d float16 (q4_K: uint8) tensors, contiguous, of any shape with
     the right number of bytes.  They must not be written while calls that read them are in flight.  router
-    [n_experts][hidden], bias float32 [n_experts]; without a router every call brings its choice."""
+    [n_experts][hidden], bias float32 [n_experts]; without a router every call brings its choice.
+
+    Calls on one layer must be ordered by streams or events, replays of graphs that hold them included, since they
+    share its workspace; layers of their own may run beside one another."""
 
     def __init__(self, quant: int, n_experts: int, hidden: int, ffn: int, gate, up, down, top_k: int,
                  router: torch.Tensor | None = None, bias: torch.Tensor | None = None, score: str = "softmax",

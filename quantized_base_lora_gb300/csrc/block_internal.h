@@ -135,6 +135,8 @@ cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gat
 
 // A mixture-of-experts call as its kernels take it.
 constexpr uint32_t kMoeTokens = 8;       // tokens of one expert that one pass over its weights serves
+constexpr uint32_t kMoeRouted = 8;       // tokens of a router CTA
+constexpr uint32_t kMoeGroups = (OVL_MOE_MAX_TOKENS + kMoeRouted - 1) / kMoeRouted;
 constexpr uint32_t kMoeMaxPairs = OVL_MOE_MAX_TOKENS * OVL_MOE_MAX_TOP;
 constexpr uint32_t kMoeMaxUnits = OVL_MOE_MAX_EXPERTS + kMoeMaxPairs / kMoeTokens;
 // Up to kMoeTokens pairs of one expert, in 41 bits.
@@ -169,7 +171,7 @@ struct MoeDev {
   int32_t* choice_out;
   float* weight_out;
   // workspace
-  uint32_t* arrived;       // router CTAs of each group of 8 tokens: 0 between calls
+  uint32_t* arrived;       // [kMoeGroups]: router CTAs of each group of 8 tokens; 0 between calls
   float* logits;           // [tokens][experts]
   int32_t* choice;         // [tokens][top] (the caller's stay where they are)
   float* weight;

@@ -3,7 +3,9 @@
 //
 // Scores are plain fp32 dot products: a CTA has 8 experts and up to 8 tokens, two warps an
 // expert.  The last CTA of 8 tokens chooses their experts, a warp a token.  Beside that,
-// further CTAs split the tokens into scaled bf16 parts.
+// further CTAs split the tokens into scaled bf16 parts.  The counters by which the last CTA
+// is known are set back by the first product of the same call, whatever they hold: calls
+// that ran beside one another against the rules leave nothing behind for later ones.
 #include <type_traits>
 
 #include "moe_rows.cuh"
@@ -13,7 +15,7 @@ namespace {
 
 using namespace moe;
 constexpr uint32_t kThreads = 512;
-constexpr int kGroup = 8;                // tokens of a router CTA, and its experts
+constexpr int kGroup = kMoeRouted;       // tokens of a router CTA, and its experts
 
 // Order-preserving bits of a score; NaN is the least.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -219,7 +221,6 @@ __global__ void __launch_bounds__(kThreads) k_moe_route(const __grid_constant__ 
     if (m.experts <= 128) choose<4>(m, t0 + warp);
     else choose<OVL_MOE_MAX_EXPERTS / 32>(m, t0 + warp);
   }
-  if (wide > 1 && threadIdx.x == 0) m.arrived[group] = 0;
 }
 
 // y of a token: its experts' weighted outputs, in the order of the choice.

@@ -180,7 +180,9 @@ __device__ __forceinline__ void sort_pairs(const MoeDev& m, uint8_t* smem, uint3
   const int32_t* choice = m.given ? m.given_choice : m.choice;
   if (m.tokens == 1 && !m.given) {                        // distinct experts with one pair each
     if (threadIdx.x < m.top) {
-      units[threadIdx.x] = MoeUnit::make(choice[threadIdx.x], 1, threadIdx.x, 1, threadIdx.x);
+      // the router's own, and an expert in any case: a workspace that calls raced on may hold anything
+      const uint32_t expert = min(static_cast<uint32_t>(choice[threadIdx.x]), m.experts - 1);
+      units[threadIdx.x] = MoeUnit::make(expert, 1, threadIdx.x, 1, threadIdx.x);
       order[threadIdx.x] = static_cast<uint16_t>(threadIdx.x);       // place threadIdx.x of token 0
     }
     if (threadIdx.x < 2) range[threadIdx.x] = share(m.top * tiles, blockIdx.x + threadIdx.x);
@@ -637,6 +639,7 @@ __global__ void __launch_bounds__(kWarps<Q, PARTS> * 32, 1) k_moe_rows(const __g
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x < kMoeGroups) m.arrived[threadIdx.x] = 0;     // the next call's routers wait for this one's end
   }
   sort_pairs<Q, PARTS>(m, smem, op.tiles, range);
   const uint16_t* order = reinterpret_cast<const uint16_t*>(smem + Shape<Q, PARTS>::kOrder);

@@ -58,6 +58,7 @@ struct MoeLayout {
   uint64_t logits, choice, weight, power, xp, hp, part, total;
 };
 constexpr uint32_t kMoeHead = 256;               // counters of arrivals
+static_assert(4 * kMoeGroups <= kMoeHead, "a word for each group of tokens");
 
 ovl_status check_moe_dims(const ovl_moe* m) {
   if (!m) return fail(OVL_E_ARG, "moe is null");

@@ -304,3 +304,21 @@ def test_activations_keep_their_bits_between_the_products(dtype, tokens):
     a, b = h[:, one] * 127 / 128, h[:, two] * 127 / 128
     off = (y.double().cpu() - (a - b)).abs()
     assert (off <= 2.0 ** -20 * (a + b) + P.HALF[dtype] * (a - b).abs() * 1.001).all(), float((off / (a + b)).max() * 2 ** 20)
+
+
+def test_a_workspace_that_calls_raced_on_is_right_again_for_the_next():
+    """Counters as overlapping calls leave them, and choices of no expert: the next call clears the counters, whatever
+    it answers itself (here no CTA finds itself the last, so nothing is chosen), and the one after it is as ever."""
+    L = Layer(O.Q4_0, 40, 128, 64, 3, max_tokens=16)         # five router CTAs of 8 experts for each 8 tokens
+    words = L.moe.workspace.view(torch.int32)
+    choice = 64 + 16 * 40                                    # behind the counters and the logits
+    for tokens in (11, 1):
+        x, other = rand(tokens, tokens, 128, dtype=BF16), rand(9, tokens, 128, dtype=BF16)
+        want = L.moe(other, routing=True)
+        assert torch.equal(words[choice:choice + 3 * tokens].view(tokens, 3), want[1])
+        words[:16] = 1000
+        words[choice:choice + 3 * tokens] = torch.tensor([-5, 40, 1 << 30], dtype=torch.int32, device="cuda").repeat(tokens)
+        L.moe(x)
+        assert (words[:16] == 0).all()
+        for a, b in zip(L.moe(other, routing=True), want):
+            assert torch.equal(a, b)
