@@ -188,12 +188,14 @@ class Norm(NamedTuple):
 
 
 class BlockNorm:
-    """x' = alpha x + beta gate * post(y), h = pre(x'): the end of one block and the beginning of the next."""
+    """x' = alpha x + beta gate * post(y), h = pre(x'): the end of one block and the beginning of the next.  Weights and
+    biases are used where they lie at construction: writes into them count, another storage (`w.data = ...`, as
+    Module.to sets it) does not."""
 
     def __init__(self, hidden: int, pre: Norm | None, post: Norm | None = None, alpha: float = 1.0, beta: float = 1.0):
         if not 0 <= hidden <= _MOST:
             raise ValueError(f"hidden {hidden} is out of range")
-        self.hidden, self.pre, self.post, self._index = hidden, pre, post, None
+        self.hidden, self.pre, self.post, self._index, self._held = hidden, pre, post, None, []
         self.plan = ovl_block_norm(hidden, alpha, beta, self._norm("post", post), self._norm("pre", pre))
         self._at = ctypes.addressof(self.plan)
 
@@ -213,6 +215,7 @@ class BlockNorm:
                 raise ValueError(f"{name}.{what} must be contiguous float32 or bfloat16 [{self.hidden}]")
             code = _DTYPE[t.dtype]
             at.append(t.data_ptr())
+            self._held.append(t.detach())                # the storage, whatever becomes of the tensor's
         if n.weight is not None and n.bias is not None and n.weight.dtype != n.bias.dtype:
             raise ValueError(f"weight and bias of {name} must have one type")
         return ovl_norm(_named(_NORM, "kind", n.kind), code, at[0], at[1], n.eps, n.offset)
@@ -304,7 +307,8 @@ class Moe:
     gate, up: (qs, d) of [n_experts * ffn] rows of hidden weights, down: of [n_experts * hidden] rows of ffn weights, in
     the base's layout of `quant`: qs int8 or uint8 and d float16 (q4_K: uint8) tensors, contiguous, of any shape with
     the right number of bytes.  They must not be written while calls that read them are in flight.  router
-    [n_experts][hidden], bias float32 [n_experts]; without a router every call brings its choice.
+    [n_experts][hidden], bias float32 [n_experts]; without a router every call brings its choice.  All are used where
+    they lie at construction, as BlockNorm's weights are.
 
     Calls on one layer must be ordered by streams or events, replays of graphs that hold them included, since they
     share its workspace; layers of their own may run beside one another."""
@@ -339,7 +343,9 @@ class Moe:
                     or bias.dtype != torch.float32:
                 raise ValueError(f"bias must be contiguous float32 [{n_experts}]")
             self.moe.bias = bias.data_ptr()
-        self._held = (gate, up, down, router, bias)
+        # the storages, whatever becomes of the tensors'
+        self._held = (*((p[0].detach(), p[1].detach()) for p in (gate, up, down)),
+                      *(None if t is None else t.detach() for t in (router, bias)))
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.moe.workspace, self.moe.workspace_bytes = self.workspace.data_ptr(), nbytes
         self._at = ctypes.addressof(self.moe)

@@ -319,3 +319,30 @@ def test_a_copied_or_pickled_rope_has_a_plan_of_its_own(q, monkeypatch):
     del rope, made
     far(pos, x)
     assert bytes((ctypes.c_char * len(want)).from_address(seen.pop())) == want
+
+
+def test_weights_whose_storage_is_swapped_stay_alive(q, monkeypatch):
+    """`parameter.data = other`, as Module.to does it, frees a storage that no one else holds: the addresses that the
+    library reads have to be of tensors that the operator keeps."""
+    from quantized_base_lora_gb300 import block as B
+    monkeypatch.setattr(B, "_index_of", lambda name, t: t.get_device())
+
+    def pointers(held):
+        for h in held:
+            yield from pointers(h) if isinstance(h, tuple) else () if h is None else (h.data_ptr(),)
+
+    def swap(tensors):
+        for t in tensors:
+            t.data = torch.zeros_like(t)
+
+    w = [torch.nn.Parameter(torch.ones(8)) for _ in range(4)]
+    n = B.BlockNorm(8, B.Norm("rms", w[0], w[1]), B.Norm("layer", w[2], w[3]))
+    swap(w)
+    assert {n.plan.pre.weight, n.plan.pre.bias, n.plan.post.weight, n.plan.post.bias} <= set(pointers(n._held))
+    assert all(torch.equal(t, torch.ones(8)) for t in n._held)
+    planes = [(torch.zeros((64, 32), dtype=torch.int8), torch.zeros((64, 1), dtype=torch.float16)) for _ in range(3)]
+    router, bias = torch.nn.Parameter(torch.ones((2, 32))), torch.nn.Parameter(torch.ones(2))
+    m = B.Moe(q.OVL_Q8_0, 2, 32, 32, *planes, top_k=1, router=router, bias=bias)
+    at = {getattr(m.moe, f) for f in ("gate_qs", "gate_d", "up_qs", "up_d", "down_qs", "down_d", "router", "bias")}
+    swap([router, bias] + [t for pair in planes for t in pair])
+    assert len(at) == 8 and at <= set(pointers(m._held))
