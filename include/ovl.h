@@ -461,6 +461,13 @@ ovl_status ovl_get_state(ovl_ctx* ctx, ovl_state* out);
  * adapter digests and scales). */
 ovl_status ovl_get_entry(ovl_ctx* ctx, uint32_t i, ovl_entry* out);
 
+/* How often the active composition's entries name the given tensors: *out = the sum, over the
+ * entries, of those of tensors[0 .. n-1] (host array) that the entry targets.  0: the forward
+ * of each is the base's alone, and its planes may be used as they lie.  Errors: OVL_E_ARG
+ * (null pointer, tensor index), OVL_E_STATE (no base).  ([MODELD] §"Observability": which
+ * adapters are attached.) */
+ovl_status ovl_count_overlays(ovl_ctx* ctx, uint32_t n, const uint32_t* tensors, uint32_t* out);
+
 /* Synchronize `stream`, read and clear the device status word.  Returns OVL_OK,
  * OVL_E_DEVICE_TIMEOUT (a bounded device wait ran out; outputs of that launch are
  * invalid) or OVL_E_CUDA.  (The pages define no counterpart: it reports the
@@ -785,7 +792,7 @@ enum { OVL_MOE_MAX_TOKENS = 128, OVL_MOE_MAX_EXPERTS = 512, OVL_MOE_MAX_TOP = 16
  * hidden and ffn: multiples of 32 (of 256 for OVL_Q4_K) up to OVL_MOE_MAX_HIDDEN.  The
  * planes are like the base: not written while calls that read them are in flight (copies
  * of them start before the kernel in front has ended).  Overlays are not applied to
- * experts. */
+ * experts: where the planes are tensors of a base, ovl_count_overlays says whether any is active. */
 typedef struct {
   uint32_t quant, n_experts, top_k, hidden, ffn, act;
   uint32_t score, renormalize;     /* OVL_MOE_SOFTMAX or _SIGMOID; weights of a token divided by their sum */

@@ -160,6 +160,7 @@ def _load():
         "ovl_base_digest": ([P, B32, P], I32),
         "ovl_get_state": ([P, C.POINTER(ovl_state)], I32),
         "ovl_get_entry": ([P, U32, C.POINTER(ovl_entry)], I32),
+        "ovl_count_overlays": ([P, U32, C.POINTER(U32), C.POINTER(U32)], I32),
         "ovl_check_device": ([P, P], I32),
         "ovl_debug_inject": ([P, U32, I32], I32),
         "ovl_last_error": ([P], C.c_char_p),
@@ -201,7 +202,7 @@ def _load():
 lib = _load()
 EXPORTED = ("ovl_create", "ovl_destroy", "ovl_load_base", "ovl_stage_adapter", "ovl_stage_sparse", "ovl_unstage_adapter",
             "ovl_activate", "ovl_rollback", "ovl_linear_forward", "ovl_linear_forward_multi", "ovl_materialize_layer",
-            "ovl_segmented_forward", "ovl_base_digest", "ovl_get_state", "ovl_get_entry",
+            "ovl_segmented_forward", "ovl_base_digest", "ovl_get_state", "ovl_get_entry", "ovl_count_overlays",
             "ovl_check_device", "ovl_debug_inject", "ovl_last_error", "ovl_sha256",
             "ovl_content_digest", "ovl_version", "ovl_dualpath_forward_noalloc", "ovl_stage_activations",
             "ovl_manifest_parse", "ovl_activate_manifest", "ovl_kv_workspace_bytes", "ovl_kv_init", "ovl_kv_extend",
@@ -376,6 +377,12 @@ def ovl_get_entry(ctx, i: int):
     st = lib.ovl_get_entry(ctx, int(i), C.byref(e))
     return st, {"handle": e.handle, "adapter_key": bytes(e.adapter_key), "scale": e.scale,
                 "total_rank": e.total_rank}
+
+
+def ovl_count_overlays(ctx, tensors):
+    ids, out = (C.c_uint32 * max(1, len(tensors)))(*tensors), C.c_uint32(0)
+    st = lib.ovl_count_overlays(ctx, len(tensors), ids, C.byref(out))
+    return st, int(out.value)
 
 
 def ovl_check_device(ctx, stream: int = 0) -> int:

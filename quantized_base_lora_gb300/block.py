@@ -20,11 +20,11 @@ from typing import NamedTuple
 
 import torch
 
-from . import (OVL_ACT_GELU, OVL_ACT_GELU_TANH, OVL_ACT_RELU, OVL_ACT_SILU, OVL_F32, OVL_MOE_SIGMOID, OVL_MOE_SOFTMAX,
-               OVL_NORM_LAYER, OVL_NORM_NONE, OVL_NORM_RMS, OVL_OK, OVL_PACKED_BLOCK_NORM, OVL_PACKED_GLU,
+from . import (OVL_ACT_GELU, OVL_ACT_GELU_TANH, OVL_ACT_RELU, OVL_ACT_SILU, OVL_E_STATE, OVL_F32, OVL_MOE_SIGMOID,
+               OVL_MOE_SOFTMAX, OVL_NORM_LAYER, OVL_NORM_NONE, OVL_NORM_RMS, OVL_OK, OVL_PACKED_BLOCK_NORM, OVL_PACKED_GLU,
                OVL_PACKED_MOE, OVL_PACKED_ROPE, OVL_Q8_0, OVL_ROPE_BANDS, OVL_ROPE_BASE, OVL_ROPE_HALF,
-               OVL_ROPE_LINEAR, OVL_ROPE_PAIRS, OVL_ROPE_PLAIN, OVL_ROPE_RAMP, OvlError, lib, ovl_block_norm,
-               ovl_last_error, ovl_moe, ovl_moe_workspace_bytes, ovl_norm, ovl_rope)
+               OVL_ROPE_LINEAR, OVL_ROPE_PAIRS, OVL_ROPE_PLAIN, OVL_ROPE_RAMP, OvlError, check, lib,
+               ovl_block_norm, ovl_count_overlays, ovl_last_error, ovl_moe, ovl_moe_workspace_bytes, ovl_norm, ovl_rope)
 from .kvcache import _DTYPE, _current_device, _raw_stream
 
 _LAYOUT = {"half": OVL_ROPE_HALF, "pairs": OVL_ROPE_PAIRS}
@@ -301,6 +301,15 @@ def glu(gate: torch.Tensor, up: torch.Tensor, act: str = "silu", dtype: torch.dt
     return out
 
 
+def _refuse_overlays(runtime, tensors):
+    if runtime.ctx:                                      # closed: no composition, and the base's planes are kept
+        st, n = ovl_count_overlays(runtime.ctx, tensors)
+        check(st, runtime.ctx)
+        if n:
+            raise OvlError(OVL_E_STATE, f"the active composition overlays an expert tensor (of {tensors}), and overlays "
+                                        "are not applied to experts")
+
+
 class Moe:
     """A mixture-of-experts layer over quantized experts, for up to max_tokens (at most 128) tokens a call.
 
@@ -349,11 +358,13 @@ class Moe:
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.moe.workspace, self.moe.workspace_bytes = self.workspace.data_ptr(), nbytes
         self._at = ctypes.addressof(self.moe)
+        self._runtime = self._tensors = None
 
     @classmethod
     def from_base(cls, runtime, gate: int, up: int, down: int, n_experts: int, top_k: int, **more) -> "Moe":
         """Experts that are tensors of a loaded base: gate and up have n_experts * ffn rows of hidden weights, down
-        n_experts * hidden rows of ffn weights.  The active composition's overlays are not applied to them."""
+        n_experts * hidden rows of ffn weights.  Overlays are not applied to experts: a call raises (OVL_E_STATE) while the
+        runtime's active composition has one on any of the three.  (Replays of a captured call are not asked.)"""
         quant = runtime.quant
         planes = []
         for i in (gate, up, down):
@@ -366,12 +377,18 @@ class Moe:
                         (down, (n_experts * hidden, ffn))):
             if tuple(runtime.tensors[i][2:4]) != want:
                 raise ValueError(f"tensor {i} is {tuple(runtime.tensors[i][2:4])}, not {want}")
-        return cls(quant, n_experts, hidden, ffn, *planes, top_k, **more)
+        tensors = tuple(range(len(runtime.tensors))[i] for i in (gate, up, down))
+        _refuse_overlays(runtime, tensors)
+        layer = cls(quant, n_experts, hidden, ffn, *planes, top_k, **more)
+        layer._runtime, layer._tensors = runtime, tensors
+        return layer
 
     def __call__(self, x: torch.Tensor, choice: torch.Tensor | None = None, weight: torch.Tensor | None = None,
                  out: torch.Tensor | None = None, routing: bool = False):
         """x [tokens][hidden] -> y of the same shape and type; with routing (y, choice int32, weight float32).
         choice int32 and weight float32 [tokens][top_k] take the router's place; a negative choice is none."""
+        if self._runtime is not None:
+            _refuse_overlays(self._runtime, self._tensors)
         index = self._index
         xp, n, code, xs = _rows("x", x, self.hidden, index)
         if n > self.max_tokens:

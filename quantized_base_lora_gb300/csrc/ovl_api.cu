@@ -1221,6 +1221,25 @@ ovl_status ovl_get_entry(ovl_ctx* ctx, uint32_t i, ovl_entry* out) {
   return ok(ctx);
 }
 
+ovl_status ovl_count_overlays(ovl_ctx* ctx, uint32_t n, const uint32_t* tensors, uint32_t* out) {
+  if (!ctx || !out) return OVL_E_ARG;
+  *out = 0;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  if (!ctx->base_loaded) return fail(ctx, OVL_E_STATE, "no base loaded");
+  if (n && !tensors) return fail(ctx, OVL_E_ARG, "tensors is null");
+  uint32_t found = 0;
+  for (uint32_t i = 0; i < n; ++i) {
+    if (tensors[i] >= ctx->tensors.size()) return fail(ctx, OVL_E_ARG, "tensor index out of range");
+    for (const auto& e : ctx->active->entries) {
+      const Adapter& a = ctx->staged.at(e.h);
+      found += target_for(a, tensors[i]) != nullptr;
+      for (const auto& t : a.sp) found += t.tensor == tensors[i];
+    }
+  }
+  *out = found;
+  return ok(ctx);
+}
+
 ovl_status ovl_check_device(ovl_ctx* ctx, void* stream) {
   if (!ctx) return OVL_E_ARG;
   std::lock_guard<std::mutex> lk(ctx->mu);

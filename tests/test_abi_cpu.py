@@ -110,3 +110,7 @@ def test_status_codes_match_the_oracles_restatement(ovl):
         text = f.read()
     for name, val in re.findall(r"\b(OVL_E_[A-Z_]+)\s*=\s*(-?\d+)", text):
         assert getattr(ovl, name) == int(val)
+
+
+def test_overlays_of_no_context_are_not_counted(ovl):
+    assert ovl.ovl_count_overlays(None, [0]) == (ovl.OVL_E_ARG, 0)

@@ -322,3 +322,50 @@ def test_a_workspace_that_calls_raced_on_is_right_again_for_the_next():
         assert (words[:16] == 0).all()
         for a, b in zip(L.moe(other, routing=True), want):
             assert torch.equal(a, b)
+
+
+def test_experts_under_an_active_overlay_are_refused():
+    """Low-rank and sparse, in a stack and in a table; on another tensor, taken back or rolled back they do not matter."""
+    from quantized_base_lora_gb300.runtime import Runtime
+    rng = np.random.default_rng(5)
+    shapes = [(64, 32), (64, 32), (64, 32), (64, 32)]        # two experts of 32 x 32, and another projection
+    base = S.build_base(S.Q8_0, [(0, i, S.gaussian(rng, s, 0.05)) for i, s in enumerate(shapes)])
+    rt = Runtime(arena_bytes=32 << 20)
+    assert q.ovl_count_overlays(rt.ctx, [0]) == (q.OVL_E_STATE, 0)
+    q.check(rt.load_base(base.quant, [(t.layer, t.proj, t.d_out, t.d_in, t.qs_off, t.d_off) for t in base.tensors], base.buf,
+                         S.content_digest(base.buf)), rt.ctx)
+
+    def lora(*tensors):
+        ad = S.build_adapter(base, list(tensors), [4] * len(tensors),
+                             [(S.gaussian(rng, (4, 32), 0.1), S.gaussian(rng, (64, 4), 0.1)) for _ in tensors])
+        st, h = rt.stage(ad, S.content_digest(ad.payload))
+        q.check(st, rt.ctx)
+        return h
+
+    def sparse(tensor):
+        sp = S.build_sparse_adapter([tensor], [S.dare_entries(rng, 64, 32, 0.1)])
+        st, h = rt.stage_sparse(sp, S.content_digest(sp.payload))
+        q.check(st, rt.ctx)
+        return h
+
+    moe = B.Moe.from_base(rt, 0, 1, -2, 2, 1, router=rand(1, 2, 32))
+    x = rand(2, 3, 32)
+    want = moe(x)
+    other, two, one = lora(3), lora(3, 2), sparse(0)
+    for handles, mode, count in (([other], q.OVL_MODE_STACK, 0), ([other, two], q.OVL_MODE_STACK, 1), ([two], q.OVL_MODE_TABLE, 1),
+                                 ([one, other, two], q.OVL_MODE_STACK, 2), ([], q.OVL_MODE_STACK, 0)):
+        q.check(rt.activate(handles, [1.0] * len(handles), mode)[0], rt.ctx)
+        assert q.ovl_count_overlays(rt.ctx, [0, 1, 2]) == (0, count)
+        if count:
+            for call in (lambda: moe(x), lambda: B.Moe.from_base(rt, 0, 1, 2, 2, 1)):
+                with pytest.raises(q.OvlError) as e:
+                    call()
+                assert e.value.status == q.OVL_E_STATE
+        else:
+            assert torch.equal(moe(x), want)
+    assert q.ovl_count_overlays(rt.ctx, [3, 4])[0] == q.OVL_E_ARG and q.ovl_count_overlays(rt.ctx, []) == (0, 0)
+    q.check(rt.rollback()[0], rt.ctx)
+    with pytest.raises(q.OvlError):
+        moe(x)
+    rt.close()
+    assert torch.equal(moe(x), want)                     # the base's planes are kept
