@@ -87,17 +87,23 @@ __device__ void choose(const MoeDev& m, uint32_t token) {
       if (i * 32 + lane < m.experts) total += expf(z[i] - top);
     inv = 1.f / warp_sum(total);
   }
-  auto score = [&](float v) { return softmax ? expf(v - top) * inv : 1.f / (1.f + expf(-v)); };
+  // A score times e^-(ref - none): a weight that is divided by the chosen ones' sum goes by
+  // the scores' ratios, which the scores themselves have lost once they are below fp32's range.
+  // A sigmoid is written as e^min(v, 0) / (1 + e^-|v|), whose divisor is 1 to 2.
+  const float none = softmax ? top : 0.f;
+  auto score = [&](float v, float ref) {
+    return softmax ? expf(v - ref) * inv : expf(fminf(v, 0.f) - ref) / (1.f + expf(-fabsf(v)));
+  };
   // Without a bias the choice goes by the logits, which order as the scores do and do not saturate.
   uint32_t key[kMost];
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const uint32_t e = i * 32 + lane;
     key[i] = 0;
-    if (e < m.experts) key[i] = order_of(m.bias ? score(z[i]) + m.bias[e] : z[i]);
+    if (e < m.experts) key[i] = order_of(m.bias ? score(z[i], none) + m.bias[e] : z[i]);
   }
   uint32_t taken = 0, mine = 0;
-  float weight = 0.f;
+  float logit = -INFINITY;
   for (uint32_t s = 0; s < m.top; ++s) {
     uint32_t best = 0;
     int at = -1;
@@ -114,8 +120,12 @@ __device__ void choose(const MoeDev& m, uint32_t token) {
       taken |= 1u << (e / 32);
     }
     v = __shfl_sync(0xffffffffu, v, e & 31);
-    if (lane == s) mine = e, weight = score(v);
+    if (lane == s) mine = e, logit = v;
   }
+  float most = logit;                              // of the chosen ones
+#pragma unroll
+  for (int s = 16; s; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+  float weight = score(logit, m.renormalize ? fminf(most, none) : none);
   if (m.renormalize) weight /= warp_sum(lane < m.top ? weight : 0.f);
   weight *= m.scale;
   if (lane < m.top) {

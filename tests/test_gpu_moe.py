@@ -369,3 +369,31 @@ def test_experts_under_an_active_overlay_are_refused():
         moe(x)
     rt.close()
     assert torch.equal(moe(x), want)                     # the base's planes are kept
+
+
+@pytest.mark.parametrize("score,bias,logits", [
+    ("sigmoid", None, [-100.0, -95.5, -110.25, -98.125, -103.0, -95.625]),       # all below what fp32 scores hold
+    ("sigmoid", None, [-89.0, -90.0, -89.5, -91.0, -300.0, -89.125]),
+    ("sigmoid", None, [3.0, -100.0, -0.5, 0.0, 12.0, -20.0]),
+    ("sigmoid", [0, 5, 4, 0, 3, 0], [2.0, -120.0, -130.0, 1.0, -121.5, 0.0]),    # far-off ones by their bias
+    ("softmax", [0, 5, 4, 0, 3, 0], [2.0, -120.0, -130.0, 1.0, -121.5, 0.0]),
+    ("softmax", [0, 5, 4, 0, 3, 0], [88.0, -20.0, -18.0, 1.0, -15.5, 0.0]),      # subnormal ones
+    ("softmax", None, [500.0, 499.0, -500.0, 498.5, 0.0, 480.0])])
+@pytest.mark.parametrize("top", [1, 3])
+def test_weights_of_scores_that_32_bits_do_not_hold(score, bias, logits, top):
+    """Divided by their sum, weights go by the scores' ratios, however small the scores are.
+
+    x is a unit, so logits are exact, and so are their differences: e^ to 2 ulp, a sum and a quotient, 2^-20 in all."""
+    n = len(logits)
+    b = None if bias is None else torch.tensor(bias, dtype=F32).cuda()
+    x, router = torch.zeros((2, 64)), torch.zeros((n, 64))
+    x[:, 0], router[:, 0] = 1.0, torch.tensor(logits)
+    for renormalize in (True, False):
+        L = Layer(O.Q4_0, n, 64, 64, top, score=score, bias=b, renormalize=renormalize, scale=0.5)
+        L.router.copy_(router)
+        y, choice, weight = L.moe(x.cuda(), routing=True)
+        c, w, _ = P.route(x, router, None if b is None else b.cpu(), score, top, renormalize, 0.5)
+        assert torch.equal(choice.cpu(), c)
+        assert ((weight.cpu().double() - w).abs() <= 2.0 ** -20 * w + 2.0 ** -148).all(), (weight, w)
+        if renormalize:                                  # else weights of 2^-140 make outputs whose steps are 2^-149
+            L.check(x.cuda(), y, c, w)
