@@ -106,12 +106,14 @@ __device__ __forceinline__ void store_f32(void* base, bool bf16, uint64_t at, co
   }
 }
 
-// act(v) of OVL_ACT_*, in fp32.  The tanh of the last but one is written as
+// act(v) of OVL_ACT_*, in fp32.  1 + erf(u) is written as erfc(-u), which keeps its bits
+// where it is small (at v = -5 the sum is off by 4 %); it costs more: 4096 x 14336 in bf16
+// 109 us, 84 with the sum.  The tanh of the last but one is written as
 // (1 + tanh u) / 2 = 1 / (1 + e^(-2u)).
 __device__ __forceinline__ float activated(float v, uint32_t act) {
   switch (act) {
     case OVL_ACT_SILU: return __fdividef(v, 1.f + expf(-v));
-    case OVL_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    case OVL_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
     case OVL_ACT_GELU_TANH:
       return __fdividef(v, 1.f + expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
     default: return v < 0.f ? 0.f : v;            // a NaN stays one

@@ -398,3 +398,19 @@ def test_rotations_of_many_heads_and_tokens():
     q2, k2 = rope(pos, qk[:, :36], qk[:, 36:], dtype=F32)
     for a, b in ((qk[:, :36], q2), (qk[:, 36:], k2)):
         check_rope("pairs", P.frequencies(48), pos, a, b)
+
+
+def tail(act, until):
+    """Negative gates down to `until`, densely, beside ups of several sizes; the result in 64 bits."""
+    gate = -torch.linspace(0.01, until, 4096, device="cuda").expand(3, 4096).contiguous()
+    up = torch.tensor([1.0, -3e5, 2e-3], device="cuda")[:, None].expand(3, 4096).contiguous()
+    v = gate.double()                                    # ndtr ends at 0 below -8.3: by erfc here
+    return gate, up, (v / 2 * torch.erfc(-v / math.sqrt(2)) if act == "gelu" else P.activated(v, act)) * up.double()
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_the_negative_tail_of_gelu(out):
+    """Relative to the result, which is far below |v u| there.  The argument of erfc is off by two roundings, 2^-23 of
+    it, which a slope of up to v^2 + 1 multiplies; erfc itself 4 ulp, 2^-21; two products: (v^2 + 6) 2^-23."""
+    gate, up, want = tail("gelu", 12.5)
+    close(B.glu(gate, up, act="gelu", dtype=out), want, (gate.double().square() + 6) * 2.0 ** -23 * want.abs(), out)
