@@ -771,8 +771,8 @@ enum { OVL_ACT_SILU = 1, OVL_ACT_GELU = 2, OVL_ACT_GELU_TANH = 3, OVL_ACT_RELU =
 /* out = act(gate) * up, element by element: device [n_tokens][width], gate and up of
  * `dtype`.  OVL_ACT_SILU v / (1 + e^-v), OVL_ACT_GELU v (1 + erf(v / sqrt 2)) / 2,
  * OVL_ACT_GELU_TANH v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2, OVL_ACT_RELU
- * max(v, 0).  out may be gate or up where type and stride agree.  No counterpart in the
- * source pages. */
+ * max(v, 0).  OVL_ACT_SILU and OVL_ACT_GELU_TANH are 0 where they are below 2^-119 in size.
+ * out may be gate or up where type and stride agree.  No counterpart in the source pages. */
 ovl_status ovl_glu(uint32_t act, uint32_t n_tokens, uint32_t width, const void* gate, uint64_t gate_stride,
                    const void* up, uint64_t up_stride, uint32_t dtype, void* out, uint64_t out_stride,
                    uint32_t out_dtype, void* stream);

@@ -414,3 +414,14 @@ def test_the_negative_tail_of_gelu(out):
     it, which a slope of up to v^2 + 1 multiplies; erfc itself 4 ulp, 2^-21; two products: (v^2 + 6) 2^-23."""
     gate, up, want = tail("gelu", 12.5)
     close(B.glu(gate, up, act="gelu", dtype=out), want, (gate.double().square() + 6) * 2.0 ** -23 * want.abs(), out)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_the_negative_tail_of_the_sigmoids(act, out):
+    """Relative to the result: e^ to 2 ulp of an argument that is off by five roundings (gelu_tanh; silu's is exact),
+    2^-21 of it, a sum, a quotient to 2 ulp and a product: 2^-20 more.  Below 2^-119 the activation may be 0."""
+    gate, up, want = tail(act, 104.0 if act == "silu" else 10.6)
+    v = gate.double()
+    slope = 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3).abs() if act == "gelu_tanh" else 0.0
+    close(B.glu(gate, up, act=act, dtype=out), want, (slope * 2.0 ** -21 + 2.0 ** -20) * want.abs() + 2.0 ** -119 * up.double().abs(), out)
