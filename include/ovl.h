@@ -699,9 +699,10 @@ typedef struct {
  *                    .. 1, a = max(0, floor(c(high))), b = min(rot_dim - 1, ceil(c(low))),
  *                    c(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), b - a at least 0.001.
  * magnitude: 0 = the scaling's own (0.1 ln(factor) + 1 for OVL_ROPE_RAMP, else 1).
- * Frequencies are computed in 64 bits and held as fractions of a turn in 64-bit
- * fixed point, so that pos * turn is reduced exactly: the angle is off by less than
- * 2^-50 pos w_i, at any position.  OVL_E_SHAPE: head_dim not even or outside 2 ..
+ * Frequencies are computed in 64 bits, to about (6 + ln base) 2^-53 of themselves, and rounded to
+ * fractions of a turn in 64-bit fixed point, so that pos * turn is reduced exactly: an angle is
+ * off by |pos| times that share of w_i and times pi 2^-64 for the fixed point, and by 2 pi 2^-32
+ * radians that the kernel cuts off, at any position.  OVL_E_SHAPE: head_dim not even or outside 2 ..
  * OVL_ROPE_MAX_DIM, rot_dim not even or outside 2 .. head_dim.  OVL_E_ARG: base <= 1,
  * factor < 1, original 0 where it is used, low >= high or low <= 0, non-finite numbers.
  * No counterpart in the source pages. */

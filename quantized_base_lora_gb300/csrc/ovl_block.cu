@@ -134,7 +134,7 @@ ovl_status ovl_rope_plan(uint32_t head_dim, uint32_t rot_dim, uint32_t layout, d
       const double s = std::fmin(1, std::fmax(0, (i - first) / std::fmax(last - first, 0.001)));
       w = (1 - s) * w + s * w / factor;
     }
-    r.turn[i] = static_cast<uint64_t>(std::ldexp(w / kTurn, 64));      // w <= 1, so below 2^62
+    r.turn[i] = static_cast<uint64_t>(std::round(std::ldexp(w / kTurn, 64)));      // w <= 1, so below 2^62
   }
   *out = r;
   return OVL_OK;

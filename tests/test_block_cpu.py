@@ -346,3 +346,15 @@ def test_weights_whose_storage_is_swapped_stay_alive(q, monkeypatch):
     at = {getattr(m.moe, f) for f in ("gate_qs", "gate_d", "up_qs", "up_d", "down_qs", "down_d", "router", "bias")}
     swap([router, bias] + [t for pair in planes for t in pair])
     assert len(at) == 8 and at <= set(pointers(m._held))
+
+
+@pytest.mark.parametrize("dim,base", [(128, 500000.0), (256, 1e6), (128, 10000.0), (512, 1e12)])
+def test_plans_frequencies_are_rounded_to_the_nearest_step(q, dim, base):
+    """2^-64 of a turn is the step: half of it, and 2^-46 of the frequency itself as above."""
+    from fractions import Fraction
+    _, plan = q.ovl_rope_plan(dim, dim, q.OVL_ROPE_HALF, base)
+    tau = Fraction(6283185307179586476925286766559, 10 ** 30)
+    for i, turn in enumerate(list(plan.turn)[:dim // 2]):
+        w = Fraction(math.pow(base, -2 * i / dim))           # off by 2^-46 of itself at most
+        want = w / tau * 2 ** 64
+        assert abs(turn - want) <= Fraction(1, 2) + want * Fraction(1, 2 ** 46)
