@@ -725,7 +725,9 @@ ovl_status ovl_rope_apply(const ovl_rope* rope, uint32_t n_tokens, const int32_t
 /* Positions of a batch's new tokens in a cache (see above): pos[t], device int32
  * [n_tokens], is the place of packed token t in its sequence, counted by length;
  * -1 for a token that tok_off gives to no sequence or whose row is out of range
- * (latched as OVL_E_ARG).  One call a step serves every layer's ovl_rope_apply.
+ * (latched as OVL_E_ARG).  n_seqs = 0 is a no-op here too and leaves pos as it is, whatever
+ * n_tokens is: a caller whose padded batch may be empty sets pos itself.  One call a step
+ * serves every layer's ovl_rope_apply.
  * No counterpart in the source pages. */
 ovl_status ovl_kv_positions(const ovl_kv* kv, const int32_t* seqs, const int32_t* tok_off, uint32_t n_seqs,
                             uint32_t n_tokens, int32_t* pos, void* stream);

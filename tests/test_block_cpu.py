@@ -358,3 +358,10 @@ def test_plans_frequencies_are_rounded_to_the_nearest_step(q, dim, base):
         w = Fraction(math.pow(base, -2 * i / dim))           # off by 2^-46 of itself at most
         want = w / tau * 2 ** 64
         assert abs(turn - want) <= Fraction(1, 2) + want * Fraction(1, 2 ** 46)
+
+
+def test_positions_of_no_sequence_are_left_as_they_are(q):
+    """No sequences are a no-op of the library, as in every call of the cache: pos is not written."""
+    kv = q.ovl_kv(AT, AT, AT, AT, AT, AT, 1 << 30, 8, 16, 1, 1, 64, 4, 4)
+    pos = (ctypes.c_int32 * 4)(7, 7, 7, 7)
+    assert q.ovl_kv_positions(kv, 0, 0, 0, 4, ctypes.addressof(pos)) == 0 and list(pos) == [7] * 4
