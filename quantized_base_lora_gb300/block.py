@@ -11,7 +11,8 @@ PyTorch provides device memory and streams only; all computation is libovl's.
 
 Calls go to the current stream of the tensors' device, whichever device is current; those of one Moe must be
 ordered by streams or events, since they share its workspace.  Tensors are float32 or
-bfloat16 with contiguous channels; tokens may have any stride.  Nothing is differentiated."""
+bfloat16 with contiguous channels; tokens may have any stride that is not below their width (an expanded row is
+refused).  Nothing is differentiated."""
 from __future__ import annotations
 
 import ctypes

@@ -547,6 +547,9 @@ cudaError_t launch_block_norm(const ovl_block_norm& norm, uint32_t n_tokens, Row
   // are bound by instructions and by the exchanges of a row's sums.  fp32 rows with gates, layer
   // norms and biases: 20001 of 299, a warp a row 19 us (eight warps 87); 3001 of 1155, four
   // warps 12 (eight 15); 2003 of 4095, eight warps 37 (sixteen 67).
+  // Rows above 8192 have 32 channels of two tensors a thread in 64 registers, and spill: 952 bytes a
+  // thread, odd rows 236.  2048 rows of 16384, x bf16 and y fp32, 196 us (50 of bytes), of 12288 172
+  // (38), of 9001 286 (28).
   if (vec) {
     if (norm.hidden <= 256) return norm_of<8, 1, 32, 256, 3, 2>(a, st);
     if (norm.hidden <= 512) return norm_of<8, 2, 32, 256, 3, 2>(a, st);
@@ -567,6 +570,8 @@ cudaError_t launch_block_norm(const ovl_block_norm& norm, uint32_t n_tokens, Row
 }
 
 cudaError_t launch_glu(uint32_t act, uint32_t n_tokens, uint32_t width, Rows gate, Rows up, Rows out, cudaStream_t st) {
+  // One long row, if contiguous, has only its end at no multiple of 8; it goes to the kernel for
+  // odd rows as a whole then, like rows that begin at any address.
   GluArgs a{width, n_tokens, gate, up, out};
   if (gate.stride == width && up.stride == width && out.stride == width) {     // one long row
     a.width = static_cast<uint64_t>(width) * n_tokens;

@@ -8,10 +8,11 @@
 // integer as well, so that Taylor's series are needed for |angle| <= pi / 4 only, where
 // nine terms of both together end below 2e-9.
 // Bound by memory: each element is read once and written once.  8192 tokens of 40 heads of
-// 128 in bf16 (168 MB): 26 us, 0.96 of the copy bandwidth; 51 us while loads were converted one
+// 128 in bf16 (168 MB): 26 us, 0.95 of the copy bandwidth; 51 us while loads were converted one
 // by one, 33 while the frequencies were kernel arguments that each lane read at its own place.
-// Where halves or rows begin at odd places, pair by pair, it is bound by instructions: 37 us
-// for 34 channels of the same heads, 60 while places were divided and heads addressed in 64 bits.
+// Where halves or rows begin at odd places, all channels go pair by pair, those that are only
+// copied too, and it is bound by instructions: 37 us for 34 of 128 channels of the same heads,
+// 60 while places were divided and heads addressed in 64 bits.
 #include "block_internal.h"
 
 namespace ovl {

@@ -15,9 +15,9 @@
 // mma.sync is idle most of the time as it is.
 //
 // Measured (graph of calls, the whole layer): one fp32 token over two q8_0 experts of 4096 x
-// 14336 (375 MB) 82 us; one bf16 token over 8 of 128 q4_0 experts of 2048 x 768 (22 MB) 20; 64
-// tokens over the same experts (336 MB) 99; 19 over 64 q4_K experts of 2048 x 1280 (240 MB) 69.
-// The copies alone take 0.7 of a product's time, the arithmetic alone as much: 72
+// 14336 (375 MB) 80 us; one bf16 token over 8 of 128 q4_0 experts of 2048 x 768 (22 MB) 20; 64
+// tokens over the same experts (336 MB) 110; 19 over 64 q4_K experts of 2048 x 1280 (240 MB) 76.
+// The first product's copies alone take 0.7 of its time, the arithmetic alone as much: 75
 // instructions a 1024 weights, half of the issue slots, waits for fixed latencies between
 // them.
 //
@@ -39,11 +39,15 @@ namespace ovl {
 namespace moe {
 
 // Warps of a CTA.  16 have 128 registers each and leave less of the SM to the cache, 12 have
-// 168; q4_K holds the most in both, then the fp32 calls.  12 against 16, the whole layer in us:
+// 168; q4_K holds the most in both, then three parts.  Both products with 12 against 16, the
+// whole layer in us:
 //                                             q8_0 bf16   fp32       q4_0 bf16   fp32       q4_K bf16   fp32
-//   1 token, 2 experts of 4096 x 14336        84.7/81.5   86.7/82.7  62.2/55.9   60.6/61.6  60.6/62.4   68.3/70.5
-//   1 token, 8 of 128 experts of 2048 x 768   21.2/22.0   22.2/22.6  19.7/20.3   20.1/22.3  20.0/21.9   21.2/24.7
-//   64 tokens over the same                   144/143     183/180    103/99.2    140/146    103/106     169/181
+//   1 token, 2 experts of 4096 x 14336        84.7/78.8   85.7/80.2  62.6/57.7   60.5/60.5  61.9/62.5   66.2/69.9
+//   1 token, 8 of 128 experts of 2048 x 768   21.2/21.2   21.8/22.2  19.7/20.7   19.7/22.0  19.6/21.7   20.9/24.2
+//   64 tokens over the same                   153/152     183/180    112/109     140/146    120/123     169/181
+// The rule is the better one over the three together, for each instance, not in each of them.  (The
+// first product of q8_0 in fp32 spills 8 bytes a thread at 16 warps.  With 12 in the second and 16
+// in the first, bf16 calls of q4_0 take 56.7, 19.8 and 109.5.)
 template <uint32_t Q, int PARTS>
 constexpr uint32_t kWarps = Q == OVL_Q4_K || (Q == OVL_Q4_0 && PARTS == 3) ? 12 : 16;
 constexpr int kStages = 2;
